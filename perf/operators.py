@@ -1,0 +1,491 @@
+"""The operators of the microscaled expert and linear layers, as a user calls them, in cases of real sizes.
+
+A layer's weight is held in MXFP4 (E2M1 codes, one E8M0 scale per 32 elements along k); its activations arrive in
+bf16 and are rounded to MXFP4 ("e2m1") or MXFP8 ("e4m3") on the way into the product. Routed experts hold one weight
+each; the tokens are sorted by expert, multiplied, weighted and summed back. Kinds of cases:
+
+  linear       x -> y = q(x) W^T
+  linear_bwd   grad_y -> the gradients of x and W, straight through the rounding inside the clip range
+  up           routing -> sorted rows; x -> the experts' first product on the gathered rows
+  up_bwd       the gradients of the same, the rows' summed back to the tokens
+  down         the experts' packed rows -> the second product, weighted and summed to the tokens
+  dispatch     routing -> sorted rows; x -> packed bf16 rows (for the per-expert tensor scales)
+  combine_bwd  the gradients of the weighted sum, to the rows and to the routing weights
+
+With `own` false, `run` is the plain form: elementary torch operations in 32 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    return [
+        # one decoded token through an attention output projection: latency counts
+        {"name": "linear_token", "kind": "linear", "tokens": 1, "k": 4096, "n": 2048, "act": "e2m1"},
+        # a serving batch, W4A8, on the large hidden size
+        {"name": "linear_batch", "kind": "linear", "tokens": 37, "k": 7168, "n": 2048, "act": "e4m3"},
+        # a prefill's tokens through the attention output projection, W4A8
+        {"name": "linear_prefill", "kind": "linear", "tokens": 16384, "k": 4096, "n": 2048, "act": "e4m3"},
+        # a short ragged training step of a narrow layer
+        {"name": "linear_bwd_ragged", "kind": "linear_bwd", "tokens": 1021, "k": 2048, "n": 768, "act": "e4m3"},
+        # a training step of the attention output projection
+        {"name": "linear_bwd", "kind": "linear_bwd", "tokens": 16384, "k": 4096, "n": 2048, "act": "e2m1"},
+        # a decoding batch through 128 experts: most experts get one token or none
+        {"name": "up_decode", "kind": "up", "tokens": 24, "experts": 128, "held": 128, "topk": 8, "k": 2048, "n": 1536,
+         "act": "e2m1", "skew": 0.3},
+        # the MoE layer's prefill: 131072 rows, gate and up projection together
+        {"name": "up_prefill", "kind": "up", "tokens": 16384, "experts": 128, "held": 128, "topk": 8, "k": 2048,
+         "n": 1536, "act": "e2m1", "skew": 0.3},
+        # the second product of an odd number of tokens, W4A8, one of two expert-parallel ranks (64 of 128 experts)
+        {"name": "down_half", "kind": "down", "tokens": 8197, "experts": 128, "held": 64, "topk": 8, "k": 768,
+         "n": 2048, "act": "e4m3", "skew": 0.3},
+        # a decoding batch's second product
+        {"name": "down_decode", "kind": "down", "tokens": 24, "experts": 128, "held": 128, "topk": 8, "k": 768,
+         "n": 2048, "act": "e2m1", "skew": 0.3},
+        # a training step's gradients through the experts' first product
+        {"name": "up_bwd", "kind": "up_bwd", "tokens": 8192, "experts": 128, "held": 128, "topk": 8, "k": 2048,
+         "n": 1536, "act": "e2m1", "skew": 0.3},
+        # packed rows for the per-expert tensor scales of the MoE layer's expert input
+        {"name": "dispatch", "kind": "dispatch", "tokens": 16384, "experts": 128, "held": 128, "topk": 8, "k": 2048,
+         "skew": 0.3},
+        # the gradients of the weighted sum over a training step's tokens
+        {"name": "combine_bwd", "kind": "combine_bwd", "tokens": 16384, "experts": 128, "held": 128, "topk": 8,
+         "n": 2048, "skew": 0.3},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(["linear", "linear", "linear_bwd", "up", "up", "up_bwd", "down", "dispatch", "combine_bwd"])
+    act = rng.choice(["e2m1", "e4m3"])
+    if kind in ("linear", "linear_bwd"):
+        tokens = _log(rng, 1 if kind == "linear" else 16, 16384)
+        k, n = 32 * _log(rng, 4, 128), 16 * _log(rng, 4, 128)
+        return {"kind": kind, "tokens": tokens, "k": k, "n": n, "act": act}
+    topk = rng.choice([1, 2, 4, 6, 8])
+    experts = _log(rng, max(8, topk), 128)
+    held = experts if rng.random() < 0.6 else max(1, experts // rng.choice([2, 4]))
+    case = {"kind": kind, "tokens": _log(rng, 1 if kind in ("up", "down", "dispatch") else 16, 8192),
+            "experts": experts, "held": held, "topk": topk, "skew": round(rng.uniform(0.0, 1.0), 2)}
+    if kind in ("up", "up_bwd", "down"):
+        case.update(k=32 * _log(rng, 4, 64), n=16 * _log(rng, 8, 128), act=act)
+        if kind == "up_bwd":
+            case["tokens"] = min(case["tokens"], 4096)
+    elif kind == "dispatch":
+        case["k"] = 32 * _log(rng, 4, 224)
+    else:
+        case["n"] = 16 * _log(rng, 8, 448)
+    return case
+
+
+# ---------------------------------------------------------------------------
+# the formats, in plain operations
+# ---------------------------------------------------------------------------
+
+def _block_exponent(x, emax):
+    """Shared exponents of the 32-element blocks of x's last dimension: floor(log2(amax)) - emax, at least -127."""
+    amax = x.abs().unflatten(-1, (-1, 32)).amax(-1)
+    e = torch.frexp(amax).exponent.to(torch.int32) - 1
+    return torch.where(amax > 0, (e - emax).clamp(-127, 127), torch.full_like(e, -127))
+
+
+def _e2m1_index(a):
+    """Index of the E2M1 magnitude nearest to a in [0, 6], ties to the even index."""
+    return ((a > 0.25).to(torch.int32) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
+
+
+def _e2m1_magnitude(i):
+    """0, 0.5, 1, 1.5, 2, 3, 4, 6 by index."""
+    return torch.where(i < 4, 0.5 * i, torch.where(i < 6, i - 2.0, 2.0 * i - 8.0))
+
+
+def _e4m3_round(z):
+    """z in [-448, 448] to the nearest E4M3 value, ties to even: steps of 2^(exponent - 3), of 2^-9 below 2^-6."""
+    e = (torch.frexp(z).exponent - 1).clamp(min=-6)
+    step = torch.exp2((e - 3).to(z.dtype))
+    return torch.round(z / step) * step
+
+
+def _rounded(x, act):
+    """(the values that x's codes stand for, where x lies in the clip range) in 32 bits."""
+    x = x.float()
+    emax, top = (2, 6.0) if act == "e2m1" else (8, 448.0)
+    s = torch.ldexp(torch.ones((), device=x.device), _block_exponent(x, emax)).unsqueeze(-1)
+    z = x.unflatten(-1, (-1, 32)) / s
+    keep = z.abs() <= top
+    z = z.clamp(-top, top)
+    q = torch.sign(z) * _e2m1_magnitude(_e2m1_index(z.abs())).float() if act == "e2m1" else _e4m3_round(z)
+    return (q * s).flatten(-2), keep.flatten(-2)
+
+
+def _pack(w):
+    """(scale bytes, code bytes) of w in MXFP4: two codes a byte, the even element in the low half."""
+    e = _block_exponent(w, 2)
+    z = w.unflatten(-1, (-1, 32)) / torch.ldexp(torch.ones((), device=w.device), e).unsqueeze(-1)
+    c = (_e2m1_index(z.abs().clamp(max=6.0)) + 8 * (z < 0)).to(torch.uint8).flatten()
+    return (e + 127).to(torch.uint8).flatten(), c[0::2] | (c[1::2] << 4)
+
+
+def _pack8(a):
+    """(scale bytes, code bytes) of a in MXFP8 (E4M3)."""
+    e = _block_exponent(a, 8)
+    s = torch.ldexp(torch.ones((), device=a.device), e).unsqueeze(-1)
+    z = _e4m3_round((a.unflatten(-1, (-1, 32)) / s).clamp(-448.0, 448.0))
+    return (e + 127).to(torch.uint8).flatten(), z.to(torch.float8_e4m3fn).view(torch.uint8).flatten()
+
+
+def _values(scales, codes, act, dtype=torch.float32):
+    """The values that scale and code bytes stand for, flat."""
+    s = torch.ldexp(torch.ones((), device=codes.device, dtype=dtype), scales.to(torch.int32) - 127).unsqueeze(-1)
+    if act == "e4m3":
+        v = codes.view(torch.float8_e4m3fn).to(dtype)
+    else:
+        c = torch.stack([codes & 15, codes >> 4], -1).flatten().to(torch.int32)
+        v = torch.where(c >= 8, -1.0, 1.0).to(dtype) * _e2m1_magnitude(c & 7).to(dtype)
+    return (v.view(-1, 32) * s).flatten()
+
+
+def _bits(flags):
+    """One bit for each element, element 8j + i in bit i of byte j."""
+    f = flags.reshape(-1, 8).to(torch.int32)
+    return (f << torch.arange(8, device=f.device, dtype=torch.int32)).sum(-1).to(torch.uint8)
+
+
+def _unbits(mask, shape):
+    f = (mask.to(torch.int32).unsqueeze(-1) >> torch.arange(8, device=mask.device, dtype=torch.int32)) & 1
+    return f.reshape(shape).bool()
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+
+def _activations(rows, cols, g, dev):
+    """Activations with heavier tails than a normal's and a few loud channels."""
+    x = torch.randn(rows, cols, generator=g, device=dev)
+    x = x * (0.5 + torch.rand(rows, cols, generator=g, device=dev) * 1.5)
+    loud = torch.randint(0, cols, (max(1, cols // 256),), generator=g, device=dev)
+    x[:, loud] *= 20.0
+    return x.to(torch.bfloat16)
+
+
+def _routing(case, g, dev):
+    """Distinct experts for each token, some more popular than others, and their weights."""
+    popular = torch.randn(case["experts"], generator=g, device=dev) * case["skew"]
+    scores = torch.randn(case["tokens"], case["experts"], generator=g, device=dev) + popular
+    top = torch.topk(scores, case["topk"], dim=1)
+    return top.indices.contiguous(), torch.softmax(top.values, 1).contiguous()
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda", torch.cuda.current_device())
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    kind, tokens = case["kind"], case["tokens"]
+    s = {"case": case}
+    if "act" in case:
+        k, n, w_rows = case["k"], case["n"], case["n"] * case.get("held", 1)
+        w = torch.randn(w_rows, k, generator=g, device=dev) * 0.02
+        s["w_scales"], s["w_codes"] = _pack(w)
+        if kind.endswith("_bwd"):
+            s["w_mask"] = _bits(_rounded(w, "e2m1")[1])
+        del w
+    if "experts" in case:
+        s["ids"], s["weights"] = _routing(case, g, dev)
+        s["cap"] = max(1, int(torch.bincount(s["ids"].flatten(), minlength=case["experts"])[:case["held"]].max()))
+        if kind in ("down", "up_bwd", "combine_bwd"):  # a later step of a layer: the routing is sorted already
+            s["offsets"], s["row_index"], s["slot"] = _sorted(s["ids"], case["held"])
+        packed = tokens * case["topk"]
+    if kind in ("linear", "up", "dispatch"):
+        s["x"] = _activations(tokens, case["k"], g, dev)
+    elif kind == "down":
+        s["x"] = _activations(packed, case["k"], g, dev)
+        s["x"][s["offsets"][-1]:] = 0
+    elif kind in ("linear_bwd", "up_bwd"):
+        x = _activations(tokens, case["k"], g, dev).float()
+        s["a_scales"], s["a_codes"] = _pack(x) if case["act"] == "e2m1" else _pack8(x)
+        s["mask"] = _bits(_rounded(x, case["act"])[1])
+        rows = tokens if kind == "linear_bwd" else packed
+        s["grad_y"] = (torch.randn(rows, case["n"], generator=g, device=dev) * 0.1).to(torch.bfloat16)
+    else:
+        s["rows"] = _activations(packed, case["n"], g, dev)
+        s["grad_out"] = (torch.randn(tokens, case["n"], generator=g, device=dev) * 0.1).to(torch.bfloat16)
+    return s
+
+
+# ---------------------------------------------------------------------------
+# the plain forms
+# ---------------------------------------------------------------------------
+
+def _sorted(ids, held):
+    """(offsets, row_index, slot): the pairs (token, expert) in the order of their experts, then of their places;
+    pairs of experts that are not held come behind all others, with row index and slot -1."""
+    flat = ids.flatten()
+    there = (flat >= 0) & (flat < held)
+    key = torch.where(there, flat, held)
+    order = torch.sort(key, stable=True).indices
+    counts = torch.bincount(key, minlength=held + 1)[:held]
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    rank = torch.empty_like(order)
+    rank[order] = torch.arange(order.numel(), device=order.device)
+    row_index = torch.where(there[order], order // ids.shape[1], -1)
+    return offsets, row_index, torch.where(there, rank, -1).view(ids.shape)
+
+
+def _places(offsets, rows, cap):
+    """For each packed row its place in a [groups, cap] padding, and whether it belongs to a group."""
+    r = torch.arange(rows, device=offsets.device)
+    e = torch.searchsorted(offsets[1:], r, right=True)
+    inside = r < offsets[-1]
+    e = e.clamp(max=offsets.numel() - 2)
+    return torch.where(inside, e * cap + (r - offsets[e]), 0), inside
+
+
+def _padded(rows, offsets, cap):
+    """Packed rows as [groups, cap, cols], zeros where a group has fewer."""
+    at, inside = _places(offsets, rows.shape[0], cap)
+    out = rows.new_zeros((offsets.numel() - 1) * cap, rows.shape[1])
+    out.index_add_(0, at, rows * inside.unsqueeze(1))
+    return out.view(offsets.numel() - 1, cap, -1)
+
+
+def _unpadded(padded, offsets, rows):
+    at, inside = _places(offsets, rows, padded.shape[1])
+    return padded.flatten(0, 1)[at] * inside.unsqueeze(1)
+
+
+def _taken(x, index):
+    """Rows x[index], zeros where the index is -1."""
+    return x[index.clamp(min=0)] * (index >= 0).unsqueeze(-1)
+
+
+def _plain(s):
+    case = s["case"]
+    kind = case["kind"]
+    if "act" in case:
+        k, n, act = case["k"], case["n"], case["act"]
+        w = _values(s["w_scales"], s["w_codes"], "e2m1").view(-1, n, k)
+    if kind == "linear":
+        return {"y": (_rounded(s["x"], act)[0] @ w[0].T).to(torch.bfloat16)}
+    if kind == "linear_bwd":
+        gy = s["grad_y"].float()
+        gx = (gy @ w[0]) * _unbits(s["mask"], (-1, k))
+        gw = (gy.T @ _values(s["a_scales"], s["a_codes"], act).view(-1, k)) * _unbits(s["w_mask"], (n, k))
+        return {"grad_x": gx.to(torch.bfloat16), "grad_w": gw.to(torch.bfloat16)}
+    if kind in ("up", "dispatch"):
+        offsets, row_index, slot = _sorted(s["ids"], case["held"])
+        out = {"offsets": offsets, "row_index": row_index, "slot": slot}
+        if kind == "dispatch":
+            return out | {"rows": _taken(s["x"], row_index)}
+        a = _padded(_taken(_rounded(s["x"], act)[0], row_index), offsets, s["cap"])
+        return out | {"y": _unpadded(torch.bmm(a, w.transpose(1, 2)), offsets, row_index.numel()).to(torch.bfloat16)}
+    offsets, slot = s["offsets"], s["slot"]
+    if kind == "down":
+        y = torch.bmm(_padded(_rounded(s["x"], act)[0], offsets, s["cap"]), w.transpose(1, 2))
+        y = _taken(_unpadded(y, offsets, slot.numel()), slot)
+        return {"out": (y * s["weights"].unsqueeze(-1)).sum(1).to(torch.bfloat16)}
+    if kind == "up_bwd":
+        gy = _padded(s["grad_y"].float(), offsets, s["cap"])
+        gx = _taken(_unpadded(torch.bmm(gy, w), offsets, slot.numel()), slot).sum(1)
+        a = _padded(_taken(_values(s["a_scales"], s["a_codes"], act).view(-1, k), s["row_index"]), offsets, s["cap"])
+        gw = torch.bmm(gy.transpose(1, 2), a) * _unbits(s["w_mask"], w.shape)
+        return {"grad_x": (gx * _unbits(s["mask"], gx.shape)).to(torch.bfloat16), "grad_w": gw.to(torch.bfloat16)}
+    go, rows = s["grad_out"].float(), s["rows"].float()
+    gw = (_taken(rows, slot) * go.unsqueeze(1)).sum(-1)
+    flat = slot.flatten()
+    gr = torch.zeros_like(rows)
+    gr.index_add_(0, flat.clamp(min=0), (go.unsqueeze(1) * s["weights"].unsqueeze(-1)).flatten(0, 1)
+                  * (flat >= 0).unsqueeze(1))
+    return {"grad_rows": gr.to(torch.bfloat16), "grad_weights": gw}
+
+
+# ---------------------------------------------------------------------------
+# the framework's calls
+# ---------------------------------------------------------------------------
+
+def _calls(s):
+    import fp4_rollout_guided_amd as tr
+    case = s["case"]
+    kind = case["kind"]
+    if "act" in case:
+        k, n, mx = case["k"], case["n"], case["act"] == "e2m1"
+    if kind == "linear":
+        return {"y": (tr.mx_linear if mx else tr.mx8_linear)(s["x"], s["w_scales"], s["w_codes"], n)}
+    if kind == "linear_bwd":
+        gx = tr.mx_matmul_bwd_input(s["grad_y"], s["w_scales"], s["w_codes"], k, mask=s["mask"])
+        gw = (tr.mx_matmul_bwd_weight if mx else tr.mx8_matmul_bwd_weight)(s["grad_y"], s["a_scales"], s["a_codes"], k,
+                                                                         mask=s["w_mask"])
+        return {"grad_x": gx, "grad_w": gw}
+    if kind in ("up", "dispatch"):
+        offsets, row_index, slot = tr.expert_sort(s["ids"], case["held"])
+        out = {"offsets": offsets, "row_index": row_index, "slot": slot}
+        if kind == "dispatch":
+            return out | {"rows": tr.expert_dispatch(s["x"], row_index)}
+        linear = tr.grouped_mx_linear if mx else tr.grouped_mx8_linear
+        return out | {"y": linear(s["x"], offsets, s["w_scales"], s["w_codes"], n, row_index=row_index)}
+    if kind == "down":
+        linear = tr.grouped_mx_linear if mx else tr.grouped_mx8_linear
+        y = linear(s["x"], s["offsets"], s["w_scales"], s["w_codes"], n)
+        return {"out": tr.expert_combine(y, s["slot"], s["weights"])}
+    if kind == "up_bwd":
+        gr = tr.grouped_mx_matmul_bwd_input(s["grad_y"], s["offsets"], s["w_scales"], s["w_codes"], k)
+        gx = tr.ste_bwd(tr.expert_combine(gr, s["slot"]), s["mask"])
+        bwd_weight = tr.grouped_mx_matmul_bwd_weight if mx else tr.grouped_mx8_matmul_bwd_weight
+        gw = bwd_weight(s["grad_y"], s["offsets"], s["a_scales"], s["a_codes"], k, row_index=s["row_index"],
+                        mask=s["w_mask"])
+        return {"grad_x": gx, "grad_w": gw.view(case["held"], n, k)}
+    gr, gw = tr.expert_combine_bwd(s["grad_out"], s["rows"], s["slot"], s["weights"], s["offsets"])
+    return {"grad_rows": gr, "grad_weights": gw}
+
+
+def run(state):
+    return _calls(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+
+def work(case):
+    """Inputs once, outputs once; of a weight what the rows reach (a decoding batch does not reach every expert),
+    of the rows the share that the held experts get."""
+    kind, tokens = case["kind"], case["tokens"]
+    k, n = case.get("k", 0), case.get("n", 0)
+    code = {"e2m1": 0.5, "e4m3": 1.0}.get(case.get("act"), 0) + 1 / 32
+    if kind == "linear":
+        return {"bytes": 2 * tokens * k + 17 / 32 * n * k + 2 * tokens * n, "flops": 2 * tokens * n * k}
+    if kind == "linear_bwd":
+        moved = 2 * tokens * n + tokens * k * (code + 2 + 1 / 8) + n * k * (17 / 32 + 1 / 8 + 2)
+        return {"bytes": moved, "flops": 4 * tokens * n * k}
+    packed, held = tokens * case["topk"], case["held"]
+    rows = packed * held / case["experts"]
+    reached = held * (1 - (1 - case["topk"] / case["experts"]) ** tokens)
+    sort = 8 * (packed * 3 + held + 1)
+    if kind == "up":
+        return {"bytes": sort + 2 * tokens * k + 17 / 32 * reached * n * k + 2 * packed * n, "flops": 2 * rows * n * k}
+    if kind == "dispatch":
+        return {"bytes": sort + 2 * tokens * k + 2 * packed * k, "flops": 0}
+    if kind == "down":
+        moved = 2 * rows * k + 17 / 32 * reached * n * k + 12 * packed + 2 * tokens * n
+        return {"bytes": moved, "flops": 2 * rows * n * k + 2 * rows * n}
+    if kind == "up_bwd":
+        moved = 2 * rows * n + tokens * k * (code + 2 + 1 / 8) + held * n * k * (17 / 32 + 1 / 8 + 2) + 16 * packed
+        return {"bytes": moved, "flops": 4 * rows * n * k}
+    return {"bytes": 2 * tokens * n + 2 * rows * n + 2 * packed * n + 16 * packed, "flops": 3 * rows * n}
+
+
+# ---------------------------------------------------------------------------
+# the definition, in 64 bits
+# ---------------------------------------------------------------------------
+
+_GRID = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def _grid(act, dev):
+    """The format's magnitudes in ascending order; those at even places end in a zero bit."""
+    if act == "e2m1":
+        v = _GRID
+    else:
+        v = [m * 2.0 ** -9 for m in range(8)] + [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8)][:-1]
+    return torch.tensor(v, dtype=torch.float64, device=dev)
+
+
+def _exact_rounded(x, act):
+    """x's blocks on the format's grid by a search for the nearest magnitude, ties to the even place."""
+    x = x.double()
+    grid = _grid(act, x.device)
+    b = x.reshape(-1, 32)
+    amax = b.abs().amax(1, keepdim=True)
+    e = torch.floor(torch.log2(torch.where(amax > 0, amax, 1.0)))
+    e = e + (torch.exp2(e + 1) <= amax).double() - (torch.exp2(e) > amax).double() * (amax > 0)
+    s = torch.where(amax > 0, torch.exp2((e - (2 if act == "e2m1" else 8)).clamp(-127, 127)), torch.exp2(-127 * torch.ones_like(amax)))
+    z = (b / s).abs().clamp(max=float(grid[-1]))
+    hi = torch.searchsorted(grid, z).clamp(1, grid.numel() - 1)
+    below, above = z - grid[hi - 1], grid[hi] - z
+    up = (above < below) | ((above == below) & (hi % 2 == 0))
+    return (torch.copysign(grid[torch.where(up, hi, hi - 1)], b) * s).view(x.shape)
+
+
+def _exact_values(scales, codes, act):
+    s = torch.exp2(scales.double() - 127).unsqueeze(1)
+    if act == "e4m3":
+        c = codes.to(torch.int64)
+        v = _grid(act, codes.device)[c & 127] * (1 - 2 * (c >> 7))
+    else:
+        c = torch.stack([codes.to(torch.int64) % 16, codes.to(torch.int64) // 16], 1).flatten()
+        v = _grid(act, codes.device)[c % 8] * (1 - 2 * (c // 8))
+    return (v.view(-1, 32) * s).flatten()
+
+
+def _exact_flags(mask):
+    return torch.stack([(mask >> i) & 1 for i in range(8)], 1).flatten().double()
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    kind, dev = case["kind"], s.get("ids", s.get("w_codes")).device
+    if "act" in case:
+        k, n, act = case["k"], case["n"], case["act"]
+        w = _exact_values(s["w_scales"], s["w_codes"], "e2m1").view(-1, n, k)
+    if kind == "linear":
+        return {"y": torch.mm(_exact_rounded(s["x"], act), w[0].t().contiguous())}
+    if kind == "linear_bwd":
+        gy = s["grad_y"].double()
+        a = _exact_values(s["a_scales"], s["a_codes"], act).view(-1, k)
+        return {"grad_x": torch.mm(gy, w[0]) * _exact_flags(s["mask"]).view(-1, k),
+                "grad_w": torch.mm(gy.t().contiguous(), a) * _exact_flags(s["w_mask"]).view(n, k)}
+    tokens, topk, held = case["tokens"], case["topk"], case["held"]
+    groups = [torch.nonzero(s["ids"].flatten() == e).flatten() for e in range(held)]  # each expert's pairs, ascending
+    ends = [0]
+    for at in groups:
+        ends.append(ends[-1] + at.numel())
+    pairs = torch.cat(groups)
+    slot = torch.full((tokens * topk,), -1, dtype=torch.int64, device=dev)
+    slot[pairs] = torch.arange(ends[-1], device=dev)
+    row_index = torch.full((tokens * topk,), -1, dtype=torch.int64, device=dev)
+    row_index[:ends[-1]] = torch.div(pairs, topk, rounding_mode="floor")
+    sort = {"offsets": torch.tensor(ends, device=dev), "row_index": row_index, "slot": slot.view(tokens, topk)}
+    if kind == "dispatch":
+        rows = torch.zeros(tokens * topk, case["k"], dtype=torch.float64, device=dev)
+        rows[:ends[-1]] = s["x"].double()[row_index[:ends[-1]]]
+        return sort | {"rows": rows}
+    if kind in ("up", "down"):
+        x = _exact_rounded(s["x"], act)
+        y = torch.zeros(tokens * topk, n, dtype=torch.float64, device=dev)
+        for e in range(held):
+            lo, hi = ends[e], ends[e + 1]
+            if lo < hi:
+                y[lo:hi] = torch.mm(x[row_index[lo:hi]] if kind == "up" else x[lo:hi], w[e].t().contiguous())
+        if kind == "up":
+            return sort | {"y": y}
+        out = torch.zeros(tokens, n, dtype=torch.float64, device=dev)
+        out.index_add_(0, row_index[:ends[-1]], y[:ends[-1]] * s["weights"].double().flatten()[pairs].unsqueeze(1))
+        return {"out": out}
+    if kind == "up_bwd":
+        gy = s["grad_y"].double()
+        a = _exact_values(s["a_scales"], s["a_codes"], act).view(-1, k)
+        gx = torch.zeros(tokens, k, dtype=torch.float64, device=dev)
+        gw = torch.zeros(held, n, k, dtype=torch.float64, device=dev)
+        for e in range(held):
+            lo, hi = ends[e], ends[e + 1]
+            if lo < hi:
+                gx.index_add_(0, row_index[lo:hi], torch.mm(gy[lo:hi], w[e]))
+                gw[e] = torch.mm(gy[lo:hi].t().contiguous(), a[row_index[lo:hi]])
+        return {"grad_x": gx * _exact_flags(s["mask"]).view(tokens, k),
+                "grad_w": gw * _exact_flags(s["w_mask"]).view(held, n, k)}
+    go, rows = s["grad_out"].double(), s["rows"].double()
+    gr = torch.zeros_like(rows)
+    gr[:ends[-1]] = go[row_index[:ends[-1]]] * s["weights"].double().flatten()[pairs].unsqueeze(1)
+    gw = torch.zeros(tokens * topk, dtype=torch.float64, device=dev)
+    gw[pairs] = (go[row_index[:ends[-1]]] * rows[:ends[-1]]).sum(1)
+    return {"grad_rows": gr, "grad_weights": gw.view(tokens, topk)}
