@@ -31,8 +31,24 @@ Functions mirror the C ABI in ``include/trace.h``:
     ste_bwd(grad_out, mask)                          -> grad_in
     mismatch_stats(x_train, scales, ts, bits, codes, stats=None) -> stats (int64[20], added to)
 
-and ``GuidedFakeQuant`` wraps the forward/backward pair as an autograd
-function.
+products of the rounded operands (weights in MXFP4; activations in MXFP4, or
+in MXFP8 with the mx8_ forms; grouped_ forms: one weight per group of rows):
+
+    mx_quantize(x, want_mask=False)                  -> (scales, codes, mask)   (and mx8_quantize)
+    mx_matmul(a_scales, a_codes, w_scales, w_codes, n, k) -> y bf16 [rows, n]   (mx8_, grouped_)
+    mx_linear(x, w_scales, w_codes, n)               -> y: quantise, then multiply (mx8_, grouped_)
+    mx_matmul_bwd_input(grad_y, w_scales, w_codes, k, mask=None)  -> grad_x     (grouped_)
+    mx_matmul_bwd_weight(grad_y, a_scales, a_codes, k, mask=None) -> grad_w     (mx8_, grouped_)
+
+routed rows (the groups of the grouped_ forms):
+
+    expert_sort(ids, experts)                        -> (offsets, row_index, slot)
+    expert_dispatch(x, row_index)                    -> packed rows
+    expert_combine(y, slot, weights=None)            -> the tokens' weighted sums
+    expert_combine_bwd(grad_out, y, slot, weights, offsets=None) -> (grad_y, grad_weights)
+
+and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch`` and ``ExpertCombine``
+wrap the forward/backward pairs as autograd functions.
 """
 import ctypes
 import os
@@ -49,6 +65,11 @@ __all__ = [
     "mx_full_info_fakequant_fwd", "mx8_capture", "mx8_guided_fakequant_fwd", "mx8_rne_fakequant_fwd",
     "mx8_full_info_fakequant_fwd", "capture_lowbits", "lowbits_fakequant_fwd", "mismatch_stats", "STAT_FIELDS",
     "GuidedFakeQuant", "tensor_scale_batch", "capture_batch", "MAX_BATCH_SITES",
+    "mx_quantize", "mx8_quantize", "mx_matmul", "mx8_matmul", "grouped_mx_matmul", "grouped_mx8_matmul", "mx_linear",
+    "mx8_linear", "grouped_mx_linear", "grouped_mx8_linear", "mx_matmul_bwd_input", "grouped_mx_matmul_bwd_input",
+    "mx_matmul_bwd_weight", "mx8_matmul_bwd_weight", "grouped_mx_matmul_bwd_weight", "grouped_mx8_matmul_bwd_weight",
+    "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_bwd", "MxMatmul", "ExpertDispatch",
+    "ExpertCombine", "MAX_EXPERTS", "MAX_TOPK", "MAX_PRODUCT_GROUPS",
     "STATUS",
 ]
 
@@ -113,7 +134,23 @@ def load_library(path):
         "trace_tensor_scale_batch_workspace_bytes": ([p, ctypes.c_int32], sz),
         "trace_tensor_scale_batch": ([p, ctypes.c_int32, p, sz, p], st),
         "trace_capture_batch": ([p, ctypes.c_int32, p], st),
+        "trace_mx_quantize": ([p, i64, i64, p, p, p, p], st),
+        "trace_mx_matmul": ([p, p, i64, p, p, i64, i64, p, p], st),
+        "trace_grouped_mx_matmul": ([p, p, i64, p, i64, p, i64, p, p, i64, i64, p, p], st),
+        "trace_mx_linear_workspace_bytes": ([i64, i64], sz),
+        "trace_mx_linear": ([p, i64, p, i64, p, i64, p, p, i64, i64, p, sz, p, p], st),
+        "trace_mx_matmul_bwd_input": ([p, i64, p, i64, p, p, i64, i64, p, p, p], st),
+        "trace_mx_matmul_bwd_weight_workspace_bytes": ([i64, i64, i64, i64], sz),
+        "trace_mx_matmul_bwd_weight": ([p, i64, p, i64, p, p, i64, p, i64, i64, p, p, p, sz, p], st),
+        "trace_expert_sort_workspace_bytes": ([i64, i64, i64], sz),
+        "trace_expert_sort": ([p, i64, i64, i64, p, sz, p, p, p, p], st),
+        "trace_expert_dispatch": ([p, i64, i64, p, i64, p, p], st),
+        "trace_expert_combine": ([p, i64, i64, p, p, i64, i64, p, p], st),
+        "trace_expert_combine_bwd": ([p, p, i64, i64, p, p, i64, i64, p, i64, p, p, p], st),
     }
+    for name in ("quantize", "matmul", "linear_workspace_bytes", "linear", "matmul_bwd_weight"):
+        sig["trace_mx8_" + name] = sig["trace_mx_" + name]
+    sig["trace_grouped_mx8_matmul"] = sig["trace_grouped_mx_matmul"]
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -707,3 +744,423 @@ class GuidedFakeQuant(torch.autograd.Function):
     def backward(ctx, grad_out):
         (mask,) = ctx.saved_tensors
         return ste_bwd(grad_out.contiguous(), mask), None, None, None
+
+
+# --------------------------------------------------------------------------
+# products of microscaled operands
+# --------------------------------------------------------------------------
+
+MAX_EXPERTS = 1024
+MAX_TOPK = 64
+MAX_PRODUCT_GROUPS = 4096
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, like, *args):
+    """Call an entry point on ``like``'s device and its current stream."""
+    dev = like.device.index
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(name, like, *args)
+    _check(getattr(lib, name)(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+
+
+def _matrix(t, name):
+    """A contiguous bf16 device tensor as (rows, cols) over its last dimension."""
+    _bf16(t, name)
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+
+
+def _dim(v, name, multiple):
+    if isinstance(v, bool) or not isinstance(v, int) or v < 0 or v % multiple:
+        raise ValueError(f"{name} must be a non-negative multiple of {multiple}, got {v!r}")
+    return v
+
+
+def _fit(t, name, like, dtypes, numel):
+    """``_arg`` for a tensor that must hold exactly ``numel`` elements."""
+    _arg(t, name, like, dtypes, numel)
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+    return t
+
+
+def _code_bytes(fmt, n):
+    return n // 2 if fmt == "mx" else n
+
+
+def _out(t, name, like, shape, dtype):
+    n = 1
+    for d in shape:
+        n *= d
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _arg(t, name, like, _BF16 if dtype == torch.bfloat16 else (dtype,), n)
+
+
+def _workspace(t, like, need):
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    return _arg(t, "workspace", like, _U8, need)
+
+
+def _groups(offsets, like):
+    """(address, groups, weights) of a product's groups; offsets None: one weight."""
+    if offsets is None:
+        return None, 0, 1
+    groups = _offsets(offsets, like)
+    if groups > MAX_PRODUCT_GROUPS:
+        raise ValueError(f"at most {MAX_PRODUCT_GROUPS} groups, got {groups}")
+    return offsets.data_ptr(), groups, groups
+
+
+def _quantize(fmt, x, want_mask, scales, codes, mask):
+    rows, cols = _matrix(x, "x")
+    n = rows * cols
+    scales = _u8(n // 32, x, scales, "scales")
+    codes = _u8(_code_bytes(fmt, n), x, codes, "codes")
+    if want_mask or mask is not None:
+        mask = _u8(n // 8, x, mask, "mask")
+    _launch(f"trace_{fmt}_quantize", x, _addr(x), rows, cols, _addr(scales), _addr(codes), _addr(mask))
+    return scales, codes, mask
+
+
+def mx_quantize(x, want_mask=False, scales=None, codes=None, mask=None):
+    """MXFP4 operand of a product: (scales u8[n/32], codes u8[n/2], clip mask
+    u8[n/8] or None), the scales and codes of ``mx_capture`` in one pass."""
+    return _quantize("mx", x, want_mask, scales, codes, mask)
+
+
+def mx8_quantize(x, want_mask=False, scales=None, codes=None, mask=None):
+    """MXFP8 operand of a product: (scales u8[n/32], codes u8[n], clip mask
+    u8[n/8] or None), the scales and codes of ``mx8_capture`` in one pass."""
+    return _quantize("mx8", x, want_mask, scales, codes, mask)
+
+
+def _record(fmt, scales, codes, like, k, prefix):
+    """Rows of a stored operand [rows, k]."""
+    _arg(scales, f"{prefix}_scales", like, _U8, 0)
+    if k == 0:
+        raise ValueError("k must be positive")
+    rows = scales.numel() * 32 // k
+    _fit(scales, f"{prefix}_scales", like, _U8, rows * (k // 32))
+    _fit(codes, f"{prefix}_codes", like, _U8, _code_bytes(fmt, rows * k))
+    return rows
+
+
+def _weight(w_scales, w_codes, like, weights, n, k):
+    _fit(w_scales, "w_scales", like, _U8, weights * n * (k // 32))
+    _fit(w_codes, "w_codes", like, _U8, weights * n * k // 2)
+
+
+def _index(row_index, like):
+    _arg(row_index, "row_index", like, _I64, 0)
+    return row_index.numel()
+
+
+def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index, y):
+    if not isinstance(a_codes, torch.Tensor) or not a_codes.is_cuda:
+        raise ValueError("a_codes must be a device tensor")
+    _dim(n, "n", 16)
+    _dim(k, "k", 32)
+    src_rows = _record(fmt, a_scales, a_codes, a_codes, k, "a")
+    at, groups, weights = _groups(offsets, a_codes)
+    _weight(w_scales, w_codes, a_codes, weights, n, k)
+    rows = src_rows if row_index is None else _index(row_index, a_codes)
+    y = _out(y, "y", a_codes, (rows, n), torch.bfloat16)
+    if offsets is None:
+        _launch(f"trace_{fmt}_matmul", a_codes, _addr(a_scales), _addr(a_codes), rows, _addr(w_scales), _addr(w_codes),
+                n, k, _addr(y))
+    else:
+        _launch(f"trace_grouped_{fmt}_matmul", a_codes, _addr(a_scales), _addr(a_codes), src_rows, _addr(row_index),
+                rows, at, groups, _addr(w_scales), _addr(w_codes), n, k, _addr(y))
+    return y
+
+
+def mx_matmul(a_scales, a_codes, w_scales, w_codes, n, k, y=None):
+    """y = A W^T (bf16 [rows, n]) of MXFP4 activations [rows, k] and an MXFP4
+    weight [n, k]; n % 16 == 0, k % 32 == 0."""
+    return _matmul("mx", a_scales, a_codes, None, w_scales, w_codes, n, k, None, y)
+
+
+def mx8_matmul(a_scales, a_codes, w_scales, w_codes, n, k, y=None):
+    """``mx_matmul`` with MXFP8 activations (W4A8)."""
+    return _matmul("mx8", a_scales, a_codes, None, w_scales, w_codes, n, k, None, y)
+
+
+def grouped_mx_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None):
+    """``mx_matmul`` of packed rows [offsets[g], offsets[g+1]) with the g-th of
+    the weights [groups, n, k].  Packed row r is row r of the activations, or,
+    with ``row_index`` (int64, one per packed row), row row_index[r].  Rows
+    behind the last group give zeros."""
+    return _matmul("mx", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y)
+
+
+def grouped_mx8_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None):
+    """``grouped_mx_matmul`` with MXFP8 activations (W4A8)."""
+    return _matmul("mx8", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y)
+
+
+def _need(offsets):
+    if offsets is None:
+        raise ValueError("offsets is required")
+    return offsets
+
+
+def _linear(fmt, x, offsets, w_scales, w_codes, n, row_index, workspace, y):
+    src_rows, k = _matrix(x, "x")
+    _dim(n, "n", 16)
+    at, groups, weights = _groups(offsets, x)
+    _weight(w_scales, w_codes, x, weights, n, k)
+    rows = src_rows if row_index is None else _index(row_index, x)
+    shape = (rows, n) if row_index is not None else (*x.shape[:-1], n)
+    y = _out(y, "y", x, shape, torch.bfloat16)
+    workspace = _workspace(workspace, x, getattr(lib, f"trace_{fmt}_linear_workspace_bytes")(src_rows, k))
+    _launch(f"trace_{fmt}_linear", x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales),
+            _addr(w_codes), n, k, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(y))
+    return y
+
+
+def mx_linear(x, w_scales, w_codes, n, workspace=None, y=None):
+    """y = q(x) W^T: bf16 activations x [..., k] rounded to MXFP4 (as
+    ``mx_quantize``) and multiplied by the MXFP4 weight [n, k]."""
+    return _linear("mx", x, None, w_scales, w_codes, n, None, workspace, y)
+
+
+def mx8_linear(x, w_scales, w_codes, n, workspace=None, y=None):
+    """``mx_linear`` with the activations rounded to MXFP8 (W4A8)."""
+    return _linear("mx8", x, None, w_scales, w_codes, n, None, workspace, y)
+
+
+def grouped_mx_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None):
+    """``mx_linear`` per group of packed rows, as ``grouped_mx_matmul``: with
+    ``row_index``, x holds the tokens, each rounded once for all its experts."""
+    return _linear("mx", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y)
+
+
+def grouped_mx8_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None):
+    """``grouped_mx_linear`` with the activations rounded to MXFP8 (W4A8)."""
+    return _linear("mx8", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y)
+
+
+def _bwd_input(grad_y, offsets, w_scales, w_codes, k, mask, grad_x):
+    rows, n = _matrix(grad_y, "grad_y")
+    _dim(k, "k", 32)
+    at, groups, weights = _groups(offsets, grad_y)
+    _weight(w_scales, w_codes, grad_y, weights, n, k)
+    if mask is not None:
+        _arg(mask, "mask", grad_y, _U8, rows * k // 8)
+    grad_x = _out(grad_x, "grad_x", grad_y, (*grad_y.shape[:-1], k), torch.bfloat16)
+    _launch("trace_mx_matmul_bwd_input", grad_y, _addr(grad_y), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k,
+            _addr(mask), _addr(grad_x))
+    return grad_x
+
+
+def mx_matmul_bwd_input(grad_y, w_scales, w_codes, k, mask=None, grad_x=None):
+    """grad_x = grad_y W (bf16 [..., k]), zero where the activations' clip
+    mask is 0; for MXFP4 and MXFP8 activations alike."""
+    return _bwd_input(grad_y, None, w_scales, w_codes, k, mask, grad_x)
+
+
+def grouped_mx_matmul_bwd_input(grad_y, offsets, w_scales, w_codes, k, mask=None, grad_x=None):
+    """``mx_matmul_bwd_input`` per group of packed rows, in packed order (sum
+    the rows of a token with ``expert_combine``)."""
+    return _bwd_input(grad_y, _need(offsets), w_scales, w_codes, k, mask, grad_x)
+
+
+def _bwd_weight(fmt, grad_y, offsets, a_scales, a_codes, k, row_index, mask, grad_w, workspace):
+    rows, n = _matrix(grad_y, "grad_y")
+    _dim(k, "k", 32)
+    at, groups, weights = _groups(offsets, grad_y)
+    src_rows = _record(fmt, a_scales, a_codes, grad_y, k, "a")
+    if row_index is not None:
+        _fit(row_index, "row_index", grad_y, _I64, rows)
+    elif src_rows != rows:
+        raise ValueError(f"grad_y has {rows} rows, the activations {src_rows}")
+    if mask is not None:
+        _arg(mask, "mask", grad_y, _U8, weights * n * k // 8)
+    grad_w = _out(grad_w, "grad_w", grad_y, (n, k) if offsets is None else (weights, n, k), torch.bfloat16)
+    workspace = _workspace(workspace, grad_y, lib.trace_mx_matmul_bwd_weight_workspace_bytes(rows, groups, n, k))
+    _launch(f"trace_{fmt}_matmul_bwd_weight", grad_y, _addr(grad_y), rows, at, groups, _addr(a_scales), _addr(a_codes),
+            src_rows, _addr(row_index), n, k, _addr(mask), _addr(grad_w), _addr(workspace),
+            0 if workspace is None else workspace.numel())
+    return grad_w
+
+
+def mx_matmul_bwd_weight(grad_y, a_scales, a_codes, k, mask=None, grad_w=None, workspace=None):
+    """grad_w = grad_y^T A (bf16 [n, k]) with MXFP4 activations A, zero where
+    the weight's clip mask is 0."""
+    return _bwd_weight("mx", grad_y, None, a_scales, a_codes, k, None, mask, grad_w, workspace)
+
+
+def mx8_matmul_bwd_weight(grad_y, a_scales, a_codes, k, mask=None, grad_w=None, workspace=None):
+    """``mx_matmul_bwd_weight`` with MXFP8 activations."""
+    return _bwd_weight("mx8", grad_y, None, a_scales, a_codes, k, None, mask, grad_w, workspace)
+
+
+def grouped_mx_matmul_bwd_weight(grad_y, offsets, a_scales, a_codes, k, row_index=None, mask=None, grad_w=None,
+                                 workspace=None):
+    """``mx_matmul_bwd_weight`` per group of packed rows: bf16 [groups, n, k],
+    zeros for a group without rows."""
+    return _bwd_weight("mx", grad_y, _need(offsets), a_scales, a_codes, k, row_index, mask, grad_w, workspace)
+
+
+def grouped_mx8_matmul_bwd_weight(grad_y, offsets, a_scales, a_codes, k, row_index=None, mask=None, grad_w=None,
+                                  workspace=None):
+    """``grouped_mx_matmul_bwd_weight`` with MXFP8 activations."""
+    return _bwd_weight("mx8", grad_y, _need(offsets), a_scales, a_codes, k, row_index, mask, grad_w, workspace)
+
+
+# --------------------------------------------------------------------------
+# routed rows
+# --------------------------------------------------------------------------
+
+def _pairs(t, name, like, dtypes):
+    """A contiguous [tokens, topk] device tensor as (tokens, topk)."""
+    _arg(t, name, like, dtypes, 0)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [tokens, topk], got {tuple(t.shape)}")
+    tokens, topk = t.shape
+    if not 1 <= topk <= MAX_TOPK:
+        raise ValueError(f"topk must be 1 to {MAX_TOPK}, got {topk}")
+    return tokens, topk
+
+
+def expert_sort(ids, experts, offsets=None, row_index=None, slot=None, workspace=None):
+    """Stable sort of the (token, expert) pairs by expert.  ids: int64
+    [tokens, topk]; pairs whose id lies outside [0, experts) are left out.
+    Returns (offsets int64[experts + 1]: the experts' packed rows, row_index
+    int64[tokens*topk]: the token of each packed row, -1 behind the last
+    group, slot int64[tokens, topk]: the packed row of each pair or -1)."""
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise ValueError("ids must be a device tensor")
+    tokens, topk = _pairs(ids, "ids", ids, _I64)
+    if isinstance(experts, bool) or not isinstance(experts, int) or not 1 <= experts <= MAX_EXPERTS:
+        raise ValueError(f"experts must be 1 to {MAX_EXPERTS}, got {experts!r}")
+    offsets = _out(offsets, "offsets", ids, (experts + 1,), torch.int64)
+    row_index = _out(row_index, "row_index", ids, (tokens * topk,), torch.int64)
+    slot = _out(slot, "slot", ids, (tokens, topk), torch.int64)
+    workspace = _workspace(workspace, ids, lib.trace_expert_sort_workspace_bytes(tokens, topk, experts))
+    _launch("trace_expert_sort", ids, _addr(ids), tokens, topk, experts, _addr(workspace),
+            0 if workspace is None else workspace.numel(), _addr(offsets), _addr(row_index), _addr(slot))
+    return offsets, row_index, slot
+
+
+def expert_dispatch(x, row_index, out=None):
+    """Packed rows: row r is row row_index[r] of x (bf16 [..., cols]), zeros
+    for an index outside x."""
+    tokens, cols = _matrix(x, "x")
+    rows = _index(row_index, x)
+    out = _out(out, "out", x, (rows, cols), torch.bfloat16)
+    _launch("trace_expert_dispatch", x, _addr(x), tokens, cols, _addr(row_index), rows, _addr(out))
+    return out
+
+
+def expert_combine(y, slot, weights=None, out=None):
+    """The tokens' sums of their packed rows, out[t] = sum over j of
+    weights[t, j] * y[slot[t, j]] (fp32 weights; None: ones); pairs whose slot
+    lies outside y are left out."""
+    rows, cols = _matrix(y, "y")
+    tokens, topk = _pairs(slot, "slot", y, _I64)
+    if weights is not None:
+        _fit(weights, "weights", y, _F32, tokens * topk)
+    out = _out(out, "out", y, (tokens, cols), torch.bfloat16)
+    _launch("trace_expert_combine", y, _addr(y), rows, cols, _addr(slot), _addr(weights), tokens, topk, _addr(out))
+    return out
+
+
+def expert_combine_bwd(grad_out, y, slot, weights, offsets=None, grad_y=None, grad_weights=None):
+    """Gradients of ``expert_combine``: (grad_y bf16, packed as y; grad_weights
+    fp32 [tokens, topk]).  Rows behind the last group of ``offsets`` become
+    zeros; without offsets, rows that no slot names are zeros in a grad_y made
+    here and are left as they are in one passed in."""
+    rows, cols = _matrix(y, "y")
+    tokens, topk = _pairs(slot, "slot", y, _I64)
+    t, c = _matrix(grad_out, "grad_out")
+    if grad_out.device != y.device or (t, c) != (tokens, cols):
+        raise ValueError(f"grad_out must be [{tokens}, {cols}] on {y.device}, got {tuple(grad_out.shape)}")
+    if weights is not None:
+        _fit(weights, "weights", y, _F32, tokens * topk)
+    at, groups, _ = _groups(offsets, y)
+    if grad_y is None and offsets is None:
+        grad_y = torch.zeros_like(y)
+    grad_y = _out(grad_y, "grad_y", y, tuple(y.shape), torch.bfloat16)
+    grad_weights = _out(grad_weights, "grad_weights", y, (tokens, topk), torch.float32)
+    _launch("trace_expert_combine_bwd", y, _addr(grad_out), _addr(y), rows, cols, _addr(slot), _addr(weights), tokens,
+            topk, at, groups, _addr(grad_y), _addr(grad_weights))
+    return grad_y, grad_weights
+
+
+class MxMatmul(torch.autograd.Function):
+    """y = q(x) q(w)^T with both operands rounded in the forward and the
+    gradients passed straight through inside the clip ranges.
+
+    x: bf16 [rows, k]; w: bf16 [n, k], or [groups, n, k] with ``offsets`` (the
+    packed rows' groups).  fmt: "mx" (MXFP4 activations) or "mx8" (MXFP8).
+    scales, bits: the rollout's record of x in that format; x is then rounded
+    by the rollout-guided rule instead of to nearest."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets=None, fmt="mx", scales=None, bits=None):
+        if fmt not in ("mx", "mx8"):
+            raise ValueError(f'fmt must be "mx" or "mx8", got {fmt!r}')
+        x, w = x.contiguous(), w.contiguous()
+        n, k = w.shape[-2:]
+        if scales is None:
+            a_scales, a_codes, a_mask = _quantize(fmt, x, True, None, None, None)
+        else:
+            guided = mx_guided_fakequant_fwd if fmt == "mx" else mx8_guided_fakequant_fwd
+            a_scales, (_, a_mask, a_codes) = scales, guided(x, scales, bits, want_codes=True)
+        w_scales, w_codes, w_mask = mx_quantize(w, want_mask=True)
+        ctx.save_for_backward(a_scales, a_codes, a_mask, w_scales, w_codes, w_mask, offsets)
+        ctx.fmt, ctx.k = fmt, k
+        y = _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, None, None)
+        return y.view(*x.shape[:-1], n)
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        a_scales, a_codes, a_mask, w_scales, w_codes, w_mask, offsets = ctx.saved_tensors
+        grad_y = grad_y.contiguous()
+        grad_x = grad_w = None
+        if ctx.needs_input_grad[0]:
+            grad_x = _bwd_input(grad_y, offsets, w_scales, w_codes, ctx.k, a_mask, None)
+        if ctx.needs_input_grad[1]:
+            grad_w = _bwd_weight(ctx.fmt, grad_y, offsets, a_scales, a_codes, ctx.k, None, w_mask, None, None)
+        return grad_x, grad_w, None, None, None, None
+
+
+class ExpertDispatch(torch.autograd.Function):
+    """``expert_dispatch`` of the packed rows of ``expert_sort``'s (row_index,
+    slot); the gradient sums a token's packed rows."""
+
+    @staticmethod
+    def forward(ctx, x, row_index, slot):
+        ctx.save_for_backward(slot)
+        ctx.shape = x.shape
+        return expert_dispatch(x.contiguous(), row_index)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (slot,) = ctx.saved_tensors
+        return expert_combine(grad.contiguous(), slot).view(ctx.shape), None, None
+
+
+class ExpertCombine(torch.autograd.Function):
+    """``expert_combine`` with gradients to the packed rows and the weights."""
+
+    @staticmethod
+    def forward(ctx, y, slot, weights, offsets):
+        y, weights = y.contiguous(), weights.contiguous()
+        ctx.save_for_backward(y, slot, weights, offsets)
+        return expert_combine(y, slot, weights)
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        y, slot, weights, offsets = ctx.saved_tensors
+        grad_y, grad_weights = expert_combine_bwd(grad_out.contiguous(), y, slot, weights, offsets)
+        return grad_y, None, grad_weights, None

@@ -5,34 +5,16 @@
 
 #include <hip/hip_runtime.h>
 
+#include "api_checks.h"
 #include "launch.h"
 
 namespace {
 
 thread_local int g_last_hip_error = 0;
 
-struct Range {
-  uintptr_t lo;
-  uint64_t len;
-};
+}  // namespace
 
-bool overlaps(Range a, Range b) {
-  if (a.len == 0 || b.len == 0) return false;
-  return a.lo < b.lo + b.len && b.lo < a.lo + a.len;
-}
-
-Range rng(const void* p, uint64_t len) { return Range{reinterpret_cast<uintptr_t>(p), len}; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// n = rows * cols with cols % 16 == 0 and 2n bytes addressable.
-trace_status site_size(int64_t rows, int64_t cols, uint64_t* n_out) {
-  if (rows < 0 || cols < 0 || (cols % 16) != 0) return TRACE_E_SHAPE;
-  int64_t n = 0;
-  if (__builtin_mul_overflow(rows, cols, &n) || n > (INT64_MAX / 4)) return TRACE_E_SHAPE;
-  *n_out = (uint64_t)n;
-  return TRACE_OK;
-}
+namespace trace_api {
 
 trace_status hip_status(hipError_t e) {
   if (e == hipSuccess) return TRACE_OK;
@@ -40,23 +22,9 @@ trace_status hip_status(hipError_t e) {
   return TRACE_E_HIP;
 }
 
-// Outputs must not overlap any input nor each other; `inplace_ok` lists an
-// (output, input) pair that may coincide exactly.
-trace_status check_alias(const Range* outs, int nout, const Range* ins, int nin, int inplace_out = -1,
-                         int inplace_in = -1) {
-  for (int i = 0; i < nout; ++i) {
-    for (int j = 0; j < nin; ++j) {
-      if (i == inplace_out && j == inplace_in && outs[i].lo == ins[j].lo && outs[i].len == ins[j].len)
-        continue;
-      if (overlaps(outs[i], ins[j])) return TRACE_E_ALIAS;
-    }
-    for (int k = i + 1; k < nout; ++k)
-      if (overlaps(outs[i], outs[k])) return TRACE_E_ALIAS;
-  }
-  return TRACE_OK;
-}
+}  // namespace trace_api
 
-}  // namespace
+using namespace trace_api;
 
 extern "C" {
 
@@ -446,12 +414,6 @@ trace_status trace_lowbits_fakequant_fwd(const uint16_t* x_train, int64_t rows, 
 // ---------------------------------------------------------------------------
 // MXFP4
 // ---------------------------------------------------------------------------
-
-// n = rows * cols with cols % 32 == 0.
-static trace_status mx_site_size(int64_t rows, int64_t cols, uint64_t* n_out) {
-  if (cols % 32 != 0) return TRACE_E_SHAPE;
-  return site_size(rows, cols, n_out);
-}
 
 trace_status trace_mx_capture(const uint16_t* x_roll, int64_t rows, int64_t cols, uint8_t* scales, uint8_t* bits,
                               uint8_t* codes, void* stream) {

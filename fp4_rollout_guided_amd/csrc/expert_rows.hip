@@ -1,0 +1,366 @@
+// libtrace routed rows for gfx950: the sort of (token, expert) pairs by
+// expert, the gather of the tokens' rows into that order, the weighted sum of
+// the experts' rows back to the tokens, and that sum's gradients.
+//
+// Sort: a stable counting sort.  A workgroup owns a chunk of kSortChunk pairs,
+// its four waves consecutive quarters of it; a wave ranks 64 pairs at a time
+// by comparing expert numbers bit by bit (one ballot per bit), so the order
+// inside an expert is the pairs' own and no result depends on the order of
+// atomics.  One chunk is one launch.  More chunks take a counting launch, a
+// scan over the chunks' counts (one launch, one lane per expert) and a
+// scatter launch.
+//
+// Dispatch, combine and combine's gradients move rows and are bound by
+// memory: 16 bytes per lane, every row read or written once, sums in fp32 in
+// the order of a token's pairs.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_math.h"
+#include "fp4_block.h"
+#include "launch.h"
+#include "launch_mx.h"
+
+namespace trace_dev {
+
+constexpr uint32_t kSortChunk = 2048;
+constexpr uint32_t kSortWaves = kThreads / 64;
+constexpr uint32_t kSortRounds = kSortChunk / kThreads;
+
+// Expert of a pair as a bin: experts that are not held share the last bin.
+__device__ __forceinline__ uint32_t expert_bin(const int64_t* __restrict__ ids, uint64_t pair, uint32_t experts) {
+  const int64_t e = ids[pair];
+  return (e >= 0 && e < (int64_t)experts) ? (uint32_t)e : experts;
+}
+
+// Lanes of the wave, among those with `active`, that hold the same bin.
+__device__ __forceinline__ uint64_t same_bin(uint32_t bin, bool active, uint32_t bits) {
+  uint64_t peers = __ballot(active);
+  for (uint32_t b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((bin >> b) & 1u);
+    peers &= ((bin >> b) & 1u) ? set : ~set;
+  }
+  return peers;
+}
+
+// Counts of a chunk's bins: counts[chunk][experts + 1].
+__global__ __launch_bounds__(kThreads) void expert_count_kernel(const int64_t* __restrict__ ids, uint64_t pairs,
+                                                                uint32_t experts, uint32_t* __restrict__ counts) {
+  __shared__ uint32_t hist[trace_host::kMaxExperts + 1];
+  for (uint32_t e = threadIdx.x; e <= experts; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  const uint64_t base = (uint64_t)blockIdx.x * kSortChunk;
+#pragma unroll
+  for (uint32_t r = 0; r < kSortRounds; ++r) {
+    const uint64_t pair = base + r * kThreads + threadIdx.x;
+    if (pair < pairs) atomicAdd(&hist[expert_bin(ids, pair, experts)], 1u);
+  }
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e <= experts; e += kThreads)
+    counts[(uint64_t)blockIdx.x * (experts + 1) + e] = hist[e];
+}
+
+// Exclusive prefix over v of the workgroup's lanes, in lane order; *total is
+// the sum.  `part` holds one word per wave.
+template <int kWaves>
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* part, uint32_t* total) {
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t up = (uint32_t)__shfl_up((int)s, d);
+    if (lane >= (uint32_t)d) s += up;
+  }
+  if (lane == 63) part[wave] = s;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += (uint32_t)w < wave ? part[w] : 0u;
+    all += part[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + s - v;
+}
+
+// One workgroup: counts[chunk][bin] become the first position of the bin's
+// pairs of that chunk in the sorted order; offsets are written.
+__global__ __launch_bounds__(1024) void expert_scan_kernel(uint32_t* __restrict__ counts, uint32_t chunks,
+                                                           uint32_t experts, int64_t* __restrict__ offsets) {
+  __shared__ uint32_t part[16];
+  uint32_t carry = 0;
+  for (uint32_t e0 = 0; e0 <= experts; e0 += 1024) {
+    const uint32_t e = e0 + threadIdx.x;
+    uint32_t sum = 0;
+    if (e <= experts) {
+#pragma unroll 8
+      for (uint32_t c = 0; c < chunks; ++c) sum += counts[(uint64_t)c * (experts + 1) + e];
+    }
+    uint32_t total;
+    uint32_t at = carry + block_prefix<16>(sum, part, &total);
+    carry += total;
+    if (e <= experts) {
+      offsets[e] = (int64_t)at;  // the last bin starts where the held experts' rows end
+#pragma unroll 8
+      for (uint32_t c = 0; c < chunks; ++c) {
+        uint32_t* p = &counts[(uint64_t)c * (experts + 1) + e];
+        const uint32_t n = *p;
+        *p = at;
+        at += n;
+      }
+    }
+  }
+}
+
+// Places a chunk's pairs.  kSingle: the only chunk; it counts and scans by
+// itself and writes the offsets.  Otherwise first[chunk][bin] comes from the
+// scan.
+template <bool kSingle>
+__global__ __launch_bounds__(kThreads) void expert_place_kernel(const int64_t* __restrict__ ids, uint64_t pairs,
+                                                                uint32_t topk, uint32_t experts, uint32_t bits,
+                                                                const uint32_t* __restrict__ first,
+                                                                int64_t* __restrict__ offsets,
+                                                                int64_t* __restrict__ row_index,
+                                                                int64_t* __restrict__ slot) {
+  __shared__ uint32_t next[kSortWaves][trace_host::kMaxExperts + 1];  // next free position, per wave and bin
+  __shared__ uint32_t part[kSortWaves];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t base = (uint64_t)blockIdx.x * kSortChunk + wave * (kSortChunk / kSortWaves);
+  for (uint32_t i = threadIdx.x; i < kSortWaves * (trace_host::kMaxExperts + 1); i += kThreads) (&next[0][0])[i] = 0;
+  __syncthreads();
+  uint32_t bin[kSortRounds];
+#pragma unroll
+  for (uint32_t r = 0; r < kSortRounds; ++r) {
+    const uint64_t pair = base + r * 64 + lane;
+    bin[r] = pair < pairs ? expert_bin(ids, pair, experts) : 0u;
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < kSortRounds; ++r)
+    if (base + r * 64 + lane < pairs) atomicAdd(&next[wave][bin[r]], 1u);
+  __syncthreads();
+  uint32_t carry = 0;
+  for (uint32_t e0 = 0; e0 <= experts; e0 += kThreads) {
+    const uint32_t e = e0 + threadIdx.x;
+    uint32_t at = 0;
+    if (kSingle) {
+      uint32_t sum = 0, total;
+      if (e <= experts)
+        for (uint32_t w = 0; w < kSortWaves; ++w) sum += next[w][e];
+      at = carry + block_prefix<kSortWaves>(sum, part, &total);
+      carry += total;
+      if (e <= experts) offsets[e] = (int64_t)at;
+    } else if (e <= experts) {
+      at = first[(uint64_t)blockIdx.x * (experts + 1) + e];
+    }
+    if (e <= experts)
+      for (uint32_t w = 0; w < kSortWaves; ++w) {
+        const uint32_t n = next[w][e];
+        next[w][e] = at;
+        at += n;
+      }
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t r = 0; r < kSortRounds; ++r) {
+    const uint64_t pair = base + r * 64 + lane;
+    const bool active = pair < pairs;
+    const uint64_t peers = same_bin(bin[r], active, bits);
+    const uint32_t rank = (uint32_t)__popcll(peers & ((1ull << lane) - 1));
+    uint32_t at = 0;
+    if (active) at = next[wave][bin[r]] + rank;
+    // every lane has read before the first of a bin's lanes moves the position on
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (active && rank == 0) next[wave][bin[r]] = at + (uint32_t)__popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (active) {
+      const bool held = bin[r] < experts;
+      row_index[at] = held ? (int64_t)(pair / topk) : -1;
+      slot[pair] = held ? (int64_t)at : -1;
+    }
+  }
+}
+
+// out row r = x row row_index[r]; zeros for an index outside [0, tokens).
+// One lane per 8-element vector.
+template <bool kNT>
+__global__ __launch_bounds__(kThreads) void expert_dispatch_kernel(const uint4* __restrict__ x, uint64_t tokens,
+                                                                   uint32_t row_vecs,
+                                                                   const int64_t* __restrict__ row_index,
+                                                                   uint64_t nvec, uint4* __restrict__ out) {
+  const uint64_t stride = (uint64_t)gridDim.x * kThreads;
+  for (uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x; g < nvec; g += stride) {
+    const uint64_t r = g / row_vecs;
+    const uint32_t c = (uint32_t)(g - r * row_vecs);
+    const int64_t t = row_index[r];
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t >= 0 && t < (int64_t)tokens) v = x[(uint64_t)t * row_vecs + c];
+    store_vec<kNT>(&out[g], v);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 p = __builtin_convertvector((f32x2){a, b}, bf16x2);
+  uint32_t u;
+  __builtin_memcpy(&u, &p, 4);
+  return u;
+}
+
+__device__ __forceinline__ void add_scaled(float (&acc)[8], const uint4& v, float w) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(w, bf16_lo(u[i]), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, bf16_hi(u[i]), acc[2 * i + 1]);
+  }
+}
+
+// out[t] = sum over j of weights[t][j] * y[slot[t][j]] in fp32, j ascending;
+// slots outside [0, rows) are left out.  One lane per 8-element vector.
+__global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* __restrict__ y, uint64_t rows,
+                                                                  uint32_t row_vecs, const int64_t* __restrict__ slot,
+                                                                  const float* __restrict__ weights, uint32_t topk,
+                                                                  uint64_t nvec, uint4* __restrict__ out) {
+  const uint64_t stride = (uint64_t)gridDim.x * kThreads;
+  for (uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x; g < nvec; g += stride) {
+    const uint64_t t = g / row_vecs;
+    const uint32_t c = (uint32_t)(g - t * row_vecs);
+    float acc[8] = {};
+#pragma unroll 8
+    for (uint32_t j = 0; j < topk; ++j) {
+      const int64_t s = slot[t * topk + j];
+      const float w = weights ? weights[t * topk + j] : 1.f;
+      if (s >= 0 && s < (int64_t)rows) add_scaled(acc, y[(uint64_t)s * row_vecs + c], w);
+    }
+    out[g] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
+                        pack_bf16(acc[6], acc[7]));
+  }
+}
+
+// Gradients of the weighted sum, one workgroup per token: grad_y[slot] =
+// bf16(w * grad_out[t]) and grad_weights[t][j] = <grad_out[t], y[slot]> in
+// fp32, summed lane by lane, then over lanes and waves in a fixed order.
+// Workgroups past the tokens clear the rows behind the last group.
+__global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
+    const uint4* __restrict__ grad_out, const uint4* __restrict__ y, uint64_t rows, uint32_t row_vecs,
+    const int64_t* __restrict__ slot, const float* __restrict__ weights, uint64_t tokens, uint32_t topk,
+    const int64_t* __restrict__ offsets, uint32_t groups, uint4* __restrict__ grad_y,
+    float* __restrict__ grad_weights) {
+  __shared__ float part[kThreads / 64][trace_host::kMaxTopk];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t units = tokens + (offsets ? rows : 0);
+  for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    if (u >= tokens) {
+      const uint64_t r = u - tokens;
+      if ((int64_t)r >= offsets[groups])
+        for (uint32_t c = threadIdx.x; c < row_vecs; c += kThreads) grad_y[r * row_vecs + c] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    for (uint32_t j = 0; j < topk; ++j) {
+      const int64_t s = slot[u * topk + j];
+      const float w = weights ? weights[u * topk + j] : 1.f;
+      float dot = 0.f;
+      if (s >= 0 && s < (int64_t)rows) {
+        for (uint32_t c = threadIdx.x; c < row_vecs; c += kThreads) {
+          const uint4 gv = grad_out[u * row_vecs + c], yv = y[(uint64_t)s * row_vecs + c];
+          const uint32_t a[4] = {gv.x, gv.y, gv.z, gv.w}, b[4] = {yv.x, yv.y, yv.z, yv.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = bf16_lo(a[i]), hi = bf16_hi(a[i]);
+            dot = fmaf(lo, bf16_lo(b[i]), dot);
+            dot = fmaf(hi, bf16_hi(b[i]), dot);
+            o[i] = pack_bf16(w * lo, w * hi);
+          }
+          grad_y[(uint64_t)s * row_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
+      if (lane == 0) part[wave][j] = dot;
+    }
+    __syncthreads();
+    if (threadIdx.x < topk) {
+      float sum = 0.f;
+#pragma unroll
+      for (uint32_t v = 0; v < kThreads / 64; ++v) sum += part[v][threadIdx.x];
+      grad_weights[u * topk + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace trace_dev
+
+namespace trace_host {
+
+using namespace trace_dev;
+
+static unsigned rows_grid(uint64_t units, uint32_t per) {
+  const uint64_t g = (units + per - 1) / per;
+  return (unsigned)(g < kMaxGroups ? g : kMaxGroups);
+}
+
+static uint64_t sort_chunks(uint64_t pairs) { return (pairs + kSortChunk - 1) / kSortChunk; }
+
+uint64_t expert_sort_workspace_words(uint64_t pairs, uint32_t experts) {
+  const uint64_t chunks = sort_chunks(pairs);
+  return chunks > 1 ? chunks * (experts + 1) : 0;
+}
+
+hipError_t launch_expert_sort(const int64_t* ids, uint64_t pairs, uint32_t topk, uint32_t experts, uint32_t* workspace,
+                              int64_t* offsets, int64_t* row_index, int64_t* slot, hipStream_t stream) {
+  uint32_t bits = 0;
+  while ((experts >> bits) != 0) ++bits;  // bins 0..experts
+  const uint64_t chunks = sort_chunks(pairs);
+  if (chunks <= 1) {
+    hipLaunchKernelGGL(expert_place_kernel<true>, dim3(1), dim3(kThreads), 0, stream, ids, pairs, topk, experts, bits,
+                       static_cast<const uint32_t*>(nullptr), offsets, row_index, slot);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)chunks), block(kThreads);
+  hipLaunchKernelGGL(expert_count_kernel, grid, block, 0, stream, ids, pairs, experts, workspace);
+  hipLaunchKernelGGL(expert_scan_kernel, dim3(1), dim3(1024), 0, stream, workspace, (uint32_t)chunks, experts,
+                     offsets);
+  hipLaunchKernelGGL(expert_place_kernel<false>, grid, block, 0, stream, ids, pairs, topk, experts, bits,
+                     static_cast<const uint32_t*>(workspace), offsets, row_index, slot);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_dispatch(const uint16_t* x, uint64_t tokens, uint64_t cols, const int64_t* row_index,
+                                  uint64_t rows, uint16_t* out, hipStream_t stream) {
+  const uint64_t nvec = rows * (cols / 8);
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  uint4* ov = reinterpret_cast<uint4*>(out);
+  if (past_cache(nvec * 16))
+    hipLaunchKernelGGL(expert_dispatch_kernel<true>, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, xv,
+                       tokens, (uint32_t)(cols / 8), row_index, nvec, ov);
+  else
+    hipLaunchKernelGGL(expert_dispatch_kernel<false>, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, xv,
+                       tokens, (uint32_t)(cols / 8), row_index, nvec, ov);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(const uint16_t* y, uint64_t rows, uint64_t cols, const int64_t* slot,
+                                 const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
+                                 hipStream_t stream) {
+  const uint64_t nvec = tokens * (cols / 8);
+  hipLaunchKernelGGL(expert_combine_kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream,
+                     reinterpret_cast<const uint4*>(y), rows, (uint32_t)(cols / 8), slot, weights, topk, nvec,
+                     reinterpret_cast<uint4*>(out));
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, uint64_t rows, uint64_t cols,
+                                     const int64_t* slot, const float* weights, uint64_t tokens, uint32_t topk,
+                                     const int64_t* offsets, uint32_t groups, uint16_t* grad_y, float* grad_weights,
+                                     hipStream_t stream) {
+  const uint64_t units = tokens + (offsets ? rows : 0);
+  hipLaunchKernelGGL(expert_combine_bwd_kernel, dim3(rows_grid(units, 1)), dim3(kThreads), 0, stream,
+                     reinterpret_cast<const uint4*>(grad_out), reinterpret_cast<const uint4*>(y), rows,
+                     (uint32_t)(cols / 8), slot, weights, tokens, topk, offsets, groups,
+                     reinterpret_cast<uint4*>(grad_y), grad_weights);
+  return hipGetLastError();
+}
+
+}  // namespace trace_host

@@ -1,0 +1,72 @@
+// Internal host-side launchers of the microscaled products and of the routed
+// rows (not part of the C ABI).  Arguments have been validated by
+// api_mx_product.cpp.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace trace_host {
+
+// Element format of the activations' codes; the weights' is E2M1.
+enum MxFormat { kE2M1 = 0, kE4M3 = 1 };
+
+// One product y = A W^T, or one per group of packed rows.
+struct MxProductArgs {
+  const uint8_t* a_codes;    // [src_rows, k]
+  const uint8_t* a_scales;   // [src_rows, k / 32]
+  const int64_t* row_index;  // row r reads source row row_index[r]; nullptr: row r (src_rows == rows)
+  uint64_t src_rows;
+  uint64_t rows;
+  const int64_t* offsets;  // [groups + 1], or nullptr for one group of all rows
+  uint32_t groups;
+  const uint8_t* w_codes;   // [groups, n, k]
+  const uint8_t* w_scales;  // [groups, n, k / 32]
+  uint32_t n, k;
+  uint16_t* y;  // [rows, n]
+};
+
+// The gradients: grad_y W (to the activations) or grad_y^T A (to the weights).
+struct MxGradArgs {
+  const uint16_t* grad_y;  // [rows, n]
+  uint64_t rows;
+  const int64_t* offsets;  // as above
+  uint32_t groups;
+  const uint8_t* q_codes;   // the other factor: W [groups, n, k], or A [src_rows, k]
+  const uint8_t* q_scales;
+  const int64_t* row_index;  // of A's rows, or nullptr
+  uint64_t src_rows;
+  uint32_t n, k;
+  const uint8_t* mask;  // clip mask of the gradient's own tensor, or nullptr
+  uint16_t* grad;       // [rows, k], or [groups, n, k]
+  float* partial;       // workspace of the split contraction, or nullptr
+};
+
+// Sizes in 32-element blocks; mask may be nullptr.
+hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks, uint8_t* scales, uint8_t* codes,
+                              uint8_t* mask, hipStream_t stream);
+hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& p, hipStream_t stream);
+
+hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream);
+// Parts of the contraction over the rows that are summed in a workspace of
+// parts * n * k fp32 words; 1: no workspace.
+uint32_t mx_grad_weight_parts(uint64_t rows, uint32_t groups, uint32_t n, uint32_t k);
+hipError_t launch_mx_grad_weight(MxFormat fmt, const MxGradArgs& p, hipStream_t stream);
+
+// Routed rows.
+constexpr uint32_t kMaxExperts = 1024;
+constexpr uint32_t kMaxTopk = 64;
+uint64_t expert_sort_workspace_words(uint64_t pairs, uint32_t experts);
+hipError_t launch_expert_sort(const int64_t* ids, uint64_t pairs, uint32_t topk, uint32_t experts, uint32_t* workspace,
+                              int64_t* offsets, int64_t* row_index, int64_t* slot, hipStream_t stream);
+hipError_t launch_expert_dispatch(const uint16_t* x, uint64_t tokens, uint64_t cols, const int64_t* row_index,
+                                  uint64_t rows, uint16_t* out, hipStream_t stream);
+hipError_t launch_expert_combine(const uint16_t* y, uint64_t rows, uint64_t cols, const int64_t* slot,
+                                 const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
+                                 hipStream_t stream);
+hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, uint64_t rows, uint64_t cols,
+                                     const int64_t* slot, const float* weights, uint64_t tokens, uint32_t topk,
+                                     const int64_t* offsets, uint32_t groups, uint16_t* grad_y, float* grad_weights,
+                                     hipStream_t stream);
+
+}  // namespace trace_host

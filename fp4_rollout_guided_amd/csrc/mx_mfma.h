@@ -1,0 +1,100 @@
+// Operands of the scaled matrix instructions and the row groups of the
+// microscaled products (gfx950).
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 and 32x32x64: lane l holds row l % R of
+// an operand (R = 16 or 32) and, with group g = l / R, either 32 E2M1 codes
+// of the block k = 32 g .. 32 g + 31 (16 bytes), or 32 E4M3 codes in two runs
+// of 16: k = 16 g .. 16 g + 15 and K/2 + 16 g .. (K = 128 or 64).  Either way
+// the lane's scale operand carries the E8M0 byte of block g of its row.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace trace_dev {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// Format selectors of the instruction.
+constexpr int kSelE4M3 = 0;
+constexpr int kSelE2M1 = 4;
+
+// A 16-byte operand: the instruction reads four registers for E2M1.
+__device__ __forceinline__ v8i widen(v4i v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+__device__ __forceinline__ v8i join(v4i a, v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// A row tile of one group: rows [first, first + count), count <= the tile's
+// height; group == groups stands for the rows behind the last group.
+struct RowTile {
+  uint32_t group;
+  uint32_t count;
+  uint64_t first;
+};
+
+// offsets[i] within [0, rows].
+__device__ __forceinline__ uint64_t clamped_offset(const int64_t* __restrict__ offsets, uint32_t i, uint64_t rows) {
+  const int64_t v = offsets[i];
+  return v <= 0 ? 0 : ((uint64_t)v > rows ? rows : (uint64_t)v);
+}
+
+// Rows of group g: offsets that decrease give an empty group, and the rows
+// behind offsets[groups] form one more.
+__device__ __forceinline__ uint32_t group_rows(const int64_t* __restrict__ offsets, uint32_t g, uint32_t groups,
+                                               uint64_t rows, uint64_t& first) {
+  first = clamped_offset(offsets, g, rows);
+  const uint64_t end = g < groups ? clamped_offset(offsets, g + 1, rows) : rows;
+  return end > first ? (uint32_t)(end - first) : 0u;
+}
+
+// Finds row tile `tile` (tiles of `height` rows, group by group; the rows
+// behind the last group come last).  Every lane of the wave must call it
+// with the same arguments: the wave adds up 64 groups' tiles at a time.
+// Returns false past the last tile; *total, where asked for, is the number of
+// tiles in all, and then every group is visited.
+__device__ __forceinline__ bool find_row_tile(const int64_t* __restrict__ offsets, uint32_t groups, uint64_t rows,
+                                              uint32_t height, uint64_t tile, RowTile& out) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint64_t before = 0;
+  for (uint32_t g0 = 0; g0 <= groups; g0 += 64) {
+    const uint32_t g = g0 + lane;
+    uint64_t first = 0;
+    const uint32_t count = g <= groups ? group_rows(offsets, g, groups, rows, first) : 0u;
+    const uint32_t tiles = (count + height - 1) / height;
+    uint32_t sum = tiles;  // inclusive prefix over the wave's 64 groups: at most rows tiles, which fit 32 bits
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t up = (uint32_t)__shfl_up((int)sum, d);
+      if (lane >= (uint32_t)d) sum += up;
+    }
+    const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
+    if (tile < before + all) {
+      const uint64_t hit = __ballot(tile < before + sum);
+      const int at = __ffsll((long long)hit) - 1;  // the first group whose tiles reach past `tile`
+      const uint32_t cnt = (uint32_t)__builtin_amdgcn_readlane((int)count, at);
+      const uint32_t ends = (uint32_t)__builtin_amdgcn_readlane((int)sum, at);
+      const uint32_t own = (uint32_t)__builtin_amdgcn_readlane((int)tiles, at);
+      const uint32_t flo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)first, at);
+      const uint32_t fhi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(first >> 32), at);
+      const uint32_t in = (uint32_t)(tile - (before + ends - own)) * height;
+      out.group = g0 + (uint32_t)at;
+      out.first = (((uint64_t)fhi << 32) | flo) + in;
+      out.count = cnt - in < height ? cnt - in : height;
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+// Most row tiles that `rows` rows in `groups` groups (and the rows behind
+// them) can make: every group but one ends in a partial tile.
+inline uint64_t max_row_tiles(uint64_t rows, uint32_t groups, uint32_t height) {
+  const uint64_t parts = (uint64_t)groups + 1;
+  const uint64_t most = rows / height + parts;
+  return most < rows ? most : rows;
+}
+
+}  // namespace trace_dev

@@ -1,0 +1,87 @@
+// libtrace quantiser for gfx950: bf16 activations or weights to the operands
+// of the microscaled products (mx_product.hip) in one pass -- MXFP4 or MXFP8
+// codes, one E8M0 scale byte per 32-element block, and, for the
+// straight-through backward, the clip mask.  Scales and codes are those of
+// mx_capture and mx8_capture, the mask that of the RNE fake-quant forwards.
+//
+// One lane per 8-element vector (a quarter block: one 128-bit load); the four
+// lanes of a block agree on its largest magnitude by two DPP moves.  Dividing
+// by a power of two is a multiplication by its exact inverse.  The kernel is
+// bound by memory: 2 bytes in, 0.53 (MXFP4) or 1.03 (MXFP8) out per element.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_math.h"
+#include "e8m0.h"
+#include "fp4_block.h"
+#include "launch.h"
+#include "launch_mx.h"
+#include "mx8_block.h"
+#include "mx_quantize_dev.h"
+
+namespace trace_dev {
+
+template <int kFmt, bool kNT>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint4* __restrict__ x, uint64_t nvec,
+                                                               uint8_t* __restrict__ scales,
+                                                               uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ mask) {
+  const uint64_t stride = (uint64_t)gridDim.x * kThreads;
+  for (uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x; g < nvec; g += stride) {
+    const uint4 v = load_vec<kNT>(&x[g]);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // nvec is a multiple of 4, so the four lanes of a block are active together
+    uint32_t amax = vec_amax_bits(w);
+    const uint32_t near = pair_swap(amax);
+    amax = amax > near ? amax : near;
+    const uint32_t far = quad_swap(amax);
+    amax = amax > far ? amax : far;
+    const uint32_t sb = mx_scale_byte<kFmt == 0 ? kE2M1Emax : kE4M3Emax>(amax);
+    const float inv = e8m0_inverse(sb);
+    if ((g & 3) == 0) scales[g >> 2] = (uint8_t)sb;
+    if (kFmt == 0) {
+      uint32_t keep;
+      const uint32_t c = e2m1_codes8(w, inv, keep);
+      store_word<kNT>(reinterpret_cast<uint32_t*>(codes) + g, c);
+      if (mask) store_word<kNT>(&mask[g], (uint8_t)keep);
+    } else {
+      float q[8];
+      uint32_t nan_bits;
+      mx8_quotients<8>(w, inv, q, nan_bits);
+      const uint32_t keep = mx8_keep_bits<8>(q) & ~nan_bits;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], -448.f, 448.f);
+      uint32_t C[2];
+      fp8_rne_codes<8>(q, C);
+      store_pair<kNT>(reinterpret_cast<uint2*>(codes) + g, make_uint2(C[0], C[1]));
+      if (mask) store_word<kNT>(&mask[g], (uint8_t)keep);
+    }
+  }
+}
+
+}  // namespace trace_dev
+
+namespace trace_host {
+
+using namespace trace_dev;
+
+hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks, uint8_t* scales, uint8_t* codes,
+                              uint8_t* mask, hipStream_t stream) {
+  if (nblocks == 0) return hipSuccess;  // an empty grid is not a valid launch
+  const uint64_t nvec = 4 * nblocks;
+  const uint64_t need = (nvec + kThreads - 1) / kThreads;
+  const dim3 grid((unsigned)(need < kMaxGroups ? need : kMaxGroups)), block(kThreads);
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  const bool nt = past_cache(nblocks * 64);
+  if (fmt == kE2M1 && nt)
+    hipLaunchKernelGGL((mx_quantize_kernel<0, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+  else if (fmt == kE2M1)
+    hipLaunchKernelGGL((mx_quantize_kernel<0, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+  else if (nt)
+    hipLaunchKernelGGL((mx_quantize_kernel<1, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+  else
+    hipLaunchKernelGGL((mx_quantize_kernel<1, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+  return hipGetLastError();
+}
+
+}  // namespace trace_host

@@ -526,6 +526,165 @@ TRACE_API trace_status trace_mx8_full_info_fakequant_fwd(const uint16_t* x_train
                                                          uint8_t* mask, uint8_t* qcodes,
                                                          void* stream);
 
+/*
+ * Products of microscaled operands: what the rounded activations and weights
+ * of a layer are for.  A weight W is [n, k] in MXFP4 (scale bytes u8[n*k/32],
+ * code bytes u8[n*k/2], as trace_mx_capture or trace_mx_quantize write them);
+ * activations A are [rows, k] in MXFP4 (trace_mx_*) or MXFP8 (trace_mx8_*,
+ * the W4A8 setting: code bytes u8[rows*k]).  A and W stand for
+ *   A[m][j] = 2^(a_scale byte - 127) * code value, W[i][j] likewise,
+ * and the product is
+ *   y[m][i] = bf16_RNE(sum over j of A[m][j] * W[i][j])
+ * with exact products and fp32 sums whose order depends on the sizes alone.
+ * Unlike the fake-quant forwards, a scale byte of 0xFF is the NaN of the MX
+ * specification here (the library's quantisers never write one), and E4M3
+ * NaN codes are NaN.
+ *   rows >= 0, below 2^31; n % 16 == 0, k % 32 == 0, both below 2^24.
+ *   Alignment: bf16 tensors and code bytes 16 bytes, masks 2 bytes, fp32 4,
+ *   int64 arrays 8; scale bytes have none.
+ *   rows == 0 or n == 0 is a no-op (a weight's gradient is then zeros); k == 0
+ *   gives zeros.
+ *
+ * Grouped products multiply packed rows by one weight per group: rows
+ * [offsets[g], offsets[g+1]) of the rows x k activations by the g-th of the
+ * groups weights [groups, n, k] (the routed experts of trace_expert_sort).
+ *   offsets : int64[groups + 1] in device memory, 8-byte aligned, offsets[0] = 0,
+ *             nondecreasing, offsets[groups] <= rows; 1 <= groups <= 4096.
+ *             Rows from offsets[groups] on belong to no group: they are not
+ *             read, and their results are zeros.  Offsets that break these
+ *             rules keep every access in bounds but give unspecified rows.
+ *   row_index : NULL, or int64[rows] in device memory: packed row r reads row
+ *             row_index[r] of activations of src_rows rows, so that a token's
+ *             codes are stored once for all its experts.  An index outside
+ *             [0, src_rows) stands for a row of zeros.  Without row_index
+ *             src_rows must equal rows.
+ */
+
+/* Codes, scale bytes and optional clip mask of x in one pass: trace_mx_capture's
+ * (trace_mx8_capture's) scales and codes, and the mask of the RNE forward under
+ * those scales (trace_ste_bwd takes it).
+ *   x : bf16[rows*cols], cols % 32 == 0; scales u8[n/32];
+ *   codes u8[n/2] (mx8: u8[n]); mask u8[n/8] or NULL. */
+TRACE_API trace_status trace_mx_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* scales,
+                                         uint8_t* codes, uint8_t* mask, void* stream);
+TRACE_API trace_status trace_mx8_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* scales,
+                                          uint8_t* codes, uint8_t* mask, void* stream);
+
+/* y = A W^T; y : bf16[rows*n]. */
+TRACE_API trace_status trace_mx_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t rows,
+                                       const uint8_t* w_scales, const uint8_t* w_codes, int64_t n, int64_t k,
+                                       uint16_t* y, void* stream);
+TRACE_API trace_status trace_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t rows,
+                                        const uint8_t* w_scales, const uint8_t* w_codes, int64_t n, int64_t k,
+                                        uint16_t* y, void* stream);
+TRACE_API trace_status trace_grouped_mx_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                               const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                               int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                               int64_t n, int64_t k, uint16_t* y, void* stream);
+TRACE_API trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                                const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                                int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                                int64_t n, int64_t k, uint16_t* y, void* stream);
+
+/* The product on bf16 activations x [src_rows, k]: trace_mx_quantize (mx8:
+ * trace_mx8_quantize) followed by the product, with the same result.  The
+ * ungrouped forms take offsets = row_index = NULL, groups = 0 and
+ * src_rows == rows.
+ *   workspace : trace_mx_linear_workspace_bytes(src_rows, k) (mx8:
+ *               trace_mx8_linear_workspace_bytes) bytes of device scratch,
+ *               16-byte aligned, caller-owned, contents not preserved; NULL
+ *               where that is 0. */
+TRACE_API size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t k);
+TRACE_API size_t trace_mx8_linear_workspace_bytes(int64_t src_rows, int64_t k);
+TRACE_API trace_status trace_mx_linear(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
+                                       const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
+                                       const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,
+                                       size_t workspace_bytes, uint16_t* y, void* stream);
+TRACE_API trace_status trace_mx8_linear(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
+                                        const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
+                                        const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,
+                                        size_t workspace_bytes, uint16_t* y, void* stream);
+
+/* Gradient of the product to the activations, grad_x = (grad_y W) where mask
+ * is 1 and +0 elsewhere (the straight-through estimator of A's rounding):
+ *   grad_y : bf16[rows*n]; mask : u8[rows*k/8], the clip mask of the packed
+ *   rows' own rounding, or NULL for all ones; grad_x : bf16[rows*k].
+ * The same for both activation formats.  offsets = NULL, groups = 0: one weight. */
+TRACE_API trace_status trace_mx_matmul_bwd_input(const uint16_t* grad_y, int64_t rows, const int64_t* offsets,
+                                                 int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                                 int64_t n, int64_t k, const uint8_t* mask, uint16_t* grad_x,
+                                                 void* stream);
+
+/* Gradient of the product to the weight(s), grad_w = (grad_y^T A) where mask
+ * is 1 and +0 elsewhere (the straight-through estimator of W's rounding):
+ *   a_scales, a_codes, src_rows, row_index : A as in the product;
+ *   mask : u8[groups*n*k/8], the clip mask of W's rounding, or NULL;
+ *   grad_w : bf16[groups*n*k] (a group without rows: zeros).
+ *   workspace : trace_mx_matmul_bwd_weight_workspace_bytes(rows, groups, n, k)
+ *   bytes, 16-byte aligned (the contraction over many rows is split and its
+ *   parts are summed in their order); NULL where that is 0.
+ * offsets = NULL, groups = 0: one weight. */
+TRACE_API size_t trace_mx_matmul_bwd_weight_workspace_bytes(int64_t rows, int64_t groups, int64_t n, int64_t k);
+TRACE_API trace_status trace_mx_matmul_bwd_weight(const uint16_t* grad_y, int64_t rows, const int64_t* offsets,
+                                                  int64_t groups, const uint8_t* a_scales, const uint8_t* a_codes,
+                                                  int64_t src_rows, const int64_t* row_index, int64_t n, int64_t k,
+                                                  const uint8_t* mask, uint16_t* grad_w, void* workspace,
+                                                  size_t workspace_bytes, void* stream);
+TRACE_API trace_status trace_mx8_matmul_bwd_weight(const uint16_t* grad_y, int64_t rows, const int64_t* offsets,
+                                                   int64_t groups, const uint8_t* a_scales, const uint8_t* a_codes,
+                                                   int64_t src_rows, const int64_t* row_index, int64_t n, int64_t k,
+                                                   const uint8_t* mask, uint16_t* grad_w, void* workspace,
+                                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Routed rows.  A router gives every token topk experts; the (token, expert)
+ * pairs, pair p = token * topk + j, are sorted by expert so that each expert's
+ * rows lie together (the packed rows that the grouped entry points take).
+ *
+ * trace_expert_sort: a stable sort of the pairs by expert.
+ *   ids       : int64[tokens*topk] in device memory; an id outside [0, experts)
+ *               is an expert that is not held here, its pair is left out;
+ *   offsets   : int64[experts + 1], the held experts' groups of packed rows;
+ *   row_index : int64[tokens*topk], the token of each packed row, -1 for rows
+ *               from offsets[experts] on;
+ *   slot      : int64[tokens*topk], the packed row of each pair, -1 if left out;
+ *   workspace : trace_expert_sort_workspace_bytes(tokens, topk, experts) bytes,
+ *               4-byte aligned, NULL where that is 0.
+ *   1 <= topk <= 64, 1 <= experts <= 1024, tokens*topk below 2^31.
+ */
+#define TRACE_MAX_EXPERTS 1024
+#define TRACE_MAX_TOPK 64
+TRACE_API size_t trace_expert_sort_workspace_bytes(int64_t tokens, int64_t topk, int64_t experts);
+TRACE_API trace_status trace_expert_sort(const int64_t* ids, int64_t tokens, int64_t topk, int64_t experts,
+                                         void* workspace, size_t workspace_bytes, int64_t* offsets,
+                                         int64_t* row_index, int64_t* slot, void* stream);
+
+/* Packed row r = token row row_index[r] of x (bf16[tokens*cols], cols % 16 == 0);
+ * an index outside [0, tokens) gives a row of zeros.  out : bf16[rows*cols]. */
+TRACE_API trace_status trace_expert_dispatch(const uint16_t* x, int64_t tokens, int64_t cols,
+                                             const int64_t* row_index, int64_t rows, uint16_t* out, void* stream);
+
+/* out[t] = bf16_RNE(sum over j of weights[t][j] * y[slot[t][j]]), summed in
+ * fp32 in the order of j; slots outside [0, rows) are left out.  weights NULL:
+ * all ones (the gradient of trace_expert_dispatch).
+ *   y : bf16[rows*cols]; slot : int64[tokens*topk]; weights : fp32[tokens*topk];
+ *   out : bf16[tokens*cols]; cols % 16 == 0; 1 <= topk <= 64. */
+TRACE_API trace_status trace_expert_combine(const uint16_t* y, int64_t rows, int64_t cols, const int64_t* slot,
+                                            const float* weights, int64_t tokens, int64_t topk, uint16_t* out,
+                                            void* stream);
+
+/* Gradients of trace_expert_combine:
+ *   grad_y[slot[t][j]] = bf16_RNE(weights[t][j] * grad_out[t]),
+ *   grad_weights[t][j] = sum over c of grad_out[t][c] * y[slot[t][j]][c] (fp32; 0 where the slot is left out).
+ * Rows of grad_y that no slot names are written only where offsets is given:
+ * rows from offsets[groups] on become zeros (offsets = NULL, groups = 0: none).
+ * No two slots may name the same row.
+ *   weights NULL: all ones. */
+TRACE_API trace_status trace_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t rows,
+                                                int64_t cols, const int64_t* slot, const float* weights,
+                                                int64_t tokens, int64_t topk, const int64_t* offsets, int64_t groups,
+                                                uint16_t* grad_y, float* grad_weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
