@@ -52,8 +52,7 @@ __device__ __forceinline__ uint32_t group_rows(const int64_t* __restrict__ offse
 // Finds row tile `tile` (tiles of `height` rows, group by group; the rows
 // behind the last group come last).  Every lane of the wave must call it
 // with the same arguments: the wave adds up 64 groups' tiles at a time.
-// Returns false past the last tile; *total, where asked for, is the number of
-// tiles in all, and then every group is visited.
+// Returns false past the last tile.
 __device__ __forceinline__ bool find_row_tile(const int64_t* __restrict__ offsets, uint32_t groups, uint64_t rows,
                                               uint32_t height, uint64_t tile, RowTile& out) {
   const uint32_t lane = threadIdx.x & 63;
@@ -87,6 +86,31 @@ __device__ __forceinline__ bool find_row_tile(const int64_t* __restrict__ offset
     before += all;
   }
   return false;
+}
+
+// Row tiles of all groups and of the rows behind them; called like
+// find_row_tile.
+__device__ __forceinline__ uint64_t count_row_tiles(const int64_t* __restrict__ offsets, uint32_t groups, uint64_t rows,
+                                                    uint32_t height) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t sum = 0;
+  for (uint32_t g = lane; g <= groups; g += 64) {
+    uint64_t first;
+    sum += (group_rows(offsets, g, groups, rows, first) + height - 1) / height;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += (uint32_t)__shfl_xor((int)sum, d);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum);
+}
+
+// Workgroups go to the 8 XCDs (each with an L2 of its own) in turn.  The
+// tiles are dealt out so that each XCD works through one run of consecutive
+// tiles, which share operands: the tile of this workgroup, or `tiles` where
+// it has none.
+__device__ __forceinline__ uint64_t xcd_tile(uint64_t block, uint64_t tiles) {
+  const uint64_t run = (tiles + 7) / 8;
+  const uint64_t at = block / 8, tile = (block % 8) * run + at;
+  return at < run && tile < tiles ? tile : tiles;
 }
 
 // Most row tiles that `rows` rows in `groups` groups (and the rows behind

@@ -130,6 +130,309 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows.  A workgroup of four waves owns a 256 x 256 tile of y, each wave
+// 128 n x 128 m of it as 4 x 4 blocks of the 32x32x64 instruction (256
+// accumulator registers, one wave per SIMD).
+//
+// The operands pass through LDS in stages of 128 k, copied there without
+// registers (global_load_lds, 16 bytes per lane) into a ring of kStages
+// stages, so that loads run two to three stages ahead of the arithmetic; one
+// barrier per stage.  A copy puts lane i's 16 bytes at place i of a 1 KiB
+// chunk, so the lanes choose which 16 bytes they fetch: the pieces of a row
+// are permuted by the row's bits, so that the eight rows that the reads of
+// eight lanes touch lie in different banks.
+//
+// Scale bytes go through registers, 16 blocks (512 k) of a row at a time,
+// into a double buffer of dwords [stage][row]; the instruction picks its byte.
+//
+// W's rows 4..7 and 8..11 of every 16 trade places on the way to the
+// instruction: a lane's eight consecutive result registers are then eight
+// consecutive n, stored as 16 bytes.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+__device__ __forceinline__ void copy_to_lds(const uint8_t* from, char* to) {
+  __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
+}
+
+// Waits until at most kLeft of this wave's copies and loads are under way and
+// its LDS reads are done, then meets the workgroup's other waves.
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+
+// The stage whose copies were issued `newer` stages (of kLoads each) before
+// the last one has arrived for every wave.
+template <int kLoads>
+__device__ __forceinline__ void stage_arrived(uint32_t newer) {
+  if (newer == 0)
+    wait_and_meet<0>();
+  else if (newer == 1)
+    wait_and_meet<kLoads>();
+  else if (newer == 2)
+    wait_and_meet<2 * kLoads>();
+  else
+    wait_and_meet<3 * kLoads>();
+}
+
+// Scale bytes of blocks b .. b + 15 of a row (0x7f past its last block).
+__device__ __forceinline__ v4i scale_span(const uint8_t* __restrict__ row, uint32_t b, uint32_t blocks) {
+  v4i s = {0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f};
+  if (b + 16 <= blocks) {
+    __builtin_memcpy(&s, row + b, 16);
+  } else {
+#pragma unroll
+    for (uint32_t d = 0; d < 4; ++d) {
+      const uint32_t at = b + 4 * d;
+      int v = 0x7f7f7f7f;
+      if (at + 4 <= blocks) {
+        __builtin_memcpy(&v, row + at, 4);
+      } else if (at < blocks) {
+#pragma unroll
+        for (uint32_t j = 0; j < 3; ++j)
+          if (at + j < blocks) v = (v & ~(0xff << (8 * j))) | ((int)row[at + j] << (8 * j));
+      }
+      s[d] = v;
+    }
+  }
+  return s;
+}
+
+// A number as a type, for lambdas that need it at compile time.
+template <uint32_t kValue>
+struct Constant {
+  static constexpr uint32_t value = kValue;
+};
+
+template <int kFmt, bool kGather>
+__global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
+  constexpr bool kFp4 = kFmt == trace_host::kE2M1;
+  constexpr uint32_t kTile = 256;
+  constexpr uint32_t kStages = kFp4 ? 4 : 3;
+  constexpr uint32_t kABytes = kFp4 ? 64 : 128;                // per row and stage
+  constexpr uint32_t kStageBytes = kTile * (64 + kABytes);
+  constexpr uint32_t kALoads = kABytes / 16, kLoads = 4 + kALoads;  // copies per wave and stage
+  __shared__ __attribute__((aligned(1024))) char ring[kStages * kStageBytes];
+  __shared__ int scale_buf[2][4][2 * kTile];  // [span][stage of the span][W's rows, A's rows]
+
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t row_tiles = p.offsets ? count_row_tiles(p.offsets, p.groups, p.rows, kTile)
+                                       : (p.rows + kTile - 1) / kTile;
+  const uint64_t tiles = row_tiles * col_tiles;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const uint64_t row_tile = tile / col_tiles;
+  const uint32_t n0 = (uint32_t)(tile - row_tile * col_tiles) * kTile;
+  RowTile t;
+  if (p.offsets) {
+    if (!find_row_tile(p.offsets, p.groups, p.rows, kTile, row_tile, t)) return;
+  } else {
+    t.group = 0;
+    t.first = row_tile * kTile;
+    t.count = (uint32_t)(p.rows - t.first < kTile ? p.rows - t.first : kTile);
+  }
+  const bool behind = t.group >= p.groups;  // rows of no group: zeros
+  const uint32_t blocks = p.k / 32;
+  const uint32_t w_pitch = p.k / 2, a_pitch = kFp4 ? p.k / 2 : p.k;
+  const uint32_t stages = behind ? 0 : (p.k + 127) / 128;
+
+  // what this lane copies: W's rows 64 wave + 16 j + lane / 4, and A's rows
+  // 64 wave + 16 j + lane / 4 (4 pieces a row) or + 8 j + lane / 8 (8 pieces)
+  const uint32_t w_piece = (lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 4) & 2));
+  const uint32_t a_piece = kFp4 ? (lane & 3) ^ ((lane >> 3) & 3) : (lane & 7) ^ (lane >> 3);
+  const uint64_t weight = behind ? 0 : t.group;
+  const uint8_t* wc = p.w_codes + (weight * p.n + n0) * w_pitch;
+  uint32_t w_from[4];
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) {
+    const uint32_t n = 64 * wave + 16 * j + lane / 4;
+    w_from[j] = (n0 + n < p.n ? n : 0) * w_pitch;  // past the last column: any row, dropped at the end
+  }
+  // source rows of packed rows m of the tile; rows past the tile's and rows
+  // without a source read row 0 and are dropped or cleared at the end
+  const auto packed_row = [&](uint32_t m) -> uint64_t { return t.first + (m < t.count ? m : 0); };
+  const auto has_source = [&](int64_t i) -> bool { return !kGather || (i >= 0 && i < (int64_t)p.src_rows); };
+  int64_t a_index[kALoads], r_index[4], s_index;
+  const uint32_t h = lane >> 5, r = lane & 31;
+  const uint32_t wn = 128 * (wave >> 1), wm = 128 * (wave & 1);
+#pragma unroll
+  for (uint32_t j = 0; j < kALoads; ++j) {
+    const uint64_t row = packed_row(kFp4 ? 64 * wave + 16 * j + lane / 4 : 64 * wave + 8 * j + lane / 8);
+    a_index[j] = kGather ? p.row_index[row] : (int64_t)row;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) r_index[j] = kGather ? p.row_index[packed_row(wm + r + 32 * j)] : 0;
+  s_index = kGather ? p.row_index[packed_row(threadIdx.x)] : (int64_t)packed_row(threadIdx.x);
+  const uint8_t* a_from[kALoads];
+#pragma unroll
+  for (uint32_t j = 0; j < kALoads; ++j)
+    a_from[j] = p.a_codes + (has_source(a_index[j]) ? (uint64_t)a_index[j] : 0) * a_pitch;
+  uint32_t sources = 0;  // which of this lane's four result rows have a source row
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j) sources |= (has_source(r_index[j]) ? 1u : 0u) << j;
+  const auto issue = [&](uint32_t st) {
+    char* to = ring + (st % kStages) * kStageBytes;
+    // the last stage may hold fewer than 128 k: pieces past the end fetch the
+    // row's first piece of the stage instead
+    const uint32_t left = p.k - 128 * st;
+    const uint32_t wp = 32 * w_piece < left ? w_piece : 0;
+    const uint32_t ap = (kFp4 ? 32 : 16) * a_piece < left ? a_piece : 0;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) copy_to_lds(wc + 64 * st + (w_from[j] + 16 * wp), to + 1024 * (4 * wave + j));
+#pragma unroll
+    for (uint32_t j = 0; j < kALoads; ++j)
+      copy_to_lds(a_from[j] + kABytes * st + 16 * ap, to + 64 * kTile + 1024 * (kALoads * wave + j));
+  };
+  // scale rows: thread i carries W's row i and A's row i
+  const uint8_t* ws_row = p.w_scales + (weight * p.n + n0 + (n0 + threadIdx.x < p.n ? threadIdx.x : 0)) * blocks;
+  const uint8_t* as_row = p.a_scales + (has_source(s_index) ? (uint64_t)s_index : 0) * blocks;
+  v4i w_span, a_span;
+  const auto load_span = [&](uint32_t span) {
+    w_span = scale_span(ws_row, 16 * span, blocks);
+    a_span = scale_span(as_row, 16 * span, blocks);
+  };
+  const auto store_span = [&](uint32_t span) {
+#pragma unroll
+    for (uint32_t d = 0; d < 4; ++d) {
+      scale_buf[span & 1][d][threadIdx.x] = w_span[d];
+      scale_buf[span & 1][d][kTile + threadIdx.x] = a_span[d];
+    }
+  };
+
+  v16f acc[4][4] = {};  // [W fragment][A fragment]
+  const uint32_t w_row = wn + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));  // bits 2 and 3 trade places
+  const uint32_t w_at = w_row * 64 + 16 * (h ^ (((w_row >> 1) & 1) | ((w_row >> 2) & 2)));
+  const uint32_t a_row_in = wm + r;
+  const uint32_t a_at = 64 * kTile + (kFp4 ? a_row_in * 64 + 16 * (h ^ ((r >> 1) & 3)) : a_row_in * 128 + 16 * (h ^ (r & 7)));
+
+  v8i wf[2][4], af[2][4];
+  uint32_t wsc[2][4], asc[2][4];  // of this stage and the next
+  // Fragments of k-step kk (64 k) of a stage.  may_end: the stage may
+  // hold fewer; blocks past the last one are cleared in A.
+  const auto read_step = [&](uint32_t st, uint32_t kk, v8i(&w)[4], v8i(&a)[4], bool may_end) {
+    const char* from = ring + (st % kStages) * kStageBytes;
+#pragma unroll
+    for (uint32_t f = 0; f < 4; ++f) w[f] = widen(*reinterpret_cast<const v4i*>(from + ((w_at ^ (32 * kk)) + 2048 * f)));
+#pragma unroll
+    for (uint32_t f = 0; f < 4; ++f) {
+      if (kFp4) {
+        a[f] = widen(*reinterpret_cast<const v4i*>(from + ((a_at ^ (32 * kk)) + 2048 * f)));
+      } else {
+        a[f] = join(*reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk)) + 4096 * f)),
+                    *reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk) ^ 32) + 4096 * f)));
+      }
+    }
+    if (may_end && p.k - 128 * st < 128) {
+      const uint32_t left = p.k - 128 * st;
+      const v4i zero = {0, 0, 0, 0};
+      const bool lo = (kFp4 ? 64 * kk + 32 * h : 64 * kk) < left, hi = 64 * kk + 32 < left;
+#pragma unroll
+      for (uint32_t f = 0; f < 4; ++f) {
+        const v4i x = __builtin_shufflevector(a[f], a[f], 0, 1, 2, 3), y = __builtin_shufflevector(a[f], a[f], 4, 5, 6, 7);
+        a[f] = kFp4 ? widen(lo ? x : zero) : join(lo ? x : zero, hi ? y : zero);
+      }
+    }
+  };
+  const auto read_scales = [&](uint32_t st, uint32_t(&w)[4], uint32_t(&a)[4]) {
+    const int* from = scale_buf[(st >> 2) & 1][st & 3];
+#pragma unroll
+    for (uint32_t f = 0; f < 4; ++f) {
+      w[f] = (uint32_t)from[w_row + 32 * f];
+      a[f] = (uint32_t)from[kTile + a_row_in + 32 * f];
+    }
+  };
+  const auto multiply = [&](const v8i(&w)[4], const v8i(&a)[4], const uint32_t(&ws)[4], const uint32_t(&as)[4], auto sel) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], a[j], acc[i][j], kSelE2M1,
+                                                                    kFp4 ? kSelE2M1 : kSelE4M3, decltype(sel)::value,
+                                                                    (int)ws[i], decltype(sel)::value, (int)as[j]);
+  };
+  // One stage, whose first step and scales have been read: the second step is
+  // read under the first one's arithmetic, the next stage's first step under
+  // the second one's.  kSteady: stages st + 1 and st + kStages exist.
+  const auto stage = [&](uint32_t st, auto part, auto steady) {
+    constexpr uint32_t kPart = decltype(part)::value;  // st % 4
+    constexpr bool kSteady = decltype(steady)::value;
+    constexpr uint32_t kNow = kPart & 1, kNext = kNow ^ 1;
+    read_step(st, 1, wf[1], af[1], !kSteady);
+    if (kPart == 0 && (kSteady || st + 4 < stages)) load_span((st >> 2) + 1);
+    if (kPart == 2 && (kSteady || st + 2 < stages)) store_span((st >> 2) + 1);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {  // byte 0: this lane's block of step 0; byte 2: of step 1
+      wsc[kNow][f] >>= 8 * h;
+      asc[kNow][f] >>= 8 * h;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(wf[0], af[0], wsc[kNow], asc[kNow], Constant<0>());
+    __builtin_amdgcn_sched_barrier(0);
+    if (kSteady || st + 1 < stages) {
+      if (kSteady) {
+        wait_and_meet<(kStages - 2) * kLoads>();
+        issue(st + kStages);  // every wave has read stage st: its place is free
+      } else {
+        const uint32_t newest = st + kStages - 1 < stages - 1 ? st + kStages - 1 : stages - 1;
+        stage_arrived<kLoads>(newest - (st + 1));
+        if (st + kStages < stages) issue(st + kStages);
+      }
+      read_step(st + 1, 0, wf[0], af[0], !kSteady);
+      read_scales(st + 1, wsc[kNext], asc[kNext]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(wf[1], af[1], wsc[kNow], asc[kNow], Constant<2>());
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (stages) {
+    load_span(0);
+    const uint32_t ahead = stages < kStages ? stages : kStages;
+    for (uint32_t st = 0; st < ahead; ++st) issue(st);
+    store_span(0);
+    stage_arrived<kLoads>(ahead - 1);
+    read_step(0, 0, wf[0], af[0], true);
+    read_scales(0, wsc[0], asc[0]);
+    uint32_t st = 0;
+    for (; st + 3 + kStages < stages; st += 4) {
+      stage(st, Constant<0>(), Constant<1>());
+      stage(st + 1, Constant<1>(), Constant<1>());
+      stage(st + 2, Constant<2>(), Constant<1>());
+      stage(st + 3, Constant<3>(), Constant<1>());
+    }
+    for (; st < stages; st += 4) {
+      stage(st, Constant<0>(), Constant<0>());
+      if (st + 1 < stages) stage(st + 1, Constant<1>(), Constant<0>());
+      if (st + 2 < stages) stage(st + 2, Constant<2>(), Constant<0>());
+      if (st + 3 < stages) stage(st + 3, Constant<3>(), Constant<0>());
+    }
+  }
+  // register e of a block: n = 16 (e / 8) + 8 h + e % 8, m = lane % 32
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t m = wm + 32 * j + r;
+    if (m >= t.count) continue;
+    const bool ok = (sources >> j) & 1;
+    uint16_t* row = p.y + (t.first + m) * p.n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 8) {
+        const uint32_t n = n0 + wn + 32 * i + 2 * e + 8 * h;
+        if (n >= p.n) continue;
+        const v16f& a = acc[i][j];
+        uint4 v = make_uint4(bf16_pair(a[e], a[e + 1]), bf16_pair(a[e + 2], a[e + 3]), bf16_pair(a[e + 4], a[e + 5]),
+                             bf16_pair(a[e + 6], a[e + 7]));
+        if (!ok) v = make_uint4(0, 0, 0, 0);  // no source row
+        *reinterpret_cast<uint4*>(row + n) = v;
+      }
+  }
+}
+
 }  // namespace trace_dev
 
 namespace trace_host {
@@ -147,7 +450,21 @@ static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
 }
 
 template <int kFmt>
+static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
+  const uint32_t cols = (p.n + 255) / 256;
+  const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 256) : (p.rows + 255) / 256;
+  const uint64_t grid = (row_tiles * cols + 7) / 8 * 8;
+  if (grid * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
+  if (p.row_index)
+    hipLaunchKernelGGL((mx_tile_kernel<kFmt, true>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<kFmt, false>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
+  return hipGetLastError();
+}
+
+template <int kFmt>
 static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
+  if (p.rows >= 128 && p.src_rows > 0) return launch_tile<kFmt>(p, stream);
   return launch_skinny<kFmt, 2, 2, 4>(p, stream);
 }
 
