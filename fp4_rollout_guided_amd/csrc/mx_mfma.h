@@ -24,6 +24,7 @@ constexpr int kSelE2M1 = 4;
 
 // A 16-byte operand: the instruction reads four registers for E2M1.
 __device__ __forceinline__ v8i widen(v4i v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+__device__ __forceinline__ v8i widen(v8i v) { return v; }
 __device__ __forceinline__ v8i join(v4i a, v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 // A row tile of one group: rows [first, first + count), count <= the tile's

@@ -135,13 +135,14 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 // 128 n x 128 m of it as 4 x 4 blocks of the 32x32x64 instruction (256
 // accumulator registers, one wave per SIMD).
 //
-// The operands pass through LDS in stages of 128 k, copied there without
-// registers (global_load_lds, 16 bytes per lane) into a ring of kStages
-// stages, so that loads run two to three stages ahead of the arithmetic; one
-// barrier per stage.  A copy puts lane i's 16 bytes at place i of a 1 KiB
-// chunk, so the lanes choose which 16 bytes they fetch: the pieces of a row
-// are permuted by the row's bits, so that the eight rows that the reads of
-// eight lanes touch lie in different banks.
+// The operands pass through LDS in stages of 128 k, two buffers, one barrier
+// per stage.  Loads run up to three stages ahead of the arithmetic, in
+// registers until their buffer is free.  (Copying to LDS without registers
+// was slower: the compiler waits for every copy under way before each LDS
+// read.)  Lane i's 16 bytes lie at place i of a 1 KiB chunk, so the lanes
+// choose which 16 bytes they fetch: the pieces of a row are permuted by the
+// row's bits, so that the eight rows that the reads of eight lanes touch lie
+// in different banks.
 //
 // Scale bytes go through registers, 16 blocks (512 k) of a row at a time,
 // into a double buffer of dwords [stage][row]; the instruction picks its byte.
@@ -150,33 +151,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 // instruction: a lane's eight consecutive result registers are then eight
 // consecutive n, stored as 16 bytes.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void global_void;
 
-__device__ __forceinline__ void copy_to_lds(const uint8_t* from, char* to) {
-  __builtin_amdgcn_global_load_lds((global_void*)from, (lds_void*)to, 16, 0, 0);
-}
-
-// Waits until at most kLeft of this wave's copies and loads are under way and
-// its LDS reads are done, then meets the workgroup's other waves.
-template <int kLeft>
-__device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
-}
-
-// The stage whose copies were issued `newer` stages (of kLoads each) before
-// the last one has arrived for every wave.
-template <int kLoads>
-__device__ __forceinline__ void stage_arrived(uint32_t newer) {
-  if (newer == 0)
-    wait_and_meet<0>();
-  else if (newer == 1)
-    wait_and_meet<kLoads>();
-  else if (newer == 2)
-    wait_and_meet<2 * kLoads>();
-  else
-    wait_and_meet<3 * kLoads>();
-}
+// This wave's LDS accesses are done; meet the workgroup's other waves.  Loads
+// to registers stay under way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Scale bytes of blocks b .. b + 15 of a row (0x7f past its last block).
 __device__ __forceinline__ v4i scale_span(const uint8_t* __restrict__ row, uint32_t b, uint32_t blocks) {
@@ -201,6 +179,16 @@ __device__ __forceinline__ v4i scale_span(const uint8_t* __restrict__ row, uint3
   return s;
 }
 
+// 32 codes of an activation row.
+template <int kFmt>
+struct Operand {
+  using type = v4i;
+};
+template <>
+struct Operand<trace_host::kE4M3> {
+  using type = v8i;
+};
+
 // A number as a type, for lambdas that need it at compile time.
 template <uint32_t kValue>
 struct Constant {
@@ -211,11 +199,11 @@ template <int kFmt, bool kGather>
 __global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
   constexpr bool kFp4 = kFmt == trace_host::kE2M1;
   constexpr uint32_t kTile = 256;
-  constexpr uint32_t kStages = kFp4 ? 4 : 3;
   constexpr uint32_t kABytes = kFp4 ? 64 : 128;                // per row and stage
   constexpr uint32_t kStageBytes = kTile * (64 + kABytes);
-  constexpr uint32_t kALoads = kABytes / 16, kLoads = 4 + kALoads;  // copies per wave and stage
-  __shared__ __attribute__((aligned(1024))) char ring[kStages * kStageBytes];
+  constexpr uint32_t kALoads = kABytes / 16, kLoads = 4 + kALoads;  // 16-byte loads per lane and stage
+  constexpr uint32_t kAhead = kFp4 ? 2 : 1;                    // stages in registers
+  __shared__ __attribute__((aligned(1024))) char ring[2 * kStageBytes];
   __shared__ int scale_buf[2][4][2 * kTile];  // [span][stage of the span][W's rows, A's rows]
 
   const uint32_t lane = threadIdx.x & 63;
@@ -240,7 +228,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductAr
   const uint32_t w_pitch = p.k / 2, a_pitch = kFp4 ? p.k / 2 : p.k;
   const uint32_t stages = behind ? 0 : (p.k + 127) / 128;
 
-  // what this lane copies: W's rows 64 wave + 16 j + lane / 4, and A's rows
+  // what this lane fetches: W's rows 64 wave + 16 j + lane / 4, and A's rows
   // 64 wave + 16 j + lane / 4 (4 pieces a row) or + 8 j + lane / 8 (8 pieces)
   const uint32_t w_piece = (lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 4) & 2));
   const uint32_t a_piece = kFp4 ? (lane & 3) ^ ((lane >> 3) & 3) : (lane & 7) ^ (lane >> 3);
@@ -274,18 +262,32 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductAr
   uint32_t sources = 0;  // which of this lane's four result rows have a source row
 #pragma unroll
   for (uint32_t j = 0; j < 4; ++j) sources |= (has_source(r_index[j]) ? 1u : 0u) << j;
-  const auto issue = [&](uint32_t st) {
-    char* to = ring + (st % kStages) * kStageBytes;
-    // the last stage may hold fewer than 128 k: pieces past the end fetch the
-    // row's first piece of the stage instead
+  v4i held[kAhead][kLoads];  // stages on their way to LDS
+  // may_end: the stage may hold fewer than 128 k; pieces past the end are zeros
+  const auto fetch = [&](uint32_t st, v4i(&to)[kLoads], bool may_end) {
     const uint32_t left = p.k - 128 * st;
-    const uint32_t wp = 32 * w_piece < left ? w_piece : 0;
-    const uint32_t ap = (kFp4 ? 32 : 16) * a_piece < left ? a_piece : 0;
+    const bool w_in = !may_end || 32 * w_piece < left;
+    const bool a_in = !may_end || (kFp4 ? 32 : 16) * a_piece < left;
 #pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) copy_to_lds(wc + 64 * st + (w_from[j] + 16 * wp), to + 1024 * (4 * wave + j));
+    for (uint32_t j = 0; j < 4; ++j) {
+      v4i v = {0, 0, 0, 0};
+      if (w_in) v = *reinterpret_cast<const v4i*>(wc + 64 * st + (w_from[j] + 16 * w_piece));
+      to[j] = v;
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kALoads; ++j) {
+      v4i v = {0, 0, 0, 0};
+      if (a_in) v = *reinterpret_cast<const v4i*>(a_from[j] + kABytes * st + 16 * a_piece);
+      to[4 + j] = v;
+    }
+  };
+  const auto place = [&](uint32_t st, const v4i(&from)[kLoads]) {
+    char* to = ring + (st & 1) * kStageBytes + 16 * lane;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(to + 1024 * (4 * wave + j)) = from[j];
 #pragma unroll
     for (uint32_t j = 0; j < kALoads; ++j)
-      copy_to_lds(a_from[j] + kABytes * st + 16 * ap, to + 64 * kTile + 1024 * (kALoads * wave + j));
+      *reinterpret_cast<v4i*>(to + 64 * kTile + 1024 * (kALoads * wave + j)) = from[4 + j];
   };
   // scale rows: thread i carries W's row i and A's row i
   const uint8_t* ws_row = p.w_scales + (weight * p.n + n0 + (n0 + threadIdx.x < p.n ? threadIdx.x : 0)) * blocks;
@@ -309,31 +311,22 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductAr
   const uint32_t a_row_in = wm + r;
   const uint32_t a_at = 64 * kTile + (kFp4 ? a_row_in * 64 + 16 * (h ^ ((r >> 1) & 3)) : a_row_in * 128 + 16 * (h ^ (r & 7)));
 
-  v8i wf[2][4], af[2][4];
+  using AFrag = typename Operand<kFmt>::type;
+  v4i wf[2][4];
+  AFrag af[2][4];
   uint32_t wsc[2][4], asc[2][4];  // of this stage and the next
-  // Fragments of k-step kk (64 k) of a stage.  may_end: the stage may
-  // hold fewer; blocks past the last one are cleared in A.
-  const auto read_step = [&](uint32_t st, uint32_t kk, v8i(&w)[4], v8i(&a)[4], bool may_end) {
-    const char* from = ring + (st % kStages) * kStageBytes;
+  // Fragments of k-step kk (64 k) of a stage.
+  const auto read_step = [&](uint32_t st, uint32_t kk, v4i(&w)[4], AFrag(&a)[4]) {
+    const char* from = ring + (st & 1) * kStageBytes;
 #pragma unroll
-    for (uint32_t f = 0; f < 4; ++f) w[f] = widen(*reinterpret_cast<const v4i*>(from + ((w_at ^ (32 * kk)) + 2048 * f)));
+    for (uint32_t f = 0; f < 4; ++f) w[f] = *reinterpret_cast<const v4i*>(from + ((w_at ^ (32 * kk)) + 2048 * f));
 #pragma unroll
     for (uint32_t f = 0; f < 4; ++f) {
-      if (kFp4) {
-        a[f] = widen(*reinterpret_cast<const v4i*>(from + ((a_at ^ (32 * kk)) + 2048 * f)));
+      if constexpr (kFp4) {
+        a[f] = *reinterpret_cast<const v4i*>(from + ((a_at ^ (32 * kk)) + 2048 * f));
       } else {
         a[f] = join(*reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk)) + 4096 * f)),
                     *reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk) ^ 32) + 4096 * f)));
-      }
-    }
-    if (may_end && p.k - 128 * st < 128) {
-      const uint32_t left = p.k - 128 * st;
-      const v4i zero = {0, 0, 0, 0};
-      const bool lo = (kFp4 ? 64 * kk + 32 * h : 64 * kk) < left, hi = 64 * kk + 32 < left;
-#pragma unroll
-      for (uint32_t f = 0; f < 4; ++f) {
-        const v4i x = __builtin_shufflevector(a[f], a[f], 0, 1, 2, 3), y = __builtin_shufflevector(a[f], a[f], 4, 5, 6, 7);
-        a[f] = kFp4 ? widen(lo ? x : zero) : join(lo ? x : zero, hi ? y : zero);
       }
     }
   };
@@ -345,60 +338,74 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductAr
       a[f] = (uint32_t)from[kTile + a_row_in + 32 * f];
     }
   };
-  const auto multiply = [&](const v8i(&w)[4], const v8i(&a)[4], const uint32_t(&ws)[4], const uint32_t(&as)[4], auto sel) {
+  const auto multiply = [&](const v4i(&w)[4], const AFrag(&a)[4], const uint32_t(&ws)[4], const uint32_t(&as)[4], auto sel) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[i], a[j], acc[i][j], kSelE2M1,
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w[i]), widen(a[j]), acc[i][j], kSelE2M1,
                                                                     kFp4 ? kSelE2M1 : kSelE4M3, decltype(sel)::value,
                                                                     (int)ws[i], decltype(sel)::value, (int)as[j]);
   };
-  // One stage, whose first step and scales have been read: the second step is
-  // read under the first one's arithmetic, the next stage's first step under
-  // the second one's.  kSteady: stages st + 1 and st + kStages exist.
+  // One stage, whose first step and scales have been read.  Under the first
+  // step's arithmetic the second step is read, the next stage is placed in
+  // LDS and the one kAhead + 1 further is fetched; under the second step's the
+  // next stage's first step is read.  kSteady: those stages exist, in full.
   const auto stage = [&](uint32_t st, auto part, auto steady) {
     constexpr uint32_t kPart = decltype(part)::value;  // st % 4
     constexpr bool kSteady = decltype(steady)::value;
-    constexpr uint32_t kNow = kPart & 1, kNext = kNow ^ 1;
-    read_step(st, 1, wf[1], af[1], !kSteady);
-    if (kPart == 0 && (kSteady || st + 4 < stages)) load_span((st >> 2) + 1);
-    if (kPart == 2 && (kSteady || st + 2 < stages)) store_span((st >> 2) + 1);
+    constexpr uint32_t kNow = kPart & 1, kNext = kNow ^ 1, kHeld = (kPart + 1) % kAhead;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {  // byte 0: this lane's block of step 0; byte 2: of step 1
       wsc[kNow][f] >>= 8 * h;
       asc[kNow][f] >>= 8 * h;
     }
-    __builtin_amdgcn_sched_barrier(0);
+    read_step(st, 1, wf[1], af[1]);
+    if (kPart == 2 && (kSteady || st + 2 < stages)) store_span((st >> 2) + 1);
+    if (kSteady || st + 1 < stages) place(st + 1, held[kHeld]);
+    if (kPart == 0 && (kSteady || st + 4 < stages)) load_span((st >> 2) + 1);
+    if (kSteady || st + 1 + kAhead < stages) fetch(st + 1 + kAhead, held[kHeld], !kSteady);
     multiply(wf[0], af[0], wsc[kNow], asc[kNow], Constant<0>());
-    __builtin_amdgcn_sched_barrier(0);
-    if (kSteady || st + 1 < stages) {
-      if (kSteady) {
-        wait_and_meet<(kStages - 2) * kLoads>();
-        issue(st + kStages);  // every wave has read stage st: its place is free
-      } else {
-        const uint32_t newest = st + kStages - 1 < stages - 1 ? st + kStages - 1 : stages - 1;
-        stage_arrived<kLoads>(newest - (st + 1));
-        if (st + kStages < stages) issue(st + kStages);
+    if (kSteady) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                // matrix instructions
+        __builtin_amdgcn_sched_group_barrier(0x100, kFp4 ? 1 : 2, 0);     // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x200, kFp4 ? 1 : 2, 0);     // LDS writes
+        __builtin_amdgcn_sched_group_barrier(0x020, kFp4 ? 1 : 2, 0);     // loads
       }
-      read_step(st + 1, 0, wf[0], af[0], !kSteady);
-      read_scales(st + 1, wsc[kNext], asc[kNext]);
     }
     __builtin_amdgcn_sched_barrier(0);
+    if (kSteady || st + 1 < stages) {
+      lds_barrier();
+      read_step(st + 1, 0, wf[0], af[0]);
+      read_scales(st + 1, wsc[kNext], asc[kNext]);
+    }
     multiply(wf[1], af[1], wsc[kNow], asc[kNow], Constant<2>());
+    if (kSteady) {
+#pragma unroll
+      for (int i = 0; i < 12; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, kFp4 ? 1 : 2, 0);
+      }
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
 
   if (stages) {
     load_span(0);
-    const uint32_t ahead = stages < kStages ? stages : kStages;
-    for (uint32_t st = 0; st < ahead; ++st) issue(st);
+    v4i first[kLoads];
+    fetch(0, first, true);
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i)
+      if (1 + i < stages) fetch(1 + i, held[(1 + i) % kAhead], true);
     store_span(0);
-    stage_arrived<kLoads>(ahead - 1);
-    read_step(0, 0, wf[0], af[0], true);
+    place(0, first);
+    lds_barrier();
+    read_step(0, 0, wf[0], af[0]);
     read_scales(0, wsc[0], asc[0]);
     uint32_t st = 0;
-    for (; st + 3 + kStages < stages; st += 4) {
+    for (; st + 5 + kAhead < stages; st += 4) {
       stage(st, Constant<0>(), Constant<1>());
       stage(st + 1, Constant<1>(), Constant<1>());
       stage(st + 2, Constant<2>(), Constant<1>());
