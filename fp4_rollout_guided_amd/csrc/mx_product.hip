@@ -131,21 +131,23 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  A workgroup of four waves owns a 256 x 256 tile of y, each wave
-// 128 n x 128 m of it as 4 x 4 blocks of the 32x32x64 instruction (256
-// accumulator registers, one wave per SIMD).
+// Many rows.  A workgroup of four waves owns a tile of 64 kMF rows m and
+// 64 kNF columns n of y, each wave a quarter of it as kNF x kMF blocks of the
+// 32x32x64 instruction.
 //
 // The operands pass through LDS in stages of 128 k, two buffers, one barrier
-// per stage.  Loads run up to three stages ahead of the arithmetic, in
+// per stage.  Loads run more than a stage ahead of the arithmetic, in
 // registers until their buffer is free.  (Copying to LDS without registers
 // was slower: the compiler waits for every copy under way before each LDS
 // read.)  Lane i's 16 bytes lie at place i of a 1 KiB chunk, so the lanes
 // choose which 16 bytes they fetch: the pieces of a row are permuted by the
-// row's bits, so that the eight rows that the reads of eight lanes touch lie
-// in different banks.
+// row's bits, so that the sixteen rows that the reads of sixteen lanes touch
+// lie in different banks.
 //
-// Scale bytes go through registers, 16 blocks (512 k) of a row at a time,
-// into a double buffer of dwords [stage][row]; the instruction picks its byte.
+// Scale bytes are fetched for 32 blocks (1024 k) of a row at a time and kept in
+// LDS as dwords [stage][row]; the instruction picks its byte.  (Every row is a
+// memory request of its own: 16 blocks at a time took a third of the loads'
+// time.)
 //
 // W's rows 4..7 and 8..11 of every 16 trade places on the way to the
 // instruction: a lane's eight consecutive result registers are then eight
@@ -156,27 +158,28 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 // to registers stay under way.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Scale bytes of blocks b .. b + 15 of a row (0x7f past its last block).
-__device__ __forceinline__ v4i scale_span(const uint8_t* __restrict__ row, uint32_t b, uint32_t blocks) {
-  v4i s = {0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f};
-  if (b + 16 <= blocks) {
-    __builtin_memcpy(&s, row + b, 16);
-  } else {
-#pragma unroll
-    for (uint32_t d = 0; d < 4; ++d) {
-      const uint32_t at = b + 4 * d;
-      int v = 0x7f7f7f7f;
-      if (at + 4 <= blocks) {
-        __builtin_memcpy(&v, row + at, 4);
-      } else if (at < blocks) {
-#pragma unroll
-        for (uint32_t j = 0; j < 3; ++j)
-          if (at + j < blocks) v = (v & ~(0xff << (8 * j))) | ((int)row[at + j] << (8 * j));
-      }
-      s[d] = v;
-    }
-  }
-  return s;
+// Scale bytes of blocks b .. b + 15 of a row of `blocks` >= 16 (0x7f past its
+// last block): the 16 bytes at `at`, which end with the row where those would
+// run past it, moved to the front.
+__device__ __forceinline__ uint32_t scale_at(uint32_t b, uint32_t blocks) { return b + 16 <= blocks ? b : blocks - 16; }
+__device__ __forceinline__ v4i scale_piece(v4i v, uint32_t b, uint32_t blocks) {
+  constexpr uint32_t kOne = 0x7f7f7f7fu;
+  const uint32_t skip = b - scale_at(b, blocks);
+  uint32_t x0 = (uint32_t)v[0], x1 = (uint32_t)v[1], x2 = (uint32_t)v[2], x3 = (uint32_t)v[3];
+  const bool by8 = (skip & 8) != 0, by4 = (skip & 4) != 0, gone = skip >= 16;
+  x0 = by8 ? x2 : x0;
+  x1 = by8 ? x3 : x1;
+  x2 = by8 ? kOne : x2;
+  x3 = by8 ? kOne : x3;
+  x0 = by4 ? x1 : x0;
+  x1 = by4 ? x2 : x1;
+  x2 = by4 ? x3 : x2;
+  x3 = by4 ? kOne : x3;
+  v[0] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x1, x0, skip & 3));
+  v[1] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x2, x1, skip & 3));
+  v[2] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x3, x2, skip & 3));
+  v[3] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(kOne, x3, skip & 3));
+  return v;
 }
 
 // 32 codes of an activation row.
@@ -195,238 +198,230 @@ struct Constant {
   static constexpr uint32_t value = kValue;
 };
 
-template <int kFmt, bool kGather>
-__global__ __launch_bounds__(256, 1) void mx_tile_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
+// Keeps what is computed from v from being computed before this point.
+__device__ __forceinline__ void not_ahead_of_time(uint32_t& v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(v));
+#endif
+}
+
+template <int kFmt, bool kGather, int kMF, int kNF, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
   constexpr bool kFp4 = kFmt == trace_host::kE2M1;
-  constexpr uint32_t kTile = 256;
-  constexpr uint32_t kABytes = kFp4 ? 64 : 128;                // per row and stage
-  constexpr uint32_t kStageBytes = kTile * (64 + kABytes);
-  constexpr uint32_t kALoads = kABytes / 16, kLoads = 4 + kALoads;  // 16-byte loads per lane and stage
-  constexpr uint32_t kAhead = kFp4 ? 2 : 1;                    // stages in registers
+  constexpr uint32_t kRows = 64 * kMF, kCols = 64 * kNF;
+  constexpr uint32_t kABytes = kFp4 ? 64 : 128;  // per row and stage
+  constexpr uint32_t kStageBytes = kCols * 64 + kRows * kABytes;
+  constexpr uint32_t kWLoads = kNF, kALoads = kFp4 ? kMF : 2 * kMF;  // 16-byte loads per lane and stage
   __shared__ __attribute__((aligned(1024))) char ring[2 * kStageBytes];
-  __shared__ int scale_buf[2][4][2 * kTile];  // [span][stage of the span][W's rows, A's rows]
+  constexpr uint32_t kSpan = 8;                        // stages of a scale span: 32 blocks
+  constexpr uint32_t kSLoads = (kCols + kRows) / 128;  // 16-byte loads per lane and span
+  __shared__ uint32_t scale_buf[kSpan][kCols + kRows];  // [stage of the span][W's rows, A's rows]
 
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint64_t row_tiles = p.offsets ? count_row_tiles(p.offsets, p.groups, p.rows, kTile)
-                                       : (p.rows + kTile - 1) / kTile;
+  const uint64_t row_tiles = p.offsets ? count_row_tiles(p.offsets, p.groups, p.rows, kRows)
+                                       : (p.rows + kRows - 1) / kRows;
   const uint64_t tiles = row_tiles * col_tiles;
   const uint64_t tile = xcd_tile(blockIdx.x, tiles);
   if (tile >= tiles) return;
   const uint64_t row_tile = tile / col_tiles;
-  const uint32_t n0 = (uint32_t)(tile - row_tile * col_tiles) * kTile;
+  const uint32_t n0 = (uint32_t)(tile - row_tile * col_tiles) * kCols;
   RowTile t;
   if (p.offsets) {
-    if (!find_row_tile(p.offsets, p.groups, p.rows, kTile, row_tile, t)) return;
+    if (!find_row_tile(p.offsets, p.groups, p.rows, kRows, row_tile, t)) return;
   } else {
     t.group = 0;
-    t.first = row_tile * kTile;
-    t.count = (uint32_t)(p.rows - t.first < kTile ? p.rows - t.first : kTile);
+    t.first = row_tile * kRows;
+    t.count = (uint32_t)(p.rows - t.first < kRows ? p.rows - t.first : kRows);
   }
   const bool behind = t.group >= p.groups;  // rows of no group: zeros
   const uint32_t blocks = p.k / 32;
   const uint32_t w_pitch = p.k / 2, a_pitch = kFp4 ? p.k / 2 : p.k;
   const uint32_t stages = behind ? 0 : (p.k + 127) / 128;
-
-  // what this lane fetches: W's rows 64 wave + 16 j + lane / 4, and A's rows
-  // 64 wave + 16 j + lane / 4 (4 pieces a row) or + 8 j + lane / 8 (8 pieces)
-  const uint32_t w_piece = (lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 4) & 2));
-  const uint32_t a_piece = kFp4 ? (lane & 3) ^ ((lane >> 3) & 3) : (lane & 7) ^ (lane >> 3);
   const uint64_t weight = behind ? 0 : t.group;
   const uint8_t* wc = p.w_codes + (weight * p.n + n0) * w_pitch;
-  uint32_t w_from[4];
+
+  // What this lane fetches, chunk by chunk of a buffer: 16 rows of 64 bytes
+  // (its row lane / 4), or 8 rows of 128 bytes (its row lane / 8).
+  const uint32_t piece4 = (lane & 3) ^ (lane >> 4);
+  const uint32_t piece8 = (lane & 7) ^ (lane >> 4);  // of even chunks; odd ones: ^ 4
+  uint32_t w_from[kWLoads];
 #pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) {
-    const uint32_t n = 64 * wave + 16 * j + lane / 4;
-    w_from[j] = (n0 + n < p.n ? n : 0) * w_pitch;  // past the last column: any row, dropped at the end
+  for (uint32_t j = 0; j < kWLoads; ++j) {
+    const uint32_t n = 16 * (kWLoads * wave + j) + lane / 4;
+    w_from[j] = (n0 + n < p.n ? n : 0) * w_pitch + 16 * piece4;  // past the last column: any row, dropped at the end
   }
   // source rows of packed rows m of the tile; rows past the tile's and rows
   // without a source read row 0 and are dropped or cleared at the end
   const auto packed_row = [&](uint32_t m) -> uint64_t { return t.first + (m < t.count ? m : 0); };
   const auto has_source = [&](int64_t i) -> bool { return !kGather || (i >= 0 && i < (int64_t)p.src_rows); };
-  int64_t a_index[kALoads], r_index[4], s_index;
   const uint32_t h = lane >> 5, r = lane & 31;
-  const uint32_t wn = 128 * (wave >> 1), wm = 128 * (wave & 1);
+  const uint32_t wn = (kCols / 2) * (wave >> 1), wm = (kRows / 2) * (wave & 1);
+  int64_t a_index[kALoads], r_index[kMF];
 #pragma unroll
   for (uint32_t j = 0; j < kALoads; ++j) {
-    const uint64_t row = packed_row(kFp4 ? 64 * wave + 16 * j + lane / 4 : 64 * wave + 8 * j + lane / 8);
+    const uint64_t row = packed_row(kFp4 ? 16 * (kALoads * wave + j) + lane / 4 : 8 * (kALoads * wave + j) + lane / 8);
     a_index[j] = kGather ? p.row_index[row] : (int64_t)row;
   }
 #pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) r_index[j] = kGather ? p.row_index[packed_row(wm + r + 32 * j)] : 0;
-  s_index = kGather ? p.row_index[packed_row(threadIdx.x)] : (int64_t)packed_row(threadIdx.x);
+  for (uint32_t j = 0; j < kMF; ++j) r_index[j] = kGather ? p.row_index[packed_row(wm + r + 32 * j)] : 0;
   const uint8_t* a_from[kALoads];
 #pragma unroll
   for (uint32_t j = 0; j < kALoads; ++j)
-    a_from[j] = p.a_codes + (has_source(a_index[j]) ? (uint64_t)a_index[j] : 0) * a_pitch;
-  uint32_t sources = 0;  // which of this lane's four result rows have a source row
+    a_from[j] = p.a_codes + (has_source(a_index[j]) ? (uint64_t)a_index[j] : 0) * a_pitch +
+                16 * (kFp4 ? piece4 : piece8 ^ (4 * (j & 1)));
+  uint32_t sources = 0;  // which of this lane's result rows have a source row
 #pragma unroll
-  for (uint32_t j = 0; j < 4; ++j) sources |= (has_source(r_index[j]) ? 1u : 0u) << j;
-  v4i held[kAhead][kLoads];  // stages on their way to LDS
+  for (uint32_t j = 0; j < kMF; ++j) sources |= (has_source(r_index[j]) ? 1u : 0u) << j;
+
+  v4i held[kWLoads + kALoads];  // a stage on its way to LDS
   // may_end: the stage may hold fewer than 128 k; pieces past the end are zeros
-  const auto fetch = [&](uint32_t st, v4i(&to)[kLoads], bool may_end) {
+  const auto fetch = [&](uint32_t st, bool may_end) {
     const uint32_t left = p.k - 128 * st;
-    const bool w_in = !may_end || 32 * w_piece < left;
-    const bool a_in = !may_end || (kFp4 ? 32 : 16) * a_piece < left;
 #pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) {
+    for (uint32_t j = 0; j < kWLoads; ++j) {
       v4i v = {0, 0, 0, 0};
-      if (w_in) v = *reinterpret_cast<const v4i*>(wc + 64 * st + (w_from[j] + 16 * w_piece));
-      to[j] = v;
+      if (!may_end || 32 * piece4 < left) v = *reinterpret_cast<const v4i*>(wc + 64 * st + w_from[j]);
+      held[j] = v;
     }
 #pragma unroll
     for (uint32_t j = 0; j < kALoads; ++j) {
+      const uint32_t piece = kFp4 ? piece4 : piece8 ^ (4 * (j & 1));
       v4i v = {0, 0, 0, 0};
-      if (a_in) v = *reinterpret_cast<const v4i*>(a_from[j] + kABytes * st + 16 * a_piece);
-      to[4 + j] = v;
+      if (!may_end || (kFp4 ? 32 : 16) * piece < left) v = *reinterpret_cast<const v4i*>(a_from[j] + kABytes * st);
+      held[kWLoads + j] = v;
     }
   };
-  const auto place = [&](uint32_t st, const v4i(&from)[kLoads]) {
+  const auto place = [&](uint32_t st) {
     char* to = ring + (st & 1) * kStageBytes + 16 * lane;
 #pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(to + 1024 * (4 * wave + j)) = from[j];
+    for (uint32_t j = 0; j < kWLoads; ++j) *reinterpret_cast<v4i*>(to + 1024 * (kWLoads * wave + j)) = held[j];
 #pragma unroll
     for (uint32_t j = 0; j < kALoads; ++j)
-      *reinterpret_cast<v4i*>(to + 64 * kTile + 1024 * (kALoads * wave + j)) = from[4 + j];
+      *reinterpret_cast<v4i*>(to + 64 * kCols + 1024 * (kALoads * wave + j)) = held[kWLoads + j];
   };
-  // scale rows: thread i carries W's row i and A's row i
-  const uint8_t* ws_row = p.w_scales + (weight * p.n + n0 + (n0 + threadIdx.x < p.n ? threadIdx.x : 0)) * blocks;
-  const uint8_t* as_row = p.a_scales + (has_source(s_index) ? (uint64_t)s_index : 0) * blocks;
-  v4i w_span, a_span;
-  const auto load_span = [&](uint32_t span) {
-    w_span = scale_span(ws_row, 16 * span, blocks);
-    a_span = scale_span(as_row, 16 * span, blocks);
-  };
-  const auto store_span = [&](uint32_t span) {
+  // Scales of the span that starts with stage `first`: load i carries half
+  // threadIdx.x % 2 of row 128 i + threadIdx.x / 2 of W's, then A's rows.
+  v4i span[kSLoads];  // on its way to LDS
+  const auto load_span = [&](uint32_t first) {
+    uint32_t id = threadIdx.x;
+    not_ahead_of_time(id);  // or the addresses fill registers throughout the loop
 #pragma unroll
-    for (uint32_t d = 0; d < 4; ++d) {
-      scale_buf[span & 1][d][threadIdx.x] = w_span[d];
-      scale_buf[span & 1][d][kTile + threadIdx.x] = a_span[d];
+    for (uint32_t i = 0; i < kSLoads; ++i) {
+      const uint32_t row = 128 * i + id / 2;
+      const uint8_t* from;
+      if (128 * i < kCols) {
+        from = p.w_scales + (weight * p.n + n0 + (n0 + row < p.n ? row : 0)) * blocks;
+      } else {
+        int64_t index = (int64_t)packed_row(row - kCols);
+        if (kGather) index = p.row_index[index];
+        from = p.a_scales + (has_source(index) ? (uint64_t)index : 0) * blocks;
+      }
+      __builtin_memcpy(&span[i], from + scale_at(4 * first + 16 * (id & 1), blocks), 16);
+    }
+  };
+  const auto store_span = [&](uint32_t first) {
+#pragma unroll
+    for (uint32_t i = 0; i < kSLoads; ++i) {
+      const v4i v = scale_piece(span[i], 4 * first + 16 * (threadIdx.x & 1), blocks);
+#pragma unroll
+      for (uint32_t d = 0; d < 4; ++d) scale_buf[4 * (threadIdx.x & 1) + d][128 * i + threadIdx.x / 2] = (uint32_t)v[d];
     }
   };
 
-  v16f acc[4][4] = {};  // [W fragment][A fragment]
+  v16f acc[kNF][kMF] = {};
   const uint32_t w_row = wn + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));  // bits 2 and 3 trade places
-  const uint32_t w_at = w_row * 64 + 16 * (h ^ (((w_row >> 1) & 1) | ((w_row >> 2) & 2)));
-  const uint32_t a_row_in = wm + r;
-  const uint32_t a_at = 64 * kTile + (kFp4 ? a_row_in * 64 + 16 * (h ^ ((r >> 1) & 3)) : a_row_in * 128 + 16 * (h ^ (r & 7)));
-
+  const uint32_t a_row = wm + r;
+  const uint32_t w_at = w_row * 64 + 16 * (h ^ ((w_row >> 2) & 3));
+  const uint32_t a_at = 64 * kCols + (kFp4 ? a_row * 64 + 16 * (h ^ ((r >> 2) & 3)) : a_row * 128 + 16 * (h ^ ((r >> 1) & 7)));
   using AFrag = typename Operand<kFmt>::type;
-  v4i wf[2][4];
-  AFrag af[2][4];
-  uint32_t wsc[2][4], asc[2][4];  // of this stage and the next
-  // Fragments of k-step kk (64 k) of a stage.
-  const auto read_step = [&](uint32_t st, uint32_t kk, v4i(&w)[4], AFrag(&a)[4]) {
+  v4i wf[kNF];
+  AFrag af[kMF];
+  uint32_t wsc[kNF], asc[kMF];
+  // fragments of k-step kk (64 k) of a stage
+  const auto read_step = [&](uint32_t st, uint32_t kk) {
     const char* from = ring + (st & 1) * kStageBytes;
 #pragma unroll
-    for (uint32_t f = 0; f < 4; ++f) w[f] = *reinterpret_cast<const v4i*>(from + ((w_at ^ (32 * kk)) + 2048 * f));
-#pragma unroll
-    for (uint32_t f = 0; f < 4; ++f) {
+    for (uint32_t f = 0; f < kMF; ++f) {
       if constexpr (kFp4) {
-        a[f] = *reinterpret_cast<const v4i*>(from + ((a_at ^ (32 * kk)) + 2048 * f));
+        af[f] = *reinterpret_cast<const v4i*>(from + ((a_at ^ (32 * kk)) + 2048 * f));
       } else {
-        a[f] = join(*reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk)) + 4096 * f)),
-                    *reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk) ^ 32) + 4096 * f)));
+        af[f] = join(*reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk)) + 4096 * f)),
+                     *reinterpret_cast<const v4i*>(from + ((a_at ^ (64 * kk) ^ 32) + 4096 * f)));
       }
     }
+#pragma unroll
+    for (uint32_t f = 0; f < kNF; ++f) wf[f] = *reinterpret_cast<const v4i*>(from + ((w_at ^ (32 * kk)) + 2048 * f));
   };
-  const auto read_scales = [&](uint32_t st, uint32_t(&w)[4], uint32_t(&a)[4]) {
-    const int* from = scale_buf[(st >> 2) & 1][st & 3];
+  const auto read_scales = [&](uint32_t st) {
+    // byte 0: this lane's block of the stage's first 64 k; byte 2: of the second
+    const uint32_t* from = scale_buf[st % kSpan];
 #pragma unroll
-    for (uint32_t f = 0; f < 4; ++f) {
-      w[f] = (uint32_t)from[w_row + 32 * f];
-      a[f] = (uint32_t)from[kTile + a_row_in + 32 * f];
-    }
+    for (uint32_t f = 0; f < kNF; ++f) wsc[f] = from[w_row + 32 * f] >> (8 * h);
+#pragma unroll
+    for (uint32_t f = 0; f < kMF; ++f) asc[f] = from[kCols + a_row + 32 * f] >> (8 * h);
   };
-  const auto multiply = [&](const v4i(&w)[4], const AFrag(&a)[4], const uint32_t(&ws)[4], const uint32_t(&as)[4], auto sel) {
+  const auto multiply = [&](auto step) {
+    constexpr uint32_t kSel = 2 * decltype(step)::value;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kNF; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w[i]), widen(a[j]), acc[i][j], kSelE2M1,
-                                                                    kFp4 ? kSelE2M1 : kSelE4M3, decltype(sel)::value,
-                                                                    (int)ws[i], decltype(sel)::value, (int)as[j]);
-  };
-  // One stage, whose first step and scales have been read.  Under the first
-  // step's arithmetic the second step is read, the next stage is placed in
-  // LDS and the one kAhead + 1 further is fetched; under the second step's the
-  // next stage's first step is read.  kSteady: those stages exist, in full.
-  const auto stage = [&](uint32_t st, auto part, auto steady) {
-    constexpr uint32_t kPart = decltype(part)::value;  // st % 4
-    constexpr bool kSteady = decltype(steady)::value;
-    constexpr uint32_t kNow = kPart & 1, kNext = kNow ^ 1, kHeld = (kPart + 1) % kAhead;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {  // byte 0: this lane's block of step 0; byte 2: of step 1
-      wsc[kNow][f] >>= 8 * h;
-      asc[kNow][f] >>= 8 * h;
-    }
-    read_step(st, 1, wf[1], af[1]);
-    if (kPart == 2 && (kSteady || st + 2 < stages)) store_span((st >> 2) + 1);
-    if (kSteady || st + 1 < stages) place(st + 1, held[kHeld]);
-    if (kPart == 0 && (kSteady || st + 4 < stages)) load_span((st >> 2) + 1);
-    if (kSteady || st + 1 + kAhead < stages) fetch(st + 1 + kAhead, held[kHeld], !kSteady);
-    multiply(wf[0], af[0], wsc[kNow], asc[kNow], Constant<0>());
-    if (kSteady) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                // matrix instructions
-        __builtin_amdgcn_sched_group_barrier(0x100, kFp4 ? 1 : 2, 0);     // LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x200, kFp4 ? 1 : 2, 0);     // LDS writes
-        __builtin_amdgcn_sched_group_barrier(0x020, kFp4 ? 1 : 2, 0);     // loads
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (kSteady || st + 1 < stages) {
-      lds_barrier();
-      read_step(st + 1, 0, wf[0], af[0]);
-      read_scales(st + 1, wsc[kNext], asc[kNext]);
-    }
-    multiply(wf[1], af[1], wsc[kNow], asc[kNow], Constant<2>());
-    if (kSteady) {
-#pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, kFp4 ? 1 : 2, 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < kMF; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(wf[i]), widen(af[j]), acc[i][j], kSelE2M1,
+                                                                    kFp4 ? kSelE2M1 : kSelE4M3, kSel, (int)wsc[i],
+                                                                    kSel, (int)asc[j]);
   };
 
   if (stages) {
+    fetch(0, true);
     load_span(0);
-    v4i first[kLoads];
-    fetch(0, first, true);
-#pragma unroll
-    for (uint32_t i = 0; i < kAhead; ++i)
-      if (1 + i < stages) fetch(1 + i, held[(1 + i) % kAhead], true);
+    place(0);
+    if (stages > 1) fetch(1, true);
     store_span(0);
-    place(0, first);
     lds_barrier();
-    read_step(0, 0, wf[0], af[0]);
-    read_scales(0, wsc[0], asc[0]);
-    uint32_t st = 0;
-    for (; st + 5 + kAhead < stages; st += 4) {
-      stage(st, Constant<0>(), Constant<1>());
-      stage(st + 1, Constant<1>(), Constant<1>());
-      stage(st + 2, Constant<2>(), Constant<1>());
-      stage(st + 3, Constant<3>(), Constant<1>());
-    }
-    for (; st < stages; st += 4) {
-      stage(st, Constant<0>(), Constant<0>());
-      if (st + 1 < stages) stage(st + 1, Constant<1>(), Constant<0>());
-      if (st + 2 < stages) stage(st + 2, Constant<2>(), Constant<0>());
-      if (st + 3 < stages) stage(st + 3, Constant<3>(), Constant<0>());
-    }
   }
+  // One stage.  kSteady: stages st + 1 and st + 2 exist in full.
+  const auto stage = [&](uint32_t st, auto steady) {
+    constexpr bool kSteady = decltype(steady)::value;
+    read_scales(st);
+    read_step(st, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    // the other buffer is free: every wave has read stage st - 1
+    if (kSteady || st + 1 < stages) place(st + 1);
+    if (kSteady || st + 2 < stages) fetch(st + 2, !kSteady);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(Constant<0>());
+    read_step(st, 1);
+    multiply(Constant<1>());
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    if (st % kSpan == kSpan - 1 && (kSteady || st + 1 < stages)) {  // every wave has read the span's last scales
+      load_span(st + 1);
+      store_span(st + 1);
+      lds_barrier();
+    }
+  };
+  if (stages) {
+    fetch(0, true);
+    load_span(0);
+    place(0);
+    if (stages > 1) fetch(1, true);
+    store_span(0);
+    lds_barrier();
+  }
+  const uint32_t full = p.k / 128;
+  uint32_t st = 0;
+  for (; st + 2 < full && st < stages; ++st) stage(st, Constant<1>());
+  for (; st < stages; ++st) stage(st, Constant<0>());
   // register e of a block: n = 16 (e / 8) + 8 h + e % 8, m = lane % 32
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < kMF; ++j) {
     const uint32_t m = wm + 32 * j + r;
     if (m >= t.count) continue;
     const bool ok = (sources >> j) & 1;
     uint16_t* row = p.y + (t.first + m) * p.n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kNF; ++i)
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
         const uint32_t n = n0 + wn + 32 * i + 2 * e + 8 * h;
@@ -456,22 +451,34 @@ static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int kFmt>
+template <int kFmt, int kMF, int kNF, int kPerCu>
 static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
-  const uint32_t cols = (p.n + 255) / 256;
-  const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 256) : (p.rows + 255) / 256;
+  constexpr uint32_t kRows = 64 * kMF, kCols = 64 * kNF;
+  const uint32_t cols = (p.n + kCols - 1) / kCols;
+  const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, kRows) : (p.rows + kRows - 1) / kRows;
   const uint64_t grid = (row_tiles * cols + 7) / 8 * 8;
   if (grid * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
   if (p.row_index)
-    hipLaunchKernelGGL((mx_tile_kernel<kFmt, true>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
+    hipLaunchKernelGGL((mx_tile_kernel<kFmt, true, kMF, kNF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
   else
-    hipLaunchKernelGGL((mx_tile_kernel<kFmt, false>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
+    hipLaunchKernelGGL((mx_tile_kernel<kFmt, false, kMF, kNF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
   return hipGetLastError();
 }
 
 template <int kFmt>
 static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
-  if (p.rows >= 128 && p.src_rows > 0) return launch_tile<kFmt>(p, stream);
+  // A row's scales must fill one 16-byte load, and row 0 must exist.
+  if (p.rows >= 128 && p.rows >= 32 * (uint64_t)p.groups && p.src_rows > 0 && p.k >= 512) {
+    // 128 x 256 tiles read W and A from the caches less often than 128 x 128
+    // ones (131072 x 1536 x 2048 per expert: 0.37 against 0.41 ms), where
+    // there are enough of them to fill every compute unit twice.  With MXFP8
+    // activations their registers would spill (16384 x 2048 x 4096: 181
+    // against 146 us).
+    const uint64_t tiles = (p.rows + 127) / 128 * ((p.n + 255) / 256);
+    if constexpr (kFmt == kE2M1)
+      if (tiles >= 512) return launch_tile<kFmt, 2, 4, 2>(p, stream);
+    return launch_tile<kFmt, 2, 2, 2>(p, stream);
+  }
   return launch_skinny<kFmt, 2, 2, 4>(p, stream);
 }
 

@@ -31,47 +31,36 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-constexpr uint32_t kTileP = 128, kTileK = 128, kTileC = 32;
-// Row pitch of a tile that is read transposed: 64 bytes more than a multiple
-// of 256, so that the four rows that 32 lanes read together lie in different
-// LDS banks.
-constexpr uint32_t kTrPitch = 2 * kTileK + 64;
-
 // The E8M0 byte as the float whose exponent the scaling conversions use.
 __device__ __forceinline__ float e8m0_operand(uint32_t b) { return __uint_as_float(b << 23); }
 
-// 16 codes to bf16: out[i] holds elements 2i and 2i + 1.
+// Eight codes to bf16: out[i] holds elements 2i and 2i + 1.
 template <int kFmt>
-__device__ __forceinline__ void decode16(const uint32_t (&c)[4], float s, uint32_t (&out)[8]) {
-  bf16x2 v[8];
+__device__ __forceinline__ uint4 decode8(const uint32_t* c, float s) {
+  bf16x2 v[4];
   if (kFmt == trace_host::kE2M1) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[4 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 0);
-      v[4 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 1);
-      v[4 * i + 2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 2);
-      v[4 * i + 3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[i], s, 3);
-    }
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], s, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], s, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], s, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[0], s, 3);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, false);
-      v[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, true);
-    }
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], s, false);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], s, true);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], s, false);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], s, true);
   }
-  __builtin_memcpy(out, v, sizeof(v));
+  uint4 out;
+  __builtin_memcpy(&out, v, sizeof(out));
+  return out;
 }
 
-// Eight consecutive c (rows 16 kk + 8 h ..) of one of 32 columns from a tile
-// of kTrPitch-byte rows; kSwap: the columns' bits 2 and 3 trade places.
-template <bool kSwap>
-__device__ __forceinline__ v8bf read_transposed(const char* tile, uint32_t col0, uint32_t kk, uint32_t lane) {
-  const uint32_t j = lane & 15;
-  const uint32_t q = kSwap ? (((j & 1) << 1) | ((j & 3) >> 1)) : (j & 3);
-  const uint32_t row = 16 * kk + 8 * (lane >> 5) + (j >> 2);
-  const uint32_t at = row * kTrPitch + 2 * (col0 + 16 * ((lane >> 4) & 1) + 4 * q);
-  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + at));
-  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + at + 4 * kTrPitch));
+// This wave's LDS accesses are done; meet the workgroup's other waves.  Loads
+// to registers stay under way.
+__device__ __forceinline__ void grad_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ v8bf transposed(const char* at, uint32_t pitch) {
+  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * pitch));
   v8bf out;
   __builtin_memcpy(&out, &lo, 8);
   __builtin_memcpy(reinterpret_cast<char*>(&out) + 8, &hi, 8);
@@ -79,139 +68,229 @@ __device__ __forceinline__ v8bf read_transposed(const char* tile, uint32_t col0,
 }
 
 // kWeight: D = gw of one group (p = n, c = the group's rows m); otherwise
-// D = gx of a row tile (p = m, c = n).  parts > 1 (kWeight, one group only):
-// the contraction's part blockIdx.y, as fp32 to p.partial.
-template <bool kWeight, int kFmt>
-__global__ __launch_bounds__(256) void mx_grad_kernel(trace_host::MxGradArgs p, uint32_t k_tiles, uint32_t p_tiles,
-                                                      uint32_t parts) {
-  __shared__ __attribute__((aligned(16))) char g_tile[kWeight ? kTileC * kTrPitch : kTileP * 2 * kTileC];
-  __shared__ __attribute__((aligned(16))) char q_tile[kTileC * kTrPitch];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t k0 = (blockIdx.x % k_tiles) * kTileK;
-  const uint64_t outer = blockIdx.x / k_tiles;
-  RowTile t{0, 0, 0};       // rows of the tile (gx) or of the group (gw)
-  uint32_t p0 = 0;          // first n (gw)
-  uint64_t c_begin = 0, c_end = p.n;
+// D = gx of a row tile (p = m, c = n).  A workgroup of 2 x 2 waves owns
+// 64 kKF k times 64 kPF p, each wave a quarter as kKF x kPF results of
+// 32 x 32.  The contraction runs in stages of kC, in two LDS buffers with one
+// barrier per stage; the next stage is decoded and placed in LDS, and the one
+// after it fetched to registers, under the arithmetic.
+//
+// LDS layouts.  Q is [c][k]: 64 bytes per block of 32 k, a lane's four
+// 16-byte pieces of a block permuted by the row's and the block's low bits so
+// that sixteen lanes write different banks; rows are 64 bytes more than a
+// multiple of 256 apart, so that the four rows that 32 lanes read transposed
+// lie in different banks.  gy is [c][p] likewise for gw; for gx it is [p][c]
+// with its pieces permuted by the row's bits.
+// parts > 1 (kWeight, one group only): the contraction's part blockIdx.y, as
+// fp32 to p.partial.
+template <bool kWeight, int kFmt, bool kGather, int kKF, int kPF, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGradArgs p, uint32_t k_tiles,
+                                                              uint32_t p_tiles, uint32_t parts) {
+  constexpr bool kFp4 = kFmt == trace_host::kE2M1;
+  constexpr uint32_t kK = 64 * kKF, kP = 64 * kPF;
+  constexpr uint32_t kC = 256 * 32 / kK;              // one block of Q per lane and stage
+  constexpr uint32_t kQPitch = 2 * kK + 64, kGPitch = kWeight ? 2 * kP + 64 : 2 * kC;
+  constexpr uint32_t kQBytes = kC * kQPitch, kGBytes = kWeight ? kC * kGPitch : kP * kGPitch;
+  constexpr uint32_t kGLoads = kP * kC * 2 / 4096;    // 16-byte loads per lane and stage
+  constexpr uint32_t kQDwords = kFp4 ? 4 : 8;
+  __shared__ __attribute__((aligned(256))) char q_buf[2][kQBytes];
+  __shared__ __attribute__((aligned(256))) char g_buf[2][kGBytes];
+
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint64_t tiles;
+  if (kWeight)
+    tiles = (uint64_t)p.groups * p_tiles * k_tiles;
+  else
+    tiles = (p.offsets ? count_row_tiles(p.offsets, p.groups, p.rows, kP) : (p.rows + kP - 1) / kP) * k_tiles;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const uint64_t outer = tile / k_tiles;
+  const uint32_t k0 = (uint32_t)(tile - outer * k_tiles) * kK;
+  RowTile t{0, 0, 0};  // rows of the tile (gx) or of the group (gw)
+  uint32_t p0 = 0;     // first n (gw)
+  uint32_t c_begin = 0, c_end = p.n;
   if (kWeight) {
-    p0 = (uint32_t)(outer % p_tiles) * kTileP;
     t.group = (uint32_t)(outer / p_tiles);
-    if (p.offsets) {
+    p0 = (uint32_t)(outer - (uint64_t)t.group * p_tiles) * kP;
+    if (p.offsets)
       t.count = group_rows(p.offsets, t.group, p.groups, p.rows, t.first);
-    } else {
+    else
       t.count = (uint32_t)p.rows;
-    }
-    const uint32_t steps = (t.count + kTileC - 1) / kTileC;
-    c_begin = (uint64_t)(blockIdx.y * (uint64_t)steps / parts) * kTileC;
-    c_end = (uint64_t)((blockIdx.y + 1) * (uint64_t)steps / parts) * kTileC;
+    const uint64_t steps = (t.count + kC - 1) / kC;
+    c_begin = (uint32_t)(blockIdx.y * steps / parts) * kC;
+    c_end = (uint32_t)((blockIdx.y + 1) * steps / parts) * kC;
     if (c_end > t.count) c_end = t.count;
   } else if (p.offsets) {
-    if (!find_row_tile(p.offsets, p.groups, p.rows, kTileP, outer, t)) return;
+    if (!find_row_tile(p.offsets, p.groups, p.rows, kP, outer, t)) return;
     if (t.group >= p.groups) c_end = 0;  // rows of no group: zeros
   } else {
-    t.first = outer * kTileP;
-    t.count = (uint32_t)(p.rows - t.first < kTileP ? p.rows - t.first : kTileP);
+    t.first = outer * kP;
+    t.count = (uint32_t)(p.rows - t.first < kP ? p.rows - t.first : kP);
   }
-  const uint32_t q_pitch = kFmt == trace_host::kE2M1 ? p.k / 2 : p.k;
-  const uint32_t blocks = p.k / 32;
-  const uint8_t* qc = p.q_codes + (kWeight ? 0 : (uint64_t)t.group * p.n * q_pitch);
-  const uint8_t* qs = p.q_scales + (kWeight ? 0 : (uint64_t)t.group * p.n * blocks);
-  const uint32_t wp = (wave >> 1) * 64, wk = (wave & 1) * 64;
-  v16f acc[2][2] = {};  // [k fragment][p fragment]
-  for (uint64_t c0 = c_begin; c0 < c_end; c0 += kTileC) {
-    __syncthreads();
-    // gy
+  const uint32_t length = c_end > c_begin ? c_end - c_begin : 0;
+  const uint32_t stages = (length + kC - 1) / kC;
+  const uint32_t q_pitch = kFp4 ? p.k / 2 : p.k, blocks = p.k / 32;
+
+  // Q: this lane's row of a stage and its block of the tile's k.  Columns
+  // past p.k and rows p past the end read something valid: their results are
+  // dropped.  Rows c past the end, and rows without a source, are zeros.
+  const uint32_t q_row = threadIdx.x / (kK / 32), q_blk = threadIdx.x % (kK / 32);
+  const uint32_t q_col = k0 + 32 * q_blk < p.k ? k0 + 32 * q_blk : k0;
+  const uint64_t q_first = kWeight ? t.first + c_begin : (uint64_t)(t.group < p.groups ? t.group : 0) * p.n;
+  const uint8_t* qc = p.q_codes + (kFp4 ? q_col / 2 : q_col);
+  const uint8_t* qs = p.q_scales + q_col / 32;
+  const uint16_t* g_from[kGLoads];
+  uint32_t g_c[kGLoads];  // c within the stage
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
+  for (uint32_t i = 0; i < kGLoads; ++i) {
+    if (kWeight) {
+      g_c[i] = (threadIdx.x + 256 * i) / (kP / 8);
+      const uint32_t col = 8 * ((threadIdx.x + 256 * i) % (kP / 8));
+      g_from[i] = p.grad_y + (t.first + c_begin + g_c[i]) * p.n + (p0 + col < p.n ? p0 + col : p0);
+    } else {
+      const uint32_t m = (threadIdx.x + 256 * i) / (kC / 8);
+      g_c[i] = 8 * ((threadIdx.x + 256 * i) % (kC / 8));
+      g_from[i] = p.grad_y + (t.first + (m < t.count ? m : 0)) * p.n + g_c[i];
+    }
+  }
+
+  uint32_t q_held[kQDwords], q_scale = 0;
+  int64_t q_index = 0;  // kGather: the source row of the stage to be fetched next
+  v4i g_held[kGLoads];
+  const auto fetch_index = [&](uint32_t st, bool may_end) {
+    if (!kGather) return;
+    const uint32_t c = kC * st + q_row;
+    q_index = !may_end || c < length ? p.row_index[q_first + c] : -1;
+  };
+  // may_end: the stage may end early
+  const auto fetch = [&](uint32_t st, bool may_end) {
+    const uint32_t c = kC * st + q_row;
+    uint64_t row = q_first + c;
+    bool ok = !may_end || c < length;
+    if (kGather) {
+      ok = ok && q_index >= 0 && q_index < (int64_t)p.src_rows;
+      row = ok ? (uint64_t)q_index : 0;
+    }
+    q_scale = 127;
+#pragma unroll
+    for (uint32_t d = 0; d < kQDwords; ++d) q_held[d] = 0;
+    if ((!may_end && !kGather) || ok) {
+      __builtin_memcpy(q_held, __builtin_assume_aligned(qc + row * q_pitch, 16), 4 * kQDwords);
+      q_scale = qs[row * blocks];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kGLoads; ++i) {
+      v4i v = {0, 0, 0, 0};
+      if (!may_end || kC * st + g_c[i] < length)
+        v = *reinterpret_cast<const v4i*>(g_from[i] + (uint64_t)kC * st * (kWeight ? p.n : 1));
+      g_held[i] = v;
+    }
+  };
+  const uint32_t q_swap = ((q_blk >> 2) & 1) | ((q_row & 1) << 1);
+  const auto place = [&](uint32_t st) {
+    char* q = q_buf[st & 1] + q_row * kQPitch + 64 * q_blk;
+    const float s = e8m0_operand(q_scale);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(q + 16 * (i ^ q_swap)) = decode8<kFmt>(q_held + (kFp4 ? i : 2 * i), s);
+    char* g = g_buf[st & 1];
+#pragma unroll
+    for (uint32_t i = 0; i < kGLoads; ++i) {
+      const uint32_t id = threadIdx.x + 256 * i;
       if (kWeight) {
-        const uint32_t c = threadIdx.x / 16 + 16 * i, col = 8 * (threadIdx.x & 15);
-        if (c0 + c < c_end && p0 + col < p.n)
-          v = *reinterpret_cast<const uint4*>(p.grad_y + (t.first + c0 + c) * p.n + p0 + col);
-        *reinterpret_cast<uint4*>(g_tile + c * kTrPitch + 2 * col) = v;
+        *reinterpret_cast<v4i*>(g + id / (kP / 8) * kGPitch + 16 * (id % (kP / 8))) = g_held[i];
       } else {
-        const uint32_t m = threadIdx.x / 4 + 64 * i, ch = threadIdx.x & 3;
-        if (m < t.count && c0 + 8 * ch < c_end)
-          v = *reinterpret_cast<const uint4*>(p.grad_y + (t.first + m) * p.n + c0 + 8 * ch);
-        *reinterpret_cast<uint4*>(g_tile + m * 64 + 16 * (ch ^ ((m >> 1) & 3))) = v;
+        const uint32_t m = id / (kC / 8), piece = id % (kC / 8);
+        *reinterpret_cast<v4i*>(g + m * kGPitch + 16 * (piece ^ (kC == 32 ? (m >> 2) & 3 : (m >> 1) & 7))) = g_held[i];
       }
     }
-    // Q: 16 codes of row c
-    {
-      const uint32_t c = threadIdx.x / 8, k = k0 + 16 * (threadIdx.x & 7);
-      uint32_t code[4] = {0, 0, 0, 0};
-      float s = 1.f;
-      bool ok = c0 + c < c_end && k < p.k;
-      uint64_t row = c0 + c;
-      if (kWeight) {
-        row += t.first;
-        if (p.row_index && ok) {
-          const int64_t src = p.row_index[row];
-          ok = src >= 0 && src < (int64_t)p.src_rows;
-          row = (uint64_t)src;
-        }
-      }
-      if (ok) {
-        s = e8m0_operand(qs[row * blocks + k / 32]);
-        if (kFmt == trace_host::kE2M1) {
-          const uint2 v = *reinterpret_cast<const uint2*>(qc + row * q_pitch + k / 2);
-          code[0] = v.x; code[1] = v.y;
-        } else {
-          const uint4 v = *reinterpret_cast<const uint4*>(qc + row * q_pitch + k);
-          code[0] = v.x; code[1] = v.y; code[2] = v.z; code[3] = v.w;
-        }
-      }
-      uint32_t out[8];
-      decode16<kFmt>(code, s, out);
-      uint4* dst = reinterpret_cast<uint4*>(q_tile + c * kTrPitch + 32 * (threadIdx.x & 7));
-      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  };
+
+  // Where this lane reads.  Transposed: lane j of 16 reads row j / 4 and four
+  // of the 16 columns, and gets column j.  Q's columns 4..7 and 8..11 of every
+  // 16 trade places, so that a lane's eight consecutive results are eight
+  // consecutive k.
+  const uint32_t wk = 32 * kKF * (wave >> 1), wp = 32 * kPF * (wave & 1);
+  const uint32_t h = lane >> 5, r = lane & 31, j = lane & 15, half = (lane >> 4) & 1;
+  const uint32_t quad = ((j & 1) << 1) | ((j >> 1) & 1);
+  const uint32_t tr_row = 8 * h + (j >> 2);
+  // piece 2 half + quad / 2 of the block, permuted by the row's lowest bit
+  // here and by bit 2 of the block below; rows 4 apart have the same bit
+  const uint32_t q_at = tr_row * kQPitch + 16 * ((2 * half + (quad >> 1)) ^ (2 * (tr_row & 1))) + 8 * (quad & 1);
+  const uint32_t g_at = kWeight ? tr_row * kGPitch + 2 * (wp + 16 * half + 4 * (j & 3))
+                                : (wp + r) * kGPitch + 16 * (h ^ (kC == 32 ? (r >> 2) & 3 : (r >> 1) & 7));
+  v16f acc[kKF][kPF] = {};
+  const auto step = [&](uint32_t st, uint32_t kk) {
+    const char* q = q_buf[st & 1] + 16 * kk * kQPitch;
+    const char* g = g_buf[st & 1];
+    v8bf qf[kKF], gf[kPF];
+#pragma unroll
+    for (uint32_t f = 0; f < kPF; ++f) {
+      if (kWeight)
+        gf[f] = transposed(g + 16 * kk * kGPitch + g_at + 64 * f, kGPitch);
+      else
+        gf[f] = *reinterpret_cast<const v8bf*>(g + (g_at ^ (32 * kk)) + 32 * f * kGPitch);
     }
-    __syncthreads();
 #pragma unroll
-    for (uint32_t kk = 0; kk < 2; ++kk) {
-      v8bf q[2], gg[2];
-#pragma unroll
-      for (uint32_t f = 0; f < 2; ++f) {
-        q[f] = read_transposed<true>(q_tile, wk + 32 * f, kk, lane);
-        if (kWeight) {
-          gg[f] = read_transposed<false>(g_tile, wp + 32 * f, kk, lane);
-        } else {
-          const uint32_t m = wp + 32 * f + (lane & 31), ch = 2 * kk + (lane >> 5);
-          gg[f] = *reinterpret_cast<const v8bf*>(g_tile + m * 64 + 16 * (ch ^ ((m >> 1) & 3)));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[i], gg[j], acc[i][j], 0, 0, 0);
+    for (uint32_t f = 0; f < kKF; ++f) {
+      const uint32_t blk = wk / 32 + f;
+      qf[f] = transposed(q + (q_at ^ (16 * ((blk >> 2) & 1))) + 64 * blk, kQPitch);
     }
+#pragma unroll
+    for (int a = 0; a < kKF; ++a)
+#pragma unroll
+      for (int b = 0; b < kPF; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[a], gf[b], acc[a][b], 0, 0, 0);
+  };
+  // One stage.  kSteady: stages st + 1 to st + 3 exist in full.
+  const auto stage = [&](uint32_t st, bool steady) {
+    if (steady || st + 1 < stages) place(st + 1);
+    if (steady || st + 2 < stages) fetch(st + 2, !steady);
+    if (steady || st + 3 < stages) fetch_index(st + 3, !steady);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (uint32_t kk = 0; kk < kC / 16; ++kk) step(st, kk);
+    __builtin_amdgcn_sched_barrier(0);
+    grad_barrier();
+  };
+  if (stages) {
+    fetch_index(0, true);
+    fetch(0, true);
+    fetch_index(1, true);
+    place(0);
+    if (stages > 1) fetch(1, true);
+    if (stages > 2) fetch_index(2, true);
+    grad_barrier();
   }
-  // register e of a fragment: k = 16 (e / 8) + 8 (lane / 32) + e % 8
+  uint32_t st = 0;
+  for (; (st + 4) * kC <= length; ++st) stage(st, true);
+  for (; st < stages; ++st) stage(st, false);
+
+  // register e of a result: k = 16 (e / 8) + 8 h + e % 8, p = lane % 32
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t pp = wp + 32 * j + (lane & 31);
+  for (int b = 0; b < kPF; ++b) {
+    const uint32_t pp = wp + 32 * b + r;
     if (kWeight ? p0 + pp >= p.n : pp >= t.count) continue;
     const uint64_t row = kWeight ? (uint64_t)t.group * p.n + p0 + pp : t.first + pp;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int a = 0; a < kKF; ++a)
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
-        const uint32_t k = k0 + wk + 32 * i + 2 * e + 8 * (lane >> 5);
+        const uint32_t k = k0 + wk + 32 * a + 2 * e + 8 * h;
         if (k >= p.k) continue;
-        const v16f& a = acc[i][j];
+        const v16f& v = acc[a][b];
         if (kWeight && parts > 1) {
           float* dst = p.partial + ((uint64_t)blockIdx.y * p.n + p0 + pp) * p.k + k;
-          *reinterpret_cast<v4f*>(dst) = (v4f){a[e], a[e + 1], a[e + 2], a[e + 3]};
-          *reinterpret_cast<v4f*>(dst + 4) = (v4f){a[e + 4], a[e + 5], a[e + 6], a[e + 7]};
+          *reinterpret_cast<v4f*>(dst) = (v4f){v[e], v[e + 1], v[e + 2], v[e + 3]};
+          *reinterpret_cast<v4f*>(dst + 4) = (v4f){v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
           continue;
         }
         const uint32_t keep = p.mask ? p.mask[(row * p.k + k) / 8] : 0xffu;
         uint32_t out[4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const float lo = (keep >> (2 * h)) & 1 ? a[e + 2 * h] : 0.f, hi = (keep >> (2 * h + 1)) & 1 ? a[e + 2 * h + 1] : 0.f;
-          const bf16x2 v = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
-          __builtin_memcpy(&out[h], &v, 4);
+        for (int d = 0; d < 4; ++d) {
+          const float lo = (keep >> (2 * d)) & 1 ? v[e + 2 * d] : 0.f, hi = (keep >> (2 * d + 1)) & 1 ? v[e + 2 * d + 1] : 0.f;
+          const bf16x2 w = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
+          __builtin_memcpy(&out[d], &w, 4);
         }
         *reinterpret_cast<uint4*>(p.grad + row * p.k + k) = make_uint4(out[0], out[1], out[2], out[3]);
       }
@@ -249,13 +328,22 @@ namespace trace_host {
 
 using namespace trace_dev;
 
-hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream) {
-  const uint32_t k_tiles = (p.k + kTileK - 1) / kTileK;
-  const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, kTileP) : (p.rows + kTileP - 1) / kTileP;
-  if (row_tiles * k_tiles * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_grad_kernel<false, kE2M1>), dim3((unsigned)(row_tiles * k_tiles)), dim3(256), 0, stream, p,
-                     k_tiles, 1u, 1u);
+// Whether tiles of 128 x 256 fill the compute units.
+static bool big_tiles(uint64_t p, uint32_t k) { return (p + 127) / 128 * ((k + 255) / 256) >= 512; }
+
+template <int kKF, int kPF, int kPerCu>
+static hipError_t grad_input(const MxGradArgs& p, hipStream_t stream) {
+  const uint32_t k_tiles = (p.k + 64 * kKF - 1) / (64 * kKF);
+  const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 64 * kPF) : (p.rows + 64 * kPF - 1) / (64 * kPF);
+  const uint64_t grid = (row_tiles * k_tiles + 7) / 8 * 8;
+  if (grid * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((mx_grad_kernel<false, kE2M1, false, kKF, kPF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream,
+                     p, k_tiles, 1u, 1u);
   return hipGetLastError();
+}
+
+hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream) {
+  return big_tiles(p.rows, p.k) ? grad_input<4, 2, 2>(p, stream) : grad_input<2, 1, 2>(p, stream);
 }
 
 uint32_t mx_grad_weight_parts(uint64_t rows, uint32_t groups, uint32_t n, uint32_t k) {
@@ -263,23 +351,34 @@ uint32_t mx_grad_weight_parts(uint64_t rows, uint32_t groups, uint32_t n, uint32
   return 1;
 }
 
-hipError_t launch_mx_grad_weight(MxFormat fmt, const MxGradArgs& p, hipStream_t stream) {
-  const uint32_t k_tiles = (p.k + kTileK - 1) / kTileK, p_tiles = (p.n + kTileP - 1) / kTileP;
-  const uint64_t tiles = (uint64_t)k_tiles * p_tiles * p.groups;
+template <int kFmt, int kKF, int kPF, int kPerCu>
+static hipError_t grad_weight(const MxGradArgs& p, uint32_t parts, hipStream_t stream) {
+  const uint32_t k_tiles = (p.k + 64 * kKF - 1) / (64 * kKF), p_tiles = (p.n + 64 * kPF - 1) / (64 * kPF);
+  const uint64_t tiles = ((uint64_t)k_tiles * p_tiles * p.groups + 7) / 8 * 8;
   if (tiles * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
-  const uint32_t parts = mx_grad_weight_parts(p.rows, p.groups, p.n, p.k);
   const dim3 grid((unsigned)tiles, parts), block(256);
-  if (fmt == kE2M1)
-    hipLaunchKernelGGL((mx_grad_kernel<true, kE2M1>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
+  if (p.row_index)
+    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, true, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
   else
-    hipLaunchKernelGGL((mx_grad_kernel<true, kE4M3>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
-  if (parts > 1) {
-    const uint64_t nvec = (uint64_t)p.n * p.k / 8;
-    const uint64_t g = (nvec + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(mx_grad_join_kernel, dim3((unsigned)(g < kMaxGroups ? g : kMaxGroups)), block, 0, stream,
-                       p.partial, parts, nvec, p.mask, reinterpret_cast<uint4*>(p.grad));
-  }
+    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, false, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
   return hipGetLastError();
+}
+
+template <int kFmt>
+static hipError_t grad_weight(const MxGradArgs& p, hipStream_t stream) {
+  const uint32_t parts = mx_grad_weight_parts(p.rows, p.offsets ? p.groups : 0, p.n, p.k);
+  const hipError_t st = big_tiles((uint64_t)p.n * p.groups, p.k) ? grad_weight<kFmt, 4, 2, 2>(p, parts, stream)
+                                                                 : grad_weight<kFmt, 2, 1, 2>(p, parts, stream);
+  if (st != hipSuccess || parts == 1) return st;
+  const uint64_t nvec = (uint64_t)p.n * p.k / 8;
+  const uint64_t g = (nvec + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL(mx_grad_join_kernel, dim3((unsigned)(g < kMaxGroups ? g : kMaxGroups)), dim3(kThreads), 0, stream,
+                     p.partial, parts, nvec, p.mask, reinterpret_cast<uint4*>(p.grad));
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_grad_weight(MxFormat fmt, const MxGradArgs& p, hipStream_t stream) {
+  return fmt == kE2M1 ? grad_weight<kE2M1>(p, stream) : grad_weight<kE4M3>(p, stream);
 }
 
 }  // namespace trace_host

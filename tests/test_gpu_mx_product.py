@@ -79,7 +79,8 @@ def test_quantize_matches_the_capture_and_the_rne_mask(device, fmt, shape):
 # ---------------------------------------------------------------------------
 
 SHAPES = [(1, 16, 32), (1, 48, 160), (2, 2048, 4096), (7, 80, 96), (16, 16, 128), (33, 272, 544), (64, 128, 256),
-          (127, 144, 768), (129, 256, 2080), (255, 528, 1056), (257, 272, 512), (300, 1024, 640), (1021, 768, 2048)]
+          (127, 144, 768), (129, 256, 2080), (255, 528, 1056), (257, 272, 512), (300, 1024, 640), (1021, 768, 2048),
+          (16390, 1040, 544), (16400, 1024, 1184)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
@@ -137,7 +138,8 @@ def _uneven(groups, rows, kind):
 
 GROUPED = [(1, 1, 16, 32, "even"), (5, 40, 48, 96, "skewed"), (3, 257, 144, 544, "tail"), (8, 700, 272, 256, "one"),
            (70, 300, 64, 160, "skewed"), (130, 1500, 256, 768, "even"), (6, 0, 32, 64, "even"),
-           (4, 1200, 512, 1024, "tail"), (9, 90, 2048, 768, "even")]
+           (4, 1200, 512, 1024, "tail"), (9, 90, 2048, 768, "even"),
+           (5, 16500, 1040, 544, "skewed"), (6, 16420, 1024, 1056, "tail")]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
@@ -210,7 +212,7 @@ def test_grouped_linear_on_routed_rows(device, fmt, tokens, topk, experts, n, k)
 # ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("rows,n,k", [(1, 16, 32), (5, 48, 160), (127, 256, 128), (129, 144, 544), (300, 512, 1024),
-                                      (1021, 768, 2048)])
+                                      (1021, 768, 2048), (16400, 80, 1056)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_grad_input(device, rows, n, k, masked):
     import fp4_rollout_guided_amd as tr
@@ -248,7 +250,7 @@ def test_grouped_grad_input(device, groups, rows, n, k, kind):
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
 @pytest.mark.parametrize("rows,n,k", [(0, 32, 64), (1, 16, 32), (31, 48, 160), (33, 272, 128), (300, 144, 544),
-                                      (1021, 768, 512), (5000, 128, 256), (9001, 64, 96)])
+                                      (1021, 768, 512), (5000, 128, 256), (9001, 64, 96), (70, 2064, 8192)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_grad_weight(device, fmt, rows, n, k, masked):
     import fp4_rollout_guided_amd as tr
