@@ -27,6 +27,36 @@ __device__ __forceinline__ v8i widen(v4i v) { return __builtin_shufflevector(v, 
 __device__ __forceinline__ v8i widen(v8i v) { return v; }
 __device__ __forceinline__ v8i join(v4i a, v4i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
+// Results leave through LDS, 32 rows of kPieces 16-byte pieces at a time: a
+// lane's registers hold pieces of one row, and stores straight from them would
+// write 32 bytes of each of 32 rows at once; memory takes whole lines more
+// than twice as fast.  Each wave has 512 kPieces bytes of its own.  The pieces
+// of a row are permuted by the row's bits, for the LDS banks.
+template <int kPieces>
+struct RowBlock {
+  static_assert(kPieces == 8 || kPieces == 16, "rows of 128 or 256 bytes");
+  char* lds;
+  __device__ __forceinline__ char* at(uint32_t row, uint32_t piece) const {
+    return lds + row * (16 * kPieces) + 16 * ((piece ^ (kPieces == 16 ? row : row >> 1)) & (kPieces - 1));
+  }
+  __device__ __forceinline__ void put(uint32_t row, uint32_t piece, uint4 v) const {
+    *reinterpret_cast<uint4*>(at(row, piece)) = v;
+  }
+  // store(row, piece, v) for every piece of the block, a row's pieces on
+  // consecutive lanes.
+  template <typename Store>
+  __device__ __forceinline__ void drain(Store store) const {
+    const uint32_t lane = threadIdx.x & 63;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (uint32_t i = 0; i < kPieces / 2; ++i) {
+      const uint32_t row = (lane + 64 * i) / kPieces, piece = lane % kPieces;
+      store(row, piece, *reinterpret_cast<const uint4*>(at(row, piece)));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+};
+
 // A row tile of one group: rows [first, first + count), count <= the tile's
 // height; group == groups stands for the rows behind the last group.
 struct RowTile {

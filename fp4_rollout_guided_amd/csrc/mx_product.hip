@@ -413,25 +413,27 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
   uint32_t st = 0;
   for (; st + 2 < full && st < stages; ++st) stage(st, Constant<1>());
   for (; st < stages; ++st) stage(st, Constant<0>());
-  // register e of a block: n = 16 (e / 8) + 8 h + e % 8, m = lane % 32
+  // register e of a block: n = 16 (e / 8) + 8 h + e % 8, m = lane % 32.  Every
+  // wave has passed the barrier after its last LDS read.
+  const RowBlock<4 * kNF> block{ring + 512 * 4 * kNF * wave};
+  static_assert(4 * 512 * 4 * kNF <= 2 * kStageBytes, "four waves' blocks fit the ring");
 #pragma unroll
   for (int j = 0; j < kMF; ++j) {
-    const uint32_t m = wm + 32 * j + r;
-    if (m >= t.count) continue;
     const bool ok = (sources >> j) & 1;
-    uint16_t* row = p.y + (t.first + m) * p.n;
 #pragma unroll
     for (int i = 0; i < kNF; ++i)
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
-        const uint32_t n = n0 + wn + 32 * i + 2 * e + 8 * h;
-        if (n >= p.n) continue;
         const v16f& a = acc[i][j];
         uint4 v = make_uint4(bf16_pair(a[e], a[e + 1]), bf16_pair(a[e + 2], a[e + 3]), bf16_pair(a[e + 4], a[e + 5]),
                              bf16_pair(a[e + 6], a[e + 7]));
         if (!ok) v = make_uint4(0, 0, 0, 0);  // no source row
-        *reinterpret_cast<uint4*>(row + n) = v;
+        block.put(r, 4 * i + e / 4 + h, v);
       }
+    block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+      const uint32_t m = wm + 32 * j + row, n = n0 + wn + 8 * piece;
+      if (m < t.count && n < p.n) *reinterpret_cast<uint4*>(p.y + (t.first + m) * p.n + n) = v;
+    });
   }
 }
 

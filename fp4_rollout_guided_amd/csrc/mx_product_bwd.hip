@@ -71,7 +71,7 @@ __device__ __forceinline__ v8bf transposed(const char* at, uint32_t pitch) {
 // D = gx of a row tile (p = m, c = n).  A workgroup of 2 x 2 waves owns
 // 64 kKF k times 64 kPF p, each wave a quarter as kKF x kPF results of
 // 32 x 32.  The contraction runs in stages of kC, in two LDS buffers with one
-// barrier per stage; the next stage is decoded and placed in LDS, and the one
+// barrier per stage; the next stage is decoded and placed in LDS, and the two
 // after it fetched to registers, under the arithmetic.
 //
 // LDS layouts.  Q is [c][k]: 64 bytes per block of 32 k, a lane's four
@@ -154,16 +154,18 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
     }
   }
 
-  uint32_t q_held[kQDwords], q_scale = 0;
+  struct Held {  // a stage on its way to LDS
+    uint32_t q[kQDwords], q_scale;
+    v4i g[kGLoads];
+  };
+  Held held[2];
   int64_t q_index = 0;  // kGather: the source row of the stage to be fetched next
-  v4i g_held[kGLoads];
-  const auto fetch_index = [&](uint32_t st, bool may_end) {
-    if (!kGather) return;
+  const auto fetch_index = [&](uint32_t st, bool may_end) -> int64_t {
     const uint32_t c = kC * st + q_row;
-    q_index = !may_end || c < length ? p.row_index[q_first + c] : -1;
+    return kGather && (!may_end || c < length) ? p.row_index[q_first + c] : -1;
   };
   // may_end: the stage may end early
-  const auto fetch = [&](uint32_t st, bool may_end) {
+  const auto fetch = [&](uint32_t st, Held& to, bool may_end) {
     const uint32_t c = kC * st + q_row;
     uint64_t row = q_first + c;
     bool ok = !may_end || c < length;
@@ -171,37 +173,37 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
       ok = ok && q_index >= 0 && q_index < (int64_t)p.src_rows;
       row = ok ? (uint64_t)q_index : 0;
     }
-    q_scale = 127;
+    to.q_scale = 127;
 #pragma unroll
-    for (uint32_t d = 0; d < kQDwords; ++d) q_held[d] = 0;
+    for (uint32_t d = 0; d < kQDwords; ++d) to.q[d] = 0;
     if ((!may_end && !kGather) || ok) {
-      __builtin_memcpy(q_held, __builtin_assume_aligned(qc + row * q_pitch, 16), 4 * kQDwords);
-      q_scale = qs[row * blocks];
+      __builtin_memcpy(to.q, __builtin_assume_aligned(qc + row * q_pitch, 16), 4 * kQDwords);
+      to.q_scale = qs[row * blocks];
     }
 #pragma unroll
     for (uint32_t i = 0; i < kGLoads; ++i) {
       v4i v = {0, 0, 0, 0};
       if (!may_end || kC * st + g_c[i] < length)
         v = *reinterpret_cast<const v4i*>(g_from[i] + (uint64_t)kC * st * (kWeight ? p.n : 1));
-      g_held[i] = v;
+      to.g[i] = v;
     }
   };
   const uint32_t q_swap = ((q_blk >> 2) & 1) | ((q_row & 1) << 1);
-  const auto place = [&](uint32_t st) {
+  const auto place = [&](uint32_t st, const Held& from) {
     char* q = q_buf[st & 1] + q_row * kQPitch + 64 * q_blk;
-    const float s = e8m0_operand(q_scale);
+    const float s = e8m0_operand(from.q_scale);
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(q + 16 * (i ^ q_swap)) = decode8<kFmt>(q_held + (kFp4 ? i : 2 * i), s);
+      *reinterpret_cast<uint4*>(q + 16 * (i ^ q_swap)) = decode8<kFmt>(from.q + (kFp4 ? i : 2 * i), s);
     char* g = g_buf[st & 1];
 #pragma unroll
     for (uint32_t i = 0; i < kGLoads; ++i) {
       const uint32_t id = threadIdx.x + 256 * i;
       if (kWeight) {
-        *reinterpret_cast<v4i*>(g + id / (kP / 8) * kGPitch + 16 * (id % (kP / 8))) = g_held[i];
+        *reinterpret_cast<v4i*>(g + id / (kP / 8) * kGPitch + 16 * (id % (kP / 8))) = from.g[i];
       } else {
         const uint32_t m = id / (kC / 8), piece = id % (kC / 8);
-        *reinterpret_cast<v4i*>(g + m * kGPitch + 16 * (piece ^ (kC == 32 ? (m >> 2) & 3 : (m >> 1) & 7))) = g_held[i];
+        *reinterpret_cast<v4i*>(g + m * kGPitch + 16 * (piece ^ (kC == 32 ? (m >> 2) & 3 : (m >> 1) & 7))) = from.g[i];
       }
     }
   };
@@ -220,80 +222,137 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
   const uint32_t g_at = kWeight ? tr_row * kGPitch + 2 * (wp + 16 * half + 4 * (j & 3))
                                 : (wp + r) * kGPitch + 16 * (h ^ (kC == 32 ? (r >> 2) & 3 : (r >> 1) & 7));
   v16f acc[kKF][kPF] = {};
-  const auto step = [&](uint32_t st, uint32_t kk) {
+  constexpr uint32_t kSteps = kC / 16;
+  v8bf qf[2][kKF], gf[2][kPF];
+  // operands of k-step kk of a stage
+  const auto read_step = [&](uint32_t st, uint32_t kk, v8bf(&qv)[kKF], v8bf(&gv)[kPF]) {
     const char* q = q_buf[st & 1] + 16 * kk * kQPitch;
     const char* g = g_buf[st & 1];
-    v8bf qf[kKF], gf[kPF];
 #pragma unroll
     for (uint32_t f = 0; f < kPF; ++f) {
       if (kWeight)
-        gf[f] = transposed(g + 16 * kk * kGPitch + g_at + 64 * f, kGPitch);
+        gv[f] = transposed(g + 16 * kk * kGPitch + g_at + 64 * f, kGPitch);
       else
-        gf[f] = *reinterpret_cast<const v8bf*>(g + (g_at ^ (32 * kk)) + 32 * f * kGPitch);
+        gv[f] = *reinterpret_cast<const v8bf*>(g + (g_at ^ (32 * kk)) + 32 * f * kGPitch);
     }
 #pragma unroll
     for (uint32_t f = 0; f < kKF; ++f) {
       const uint32_t blk = wk / 32 + f;
-      qf[f] = transposed(q + (q_at ^ (16 * ((blk >> 2) & 1))) + 64 * blk, kQPitch);
+      qv[f] = transposed(q + (q_at ^ (16 * ((blk >> 2) & 1))) + 64 * blk, kQPitch);
     }
+  };
+  const auto multiply = [&](const v8bf(&qv)[kKF], const v8bf(&gv)[kPF]) {
 #pragma unroll
     for (int a = 0; a < kKF; ++a)
 #pragma unroll
-      for (int b = 0; b < kPF; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[a], gf[b], acc[a][b], 0, 0, 0);
+      for (int b = 0; b < kPF; ++b) acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qv[a], gv[b], acc[a][b], 0, 0, 0);
   };
-  // One stage.  kSteady: stages st + 1 to st + 3 exist in full.
-  const auto stage = [&](uint32_t st, bool steady) {
-    if (steady || st + 1 < stages) place(st + 1);
-    if (steady || st + 2 < stages) fetch(st + 2, !steady);
-    if (steady || st + 3 < stages) fetch_index(st + 3, !steady);
+  // One stage, whose first k-step has been read: each further step is read
+  // under the arithmetic of the one before, and the next stage's first step
+  // under the last one's.  next: what holds stage st + 1, and then st + 3.
+  // steady: stages st + 1 to st + 4 exist in full.
+  const auto stage = [&](uint32_t st, Held& next, bool steady) {
+    read_step(st, 1, qf[1], gf[1]);
+    if (steady || st + 1 < stages) place(st + 1, next);
+    if (steady || st + 3 < stages) fetch(st + 3, next, !steady);
+    if (steady || st + 4 < stages) q_index = fetch_index(st + 4, !steady);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (uint32_t kk = 0; kk < kC / 16; ++kk) step(st, kk);
+    for (uint32_t kk = 0; kk + 1 < kSteps; ++kk) {
+      multiply(qf[kk & 1], gf[kk & 1]);
+      if (kk + 2 < kSteps) read_step(st, kk + 2, qf[kk & 1], gf[kk & 1]);
+    }
     __builtin_amdgcn_sched_barrier(0);
     grad_barrier();
+    if (steady || st + 1 < stages) read_step(st + 1, 0, qf[kSteps & 1], gf[kSteps & 1]);
+    multiply(qf[(kSteps - 1) & 1], gf[(kSteps - 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
   };
+  static_assert(kSteps % 2 == 0, "a stage starts with the first of the two sets of operands");
   if (stages) {
-    fetch_index(0, true);
-    fetch(0, true);
-    fetch_index(1, true);
-    place(0);
-    if (stages > 1) fetch(1, true);
-    if (stages > 2) fetch_index(2, true);
+    q_index = fetch_index(0, true);
+    const int64_t index1 = fetch_index(1, true), index2 = fetch_index(2, true), index3 = fetch_index(3, true);
+    fetch(0, held[0], true);
+    q_index = index1;
+    if (stages > 1) fetch(1, held[1], true);
+    place(0, held[0]);
+    q_index = index2;
+    if (stages > 2) fetch(2, held[0], true);
+    q_index = index3;
     grad_barrier();
+    read_step(0, 0, qf[0], gf[0]);
   }
   uint32_t st = 0;
-  for (; (st + 4) * kC <= length; ++st) stage(st, true);
-  for (; st < stages; ++st) stage(st, false);
+  for (; (st + 6) * kC <= length; st += 2) {
+    stage(st, held[1], true);
+    stage(st + 1, held[0], true);
+  }
+  for (; st < stages; st += 2) {
+    stage(st, held[1], false);
+    if (st + 1 < stages) stage(st + 1, held[0], false);
+  }
 
   // register e of a result: k = 16 (e / 8) + 8 h + e % 8, p = lane % 32
+  const bool masked = p.mask && !(kWeight && parts > 1);
+  uint32_t keep[kPF][kKF];
 #pragma unroll
   for (int b = 0; b < kPF; ++b) {
     const uint32_t pp = wp + 32 * b + r;
-    if (kWeight ? p0 + pp >= p.n : pp >= t.count) continue;
+    const bool in = kWeight ? p0 + pp < p.n : pp < t.count;
     const uint64_t row = kWeight ? (uint64_t)t.group * p.n + p0 + pp : t.first + pp;
+#pragma unroll
+    for (int a = 0; a < kKF; ++a) {
+      const uint32_t k = k0 + wk + 32 * a;  // the mask's bits of 32 k are a dword, at any byte multiple of 4 of the mask
+      keep[b][a] = ~0u;
+      if (masked && in && k < p.k) __builtin_memcpy(&keep[b][a], p.mask + (row * p.k + k) / 8, 4);
+    }
+  }
+  if (kWeight && parts > 1) {
+#pragma unroll
+    for (int b = 0; b < kPF; ++b) {
+      const uint32_t pp = p0 + wp + 32 * b + r;
+      if (pp >= p.n) continue;
+#pragma unroll
+      for (int a = 0; a < kKF; ++a) {
+        if (k0 + wk + 32 * a >= p.k) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float* dst = p.partial + ((uint64_t)blockIdx.y * p.n + pp) * p.k + k0 + wk + 32 * a + 2 * e + 8 * h;
+          const v16f& v = acc[a][b];
+          *reinterpret_cast<v4f*>(dst) = (v4f){v[e], v[e + 1], v[e + 2], v[e + 3]};
+          *reinterpret_cast<v4f*>(dst + 4) = (v4f){v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
+        }
+      }
+    }
+    return;
+  }
+  // every wave has passed the barrier after its last LDS read
+  const RowBlock<4 * kKF> block{q_buf[0] + 512 * 4 * kKF * wave};
+  static_assert(4 * 512 * 4 * kKF <= 2 * kQBytes, "four waves' blocks fit the tiles' buffers");
+#pragma unroll
+  for (int b = 0; b < kPF; ++b) {
 #pragma unroll
     for (int a = 0; a < kKF; ++a)
 #pragma unroll
       for (int e = 0; e < 16; e += 8) {
-        const uint32_t k = k0 + wk + 32 * a + 2 * e + 8 * h;
-        if (k >= p.k) continue;
         const v16f& v = acc[a][b];
-        if (kWeight && parts > 1) {
-          float* dst = p.partial + ((uint64_t)blockIdx.y * p.n + p0 + pp) * p.k + k;
-          *reinterpret_cast<v4f*>(dst) = (v4f){v[e], v[e + 1], v[e + 2], v[e + 3]};
-          *reinterpret_cast<v4f*>(dst + 4) = (v4f){v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
-          continue;
-        }
-        const uint32_t keep = p.mask ? p.mask[(row * p.k + k) / 8] : 0xffu;
+        const uint32_t bits = keep[b][a] >> (2 * e + 8 * h);
         uint32_t out[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const float lo = (keep >> (2 * d)) & 1 ? v[e + 2 * d] : 0.f, hi = (keep >> (2 * d + 1)) & 1 ? v[e + 2 * d + 1] : 0.f;
+          const float lo = (bits >> (2 * d)) & 1 ? v[e + 2 * d] : 0.f, hi = (bits >> (2 * d + 1)) & 1 ? v[e + 2 * d + 1] : 0.f;
           const bf16x2 w = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
           __builtin_memcpy(&out[d], &w, 4);
         }
-        *reinterpret_cast<uint4*>(p.grad + row * p.k + k) = make_uint4(out[0], out[1], out[2], out[3]);
+        block.put(r, 4 * a + e / 4 + h, make_uint4(out[0], out[1], out[2], out[3]));
       }
+    block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+      const uint32_t pp = wp + 32 * b + row, k = k0 + wk + 8 * piece;
+      if (k < p.k && (kWeight ? p0 + pp < p.n : pp < t.count)) {
+        const uint64_t to = kWeight ? (uint64_t)t.group * p.n + p0 + pp : t.first + pp;
+        *reinterpret_cast<uint4*>(p.grad + to * p.k + k) = v;
+      }
+    });
   }
 }
 
