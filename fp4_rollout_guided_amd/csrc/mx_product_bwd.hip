@@ -405,9 +405,29 @@ hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream) {
   return big_tiles(p.rows, p.k) ? grad_input<4, 2, 2>(p, stream) : grad_input<2, 1, 2>(p, stream);
 }
 
+// Tiles and parts of a weight's gradient.  Tiles of 128 x 256 where, with the
+// contraction over one weight's rows in up to a part per 1024 rows, they fill
+// three quarters of the compute units twice; else tiles of 64 x 128 and a part
+// per 512 rows.
+struct GradWeightPlan {
+  bool big;
+  uint32_t parts;
+};
+static GradWeightPlan grad_weight_plan(uint64_t rows, uint32_t groups, uint32_t n, uint32_t k) {
+  const uint64_t weights = groups ? groups : 1;
+  const uint64_t big = (uint64_t)((n + 127) / 128) * ((k + 255) / 256) * weights;
+  const uint64_t small = (uint64_t)((n + 63) / 64) * ((k + 127) / 128) * weights;
+  if (big >= 512) return {true, 1};
+  if (groups || small == 0) return {false, 1};
+  const uint64_t big_parts = (512 + big - 1) / big, small_parts = (512 + small - 1) / small;
+  if (big_parts <= rows / 1024 && big_parts <= 8) return {true, (uint32_t)big_parts};
+  const uint64_t most = rows / 512 < 32 ? rows / 512 : 32;
+  const uint64_t parts = small_parts < most ? small_parts : most;
+  return {false, parts > 1 ? (uint32_t)parts : 1u};
+}
+
 uint32_t mx_grad_weight_parts(uint64_t rows, uint32_t groups, uint32_t n, uint32_t k) {
-  (void)rows; (void)groups; (void)n; (void)k;
-  return 1;
+  return grad_weight_plan(rows, groups, n, k).parts;
 }
 
 template <int kFmt, int kKF, int kPF, int kPerCu>
@@ -425,9 +445,9 @@ static hipError_t grad_weight(const MxGradArgs& p, uint32_t parts, hipStream_t s
 
 template <int kFmt>
 static hipError_t grad_weight(const MxGradArgs& p, hipStream_t stream) {
-  const uint32_t parts = mx_grad_weight_parts(p.rows, p.offsets ? p.groups : 0, p.n, p.k);
-  const hipError_t st = big_tiles((uint64_t)p.n * p.groups, p.k) ? grad_weight<kFmt, 4, 2, 2>(p, parts, stream)
-                                                                 : grad_weight<kFmt, 2, 1, 2>(p, parts, stream);
+  const GradWeightPlan plan = grad_weight_plan(p.rows, p.offsets ? p.groups : 0, p.n, p.k);
+  const uint32_t parts = plan.parts;
+  const hipError_t st = plan.big ? grad_weight<kFmt, 4, 2, 2>(p, parts, stream) : grad_weight<kFmt, 2, 1, 2>(p, parts, stream);
   if (st != hipSuccess || parts == 1) return st;
   const uint64_t nvec = (uint64_t)p.n * p.k / 8;
   const uint64_t g = (nvec + kThreads - 1) / kThreads;

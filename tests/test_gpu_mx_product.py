@@ -250,7 +250,7 @@ def test_grouped_grad_input(device, groups, rows, n, k, kind):
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
 @pytest.mark.parametrize("rows,n,k", [(0, 32, 64), (1, 16, 32), (31, 48, 160), (33, 272, 128), (300, 144, 544),
-                                      (1021, 768, 512), (5000, 128, 256), (9001, 64, 96), (70, 2064, 8192)])
+                                      (1021, 768, 512), (5000, 128, 256), (9001, 64, 96), (70, 2064, 8192), (4100, 1040, 2080)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_grad_weight(device, fmt, rows, n, k, masked):
     import fp4_rollout_guided_amd as tr
