@@ -137,7 +137,7 @@ def load_library(path):
         "trace_mx_quantize": ([p, i64, i64, p, p, p, p], st),
         "trace_mx_matmul": ([p, p, i64, p, p, i64, i64, p, p], st),
         "trace_grouped_mx_matmul": ([p, p, i64, p, i64, p, i64, p, p, i64, i64, p, p], st),
-        "trace_mx_linear_workspace_bytes": ([i64, i64], sz),
+        "trace_mx_linear_workspace_bytes": ([i64, i64, i64, i64], sz),
         "trace_mx_linear": ([p, i64, p, i64, p, i64, p, p, i64, i64, p, sz, p, p], st),
         "trace_mx_matmul_bwd_input": ([p, i64, p, i64, p, p, i64, i64, p, p, p], st),
         "trace_mx_matmul_bwd_weight_workspace_bytes": ([i64, i64, i64, i64], sz),
@@ -920,7 +920,7 @@ def _linear(fmt, x, offsets, w_scales, w_codes, n, row_index, workspace, y):
     rows = src_rows if row_index is None else _index(row_index, x)
     shape = (rows, n) if row_index is not None else (*x.shape[:-1], n)
     y = _out(y, "y", x, shape, torch.bfloat16)
-    workspace = _workspace(workspace, x, getattr(lib, f"trace_{fmt}_linear_workspace_bytes")(src_rows, k))
+    workspace = _workspace(workspace, x, getattr(lib, f"trace_{fmt}_linear_workspace_bytes")(src_rows, rows, groups, k))
     _launch(f"trace_{fmt}_linear", x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales),
             _addr(w_codes), n, k, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(y))
     return y

@@ -40,9 +40,11 @@ trace_status product_groups(const int64_t* offsets, int64_t groups, int64_t* gro
 
 uint64_t code_bytes(MxFormat fmt, uint64_t elements) { return fmt == kE2M1 ? elements / 2 : elements; }
 
-size_t linear_workspace(MxFormat fmt, int64_t src_rows, int64_t k) {
+size_t linear_workspace(MxFormat fmt, int64_t src_rows, int64_t rows, int64_t groups, int64_t k) {
   uint64_t n = 0;
-  if (mx_site_size(src_rows, k, &n) != TRACE_OK) return 0;
+  if (mx_site_size(src_rows, k, &n) != TRACE_OK || product_sizes(src_rows, rows, groups == 0 ? 1 : groups, 0, k) != TRACE_OK)
+    return 0;
+  if (trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0)) return 0;
   return (size_t)(code_bytes(fmt, n) + (n / 32 + 15) / 16 * 16);
 }
 
@@ -69,14 +71,15 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
   int64_t weights = 0;
   if (trace_status st = product_groups(offsets, groups, &weights)) return st;
   if (trace_status st = product_sizes(src_rows, rows, weights, n, k)) return st;
+  if (row_index && !offsets) return TRACE_E_NULL;
   if (!row_index && rows > 0 && src_rows != rows) return TRACE_E_SHAPE;  // no rows need no index
   uint64_t na = 0;
   if (trace_status st = mx_site_size(src_rows, k, &na)) return st;
-  const size_t need = linear ? linear_workspace(fmt, src_rows, k) : 0;
+  const size_t need = linear ? linear_workspace(fmt, src_rows, rows, groups, k) : 0;
   if (rows == 0 || n == 0) return TRACE_OK;
   const uint64_t nw = (uint64_t)weights * (uint64_t)n * (uint64_t)k, ny = (uint64_t)rows * (uint64_t)n;
   if (!y || (nw > 0 && (!w_scales || !w_codes))) return TRACE_E_NULL;
-  if (na > 0 && (linear ? !x || !workspace : !a_scales || !a_codes)) return TRACE_E_NULL;
+  if (na > 0 && (linear ? !x || (need > 0 && !workspace) : !a_scales || !a_codes)) return TRACE_E_NULL;
   if (linear && workspace_bytes < need) return TRACE_E_SHAPE;
   if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 16) ||
       !aligned(row_index, 8))
@@ -91,15 +94,16 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
                         rng(offsets, offsets ? 8 * ((uint64_t)weights + 1) : 0)};
   if (trace_status st = check_alias(outs, 2, ins, 7)) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (linear && na > 0) {
+  if (need > 0) {
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + code_bytes(fmt, na);
     if (trace_status st = hip_status(trace_host::launch_mx_quantize(fmt, x, na / 32, scales, codes, nullptr, s))) return st;
     a_codes = codes;
     a_scales = scales;
   }
-  const trace_host::MxProductArgs p{a_codes, a_scales, row_index, (uint64_t)src_rows, (uint64_t)rows, offsets,
-                                    (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y};
+  const bool rounds = linear && trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0);
+  const trace_host::MxProductArgs p{rounds ? x : nullptr, a_codes, a_scales, row_index, (uint64_t)src_rows, (uint64_t)rows,
+                                    offsets, (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y};
   return hip_status(trace_host::launch_mx_product(fmt, p, s));
 }
 
@@ -138,6 +142,7 @@ trace_status grad_weight(MxFormat fmt, const uint16_t* grad_y, int64_t rows, con
   int64_t weights = 0;
   if (trace_status st = product_groups(offsets, groups, &weights)) return st;
   if (trace_status st = product_sizes(src_rows, rows, weights, n, k)) return st;
+  if (row_index && !offsets) return TRACE_E_NULL;
   if (!row_index && rows > 0 && src_rows != rows) return TRACE_E_SHAPE;  // no rows need no index
   uint64_t na = 0;
   if (trace_status st = mx_site_size(src_rows, k, &na)) return st;
@@ -209,8 +214,13 @@ trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_
                  w_codes, n, k, false, y, stream);
 }
 
-size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t k) { return linear_workspace(kE2M1, src_rows, k); }
-size_t trace_mx8_linear_workspace_bytes(int64_t src_rows, int64_t k) { return linear_workspace(kE4M3, src_rows, k); }
+size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t rows, int64_t groups, int64_t k) {
+  return linear_workspace(kE2M1, src_rows, rows, groups, k);
+}
+
+size_t trace_mx8_linear_workspace_bytes(int64_t src_rows, int64_t rows, int64_t groups, int64_t k) {
+  return linear_workspace(kE4M3, src_rows, rows, groups, k);
+}
 
 trace_status trace_mx_linear(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
                              const int64_t* offsets, int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,

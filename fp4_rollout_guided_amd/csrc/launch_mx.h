@@ -13,6 +13,7 @@ enum MxFormat { kE2M1 = 0, kE4M3 = 1 };
 
 // One product y = A W^T, or one per group of packed rows.
 struct MxProductArgs {
+  const uint16_t* x;         // [rows, k] in bf16, where mx_product_rounds; else nullptr
   const uint8_t* a_codes;    // [src_rows, k]
   const uint8_t* a_scales;   // [src_rows, k / 32]
   const int64_t* row_index;  // row r reads source row row_index[r]; nullptr: row r (src_rows == rows)
@@ -45,6 +46,8 @@ struct MxGradArgs {
 // Sizes in 32-element blocks; mask may be nullptr.
 hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks, uint8_t* scales, uint8_t* codes,
                               uint8_t* mask, hipStream_t stream);
+// Whether a product of so many rows takes bf16 activations as they are.
+bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped);
 hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& p, hipStream_t stream);
 
 hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream);

@@ -15,6 +15,7 @@
 #include "launch.h"
 #include "launch_mx.h"
 #include "mx_mfma.h"
+#include "mx_quantize_dev.h"
 
 namespace trace_dev {
 
@@ -25,16 +26,41 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return u;
 }
 
+// 32 codes of an activation row.
+template <int kFmt>
+struct Operand {
+  using type = v4i;
+};
+template <>
+struct Operand<trace_host::kE4M3> {
+  using type = v8i;
+};
+
 // ---------------------------------------------------------------------------
-// Few rows.  A workgroup owns 16 columns of W's rows n times kNF and up to
-// 16 * kMF rows of one group; its kWaves waves take the 128-long steps of k
-// in turn and their partial sums meet in LDS, added in the order of the
-// waves.  Operands go straight from memory to registers: no row of W is used
-// twice, and this is bound by W's bytes (or, for one token, by latency).
+// Few rows.  A workgroup owns 16 kNF columns n and up to 16 kMF rows of one
+// group; its kWaves waves take the 128-long steps of k in turn, kUnroll steps'
+// loads at a time, and their partial sums meet in LDS, added in the order of
+// the waves.  Operands go straight from memory to registers: no row of W is
+// used twice by a workgroup, and this is bound by W's bytes or, for one token
+// on one weight, by latency.
+//
+// kRound: the activations are bf16, rows k of them at most kRoundMax, and each
+// workgroup rounds them all into LDS as mx_quantize would, while its first
+// loads of W are under way.  Against a launch of its own for the rounding (n
+// 2048, k 4096, MXFP4): 1 row 5.1 us against 6.5, 4 rows 6.3 against 6.8, 8
+// rows 7.9 against 7.1; one launch fewer on the host as well.
 // ---------------------------------------------------------------------------
-template <int kFmt, int kMF, int kNF, int kWaves>
+
+constexpr uint32_t kCUs = 256;
+constexpr uint32_t kRoundMax = 16384;
+
+template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kUnroll>
 __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
+  constexpr bool kFp4 = kFmt == trace_host::kE2M1;
+  using AFrag = typename Operand<kFmt>::type;
   __shared__ v4f sums[kWaves][kMF * kNF][64];
+  __shared__ __attribute__((aligned(16))) uint8_t rounded[kRound ? kRoundMax / (kFp4 ? 2 : 1) : 1];
+  __shared__ uint8_t rounded_scales[kRound ? kRoundMax / 32 : 1];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t r = lane & 15, g = lane >> 4;
   const uint64_t row_tile = blockIdx.x / col_tiles;
@@ -49,70 +75,100 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
   }
   const bool behind = t.group >= p.groups;  // rows of no group: zeros
   const uint32_t blocks = p.k / 32;
-  const uint32_t a_pitch = kFmt == trace_host::kE2M1 ? p.k / 2 : p.k;
   v4f acc[kMF][kNF] = {};
   if (!behind) {
-    const uint8_t* wc = p.w_codes + ((uint64_t)t.group * p.n + n0) * (p.k / 2);
-    const uint8_t* ws = p.w_scales + ((uint64_t)t.group * p.n + n0) * blocks;
-    uint32_t w_row[kNF];
+    // W's columns past the last one: any row of the tile, its results are dropped
+    const uint8_t* wc[kNF];
+    const uint8_t* ws[kNF];
 #pragma unroll
     for (int f = 0; f < kNF; ++f) {
-      const uint32_t n = 16 * f + r;
-      w_row[f] = n0 + n < p.n ? n : r;  // past the last column: any row of the tile, its results are dropped
+      const uint64_t n = (uint64_t)t.group * p.n + n0 + (n0 + 16 * f < p.n ? 16 * f : 0) + r;
+      wc[f] = p.w_codes + n * (p.k / 2);
+      ws[f] = p.w_scales + n * blocks;
     }
-    const uint8_t* ac[kMF];
-    const uint8_t* as[kMF];
+    const uint32_t steps = (p.k + 127) / 128;
+    v4i w[kUnroll][kNF];
+    uint32_t wsc[kUnroll][kNF];
+    auto load_w = [&](uint32_t s0) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t b = 4 * (s0 + u * kWaves) + g;  // this lane's block of k
+#pragma unroll
+        for (int f = 0; f < kNF; ++f) {
+          w[u][f] = v4i{0, 0, 0, 0};
+          wsc[u][f] = 127;
+          if (b < blocks) {
+            w[u][f] = *reinterpret_cast<const v4i*>(wc[f] + 16 * (uint64_t)b);
+            wsc[u][f] = ws[f][b];
+          }
+        }
+      }
+    };
+    load_w(wave);
+    uint64_t src[kMF];
     bool a_ok[kMF];
 #pragma unroll
     for (int f = 0; f < kMF; ++f) {
       const uint32_t m = 16 * f + r;
       a_ok[f] = m < t.count;
-      uint64_t src = t.first + (a_ok[f] ? m : 0);
+      src[f] = t.first + (a_ok[f] ? m : 0);
       if (p.row_index) {
-        const int64_t i = p.row_index[src];
+        const int64_t i = p.row_index[src[f]];
         a_ok[f] = a_ok[f] && i >= 0 && i < (int64_t)p.src_rows;
-        src = a_ok[f] ? (uint64_t)i : 0;
+        src[f] = a_ok[f] ? (uint64_t)i : 0;
       }
-      ac[f] = p.a_codes + src * a_pitch;
-      as[f] = p.a_scales + src * blocks;
     }
-    const uint32_t steps = (p.k + 127) / 128;
-    for (uint32_t s = wave; s < steps; s += kWaves) {
-      const uint32_t b = 4 * s + g;  // this lane's block of k
-      const bool in = b < blocks;
-      v8i wv[kNF], av[kMF];
-      int wsc[kNF], asc[kMF];
+    const uint8_t* a_codes = p.a_codes;
+    const uint8_t* a_scales = p.a_scales;
+    if constexpr (kRound) {
+      const uint32_t nvec = (uint32_t)p.rows * (p.k / 8);
+      for (uint32_t i = threadIdx.x; i < nvec; i += 64 * kWaves) {
+        uint32_t sb, keep;
+        const uint2 c = quantize_vector<kFp4>(reinterpret_cast<const uint4*>(p.x)[i], sb, keep);
+        if ((i & 3) == 0) rounded_scales[i >> 2] = (uint8_t)sb;
+        if constexpr (kFp4)
+          reinterpret_cast<uint32_t*>(rounded)[i] = c.x;
+        else
+          reinterpret_cast<uint2*>(rounded)[i] = c;
+      }
+      a_codes = rounded;
+      a_scales = rounded_scales;
+      __syncthreads();
+    }
+    for (uint32_t s0 = wave; s0 < steps; s0 += kWaves * kUnroll) {
+      AFrag a[kUnroll][kMF];
+      uint32_t asc[kUnroll][kMF];
 #pragma unroll
-      for (int f = 0; f < kNF; ++f) {
-        v4i c = {0, 0, 0, 0};
-        wsc[f] = 127;
-        if (in) {
-          c = *reinterpret_cast<const v4i*>(wc + (uint64_t)w_row[f] * (p.k / 2) + 16 * b);
-          wsc[f] = ws[(uint64_t)w_row[f] * blocks + b];
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t s = s0 + u * kWaves, b = 4 * s + g;
+        const bool in = b < blocks;
+        // MXFP8: runs of 16 at k0 and k0 + 64
+        const uint64_t k0 = 128 * (uint64_t)s + 16 * g;
+#pragma unroll
+        for (int f = 0; f < kMF; ++f) {
+          asc[u][f] = 127;
+          if (in && a_ok[f]) asc[u][f] = a_scales[src[f] * blocks + b];
+          if constexpr (kFp4) {
+            a[u][f] = v4i{0, 0, 0, 0};
+            if (in && a_ok[f]) a[u][f] = *reinterpret_cast<const v4i*>(a_codes + src[f] * (p.k / 2) + 16 * (uint64_t)b);
+          } else {
+            v4i lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+            if (k0 < p.k && a_ok[f]) lo = *reinterpret_cast<const v4i*>(a_codes + src[f] * p.k + k0);
+            if (k0 + 64 < p.k && a_ok[f]) hi = *reinterpret_cast<const v4i*>(a_codes + src[f] * p.k + k0 + 64);
+            a[u][f] = join(lo, hi);
+          }
         }
-        wv[f] = widen(c);
       }
 #pragma unroll
-      for (int f = 0; f < kMF; ++f) {
-        v4i c = {0, 0, 0, 0}, d = {0, 0, 0, 0};
-        asc[f] = 127;
-        if (kFmt == trace_host::kE2M1) {
-          if (in && a_ok[f]) c = *reinterpret_cast<const v4i*>(ac[f] + 16 * b);
-          av[f] = widen(c);
-        } else {
-          const uint32_t k0 = 128 * s + 16 * g;
-          if (k0 < p.k && a_ok[f]) c = *reinterpret_cast<const v4i*>(ac[f] + k0);
-          if (k0 + 64 < p.k && a_ok[f]) d = *reinterpret_cast<const v4i*>(ac[f] + k0 + 64);
-          av[f] = join(c, d);
-        }
-        if (in && a_ok[f]) asc[f] = as[f][b];
-      }
+      for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int i = 0; i < kMF; ++i)
+        for (int i = 0; i < kMF; ++i)
 #pragma unroll
-        for (int j = 0; j < kNF; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              wv[j], av[i], acc[i][j], kSelE2M1, kFmt == trace_host::kE2M1 ? kSelE2M1 : kSelE4M3, 0, wsc[j], 0, asc[i]);
+          for (int j = 0; j < kNF; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                widen(w[u][j]), widen(a[u][i]), acc[i][j], kSelE2M1, kFp4 ? kSelE2M1 : kSelE4M3, 0, (int)wsc[u][j], 0,
+                (int)asc[u][i]);
+      if (s0 + kWaves * kUnroll < steps) load_w(s0 + kWaves * kUnroll);
     }
   }
 #pragma unroll
@@ -181,16 +237,6 @@ __device__ __forceinline__ v4i scale_piece(v4i v, uint32_t b, uint32_t blocks) {
   v[3] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(kOne, x3, skip & 3));
   return v;
 }
-
-// 32 codes of an activation row.
-template <int kFmt>
-struct Operand {
-  using type = v4i;
-};
-template <>
-struct Operand<trace_host::kE4M3> {
-  using type = v8i;
-};
 
 // A number as a type, for lambdas that need it at compile time.
 template <uint32_t kValue>
@@ -443,13 +489,13 @@ namespace trace_host {
 
 using namespace trace_dev;
 
-template <int kFmt, int kMF, int kNF, int kWaves>
+template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kUnroll>
 static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
   const uint32_t cols = (p.n + 16 * kNF - 1) / (16 * kNF);
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 16 * kMF) : (p.rows + 16 * kMF - 1) / (16 * kMF);
   if (row_tiles * cols * (64 * kWaves) > 0xffffffffull) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_skinny_kernel<kFmt, kMF, kNF, kWaves>), dim3((unsigned)(row_tiles * cols)), dim3(64 * kWaves),
-                     0, stream, p, cols);
+  hipLaunchKernelGGL((mx_skinny_kernel<kFmt, kRound, kMF, kNF, kWaves, kUnroll>), dim3((unsigned)(row_tiles * cols)),
+                     dim3(64 * kWaves), 0, stream, p, cols);
   return hipGetLastError();
 }
 
@@ -467,10 +513,55 @@ static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// One weight: the smallest tile that gives each CU at most one workgroup, since
+// a larger one leaves CUs idle and a smaller one reads its operands more often
+// (rows x n x k, MXFP4, us: 16 x 2048 x 4096 5.8 with 16 x 16, 7.6 with 16 x 32;
+// 64 x 2048 x 4096 7.7 with 16 x 32, 9.7 with 32 x 32; 128 x 2048 x 4096 9.8
+// with 32 x 32, 13.4 with 32 x 64; 64 x 7168 x 2048 8.4 with 32 x 64, 9.8 and
+// 10.5 with 32 x 32 and 64 x 64; 128 x 7168 x 2048 10.7 with 64 x 64, 13.5 with
+// 32 x 64, 11.7 in tiles of many rows; 256 x 7168 x 2048 18.0 with 64 x 64,
+// 12.3 in tiles of many rows).
+template <int kFmt, bool kRound>
+static hipError_t launch_few_rows(const MxProductArgs& p, hipStream_t stream) {
+  const auto tiles = [&](uint32_t rows, uint32_t cols) {
+    return (p.rows + rows - 1) / rows * ((p.n + cols - 1) / cols);
+  };
+  if (tiles(16, 16) <= kCUs) return launch_skinny<kFmt, kRound, 1, 1, 8, 2>(p, stream);
+  if (kRound || tiles(16, 32) <= kCUs) return launch_skinny<kFmt, kRound, 1, 2, 8, 2>(p, stream);
+  if constexpr (!kRound) {
+    if (tiles(32, 32) <= kCUs) return launch_skinny<kFmt, false, 2, 2, 4, 2>(p, stream);
+    if (tiles(32, 64) <= kCUs) return launch_skinny<kFmt, false, 2, 4, 4, 1>(p, stream);
+  }
+  return launch_skinny<kFmt, false, 4, 4, 4, 1>(p, stream);
+}
+
+// Groups of few rows.  Up to 8 rows each: tiles of 16 x 64, which read W's rows
+// once and keep many loads under way (192 rows of 128 groups, 1536 x 2048: 46
+// us, 52 with 32 x 32), or of 16 x 16 where there are few of those (8 rows: 6.2
+// us, 8.0).  More rows: 32 x 32.
+template <int kFmt>
+static hipError_t launch_few_rows_each(const MxProductArgs& p, hipStream_t stream) {
+  if (p.rows > 8 * (uint64_t)p.groups) return launch_skinny<kFmt, false, 2, 2, 4, 2>(p, stream);
+  if (p.rows * ((p.n + 63) / 64) < 2 * kCUs) return launch_skinny<kFmt, false, 1, 1, 4, 2>(p, stream);
+  return launch_skinny<kFmt, false, 1, 4, 4, 1>(p, stream);
+}
+
+// Whether the rows are many: past the grids of launch_few_rows for one weight;
+// for groups from 32 rows each, or from 8 where the groups' tiles of 128
+// columns alone fill the card (128 groups, 1536 x 2048, us in tiles of few and
+// of many rows: 8 rows each 63 and 56, MXFP8 64 and 72; 12 each 77 and 56, MXFP8
+// 92 and 77.  16 groups: 16 each 12 and 13, 32 each 21 and 14).  A row's
+// scales must fill one 16-byte load, and row 0 must exist.
+static bool many_rows(const MxProductArgs& p) {
+  if (p.k < 512 || p.src_rows == 0) return false;
+  if (!p.offsets) return (p.rows + 63) / 64 * ((p.n + 63) / 64) > kCUs;
+  return p.rows >= 32 * (uint64_t)p.groups ||
+         (p.rows > 8 * (uint64_t)p.groups && p.groups * (uint64_t)((p.n + 127) / 128) >= kCUs);
+}
+
 template <int kFmt>
 static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
-  // A row's scales must fill one 16-byte load, and row 0 must exist.
-  if (p.rows >= 128 && p.rows >= 32 * (uint64_t)p.groups && p.src_rows > 0 && p.k >= 512) {
+  if (many_rows(p)) {
     // 128 x 256 tiles read W and A from the caches less often than 128 x 128
     // ones (131072 x 1536 x 2048 per expert: 0.37 against 0.41 ms), where
     // there are enough of them to fill every compute unit twice.  With MXFP8
@@ -481,10 +572,16 @@ static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
       if (tiles >= 512) return launch_tile<kFmt, 2, 4, 2>(p, stream);
     return launch_tile<kFmt, 2, 2, 2>(p, stream);
   }
-  return launch_skinny<kFmt, 2, 2, 4>(p, stream);
+  if (!p.offsets) return launch_few_rows<kFmt, false>(p, stream);
+  return launch_few_rows_each<kFmt>(p, stream);
+}
+
+bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped) {
+  return !grouped && rows <= 16 && rows * k <= kRoundMax;
 }
 
 hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& p, hipStream_t stream) {
+  if (p.x) return fmt == kE2M1 ? launch_few_rows<kE2M1, true>(p, stream) : launch_few_rows<kE4M3, true>(p, stream);
   return fmt == kE2M1 ? launch_product<kE2M1>(p, stream) : launch_product<kE4M3>(p, stream);
 }
 

@@ -12,11 +12,9 @@
 #include <stdint.h>
 
 #include "device_math.h"
-#include "e8m0.h"
 #include "fp4_block.h"
 #include "launch.h"
 #include "launch_mx.h"
-#include "mx8_block.h"
 #include "mx_quantize_dev.h"
 
 namespace trace_dev {
@@ -28,34 +26,15 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint4* __re
                                                                uint8_t* __restrict__ mask) {
   const uint64_t stride = (uint64_t)gridDim.x * kThreads;
   for (uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x; g < nvec; g += stride) {
-    const uint4 v = load_vec<kNT>(&x[g]);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    // nvec is a multiple of 4, so the four lanes of a block are active together
-    uint32_t amax = vec_amax_bits(w);
-    const uint32_t near = pair_swap(amax);
-    amax = amax > near ? amax : near;
-    const uint32_t far = quad_swap(amax);
-    amax = amax > far ? amax : far;
-    const uint32_t sb = mx_scale_byte<kFmt == 0 ? kE2M1Emax : kE4M3Emax>(amax);
-    const float inv = e8m0_inverse(sb);
+    const uint4 v = load_vec<kNT>(&x[g]);  // nvec is a multiple of 4: a block's four lanes are active together
+    uint32_t sb, keep;
+    const uint2 c = quantize_vector<kFmt == trace_host::kE2M1>(v, sb, keep);
     if ((g & 3) == 0) scales[g >> 2] = (uint8_t)sb;
-    if (kFmt == 0) {
-      uint32_t keep;
-      const uint32_t c = e2m1_codes8(w, inv, keep);
-      store_word<kNT>(reinterpret_cast<uint32_t*>(codes) + g, c);
-      if (mask) store_word<kNT>(&mask[g], (uint8_t)keep);
-    } else {
-      float q[8];
-      uint32_t nan_bits;
-      mx8_quotients<8>(w, inv, q, nan_bits);
-      const uint32_t keep = mx8_keep_bits<8>(q) & ~nan_bits;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], -448.f, 448.f);
-      uint32_t C[2];
-      fp8_rne_codes<8>(q, C);
-      store_pair<kNT>(reinterpret_cast<uint2*>(codes) + g, make_uint2(C[0], C[1]));
-      if (mask) store_word<kNT>(&mask[g], (uint8_t)keep);
-    }
+    if (kFmt == trace_host::kE2M1)
+      store_word<kNT>(reinterpret_cast<uint32_t*>(codes) + g, c.x);
+    else
+      store_pair<kNT>(reinterpret_cast<uint2*>(codes) + g, c);
+    if (mask) store_word<kNT>(&mask[g], (uint8_t)keep);
   }
 }
 
@@ -74,13 +53,13 @@ hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks,
   const uint4* xv = reinterpret_cast<const uint4*>(x);
   const bool nt = past_cache(nblocks * 64);
   if (fmt == kE2M1 && nt)
-    hipLaunchKernelGGL((mx_quantize_kernel<0, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
   else if (fmt == kE2M1)
-    hipLaunchKernelGGL((mx_quantize_kernel<0, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
   else if (nt)
-    hipLaunchKernelGGL((mx_quantize_kernel<1, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
   else
-    hipLaunchKernelGGL((mx_quantize_kernel<1, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
   return hipGetLastError();
 }
 

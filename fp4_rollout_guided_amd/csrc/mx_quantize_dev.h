@@ -1,12 +1,14 @@
-// Device helpers of the MXFP4 quantiser, on 8-element vectors (four packed
-// bf16 pairs).
+// Device helpers of the MXFP4 and MXFP8 quantisers, on 8-element vectors (four
+// packed bf16 pairs).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "device_math.h"
+#include "e8m0.h"
 #include "fp4_block.h"
+#include "mx8_block.h"
 
 namespace trace_dev {
 
@@ -56,6 +58,34 @@ __device__ __forceinline__ uint32_t e2m1_codes8(const uint32_t (&w)[4], float in
   c = FP4_RNE(c, q[4], q[5], 2);
   c = FP4_RNE(c, q[6], q[7], 3);
   return c;
+}
+
+// Codes, scale byte and clip-mask byte of a lane's vector.  The four lanes of
+// a 32-element block hold consecutive vectors and are active together; MXFP4
+// codes are in .x.
+template <bool kFp4>
+__device__ __forceinline__ uint2 quantize_vector(const uint4& v, uint32_t& scale, uint32_t& keep) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t amax = vec_amax_bits(w);
+  const uint32_t near = pair_swap(amax);
+  amax = amax > near ? amax : near;
+  const uint32_t far = quad_swap(amax);
+  amax = amax > far ? amax : far;
+  scale = mx_scale_byte<kFp4 ? kE2M1Emax : kE4M3Emax>(amax);
+  const float inv = e8m0_inverse(scale);
+  if constexpr (kFp4) {
+    return make_uint2(e2m1_codes8(w, inv, keep), 0);
+  } else {
+    float q[8];
+    uint32_t nan_bits;
+    mx8_quotients<8>(w, inv, q, nan_bits);
+    keep = mx8_keep_bits<8>(q) & ~nan_bits;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(q[j], -448.f, 448.f);
+    uint32_t C[2];
+    fp8_rne_codes<8>(q, C);
+    return make_uint2(C[0], C[1]);
+  }
 }
 
 }  // namespace trace_dev

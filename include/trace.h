@@ -590,12 +590,12 @@ TRACE_API trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const u
  * trace_mx8_quantize) followed by the product, with the same result.  The
  * ungrouped forms take offsets = row_index = NULL, groups = 0 and
  * src_rows == rows.
- *   workspace : trace_mx_linear_workspace_bytes(src_rows, k) (mx8:
+ *   workspace : trace_mx_linear_workspace_bytes(src_rows, rows, groups, k) (mx8:
  *               trace_mx8_linear_workspace_bytes) bytes of device scratch,
  *               16-byte aligned, caller-owned, contents not preserved; NULL
- *               where that is 0. */
-TRACE_API size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t k);
-TRACE_API size_t trace_mx8_linear_workspace_bytes(int64_t src_rows, int64_t k);
+ *               where that is 0 (few rows are rounded by the product itself). */
+TRACE_API size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t rows, int64_t groups, int64_t k);
+TRACE_API size_t trace_mx8_linear_workspace_bytes(int64_t src_rows, int64_t rows, int64_t groups, int64_t k);
 TRACE_API trace_status trace_mx_linear(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
                                        const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
                                        const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,

@@ -80,7 +80,7 @@ def test_quantize_matches_the_capture_and_the_rne_mask(device, fmt, shape):
 
 SHAPES = [(1, 16, 32), (1, 48, 160), (2, 2048, 4096), (7, 80, 96), (16, 16, 128), (33, 272, 544), (64, 128, 256),
           (127, 144, 768), (129, 256, 2080), (255, 528, 1056), (257, 272, 512), (300, 1024, 640), (1021, 768, 2048),
-          (16390, 1040, 544), (16400, 1024, 1184)]
+          (64, 4112, 96), (2100, 592, 96), (2100, 592, 544), (16390, 1040, 544), (16400, 1024, 1184)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
@@ -138,7 +138,8 @@ def _uneven(groups, rows, kind):
 
 GROUPED = [(1, 1, 16, 32, "even"), (5, 40, 48, 96, "skewed"), (3, 257, 144, 544, "tail"), (8, 700, 272, 256, "one"),
            (70, 300, 64, 160, "skewed"), (130, 1500, 256, 768, "even"), (6, 0, 32, 64, "even"),
-           (4, 1200, 512, 1024, "tail"), (9, 90, 2048, 768, "even"),
+           (4, 1200, 512, 1024, "tail"), (9, 90, 2048, 768, "even"), (64, 300, 336, 192, "tail"),
+           (64, 300, 336, 192, "one"),
            (5, 16500, 1040, 544, "skewed"), (6, 16420, 1024, 1056, "tail")]
 
 
@@ -168,7 +169,7 @@ def test_grouped_matmul(device, fmt, groups, rows, n, k, kind, gather):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "mx8"])
-@pytest.mark.parametrize("rows,n,k", [(1, 16, 32), (4, 2048, 4096), (37, 96, 544), (300, 256, 1056)])
+@pytest.mark.parametrize("rows,n,k", [(1, 16, 32), (4, 2048, 4096), (16, 4112, 1024), (3, 528, 96), (37, 96, 544), (300, 256, 1056)])
 def test_linear_is_quantize_and_matmul(device, fmt, rows, n, k):
     import fp4_rollout_guided_amd as tr
     _say("case linear", fmt, rows, n, k)
@@ -454,7 +455,7 @@ def test_binding_refusals(device):
     with pytest.raises(ValueError, match="contiguous"):
         tr.mx_linear(_bf16(k, rows, g, device).T, sw, cw, n)
     with pytest.raises(ValueError, match="at least"):
-        tr.mx_linear(x, sw, cw, n, workspace=torch.empty(16, dtype=torch.uint8, device=device))
+        tr.mx_linear(_bf16(24, k, g, device), sw, cw, n, workspace=torch.empty(16, dtype=torch.uint8, device=device))
     with pytest.raises(TypeError):
         tr.grouped_mx_linear(x, off.int(), sw, cw, n)
     with pytest.raises(ValueError, match="at least"):

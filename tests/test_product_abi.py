@@ -77,10 +77,12 @@ def test_linear(fn):
 
 
 def test_linear_workspace():
-    assert L.trace_mx_linear_workspace_bytes(40, 96) == 40 * 48 + 128
-    assert L.trace_mx8_linear_workspace_bytes(40, 96) == 40 * 96 + 128
-    assert L.trace_mx_linear_workspace_bytes(0, 96) == L.trace_mx_linear_workspace_bytes(-1, 96) == 0
-    assert L.trace_mx8_linear_workspace_bytes(4, 40) == 0
+    f, f8 = L.trace_mx_linear_workspace_bytes, L.trace_mx8_linear_workspace_bytes
+    assert f(40, 40, 0, 96) == 40 * 48 + 128 and f8(40, 40, 0, 96) == 40 * 96 + 128
+    assert f(40, 64, 3, 96) == 40 * 48 + 128  # the tokens' record, not the packed rows'
+    assert f(16, 16, 0, 96) == f8(1, 1, 0, 4096) == 0  # rounded by the product itself
+    assert f(16, 16, 0, 4096) == 16 * 2048 + 2048 and f(24, 192, 128, 2048) == 24 * 1024 + 1536
+    assert f(0, 0, 0, 96) == f(-1, 4, 0, 96) == f8(40, 40, 0, 40) == f(40, 40, 5000, 96) == 0
 
 
 GX = dict(grad_y=buf(0), rows=64, offsets=buf(6), groups=3, w_scales=buf(2), w_codes=buf(3), n=48, k=96, mask=buf(5),
