@@ -36,32 +36,75 @@ struct Operand<trace_host::kE4M3> {
   using type = v8i;
 };
 
+// Scale bytes of blocks b .. b + 15 of a row of `blocks` >= 16 (0x7f past its
+// last block): the 16 bytes at `at`, which end with the row where those would
+// run past it, moved to the front.
+__device__ __forceinline__ uint32_t scale_at(uint32_t b, uint32_t blocks) { return b + 16 <= blocks ? b : blocks - 16; }
+__device__ __forceinline__ v4i scale_piece(v4i v, uint32_t b, uint32_t blocks) {
+  constexpr uint32_t kOne = 0x7f7f7f7fu;
+  const uint32_t skip = b - scale_at(b, blocks);
+  uint32_t x0 = (uint32_t)v[0], x1 = (uint32_t)v[1], x2 = (uint32_t)v[2], x3 = (uint32_t)v[3];
+  const bool by8 = (skip & 8) != 0, by4 = (skip & 4) != 0, gone = skip >= 16;
+  x0 = by8 ? x2 : x0;
+  x1 = by8 ? x3 : x1;
+  x2 = by8 ? kOne : x2;
+  x3 = by8 ? kOne : x3;
+  x0 = by4 ? x1 : x0;
+  x1 = by4 ? x2 : x1;
+  x2 = by4 ? x3 : x2;
+  x3 = by4 ? kOne : x3;
+  v[0] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x1, x0, skip & 3));
+  v[1] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x2, x1, skip & 3));
+  v[2] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x3, x2, skip & 3));
+  v[3] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(kOne, x3, skip & 3));
+  return v;
+}
+
+// A number as a type, for lambdas that need it at compile time.
+template <uint32_t kValue>
+struct Constant {
+  static constexpr uint32_t value = kValue;
+};
+
+// Keeps what is computed from v from being computed before this point.
+__device__ __forceinline__ void not_ahead_of_time(uint32_t& v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(v));
+#endif
+}
+
 // ---------------------------------------------------------------------------
 // Few rows.  A workgroup owns 16 kNF columns n and up to 16 kMF rows of one
-// group; its kWaves waves take the 128-long steps of k in turn, kUnroll steps'
-// loads at a time, and their partial sums meet in LDS, added in the order of
-// the waves.  Operands go straight from memory to registers: no row of W is
-// used twice by a workgroup, and this is bound by W's bytes or, for one token
-// on one weight, by latency.
+// group; its kWaves waves take quads of four 128-long steps of k in turn, and
+// their partial sums meet in LDS, added in the order of the waves.  Operands go
+// straight from memory to registers, kSteps steps at a time and as many ahead.
+// A load that touches sixteen rows takes the compute unit some sixty cycles,
+// whatever it fetches of each, and that, not the bytes, bounds a workgroup: a
+// quad's scale bytes are therefore one load (one per step: a third more time).
+//
+// Loads have no conditions of their own, or each would be waited for before the
+// next: past the end of k they read some other block of the row and W's codes
+// are cleared, past the tile's rows they read its first row, and rows without a
+// source are cleared at the end.
 //
 // kRound: the activations are bf16, rows k of them at most kRoundMax, and each
 // workgroup rounds them all into LDS as mx_quantize would, while its first
 // loads of W are under way.  Against a launch of its own for the rounding (n
-// 2048, k 4096, MXFP4): 1 row 5.1 us against 6.5, 4 rows 6.3 against 6.8, 8
-// rows 7.9 against 7.1; one launch fewer on the host as well.
+// 2048, k 4096): 1 row 4.3 us against 5.6, 4 rows 5.6 against 5.9; 8 rows
+// (twice kRoundMax) took a fifth longer than with a launch of its own.
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kCUs = 256;
 constexpr uint32_t kRoundMax = 16384;
 
-template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kUnroll>
+template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kSteps>
 __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
   constexpr bool kFp4 = kFmt == trace_host::kE2M1;
   using AFrag = typename Operand<kFmt>::type;
   __shared__ v4f sums[kWaves][kMF * kNF][64];
   __shared__ __attribute__((aligned(16))) uint8_t rounded[kRound ? kRoundMax / (kFp4 ? 2 : 1) : 1];
   __shared__ uint8_t rounded_scales[kRound ? kRoundMax / 32 : 1];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = lane & 15, g = lane >> 4;
   const uint64_t row_tile = blockIdx.x / col_tiles;
   const uint32_t n0 = (uint32_t)(blockIdx.x - row_tile * col_tiles) * (16 * kNF);
@@ -75,6 +118,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
   }
   const bool behind = t.group >= p.groups;  // rows of no group: zeros
   const uint32_t blocks = p.k / 32;
+  uint32_t sources = ~0u;  // which of this lane's rows have a source row
   v4f acc[kMF][kNF] = {};
   if (!behind) {
     // W's columns past the last one: any row of the tile, its results are dropped
@@ -86,40 +130,125 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
       wc[f] = p.w_codes + n * (p.k / 2);
       ws[f] = p.w_scales + n * blocks;
     }
-    const uint32_t steps = (p.k + 127) / 128;
-    v4i w[kUnroll][kNF];
-    uint32_t wsc[kUnroll][kNF];
-    auto load_w = [&](uint32_t s0) {
+    const uint8_t* ac[kMF];
+    const uint8_t* as[kMF];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const uint32_t b = 4 * (s0 + u * kWaves) + g;  // this lane's block of k
+    for (int f = 0; f < kMF; ++f) {
+      uint64_t src = t.first + (16 * f + r < t.count ? 16 * f + r : 0);
+      if (p.row_index) {
+        const int64_t i = p.row_index[src];
+        const bool ok = i >= 0 && i < (int64_t)p.src_rows;
+        sources &= ~((ok ? 0u : 1u) << f);
+        src = ok ? (uint64_t)i : 0;
+      }
+      ac[f] = (kRound ? rounded : p.a_codes) + src * (kFp4 ? p.k / 2 : p.k);
+      as[f] = (kRound ? rounded_scales : p.a_scales) + src * blocks;
+    }
+    const uint32_t steps = p.src_rows ? (p.k + 127) / 128 : 0, quads = (steps + 3) / 4;
+    const bool short_row = blocks < 16;  // of scales: one quad
+    // Scale bytes of a quad, [step] in byte g; of a row of 16 blocks or more in
+    // its last quad as scale_at has them
+    struct Scales {
+      v4i w[kNF], a[kMF];
+    };
+    const auto bytes_of = [&](const uint8_t* row, uint32_t q) {
+      v4i v;
 #pragma unroll
-        for (int f = 0; f < kNF; ++f) {
-          w[u][f] = v4i{0, 0, 0, 0};
-          wsc[u][f] = 127;
-          if (b < blocks) {
-            w[u][f] = *reinterpret_cast<const v4i*>(wc[f] + 16 * (uint64_t)b);
-            wsc[u][f] = ws[f][b];
-          }
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t b = 16 * q + 4 * u + g;
+        v[u] = (int)((uint32_t)row[b < blocks ? b : blocks - 1] << (8 * g));
+      }
+      return v;
+    };
+    const auto piece_of = [&](const uint8_t* row, uint32_t q) {
+      v4i v;
+      __builtin_memcpy(&v, row + scale_at(16 * q, blocks), 16);
+      return v;
+    };
+    struct Set {
+      v4i w[kSteps][kNF];
+      AFrag a[kSteps][kMF];
+    };
+    const auto load_w = [&](Set& set, uint32_t s) {
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const uint32_t b = 4 * (s + u) + g, at = b < blocks ? b : blocks - 1;  // this lane's block of k
+#pragma unroll
+        for (int f = 0; f < kNF; ++f) set.w[u][f] = *reinterpret_cast<const v4i*>(wc[f] + 16 * at);
+      }
+    };
+    const auto load_a = [&](Set& set, uint32_t s) {
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const uint32_t b = 4 * (s + u) + g, at = b < blocks ? b : blocks - 1;
+        const uint32_t k0 = 128 * (s + u) + 16 * g;  // MXFP8: runs of 16 at k0 and k0 + 64
+        const uint32_t lo = k0 < p.k ? k0 : 0, hi = k0 + 64 < p.k ? k0 + 64 : 0;
+#pragma unroll
+        for (int f = 0; f < kMF; ++f) {
+          if constexpr (kFp4)
+            set.a[u][f] = *reinterpret_cast<const v4i*>(ac[f] + 16 * at);
+          else
+            set.a[u][f] = join(*reinterpret_cast<const v4i*>(ac[f] + lo), *reinterpret_cast<const v4i*>(ac[f] + hi));
         }
       }
     };
-    load_w(wave);
-    uint64_t src[kMF];
-    bool a_ok[kMF];
+    Scales sc, next;
+    Set set[2];
+    // kCount sets of quad q; kMore: the quad is whole and its last set's turn
+    // loads the first one of this wave's next quad
+    const auto quad = [&](uint32_t q, auto more, auto count) {
+      constexpr bool kMore = decltype(more)::value;
+      constexpr uint32_t kCount = decltype(count)::value;
+      if constexpr (kMore) {
 #pragma unroll
-    for (int f = 0; f < kMF; ++f) {
-      const uint32_t m = 16 * f + r;
-      a_ok[f] = m < t.count;
-      src[f] = t.first + (a_ok[f] ? m : 0);
-      if (p.row_index) {
-        const int64_t i = p.row_index[src[f]];
-        a_ok[f] = a_ok[f] && i >= 0 && i < (int64_t)p.src_rows;
-        src[f] = a_ok[f] ? (uint64_t)i : 0;
+        for (int f = 0; f < kNF; ++f) next.w[f] = piece_of(ws[f], q + kWaves);
+#pragma unroll
+        for (int f = 0; f < kMF; ++f) next.a[f] = kRound ? bytes_of(as[f], q + kWaves) : piece_of(as[f], q + kWaves);
+      } else if (!short_row) {
+#pragma unroll
+        for (int f = 0; f < kNF; ++f) sc.w[f] = scale_piece(sc.w[f], 16 * q, blocks);
+#pragma unroll
+        for (int f = 0; f < kMF; ++f)
+          if (!kRound) sc.a[f] = scale_piece(sc.a[f], 16 * q, blocks);
       }
+#pragma unroll
+      for (uint32_t j = 0; j < kCount; ++j) {
+        if (kMore || j + 1 < kCount) {
+          const uint32_t s = j + 1 < kCount ? 4 * q + (j + 1) * kSteps : 4 * (q + kWaves);
+          load_w(set[(j + 1) & 1], s);
+          load_a(set[(j + 1) & 1], s);
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+          const uint32_t step = j * kSteps + u;
+          const bool in = kMore || 16 * q + 4 * step + g < blocks;
+          uint32_t asc[kMF];
+#pragma unroll
+          for (int i = 0; i < kMF; ++i) asc[i] = (uint32_t)sc.a[i][step] >> (8 * g);
+#pragma unroll
+          for (int n = 0; n < kNF; ++n) {
+            v4i w = set[j & 1].w[u][n];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) w[d] = in ? w[d] : 0;
+            const uint32_t wsc = (uint32_t)sc.w[n][step] >> (8 * g);
+#pragma unroll
+            for (int i = 0; i < kMF; ++i)
+              acc[i][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  widen(w), widen(set[j & 1].a[u][i]), acc[i][n], kSelE2M1, kFp4 ? kSelE2M1 : kSelE4M3, 0, (int)wsc, 0,
+                  (int)asc[i]);
+          }
+        }
+      }
+      if constexpr (kMore) sc = next;
+    };
+    static_assert(kSteps == 1 || kSteps == 2, "an even number of sets in a quad");
+    constexpr uint32_t kSets = 4 / kSteps;
+    uint32_t q = wave;
+    if (q < quads) {
+#pragma unroll
+      for (int f = 0; f < kNF; ++f) sc.w[f] = short_row ? bytes_of(ws[f], q) : piece_of(ws[f], q);
+      load_w(set[0], 4 * q);
     }
-    const uint8_t* a_codes = p.a_codes;
-    const uint8_t* a_scales = p.a_scales;
     if constexpr (kRound) {
       const uint32_t nvec = (uint32_t)p.rows * (p.k / 8);
       for (uint32_t i = threadIdx.x; i < nvec; i += 64 * kWaves) {
@@ -131,50 +260,28 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
         else
           reinterpret_cast<uint2*>(rounded)[i] = c;
       }
-      a_codes = rounded;
-      a_scales = rounded_scales;
       __syncthreads();
     }
-    for (uint32_t s0 = wave; s0 < steps; s0 += kWaves * kUnroll) {
-      AFrag a[kUnroll][kMF];
-      uint32_t asc[kUnroll][kMF];
+    if (q < quads) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const uint32_t s = s0 + u * kWaves, b = 4 * s + g;
-        const bool in = b < blocks;
-        // MXFP8: runs of 16 at k0 and k0 + 64
-        const uint64_t k0 = 128 * (uint64_t)s + 16 * g;
-#pragma unroll
-        for (int f = 0; f < kMF; ++f) {
-          asc[u][f] = 127;
-          if (in && a_ok[f]) asc[u][f] = a_scales[src[f] * blocks + b];
-          if constexpr (kFp4) {
-            a[u][f] = v4i{0, 0, 0, 0};
-            if (in && a_ok[f]) a[u][f] = *reinterpret_cast<const v4i*>(a_codes + src[f] * (p.k / 2) + 16 * (uint64_t)b);
-          } else {
-            v4i lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-            if (k0 < p.k && a_ok[f]) lo = *reinterpret_cast<const v4i*>(a_codes + src[f] * p.k + k0);
-            if (k0 + 64 < p.k && a_ok[f]) hi = *reinterpret_cast<const v4i*>(a_codes + src[f] * p.k + k0 + 64);
-            a[u][f] = join(lo, hi);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < kMF; ++i)
-#pragma unroll
-          for (int j = 0; j < kNF; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                widen(w[u][j]), widen(a[u][i]), acc[i][j], kSelE2M1, kFp4 ? kSelE2M1 : kSelE4M3, 0, (int)wsc[u][j], 0,
-                (int)asc[u][i]);
-      if (s0 + kWaves * kUnroll < steps) load_w(s0 + kWaves * kUnroll);
+      for (int f = 0; f < kMF; ++f) sc.a[f] = kRound || short_row ? bytes_of(as[f], q) : piece_of(as[f], q);
+      load_a(set[0], 4 * q);
+      for (; q + kWaves < quads; q += kWaves) quad(q, Constant<1>{}, Constant<kSets>{});
+      const uint32_t left = (steps - 4 * q + kSteps - 1) / kSteps;  // sets of the last quad
+      if (left >= kSets)
+        quad(q, Constant<0>{}, Constant<kSets>{});
+      else if (left == 1)
+        quad(q, Constant<0>{}, Constant<1>{});
+      else if (left == 2)
+        quad(q, Constant<0>{}, Constant<(kSets > 2 ? 2 : 1)>{});
+      else
+        quad(q, Constant<0>{}, Constant<(kSets > 3 ? 3 : 1)>{});
     }
   }
 #pragma unroll
   for (int i = 0; i < kMF; ++i)
 #pragma unroll
-    for (int j = 0; j < kNF; ++j) sums[wave][i * kNF + j][lane] = acc[i][j];
+    for (int j = 0; j < kNF; ++j) sums[wave][i * kNF + j][lane] = (sources >> i & 1) ? acc[i][j] : v4f{0, 0, 0, 0};
   __syncthreads();
   for (uint32_t f = wave; f < kMF * kNF; f += kWaves) {
     v4f v = sums[0][f][lane];
@@ -213,43 +320,6 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 // This wave's LDS accesses are done; meet the workgroup's other waves.  Loads
 // to registers stay under way.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// Scale bytes of blocks b .. b + 15 of a row of `blocks` >= 16 (0x7f past its
-// last block): the 16 bytes at `at`, which end with the row where those would
-// run past it, moved to the front.
-__device__ __forceinline__ uint32_t scale_at(uint32_t b, uint32_t blocks) { return b + 16 <= blocks ? b : blocks - 16; }
-__device__ __forceinline__ v4i scale_piece(v4i v, uint32_t b, uint32_t blocks) {
-  constexpr uint32_t kOne = 0x7f7f7f7fu;
-  const uint32_t skip = b - scale_at(b, blocks);
-  uint32_t x0 = (uint32_t)v[0], x1 = (uint32_t)v[1], x2 = (uint32_t)v[2], x3 = (uint32_t)v[3];
-  const bool by8 = (skip & 8) != 0, by4 = (skip & 4) != 0, gone = skip >= 16;
-  x0 = by8 ? x2 : x0;
-  x1 = by8 ? x3 : x1;
-  x2 = by8 ? kOne : x2;
-  x3 = by8 ? kOne : x3;
-  x0 = by4 ? x1 : x0;
-  x1 = by4 ? x2 : x1;
-  x2 = by4 ? x3 : x2;
-  x3 = by4 ? kOne : x3;
-  v[0] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x1, x0, skip & 3));
-  v[1] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x2, x1, skip & 3));
-  v[2] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(x3, x2, skip & 3));
-  v[3] = (int)(gone ? kOne : __builtin_amdgcn_alignbyte(kOne, x3, skip & 3));
-  return v;
-}
-
-// A number as a type, for lambdas that need it at compile time.
-template <uint32_t kValue>
-struct Constant {
-  static constexpr uint32_t value = kValue;
-};
-
-// Keeps what is computed from v from being computed before this point.
-__device__ __forceinline__ void not_ahead_of_time(uint32_t& v) {
-#ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("" : "+v"(v));
-#endif
-}
 
 template <int kFmt, bool kGather, int kMF, int kNF, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProductArgs p, uint32_t col_tiles) {
@@ -489,12 +559,12 @@ namespace trace_host {
 
 using namespace trace_dev;
 
-template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kUnroll>
+template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kSteps>
 static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
   const uint32_t cols = (p.n + 16 * kNF - 1) / (16 * kNF);
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 16 * kMF) : (p.rows + 16 * kMF - 1) / (16 * kMF);
   if (row_tiles * cols * (64 * kWaves) > 0xffffffffull) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_skinny_kernel<kFmt, kRound, kMF, kNF, kWaves, kUnroll>), dim3((unsigned)(row_tiles * cols)),
+  hipLaunchKernelGGL((mx_skinny_kernel<kFmt, kRound, kMF, kNF, kWaves, kSteps>), dim3((unsigned)(row_tiles * cols)),
                      dim3(64 * kWaves), 0, stream, p, cols);
   return hipGetLastError();
 }
@@ -515,12 +585,12 @@ static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
 
 // One weight: the smallest tile that gives each CU at most one workgroup, since
 // a larger one leaves CUs idle and a smaller one reads its operands more often
-// (rows x n x k, MXFP4, us: 16 x 2048 x 4096 5.8 with 16 x 16, 7.6 with 16 x 32;
-// 64 x 2048 x 4096 7.7 with 16 x 32, 9.7 with 32 x 32; 128 x 2048 x 4096 9.8
-// with 32 x 32, 13.4 with 32 x 64; 64 x 7168 x 2048 8.4 with 32 x 64, 9.8 and
-// 10.5 with 32 x 32 and 64 x 64; 128 x 7168 x 2048 10.7 with 64 x 64, 13.5 with
-// 32 x 64, 11.7 in tiles of many rows; 256 x 7168 x 2048 18.0 with 64 x 64,
-// 12.3 in tiles of many rows).
+// (rows x n x k, MXFP4, us: 16 x 2048 x 4096 4.5 with 16 x 16, 5.5 with 16 x 32;
+// 64 x 2048 x 4096 5.7 with 16 x 32, 6.7 with 16 x 16; 100 x 2048 x 4096 6.9
+// with 32 x 32, 8.1 with 16 x 64; 64 x 7168 x 2048 6.2 with 32 x 64, 6.8 with 32
+// x 32; 128 x 7168 x 2048 8.5 with 64 x 64, 9.4 with 32 x 64; 512 x 2048 x 4096
+// 13 with 64 x 64, 17 with 32 x 64, 20 in tiles of many rows; 768 x 2048 x 4096
+// 24 with 64 x 64, 20 in tiles of many rows).
 template <int kFmt, bool kRound>
 static hipError_t launch_few_rows(const MxProductArgs& p, hipStream_t stream) {
   const auto tiles = [&](uint32_t rows, uint32_t cols) {
@@ -535,28 +605,32 @@ static hipError_t launch_few_rows(const MxProductArgs& p, hipStream_t stream) {
   return launch_skinny<kFmt, false, 4, 4, 4, 1>(p, stream);
 }
 
-// Groups of few rows.  Up to 8 rows each: tiles of 16 x 64, which read W's rows
-// once and keep many loads under way (192 rows of 128 groups, 1536 x 2048: 46
-// us, 52 with 32 x 32), or of 16 x 16 where there are few of those (8 rows: 6.2
-// us, 8.0).  More rows: 32 x 32.
+// Groups of few rows.  Where there are many tiles, one wave to each: 16 x 64 up
+// to 12 rows a group, 32 x 64 from there (128 groups, 1536 x 2048, MXFP4: 1.5
+// rows each 35 us, 43 with 32 x 64; 8 rows each 50 us; 16 rows each 64 us, 54
+// with 32 x 64).  Where there are few, four waves share the smaller tiles 16 x
+// 16 (8 rows of 128 groups: 4.9 us) and 32 x 32 (256 rows of 16 groups: 9.3 us,
+// 10.8 with 32 x 64 to a wave).
 template <int kFmt>
 static hipError_t launch_few_rows_each(const MxProductArgs& p, hipStream_t stream) {
-  if (p.rows > 8 * (uint64_t)p.groups) return launch_skinny<kFmt, false, 2, 2, 4, 2>(p, stream);
-  if (p.rows * ((p.n + 63) / 64) < 2 * kCUs) return launch_skinny<kFmt, false, 1, 1, 4, 2>(p, stream);
-  return launch_skinny<kFmt, false, 1, 4, 4, 1>(p, stream);
+  const uint64_t cols = (p.n + 63) / 64, groups = p.rows < p.groups ? p.rows : p.groups;
+  if (p.rows <= 12 * (uint64_t)p.groups) {
+    if (groups * cols < kCUs) return launch_skinny<kFmt, false, 1, 1, 4, 2>(p, stream);
+    return launch_skinny<kFmt, false, 1, 4, 1, 2>(p, stream);
+  }
+  if (groups * cols < 4 * kCUs) return launch_skinny<kFmt, false, 2, 2, 4, 2>(p, stream);
+  return launch_skinny<kFmt, false, 2, 4, 1, 1>(p, stream);
 }
 
-// Whether the rows are many: past the grids of launch_few_rows for one weight;
-// for groups from 32 rows each, or from 8 where the groups' tiles of 128
-// columns alone fill the card (128 groups, 1536 x 2048, us in tiles of few and
-// of many rows: 8 rows each 63 and 56, MXFP8 64 and 72; 12 each 77 and 56, MXFP8
-// 92 and 77.  16 groups: 16 each 12 and 13, 32 each 21 and 14).  A row's
-// scales must fill one 16-byte load, and row 0 must exist.
+// Whether the rows are many: past the grids of launch_few_rows for one weight,
+// from 32 rows each for groups (128 groups, 1536 x 2048, MXFP4, us in tiles of
+// few and of many rows: 16 rows each 54 and 60, 32 each 76 and 63; 16 groups: 16
+// each 9.3 and 13, 32 each 14 and 14, 64 each 17 and 14).  A row's scales must
+// fill one 16-byte load, and row 0 must exist.
 static bool many_rows(const MxProductArgs& p) {
   if (p.k < 512 || p.src_rows == 0) return false;
   if (!p.offsets) return (p.rows + 63) / 64 * ((p.n + 63) / 64) > kCUs;
-  return p.rows >= 32 * (uint64_t)p.groups ||
-         (p.rows > 8 * (uint64_t)p.groups && p.groups * (uint64_t)((p.n + 127) / 128) >= kCUs);
+  return p.rows >= 32 * (uint64_t)p.groups;
 }
 
 template <int kFmt>
