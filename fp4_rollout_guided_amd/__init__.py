@@ -759,13 +759,21 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# A device's current stream as an integer.  A Stream object for each call would
+# take a microsecond of the ten that a small product's call takes.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(name, like, *args):
     """Call an entry point on ``like``'s device and its current stream."""
     dev = like.device.index
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(name, like, *args)
-    _check(getattr(lib, name)(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    status = getattr(lib, name)(*args, _current_stream(dev))
+    if status != 0:
+        raise TraceError(status, name)
 
 
 def _matrix(t, name):
@@ -799,13 +807,13 @@ def _out(t, name, like, shape, dtype):
     for d in shape:
         n *= d
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     return _arg(t, name, like, _BF16 if dtype == torch.bfloat16 else (dtype,), n)
 
 
 def _workspace(t, like, need):
     if t is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+        return like.new_empty(need, dtype=torch.uint8) if need else None
     return _arg(t, "workspace", like, _U8, need)
 
 
