@@ -488,14 +488,6 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
                                                                     kSel, (int)asc[j]);
   };
 
-  if (stages) {
-    fetch(0, true);
-    load_span(0);
-    place(0);
-    if (stages > 1) fetch(1, true);
-    store_span(0);
-    lds_barrier();
-  }
   // One stage.  kSteady: stages st + 1 and st + 2 exist in full.
   const auto stage = [&](uint32_t st, auto steady) {
     constexpr bool kSteady = decltype(steady)::value;
