@@ -2,13 +2,16 @@
 // expert, the gather of the tokens' rows into that order, the weighted sum of
 // the experts' rows back to the tokens, and that sum's gradients.
 //
-// Sort: a stable counting sort.  A workgroup owns a chunk of kSortChunk pairs,
-// its four waves consecutive quarters of it; a wave ranks 64 pairs at a time
+// Sort: a stable counting sort.  A workgroup owns a chunk of pairs, its four
+// waves consecutive quarters of it; a wave ranks 64 pairs at a time
 // by comparing expert numbers bit by bit (one ballot per bit), so the order
 // inside an expert is the pairs' own and no result depends on the order of
-// atomics.  One chunk is one launch.  More chunks take a counting launch, a
-// scan over the chunks' counts (one launch, one lane per expert) and a
-// scatter launch.
+// atomics.  One chunk is one launch.  More chunks take a counting launch and a
+// scatter launch, whose workgroups each sum the counts of the chunks before
+// theirs; past kSumChunks a scan over the chunks' counts (one workgroup, one
+// lane per expert) runs between the two (128 experts, with the sums and with
+// the scan: 131072 pairs 15 and 19 us, 2097152 pairs 83 and 123 us, but the
+// sums grow with the square).
 //
 // Dispatch, combine and combine's gradients move rows and are bound by
 // memory: 16 bytes per lane, every row read or written once, sums in fp32 in
@@ -23,9 +26,10 @@
 
 namespace trace_dev {
 
-constexpr uint32_t kSortChunk = 2048;
+constexpr uint32_t kSortChunk = 2048;  // at most
 constexpr uint32_t kSortWaves = kThreads / 64;
 constexpr uint32_t kSortRounds = kSortChunk / kThreads;
+constexpr uint32_t kSumChunks = 1024;
 
 // Expert of a pair as a bin: experts that are not held share the last bin.
 __device__ __forceinline__ uint32_t expert_bin(const int64_t* __restrict__ ids, uint64_t pair, uint32_t experts) {
@@ -45,15 +49,16 @@ __device__ __forceinline__ uint64_t same_bin(uint32_t bin, bool active, uint32_t
 
 // Counts of a chunk's bins: counts[chunk][experts + 1].
 __global__ __launch_bounds__(kThreads) void expert_count_kernel(const int64_t* __restrict__ ids, uint64_t pairs,
-                                                                uint32_t experts, uint32_t* __restrict__ counts) {
+                                                                uint32_t experts, uint32_t chunk,
+                                                                uint32_t* __restrict__ counts) {
   __shared__ uint32_t hist[trace_host::kMaxExperts + 1];
   for (uint32_t e = threadIdx.x; e <= experts; e += kThreads) hist[e] = 0;
   __syncthreads();
-  const uint64_t base = (uint64_t)blockIdx.x * kSortChunk;
+  const uint64_t base = (uint64_t)blockIdx.x * chunk;
 #pragma unroll
   for (uint32_t r = 0; r < kSortRounds; ++r) {
     const uint64_t pair = base + r * kThreads + threadIdx.x;
-    if (pair < pairs) atomicAdd(&hist[expert_bin(ids, pair, experts)], 1u);
+    if (r * kThreads < chunk && pair < pairs) atomicAdd(&hist[expert_bin(ids, pair, experts)], 1u);
   }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e <= experts; e += kThreads)
@@ -113,45 +118,69 @@ __global__ __launch_bounds__(1024) void expert_scan_kernel(uint32_t* __restrict_
   }
 }
 
-// Places a chunk's pairs.  kSingle: the only chunk; it counts and scans by
-// itself and writes the offsets.  Otherwise first[chunk][bin] comes from the
-// scan.
-template <bool kSingle>
+// Where expert_place_kernel has the first positions of its chunk's bins from:
+// its own counts, the only chunk's; all chunks' counts; or their scan.
+enum SortFirst { kOnlyChunk, kSumCounts, kScanned };
+
+// Places a chunk's pairs; all but kScanned write the offsets.
+template <SortFirst kFirst>
 __global__ __launch_bounds__(kThreads) void expert_place_kernel(const int64_t* __restrict__ ids, uint64_t pairs,
                                                                 uint32_t topk, uint32_t experts, uint32_t bits,
-                                                                const uint32_t* __restrict__ first,
+                                                                uint32_t chunk, const uint32_t* __restrict__ counts,
                                                                 int64_t* __restrict__ offsets,
                                                                 int64_t* __restrict__ row_index,
                                                                 int64_t* __restrict__ slot) {
   __shared__ uint32_t next[kSortWaves][trace_host::kMaxExperts + 1];  // next free position, per wave and bin
   __shared__ uint32_t part[kSortWaves];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint64_t base = (uint64_t)blockIdx.x * kSortChunk + wave * (kSortChunk / kSortWaves);
-  for (uint32_t i = threadIdx.x; i < kSortWaves * (trace_host::kMaxExperts + 1); i += kThreads) (&next[0][0])[i] = 0;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t share = chunk / kSortWaves;
+  const uint64_t base = (uint64_t)blockIdx.x * chunk + wave * share;
+  const auto in_share = [&](uint32_t r) { return r * 64 < share && base + r * 64 < pairs; };
+  for (uint32_t w = 0; w < kSortWaves; ++w)
+    for (uint32_t e = threadIdx.x; e <= experts; e += kThreads) next[w][e] = 0;
   __syncthreads();
   uint32_t bin[kSortRounds];
 #pragma unroll
   for (uint32_t r = 0; r < kSortRounds; ++r) {
     const uint64_t pair = base + r * 64 + lane;
-    bin[r] = pair < pairs ? expert_bin(ids, pair, experts) : 0u;
+    bin[r] = in_share(r) && pair < pairs ? expert_bin(ids, pair, experts) : 0u;
   }
 #pragma unroll
   for (uint32_t r = 0; r < kSortRounds; ++r)
-    if (base + r * 64 + lane < pairs) atomicAdd(&next[wave][bin[r]], 1u);
+    if (in_share(r) && base + r * 64 + lane < pairs) atomicAdd(&next[wave][bin[r]], 1u);
   __syncthreads();
   uint32_t carry = 0;
   for (uint32_t e0 = 0; e0 <= experts; e0 += kThreads) {
     const uint32_t e = e0 + threadIdx.x;
     uint32_t at = 0;
-    if (kSingle) {
-      uint32_t sum = 0, total;
-      if (e <= experts)
-        for (uint32_t w = 0; w < kSortWaves; ++w) sum += next[w][e];
+    if (kFirst == kScanned) {
+      if (e <= experts) at = counts[(uint64_t)blockIdx.x * (experts + 1) + e];
+    } else {
+      uint32_t sum = 0, before = 0, total;  // of all chunks, and of those before this one
+      if (e <= experts) {
+        if (kFirst == kOnlyChunk) {
+          for (uint32_t w = 0; w < kSortWaves; ++w) sum += next[w][e];
+        } else {
+          constexpr uint32_t kAtOnce = 16;
+          for (uint32_t c0 = 0; c0 < gridDim.x; c0 += kAtOnce) {
+            uint32_t n[kAtOnce];
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+              const uint32_t c = c0 + i < gridDim.x ? c0 + i : gridDim.x - 1;
+              n[i] = counts[(uint64_t)c * (experts + 1) + e];
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+              if (c0 + i < gridDim.x) sum += n[i];
+              if (c0 + i < blockIdx.x) before += n[i];
+            }
+          }
+        }
+      }
       at = carry + block_prefix<kSortWaves>(sum, part, &total);
       carry += total;
-      if (e <= experts) offsets[e] = (int64_t)at;
-    } else if (e <= experts) {
-      at = first[(uint64_t)blockIdx.x * (experts + 1) + e];
+      if (blockIdx.x == 0 && e <= experts) offsets[e] = (int64_t)at;  // the last bin starts where the held rows end
+      at += before;
     }
     if (e <= experts)
       for (uint32_t w = 0; w < kSortWaves; ++w) {
@@ -163,6 +192,7 @@ __global__ __launch_bounds__(kThreads) void expert_place_kernel(const int64_t* _
   __syncthreads();
 #pragma unroll
   for (uint32_t r = 0; r < kSortRounds; ++r) {
+    if (!in_share(r)) break;
     const uint64_t pair = base + r * 64 + lane;
     const bool active = pair < pairs;
     const uint64_t peers = same_bin(bin[r], active, bits);
@@ -301,7 +331,16 @@ static unsigned rows_grid(uint64_t units, uint32_t per) {
   return (unsigned)(g < kMaxGroups ? g : kMaxGroups);
 }
 
-static uint64_t sort_chunks(uint64_t pairs) { return (pairs + kSortChunk - 1) / kSortChunk; }
+// Pairs to a chunk.  The only one is cut to fit (192 pairs: 3.4 us, 6.2 uncut;
+// 1600 pairs: 7.5 us, 9.0 in two chunks); then 1024 (4096 pairs: 8.5 us, 12 with
+// 2048; 131072: 13.6 and 14.9) until their number tells (524288: 35 us, 23 with
+// 2048).
+static uint32_t sort_chunk(uint64_t pairs) {
+  if (pairs <= kSortChunk) return pairs ? (uint32_t)((pairs + kThreads - 1) / kThreads) * kThreads : kThreads;
+  return pairs <= 262144 ? 1024 : kSortChunk;
+}
+
+static uint64_t sort_chunks(uint64_t pairs) { return (pairs + sort_chunk(pairs) - 1) / sort_chunk(pairs); }
 
 uint64_t expert_sort_workspace_words(uint64_t pairs, uint32_t experts) {
   const uint64_t chunks = sort_chunks(pairs);
@@ -312,18 +351,24 @@ hipError_t launch_expert_sort(const int64_t* ids, uint64_t pairs, uint32_t topk,
                               int64_t* offsets, int64_t* row_index, int64_t* slot, hipStream_t stream) {
   uint32_t bits = 0;
   while ((experts >> bits) != 0) ++bits;  // bins 0..experts
+  const uint32_t chunk = sort_chunk(pairs);
   const uint64_t chunks = sort_chunks(pairs);
+  const dim3 grid((unsigned)(chunks > 1 ? chunks : 1)), block(kThreads);
   if (chunks <= 1) {
-    hipLaunchKernelGGL(expert_place_kernel<true>, dim3(1), dim3(kThreads), 0, stream, ids, pairs, topk, experts, bits,
+    hipLaunchKernelGGL(expert_place_kernel<kOnlyChunk>, grid, block, 0, stream, ids, pairs, topk, experts, bits, chunk,
                        static_cast<const uint32_t*>(nullptr), offsets, row_index, slot);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)chunks), block(kThreads);
-  hipLaunchKernelGGL(expert_count_kernel, grid, block, 0, stream, ids, pairs, experts, workspace);
-  hipLaunchKernelGGL(expert_scan_kernel, dim3(1), dim3(1024), 0, stream, workspace, (uint32_t)chunks, experts,
-                     offsets);
-  hipLaunchKernelGGL(expert_place_kernel<false>, grid, block, 0, stream, ids, pairs, topk, experts, bits,
-                     static_cast<const uint32_t*>(workspace), offsets, row_index, slot);
+  hipLaunchKernelGGL(expert_count_kernel, grid, block, 0, stream, ids, pairs, experts, chunk, workspace);
+  const uint32_t* counts = workspace;
+  if (chunks <= kSumChunks) {
+    hipLaunchKernelGGL(expert_place_kernel<kSumCounts>, grid, block, 0, stream, ids, pairs, topk, experts, bits, chunk,
+                       counts, offsets, row_index, slot);
+  } else {
+    hipLaunchKernelGGL(expert_scan_kernel, dim3(1), dim3(1024), 0, stream, workspace, (uint32_t)chunks, experts, offsets);
+    hipLaunchKernelGGL(expert_place_kernel<kScanned>, grid, block, 0, stream, ids, pairs, topk, experts, bits, chunk,
+                       counts, offsets, row_index, slot);
+  }
   return hipGetLastError();
 }
 

@@ -46,7 +46,8 @@ def _sorted(ids, experts):
 @pytest.mark.parametrize("tokens,topk,experts,pool", [
     (0, 2, 8, "all"), (1, 1, 1, "all"), (1, 8, 128, "all"), (24, 8, 128, "all"), (63, 3, 5, "half"), (100, 2, 1, "none"),
     (256, 8, 128, "all"), (257, 8, 127, "half"), (300, 7, 1024, "all"), (3000, 4, 9, "one"), (5000, 6, 200, "half"),
-    (16384, 8, 128, "all"), (33, 64, 64, "all"), (700, 3, 1023, "half")])
+    (16384, 8, 128, "all"), (33, 64, 64, "all"), (700, 3, 1023, "half"),
+    (32769, 8, 40, "half"), (262145, 8, 9, "half")])
 def test_sort(device, tokens, topk, experts, pool):
     import fp4_rollout_guided_amd as tr
     _say("case sort", tokens, topk, experts, pool)

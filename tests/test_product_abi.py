@@ -142,7 +142,8 @@ def test_sort():
         assert c(**{name: buf(0)}) == E_ALIAS, name
     assert c(slot=buf(3)) == E_ALIAS
     f = L.trace_expert_sort_workspace_bytes
-    assert f(256, 8, 128) == 0 and f(257, 8, 128) == 2 * 129 * 4 and f(-1, 8, 128) == f(4, 8, 2000) == 0
+    assert f(256, 8, 128) == 0 and f(257, 8, 128) == 3 * 129 * 4 and f(-1, 8, 128) == f(4, 8, 2000) == 0
+    assert f(32768, 8, 128) == 256 * 129 * 4 and f(32769, 8, 128) == 129 * 129 * 4
 
 
 DISP = dict(x=buf(0), tokens=30, cols=48, row_index=buf(1), rows=60, out=buf(2), stream=None)
