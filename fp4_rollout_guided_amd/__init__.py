@@ -51,6 +51,7 @@ and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch`` and ``ExpertCombine``
 wrap the forward/backward pairs as autograd functions.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -781,7 +782,7 @@ def _matrix(t, name):
     _bf16(t, name)
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
-    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+    return math.prod(t.shape[:-1]), t.shape[-1]
 
 
 def _dim(v, name, multiple):
@@ -1119,6 +1120,8 @@ class MxMatmul(torch.autograd.Function):
             raise ValueError(f'fmt must be "mx" or "mx8", got {fmt!r}')
         x, w = x.contiguous(), w.contiguous()
         n, k = w.shape[-2:]
+        if x.shape[-1] != k:
+            raise ValueError(f"x has rows of {x.shape[-1]}, w of {k}")
         if scales is None:
             a_scales, a_codes, a_mask = _quantize(fmt, x, True, None, None, None)
         else:

@@ -38,6 +38,9 @@ trace_status product_groups(const int64_t* offsets, int64_t groups, int64_t* gro
   return TRACE_OK;
 }
 
+// A launcher's answer; a grid past the hardware's limit is the sizes' fault.
+trace_status launch_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? TRACE_E_SHAPE : hip_status(e); }
+
 uint64_t code_bytes(MxFormat fmt, uint64_t elements) { return fmt == kE2M1 ? elements / 2 : elements; }
 
 size_t linear_workspace(MxFormat fmt, int64_t src_rows, int64_t rows, int64_t groups, int64_t k) {
@@ -104,7 +107,7 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
   const bool rounds = linear && trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0);
   const trace_host::MxProductArgs p{rounds ? x : nullptr, a_codes, a_scales, row_index, (uint64_t)src_rows, (uint64_t)rows,
                                     offsets, (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y};
-  return hip_status(trace_host::launch_mx_product(fmt, p, s));
+  return launch_status(trace_host::launch_mx_product(fmt, p, s));
 }
 
 trace_status grad_input(const uint16_t* grad_y, int64_t rows, const int64_t* offsets, int64_t groups,
@@ -124,7 +127,7 @@ trace_status grad_input(const uint16_t* grad_y, int64_t rows, const int64_t* off
   if (trace_status st = check_alias(outs, 1, ins, 5)) return st;
   const trace_host::MxGradArgs p{grad_y, (uint64_t)rows, offsets, (uint32_t)weights, w_codes, w_scales, nullptr,
                                  (uint64_t)rows, (uint32_t)n, (uint32_t)k, mask, grad_x, nullptr};
-  return hip_status(trace_host::launch_mx_grad_input(p, static_cast<hipStream_t>(stream)));
+  return launch_status(trace_host::launch_mx_grad_input(p, static_cast<hipStream_t>(stream)));
 }
 
 size_t grad_weight_workspace(int64_t rows, int64_t groups, int64_t n, int64_t k) {
@@ -164,7 +167,7 @@ trace_status grad_weight(MxFormat fmt, const uint16_t* grad_y, int64_t rows, con
   const trace_host::MxGradArgs p{grad_y, (uint64_t)rows, offsets, (uint32_t)weights, a_codes, a_scales, row_index,
                                  (uint64_t)src_rows, (uint32_t)n, (uint32_t)k, mask, grad_w,
                                  static_cast<float*>(workspace)};
-  return hip_status(trace_host::launch_mx_grad_weight(fmt, p, static_cast<hipStream_t>(stream)));
+  return launch_status(trace_host::launch_mx_grad_weight(fmt, p, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

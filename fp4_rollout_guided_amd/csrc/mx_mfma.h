@@ -93,22 +93,22 @@ __device__ __forceinline__ bool find_row_tile(const int64_t* __restrict__ offset
     uint64_t first = 0;
     const uint32_t count = g <= groups ? group_rows(offsets, g, groups, rows, first) : 0u;
     const uint32_t tiles = (count + height - 1) / height;
-    uint32_t sum = tiles;  // inclusive prefix over the wave's 64 groups: at most rows tiles, which fit 32 bits
+    // inclusive prefix over the wave's 64 groups; offsets that overlap could pass 32 bits
+    uint32_t sum = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const uint32_t up = (uint32_t)__shfl_up((int)sum, d);
-      if (lane >= (uint32_t)d) sum += up;
+      if (lane >= (uint32_t)d) sum = __builtin_elementwise_add_sat(sum, up);
     }
     const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
     if (tile < before + all) {
       const uint64_t hit = __ballot(tile < before + sum);
       const int at = __ffsll((long long)hit) - 1;  // the first group whose tiles reach past `tile`
       const uint32_t cnt = (uint32_t)__builtin_amdgcn_readlane((int)count, at);
-      const uint32_t ends = (uint32_t)__builtin_amdgcn_readlane((int)sum, at);
-      const uint32_t own = (uint32_t)__builtin_amdgcn_readlane((int)tiles, at);
+      const uint32_t start = at ? (uint32_t)__builtin_amdgcn_readlane((int)sum, at - 1) : 0u;
       const uint32_t flo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)first, at);
       const uint32_t fhi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(first >> 32), at);
-      const uint32_t in = (uint32_t)(tile - (before + ends - own)) * height;
+      const uint32_t in = (uint32_t)(tile - (before + start)) * height;
       out.group = g0 + (uint32_t)at;
       out.first = (((uint64_t)fhi << 32) | flo) + in;
       out.count = cnt - in < height ? cnt - in : height;
@@ -127,10 +127,10 @@ __device__ __forceinline__ uint64_t count_row_tiles(const int64_t* __restrict__ 
   uint32_t sum = 0;
   for (uint32_t g = lane; g <= groups; g += 64) {
     uint64_t first;
-    sum += (group_rows(offsets, g, groups, rows, first) + height - 1) / height;
+    sum = __builtin_elementwise_add_sat(sum, (group_rows(offsets, g, groups, rows, first) + height - 1) / height);
   }
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += (uint32_t)__shfl_xor((int)sum, d);
+  for (int d = 32; d > 0; d >>= 1) sum = __builtin_elementwise_add_sat(sum, (uint32_t)__shfl_xor((int)sum, d));
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum);
 }
 

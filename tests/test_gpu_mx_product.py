@@ -359,6 +359,21 @@ def test_gradients_match_differences(device):
             assert abs(diff - grad[i, j]) <= 2.0 ** -8 * abs(diff) + 1e-4
 
 
+def test_empty_contractions_give_zeros(device):
+    import fp4_rollout_guided_amd as tr
+    none = torch.empty(0, dtype=torch.uint8, device=device)
+    x, y = torch.empty(5, 0, dtype=torch.bfloat16, device=device), torch.full((5, 32), 7.0, device=device).bfloat16()
+    for lin in (tr.mx_linear, tr.mx8_linear):
+        assert lin(x, none, none, 32, y=y) is y and (y == 0).all()
+        y.fill_(7)
+    off = torch.tensor([0, 2, 4], device=device)
+    assert (tr.grouped_mx_linear(x, off, none, none, 32, y=y) == 0).all()
+    gx = torch.full((5, 64), 7.0, device=device).bfloat16()
+    assert (tr.mx_matmul_bwd_input(x, none, none, 64, grad_x=gx) == 0).all()
+    with pytest.raises(ValueError, match="rows of"):
+        tr.MxMatmul.apply(_bf16(4, 64, _gen(device, "k"), device), _bf16(16, 32, _gen(device, "k"), device))
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, devices
 # ---------------------------------------------------------------------------
@@ -404,6 +419,64 @@ def test_products_on_a_side_stream_and_in_a_graph(device):
         torch.cuda.synchronize()
         for a, b in zip(held, layer()):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+def test_autograd_in_a_graph(device, fmt):
+    """Token rounded in the product, routed rows and both gradients through
+    autograd, captured after an eager pass whose graph is gone."""
+    import fp4_rollout_guided_amd as tr
+    g = _gen(device, fmt, "autograd graph")
+    tokens, topk, experts, n, k = 24, 2, 4, 64, 96
+    x, w = _bf16(tokens, k, g, device), _bf16(experts * n, k, g, device, 0.1).view(experts, n, k)
+    ids = torch.topk(torch.rand(tokens, experts, generator=g, device=device), topk).indices.contiguous()
+    wt, go = torch.rand(tokens, topk, generator=g, device=device), _bf16(tokens, n, g, device)
+    sw, cw = random_record("mx", n, k, g, device)
+
+    def layer():
+        leaves = [t.detach().requires_grad_() for t in (x, w, wt)]
+        off, index, slot = tr.expert_sort(ids, experts)
+        y = tr.MxMatmul.apply(tr.ExpertDispatch.apply(leaves[0], index, slot), leaves[1], off, fmt)
+        out = tr.ExpertCombine.apply(y, slot, leaves[2], off)
+        one = (tr.mx_linear if fmt == "mx" else tr.mx8_linear)(x[:1], sw, cw, n)
+        return [out.detach(), one, *torch.autograd.grad(out, leaves, go)]
+
+    side = torch.cuda.Stream(device)
+    side.wait_stream(torch.cuda.current_stream(device))
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream(device).wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = layer()
+    for i in range(4):
+        x.copy_(_bf16(tokens, k, g, device))
+        go.copy_(_bf16(tokens, n, g, device))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, layer()):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [5, -7, 1 << 40, 30], [90, 90, 0, 0], [0, 90, 0, 90]])
+@pytest.mark.parametrize("rows", [90, 300])
+def test_offsets_out_of_order_stay_in_bounds(device, offsets, rows):
+    """Their results are unspecified, but nothing past the arrays is written."""
+    import fp4_rollout_guided_amd as tr
+    g = _gen(device, rows, *offsets)
+    n, k, groups = 80, 544, 3
+    off = torch.tensor(offsets, device=device)
+    x, gy = _bf16(rows, k, g, device), _bf16(rows, n, g, device)
+    sa, ca = random_record("mx", rows, k, g, device)
+    sw, cw = random_record("mx", groups * n, k, g, device)
+    for shape, call in (((rows, n), lambda t: tr.grouped_mx_linear(x, off, sw, cw, n, y=t)),
+                        ((rows, n), lambda t: tr.grouped_mx_matmul(sa, ca, off, sw, cw, n, k, y=t)),
+                        ((rows, k), lambda t: tr.grouped_mx_matmul_bwd_input(gy, off, sw, cw, k, grad_x=t)),
+                        ((groups * n, k), lambda t: tr.grouped_mx_matmul_bwd_weight(gy, off, sa, ca, k, grad_w=t))):
+        buf = torch.full((shape[0] + 200, shape[1]), 7.0, dtype=torch.bfloat16, device=device)
+        call(buf[:shape[0]])
+        assert (buf[shape[0]:] == 7).all()
 
 
 def test_results_do_not_change_between_calls(device):

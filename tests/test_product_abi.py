@@ -76,6 +76,12 @@ def test_linear(fn):
     assert c(workspace=buf(0)) == c(workspace=buf(4)) == c(y=buf(7, 64)) == c(y=buf(0)) == E_ALIAS
 
 
+def test_results_past_one_launch():
+    at = [(1 << 44) + (i << 40) for i in range(5)]
+    f = L.trace_mx_matmul
+    assert f(at[0], at[1], (1 << 31) - 1, at[2], at[3], 16, 32, at[4], None) == E_SHAPE
+
+
 def test_linear_workspace():
     f, f8 = L.trace_mx_linear_workspace_bytes, L.trace_mx8_linear_workspace_bytes
     assert f(40, 40, 0, 96) == 40 * 48 + 128 and f8(40, 40, 0, 96) == 40 * 96 + 128
