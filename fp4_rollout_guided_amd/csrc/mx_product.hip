@@ -540,7 +540,7 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
       }
     block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
       const uint32_t m = wm + 32 * j + row, n = n0 + wn + 8 * piece;
-      if (m < t.count && n < p.n) *reinterpret_cast<uint4*>(p.y + (t.first + m) * p.n + n) = v;
+      if (m < t.count && n < p.n) store_result(p.y + (t.first + m) * p.n + n, v, p.stream_out);
     });
   }
 }
@@ -646,7 +646,9 @@ bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped) {
   return !grouped && rows <= 16 && rows * k <= kRoundMax;
 }
 
-hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& p, hipStream_t stream) {
+hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& args, hipStream_t stream) {
+  MxProductArgs p = args;
+  p.stream_out = past_cache(2 * p.rows * p.n);
   if (p.x) return fmt == kE2M1 ? launch_few_rows<kE2M1, true>(p, stream) : launch_few_rows<kE4M3, true>(p, stream);
   return fmt == kE2M1 ? launch_product<kE2M1>(p, stream) : launch_product<kE4M3>(p, stream);
 }

@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
       const uint32_t pp = wp + 32 * b + row, k = k0 + wk + 8 * piece;
       if (k < p.k && (kWeight ? p0 + pp < p.n : pp < t.count)) {
         const uint64_t to = kWeight ? (uint64_t)t.group * p.n + p0 + pp : t.first + pp;
-        *reinterpret_cast<uint4*>(p.grad + to * p.k + k) = v;
+        store_result(p.grad + to * p.k + k, v, p.stream_out);
       }
     });
   }
@@ -405,7 +405,9 @@ static hipError_t grad_input(const MxGradArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx_grad_input(const MxGradArgs& p, hipStream_t stream) {
+hipError_t launch_mx_grad_input(const MxGradArgs& args, hipStream_t stream) {
+  MxGradArgs p = args;
+  p.stream_out = past_cache(2 * p.rows * p.k);
   return big_tiles(p.rows, p.k) ? grad_input<4, 2, 2>(p, stream) : grad_input<2, 1, 2>(p, stream);
 }
 
@@ -460,7 +462,9 @@ static hipError_t grad_weight(const MxGradArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx_grad_weight(MxFormat fmt, const MxGradArgs& p, hipStream_t stream) {
+hipError_t launch_mx_grad_weight(MxFormat fmt, const MxGradArgs& args, hipStream_t stream) {
+  MxGradArgs p = args;
+  p.stream_out = past_cache(2 * (uint64_t)p.groups * p.n * p.k);
   return fmt == kE2M1 ? grad_weight<kE2M1>(p, stream) : grad_weight<kE4M3>(p, stream);
 }
 

@@ -146,3 +146,30 @@ def test_combine_bwd_leaves_unnamed_rows(device):
     assert out[[1, 4]].eq(1).all() and out[[0, 2, 3, 5]].eq(9).all() and gw.flatten().tolist() == [16.0, 16.0, 0.0]
     fresh, _ = tr.expert_combine_bwd(go, y, slot, None)
     assert fresh[[0, 2, 3, 5]].eq(0).all()
+
+
+def test_small_grid_build_gives_the_same(device):
+    """The test build sends every row past the cache and runs its grid-stride
+    loops several times: the same bits."""
+    import fp4_rollout_guided_amd as tr
+    g = _gen(device, "small grid")
+    tokens, topk, experts, cols = 333, 4, 12, 528
+    ids = torch.randint(0, experts + 3, (tokens, topk), generator=g, device=device)
+    x = torch.randn(tokens, cols, generator=g, device=device).to(torch.bfloat16)
+    wt = torch.rand(tokens, topk, generator=g, device=device)
+
+    def run():
+        off, index, slot = tr.expert_sort(ids, experts)
+        rows = tr.expert_dispatch(x, index)
+        return [off, index, slot, rows, tr.expert_combine(rows, slot, wt), *tr.expert_combine_bwd(x, rows, slot, wt, off)]
+
+    want = run()
+    held = tr.lib
+    try:
+        tr.lib = tr.load_library(tr.SMALLGRID_LIB_PATH)
+        got = run()
+        torch.cuda.synchronize()
+    finally:
+        tr.lib = held
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -492,6 +492,36 @@ def test_results_do_not_change_between_calls(device):
         assert torch.equal(f(), f())
 
 
+def test_small_grid_build_gives_the_same(device):
+    """The test build sends every result past the cache and runs its grid-stride
+    loops several times: the same bits."""
+    import fp4_rollout_guided_amd as tr
+    g = _gen(device, "small grid")
+    groups, rows, n, k = 4, 1500, 272, 1056
+    off = torch.tensor([0, 700, 700, 1400, 1450], device=device)
+    sa, ca = random_record("mx8", rows, k, g, device)
+    sw, cw = random_record("mx", groups * n, k, g, device)
+    gy, gz = _bf16(rows, n, g, device), _bf16(2100, 592, g, device)
+    wm = torch.randint(0, 256, (groups * n * k // 8,), generator=g, device=device, dtype=torch.uint8)
+    sb, cb = random_record("mx", 2100, 544, g, device)
+    sv, cv = random_record("mx", 592, 544, g, device)
+    calls = [lambda: tr.grouped_mx8_matmul(sa, ca, off, sw, cw, n, k),
+             lambda: tr.mx_matmul(sb, cb, sv, cv, 592, 544), lambda: tr.mx_matmul_bwd_input(gz, sv, cv, 544),
+             lambda: tr.mx_matmul_bwd_weight(gz, sb, cb, 544),
+             lambda: tr.grouped_mx_matmul_bwd_input(gy, off, sw, cw, k),
+             lambda: tr.grouped_mx8_matmul_bwd_weight(gy, off, sa, ca, k, mask=wm)]
+    want = [f() for f in calls]
+    held = tr.lib
+    try:
+        tr.lib = tr.load_library(tr.SMALLGRID_LIB_PATH)
+        got = [f() for f in calls]
+        torch.cuda.synchronize()
+    finally:
+        tr.lib = held
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)), i
+
+
 def test_binding_refusals(device):
     """The binding turns down tensors of the wrong device, type, shape or size
     before the C ABI, which sees bare pointers, is called."""
