@@ -61,7 +61,7 @@ trace_status quantize(MxFormat fmt, const uint16_t* x, int64_t rows, int64_t col
   const Range outs[3] = {rng(scales, n / 32), rng(codes, code_bytes(fmt, n)), rng(mask, mask ? n / 8 : 0)};
   const Range ins[1] = {rng(x, 2 * n)};
   if (trace_status st = check_alias(outs, 3, ins, 1)) return st;
-  return hip_status(trace_host::launch_mx_quantize(fmt, x, n / 32, scales, codes, mask,
+  return hip_status(trace_host::launch_mx_quantize(fmt, x, n / 32, scales, codes, mask, nullptr, 0,
                                                    static_cast<hipStream_t>(stream)));
 }
 
@@ -100,7 +100,10 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
   if (need > 0) {
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + code_bytes(fmt, na);
-    if (trace_status st = hip_status(trace_host::launch_mx_quantize(fmt, x, na / 32, scales, codes, nullptr, s))) return st;
+    const int64_t* used = offsets && !row_index ? offsets + groups : nullptr;  // rows behind the last group are not read
+    if (trace_status st = hip_status(trace_host::launch_mx_quantize(fmt, x, na / 32, scales, codes, nullptr, used,
+                                                                    (uint32_t)(k / 32), s)))
+      return st;
     a_codes = codes;
     a_scales = scales;
   }

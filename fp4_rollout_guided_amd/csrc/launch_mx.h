@@ -45,9 +45,10 @@ struct MxGradArgs {
   bool stream_out = false;  // grad is past the last-level cache: the launcher's
 };
 
-// Sizes in 32-element blocks; mask may be nullptr.
+// Sizes in 32-element blocks; mask may be nullptr.  used: nullptr, or where
+// the device has how many rows of row_blocks blocks are wanted.
 hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks, uint8_t* scales, uint8_t* codes,
-                              uint8_t* mask, hipStream_t stream);
+                              uint8_t* mask, const int64_t* used, uint32_t row_blocks, hipStream_t stream);
 // Whether a product of so many rows takes bf16 activations as they are.
 bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped);
 hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& p, hipStream_t stream);

@@ -93,6 +93,22 @@ __device__ __forceinline__ uint32_t group_rows(const int64_t* __restrict__ offse
   return end > first ? (uint32_t)(end - first) : 0u;
 }
 
+// Inclusive prefix of v over the wave's 64 lanes by DPP moves (a shuffle
+// through LDS takes ten times as long, and every tile waits for this),
+// saturating: offsets that overlap could pass 32 bits.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t add_moved(uint32_t v) {
+  return __builtin_elementwise_add_sat(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
+  v = add_moved<0x111, 0xf>(v);  // one lane up within 16, then 2, 4 and 8
+  v = add_moved<0x112, 0xf>(v);
+  v = add_moved<0x114, 0xf>(v);
+  v = add_moved<0x118, 0xf>(v);
+  v = add_moved<0x142, 0xa>(v);     // lane 15 to the second 16, lane 47 to the fourth
+  return add_moved<0x143, 0xc>(v);  // lane 31 to the upper half
+}
+
 // Finds row tile `tile` (tiles of `height` rows, group by group; the rows
 // behind the last group come last).  Every lane of the wave must call it
 // with the same arguments: the wave adds up 64 groups' tiles at a time.
@@ -106,13 +122,7 @@ __device__ __forceinline__ bool find_row_tile(const int64_t* __restrict__ offset
     uint64_t first = 0;
     const uint32_t count = g <= groups ? group_rows(offsets, g, groups, rows, first) : 0u;
     const uint32_t tiles = (count + height - 1) / height;
-    // inclusive prefix over the wave's 64 groups; offsets that overlap could pass 32 bits
-    uint32_t sum = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t up = (uint32_t)__shfl_up((int)sum, d);
-      if (lane >= (uint32_t)d) sum = __builtin_elementwise_add_sat(sum, up);
-    }
+    const uint32_t sum = wave_prefix(tiles);
     const uint32_t all = (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
     if (tile < before + all) {
       const uint64_t hit = __ballot(tile < before + sum);
@@ -142,9 +152,7 @@ __device__ __forceinline__ uint64_t count_row_tiles(const int64_t* __restrict__ 
     uint64_t first;
     sum = __builtin_elementwise_add_sat(sum, (group_rows(offsets, g, groups, rows, first) + height - 1) / height);
   }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum = __builtin_elementwise_add_sat(sum, (uint32_t)__shfl_xor((int)sum, d));
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum);
+  return (uint32_t)__builtin_amdgcn_readlane((int)wave_prefix(sum), 63);
 }
 
 // Workgroups go to the 8 XCDs (each with an L2 of its own) in turn.  The

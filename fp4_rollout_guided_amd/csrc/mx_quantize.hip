@@ -23,7 +23,12 @@ template <int kFmt, bool kNT>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const uint4* __restrict__ x, uint64_t nvec,
                                                                uint8_t* __restrict__ scales,
                                                                uint8_t* __restrict__ codes,
-                                                               uint8_t* __restrict__ mask) {
+                                                               uint8_t* __restrict__ mask,
+                                                               const int64_t* __restrict__ used, uint32_t row_vecs) {
+  if (used) {  // rows from *used on are left out
+    const int64_t n = *used;
+    nvec = n <= 0 ? 0 : ((uint64_t)n >= nvec / row_vecs ? nvec : (uint64_t)n * row_vecs);
+  }
   const uint64_t stride = (uint64_t)gridDim.x * kThreads;
   for (uint64_t g = (uint64_t)blockIdx.x * kThreads + threadIdx.x; g < nvec; g += stride) {
     const uint4 v = load_vec<kNT>(&x[g]);  // nvec is a multiple of 4: a block's four lanes are active together
@@ -45,7 +50,7 @@ namespace trace_host {
 using namespace trace_dev;
 
 hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks, uint8_t* scales, uint8_t* codes,
-                              uint8_t* mask, hipStream_t stream) {
+                              uint8_t* mask, const int64_t* used, uint32_t row_blocks, hipStream_t stream) {
   if (nblocks == 0) return hipSuccess;  // an empty grid is not a valid launch
   const uint64_t nvec = 4 * nblocks;
   const uint64_t need = (nvec + kThreads - 1) / kThreads;
@@ -53,13 +58,17 @@ hipError_t launch_mx_quantize(MxFormat fmt, const uint16_t* x, uint64_t nblocks,
   const uint4* xv = reinterpret_cast<const uint4*>(x);
   const bool nt = past_cache(nblocks * 64);
   if (fmt == kE2M1 && nt)
-    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask,
+                       used, 4 * row_blocks);
   else if (fmt == kE2M1)
-    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE2M1, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask,
+                       used, 4 * row_blocks);
   else if (nt)
-    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, true>), grid, block, 0, stream, xv, nvec, scales, codes, mask,
+                       used, 4 * row_blocks);
   else
-    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask);
+    hipLaunchKernelGGL((mx_quantize_kernel<kE4M3, false>), grid, block, 0, stream, xv, nvec, scales, codes, mask,
+                       used, 4 * row_blocks);
   return hipGetLastError();
 }
 

@@ -206,6 +206,9 @@ def test_grouped_linear_on_routed_rows(device, fmt, tokens, topk, experts, n, k)
         if lo < hi:
             _check_product(fmt, y[lo:hi], a[index[lo:hi]], w[e])
     assert (y[int(off[-1]):].view(torch.int16) == 0).all()
+    packed = tr.expert_dispatch(x, index)
+    packed[int(off[-1]):] = float("nan")  # rows behind the last group are not read
+    assert torch.equal(lin(packed, off, sw, cw, n).view(torch.int16), y.view(torch.int16))
 
 
 # ---------------------------------------------------------------------------
