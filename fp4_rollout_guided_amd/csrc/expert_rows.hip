@@ -14,8 +14,11 @@
 // sums grow with the square).
 //
 // Dispatch, combine and combine's gradients move rows and are bound by
-// memory: 16 bytes per lane, every row read or written once, sums in fp32 in
-// the order of a token's pairs.
+// memory: 16 bytes per lane, sums in fp32 in the order of a token's pairs.
+// 16384 tokens of 2048, 8 experts each: dispatch 142 us (537 MB written and,
+// since a token's rows lie far apart, as much read, most of it from the
+// last-level cache: 7.5 TB/s), combine 124 us (4.9 TB/s), its gradients 238 us
+// (4.8 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -315,6 +315,13 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(trace_host::MxPr
 // W's rows 4..7 and 8..11 of every 16 trade places on the way to the
 // instruction: a lane's eight consecutive result registers are then eight
 // consecutive n, stored as 16 bytes.
+//
+// Measured: 16384 x 2048 x 4096 at 2.7 PFLOP/s (MXFP4, 100 us) and 2.0 PFLOP/s
+// (MXFP8, 138 us), the matrix units busy half of the time; 131072 rows in 128
+// groups at 2.5 (1536 x 2048) and 2.0 PFLOP/s (2048 x 768), busy a third: their
+// k is short, and a tile's first loads and its stores are not under arithmetic
+// of its own.  What holds the long products is the hand-over of stages: the
+// other workgroup of the CU fills some of each barrier's wait, not all.
 // ---------------------------------------------------------------------------
 
 // This wave's LDS accesses are done; meet the workgroup's other waves.  Loads
@@ -629,10 +636,10 @@ template <int kFmt>
 static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
   if (many_rows(p)) {
     // 128 x 256 tiles read W and A from the caches less often than 128 x 128
-    // ones (131072 x 1536 x 2048 per expert: 0.37 against 0.41 ms), where
+    // ones (131072 x 1536 x 2048 in 128 groups: 327 us against 351), where
     // there are enough of them to fill every compute unit twice.  With MXFP8
-    // activations their registers would spill (16384 x 2048 x 4096: 181
-    // against 146 us).
+    // activations their registers would spill (16384 x 2048 x 4096: 153 us
+    // against 138).
     const uint64_t tiles = (p.rows + 127) / 128 * ((p.n + 255) / 256);
     if constexpr (kFmt == kE2M1)
       if (tiles >= 512) return launch_tile<kFmt, 2, 4, 2>(p, stream);
