@@ -6,9 +6,9 @@
 //
 // W and A are the codes' values; the rounding that made them passes the
 // gradient straight through inside its clip range, so each result is zeroed
-// where its tensor's clip mask is 0.  gy is bf16 and the codes' values are
-// exact in bf16, so both run on the bf16 matrix instructions with fp32 sums,
-// rounded once.
+// where its tensor's clip mask is 0.  gy is bf16 and the codes' values from
+// 2^-130 up are exact in bf16, so both run on the bf16 matrix instructions with
+// fp32 sums, rounded once.
 //
 // Both are one kernel: D[p, k] = sum over c of G(p, c) Q[c, k], where Q's
 // codes lie row by row along k and are turned into bf16 on the way into LDS.
