@@ -375,6 +375,18 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
     const uint32_t n = 16 * (kWLoads * wave + j) + lane / 4;
     w_from[j] = (n0 + n < p.n ? n : 0) * w_pitch + 16 * piece4;  // past the last column: any row, dropped at the end
   }
+  v4i held[kWLoads + kALoads];  // a stage on its way to LDS
+  // may_end: the stage may hold fewer than 128 k; pieces past the end are zeros
+  const auto fetch_w = [&](uint32_t st, bool may_end) {
+    const uint32_t left = p.k - 128 * st;
+#pragma unroll
+    for (uint32_t j = 0; j < kWLoads; ++j) {
+      v4i v = {0, 0, 0, 0};
+      if (!may_end || 32 * piece4 < left) v = *reinterpret_cast<const v4i*>(wc + 64 * st + w_from[j]);
+      held[j] = v;
+    }
+  };
+  if (stages) fetch_w(0, false);  // k >= 512; under way while the rows' sources are read
   // source rows of packed rows m of the tile; rows past the tile's and rows
   // without a source read row 0 and are dropped or cleared at the end
   const auto packed_row = [&](uint32_t m) -> uint64_t { return t.first + (m < t.count ? m : 0); };
@@ -398,16 +410,8 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
 #pragma unroll
   for (uint32_t j = 0; j < kMF; ++j) sources |= (has_source(r_index[j]) ? 1u : 0u) << j;
 
-  v4i held[kWLoads + kALoads];  // a stage on its way to LDS
-  // may_end: the stage may hold fewer than 128 k; pieces past the end are zeros
-  const auto fetch = [&](uint32_t st, bool may_end) {
+  const auto fetch_a = [&](uint32_t st, bool may_end) {
     const uint32_t left = p.k - 128 * st;
-#pragma unroll
-    for (uint32_t j = 0; j < kWLoads; ++j) {
-      v4i v = {0, 0, 0, 0};
-      if (!may_end || 32 * piece4 < left) v = *reinterpret_cast<const v4i*>(wc + 64 * st + w_from[j]);
-      held[j] = v;
-    }
 #pragma unroll
     for (uint32_t j = 0; j < kALoads; ++j) {
       const uint32_t piece = kFp4 ? piece4 : piece8 ^ (4 * (j & 1));
@@ -504,7 +508,10 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
     __builtin_amdgcn_sched_barrier(0);
     // the other buffer is free: every wave has read stage st - 1
     if (kSteady || st + 1 < stages) place(st + 1);
-    if (kSteady || st + 2 < stages) fetch(st + 2, !kSteady);
+    if (kSteady || st + 2 < stages) {
+      fetch_w(st + 2, !kSteady);
+      fetch_a(st + 2, !kSteady);
+    }
     __builtin_amdgcn_sched_barrier(0);
     multiply(Constant<0>());
     read_step(st, 1);
@@ -518,10 +525,11 @@ __global__ __launch_bounds__(256, kPerCu) void mx_tile_kernel(trace_host::MxProd
     }
   };
   if (stages) {
-    fetch(0, true);
+    fetch_a(0, false);
     load_span(0);
     place(0);
-    if (stages > 1) fetch(1, true);
+    fetch_w(1, false);
+    fetch_a(1, false);
     store_span(0);
     lds_barrier();
   }
