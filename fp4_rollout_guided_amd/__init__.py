@@ -44,7 +44,8 @@ routed rows (the groups of the grouped_ forms):
 
     expert_sort(ids, experts)                        -> (offsets, row_index, slot)
     expert_dispatch(x, row_index)                    -> packed rows
-    expert_combine(y, slot, weights=None)            -> the tokens' weighted sums
+    expert_combine(y, slot, weights=None)            -> the tokens' weighted sums (y bf16, or fp32 from the grouped_
+                                                        products with dtype=torch.float32)
     expert_combine_bwd(grad_out, y, slot, weights, offsets=None) -> (grad_y, grad_weights)
 
 and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch`` and ``ExpertCombine``
@@ -152,6 +153,10 @@ def load_library(path):
     for name in ("quantize", "matmul", "linear_workspace_bytes", "linear", "matmul_bwd_weight"):
         sig["trace_mx8_" + name] = sig["trace_mx_" + name]
     sig["trace_grouped_mx8_matmul"] = sig["trace_grouped_mx_matmul"]
+    for name, like in (("grouped_mx_matmul", "grouped_mx_matmul"), ("grouped_mx8_matmul", "grouped_mx_matmul"),
+                       ("grouped_mx_linear", "mx_linear"), ("grouped_mx8_linear", "mx_linear"),
+                       ("grouped_mx_matmul_bwd_input", "mx_matmul_bwd_input"), ("expert_combine", "expert_combine")):
+        sig[f"trace_{name}_f32"] = sig["trace_" + like]  # the same on fp32 packed rows
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -777,9 +782,14 @@ def _launch(name, like, *args):
         raise TraceError(status, name)
 
 
-def _matrix(t, name):
-    """A contiguous bf16 device tensor as (rows, cols) over its last dimension."""
-    _bf16(t, name)
+def _matrix(t, name, dtypes=_BF16):
+    """A contiguous bf16 (or fp32) device tensor as (rows, cols) over its last dimension."""
+    if dtypes is _BF16:
+        _bf16(t, name)
+    else:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        _arg(t, name, t, dtypes, 0)
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     return math.prod(t.shape[:-1]), t.shape[-1]
@@ -810,6 +820,13 @@ def _out(t, name, like, shape, dtype):
     if t is None:
         return like.new_empty(shape, dtype=dtype)
     return _arg(t, name, like, _BF16 if dtype == torch.bfloat16 else (dtype,), n)
+
+
+def _rows_type(dtype):
+    """The suffix of the entry points for packed rows in dtype."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    return "_f32" if dtype == torch.float32 else ""
 
 
 def _workspace(t, like, need):
@@ -872,7 +889,7 @@ def _index(row_index, like):
     return row_index.numel()
 
 
-def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index, y):
+def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index, y, dtype=torch.bfloat16):
     if not isinstance(a_codes, torch.Tensor) or not a_codes.is_cuda:
         raise ValueError("a_codes must be a device tensor")
     _dim(n, "n", 16)
@@ -881,12 +898,13 @@ def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index,
     at, groups, weights = _groups(offsets, a_codes)
     _weight(w_scales, w_codes, a_codes, weights, n, k)
     rows = src_rows if row_index is None else _index(row_index, a_codes)
-    y = _out(y, "y", a_codes, (rows, n), torch.bfloat16)
+    rows_type = _rows_type(dtype)
+    y = _out(y, "y", a_codes, (rows, n), dtype)
     if offsets is None:
         _launch(f"trace_{fmt}_matmul", a_codes, _addr(a_scales), _addr(a_codes), rows, _addr(w_scales), _addr(w_codes),
                 n, k, _addr(y))
     else:
-        _launch(f"trace_grouped_{fmt}_matmul", a_codes, _addr(a_scales), _addr(a_codes), src_rows, _addr(row_index),
+        _launch(f"trace_grouped_{fmt}_matmul{rows_type}", a_codes, _addr(a_scales), _addr(a_codes), src_rows, _addr(row_index),
                 rows, at, groups, _addr(w_scales), _addr(w_codes), n, k, _addr(y))
     return y
 
@@ -902,17 +920,21 @@ def mx8_matmul(a_scales, a_codes, w_scales, w_codes, n, k, y=None):
     return _matmul("mx8", a_scales, a_codes, None, w_scales, w_codes, n, k, None, y)
 
 
-def grouped_mx_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None):
+def grouped_mx_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None,
+                      dtype=torch.bfloat16):
     """``mx_matmul`` of packed rows [offsets[g], offsets[g+1]) with the g-th of
     the weights [groups, n, k].  Packed row r is row r of the activations, or,
     with ``row_index`` (int64, one per packed row), row row_index[r].  Rows
-    behind the last group give zeros."""
-    return _matmul("mx", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y)
+    behind the last group give zeros.  dtype torch.float32: the sums as they
+    are, for rows that ``expert_combine`` sums further (in bf16 each row is
+    rounded once more on the way)."""
+    return _matmul("mx", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y, dtype)
 
 
-def grouped_mx8_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None):
+def grouped_mx8_matmul(a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index=None, y=None,
+                       dtype=torch.bfloat16):
     """``grouped_mx_matmul`` with MXFP8 activations (W4A8)."""
-    return _matmul("mx8", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y)
+    return _matmul("mx8", a_scales, a_codes, _need(offsets), w_scales, w_codes, n, k, row_index, y, dtype)
 
 
 def _need(offsets):
@@ -921,16 +943,17 @@ def _need(offsets):
     return offsets
 
 
-def _linear(fmt, x, offsets, w_scales, w_codes, n, row_index, workspace, y):
+def _linear(fmt, x, offsets, w_scales, w_codes, n, row_index, workspace, y, dtype=torch.bfloat16):
     src_rows, k = _matrix(x, "x")
     _dim(n, "n", 16)
     at, groups, weights = _groups(offsets, x)
     _weight(w_scales, w_codes, x, weights, n, k)
     rows = src_rows if row_index is None else _index(row_index, x)
     shape = (rows, n) if row_index is not None else (*x.shape[:-1], n)
-    y = _out(y, "y", x, shape, torch.bfloat16)
+    rows_type = _rows_type(dtype)
+    y = _out(y, "y", x, shape, dtype)
     workspace = _workspace(workspace, x, getattr(lib, f"trace_{fmt}_linear_workspace_bytes")(src_rows, rows, groups, k))
-    _launch(f"trace_{fmt}_linear", x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales),
+    _launch(f"trace_grouped_{fmt}_linear_f32" if rows_type else f"trace_{fmt}_linear", x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales),
             _addr(w_codes), n, k, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(y))
     return y
 
@@ -946,26 +969,27 @@ def mx8_linear(x, w_scales, w_codes, n, workspace=None, y=None):
     return _linear("mx8", x, None, w_scales, w_codes, n, None, workspace, y)
 
 
-def grouped_mx_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None):
+def grouped_mx_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None, dtype=torch.bfloat16):
     """``mx_linear`` per group of packed rows, as ``grouped_mx_matmul``: with
     ``row_index``, x holds the tokens, each rounded once for all its experts."""
-    return _linear("mx", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y)
+    return _linear("mx", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y, dtype)
 
 
-def grouped_mx8_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None):
+def grouped_mx8_linear(x, offsets, w_scales, w_codes, n, row_index=None, workspace=None, y=None, dtype=torch.bfloat16):
     """``grouped_mx_linear`` with the activations rounded to MXFP8 (W4A8)."""
-    return _linear("mx8", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y)
+    return _linear("mx8", x, _need(offsets), w_scales, w_codes, n, row_index, workspace, y, dtype)
 
 
-def _bwd_input(grad_y, offsets, w_scales, w_codes, k, mask, grad_x):
+def _bwd_input(grad_y, offsets, w_scales, w_codes, k, mask, grad_x, dtype=torch.bfloat16):
     rows, n = _matrix(grad_y, "grad_y")
     _dim(k, "k", 32)
     at, groups, weights = _groups(offsets, grad_y)
     _weight(w_scales, w_codes, grad_y, weights, n, k)
     if mask is not None:
         _arg(mask, "mask", grad_y, _U8, rows * k // 8)
-    grad_x = _out(grad_x, "grad_x", grad_y, (*grad_y.shape[:-1], k), torch.bfloat16)
-    _launch("trace_mx_matmul_bwd_input", grad_y, _addr(grad_y), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k,
+    rows_type = _rows_type(dtype)
+    grad_x = _out(grad_x, "grad_x", grad_y, (*grad_y.shape[:-1], k), dtype)
+    _launch("trace_grouped_mx_matmul_bwd_input_f32" if rows_type else "trace_mx_matmul_bwd_input", grad_y, _addr(grad_y), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k,
             _addr(mask), _addr(grad_x))
     return grad_x
 
@@ -976,10 +1000,11 @@ def mx_matmul_bwd_input(grad_y, w_scales, w_codes, k, mask=None, grad_x=None):
     return _bwd_input(grad_y, None, w_scales, w_codes, k, mask, grad_x)
 
 
-def grouped_mx_matmul_bwd_input(grad_y, offsets, w_scales, w_codes, k, mask=None, grad_x=None):
+def grouped_mx_matmul_bwd_input(grad_y, offsets, w_scales, w_codes, k, mask=None, grad_x=None, dtype=torch.bfloat16):
     """``mx_matmul_bwd_input`` per group of packed rows, in packed order (sum
-    the rows of a token with ``expert_combine``)."""
-    return _bwd_input(grad_y, _need(offsets), w_scales, w_codes, k, mask, grad_x)
+    the rows of a token with ``expert_combine``; dtype torch.float32 keeps
+    them unrounded until then)."""
+    return _bwd_input(grad_y, _need(offsets), w_scales, w_codes, k, mask, grad_x, dtype)
 
 
 def _bwd_weight(fmt, grad_y, offsets, a_scales, a_codes, k, row_index, mask, grad_w, workspace):
@@ -1072,14 +1097,15 @@ def expert_dispatch(x, row_index, out=None):
 
 def expert_combine(y, slot, weights=None, out=None):
     """The tokens' sums of their packed rows, out[t] = sum over j of
-    weights[t, j] * y[slot[t, j]] (fp32 weights; None: ones); pairs whose slot
-    lies outside y are left out."""
-    rows, cols = _matrix(y, "y")
+    weights[t, j] * y[slot[t, j]] (fp32 weights; None: ones; y in bf16 or
+    fp32, out in bf16); pairs whose slot lies outside y are left out."""
+    f32 = isinstance(y, torch.Tensor) and y.dtype == torch.float32
+    rows, cols = _matrix(y, "y", _F32 if f32 else _BF16)
     tokens, topk = _pairs(slot, "slot", y, _I64)
     if weights is not None:
         _fit(weights, "weights", y, _F32, tokens * topk)
     out = _out(out, "out", y, (tokens, cols), torch.bfloat16)
-    _launch("trace_expert_combine", y, _addr(y), rows, cols, _addr(slot), _addr(weights), tokens, topk, _addr(out))
+    _launch("trace_expert_combine_f32" if f32 else "trace_expert_combine", y, _addr(y), rows, cols, _addr(slot), _addr(weights), tokens, topk, _addr(out))
     return out
 
 
@@ -1166,7 +1192,7 @@ class ExpertCombine(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, y, slot, weights, offsets):
-        y, weights = y.contiguous(), weights.contiguous()
+        y, weights = _bf16(y.contiguous(), "y"), weights.contiguous()  # the gradients' type too
         ctx.save_for_backward(y, slot, weights, offsets)
         return expert_combine(y, slot, weights)
 

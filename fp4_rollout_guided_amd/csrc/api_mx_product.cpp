@@ -70,7 +70,7 @@ trace_status quantize(MxFormat fmt, const uint16_t* x, int64_t rows, int64_t col
 trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t workspace_bytes,
                      const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows, const int64_t* row_index,
                      int64_t rows, const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
-                     const uint8_t* w_codes, int64_t n, int64_t k, bool linear, uint16_t* y, void* stream) {
+                     const uint8_t* w_codes, int64_t n, int64_t k, bool linear, void* y, bool f32, void* stream) {
   int64_t weights = 0;
   if (trace_status st = product_groups(offsets, groups, &weights)) return st;
   if (trace_status st = product_sizes(src_rows, rows, weights, n, k)) return st;
@@ -87,7 +87,7 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
   if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 16) ||
       !aligned(row_index, 8))
     return TRACE_E_ALIGN;
-  const Range outs[2] = {rng(y, 2 * ny), rng(workspace, need)};
+  const Range outs[2] = {rng(y, (f32 ? 4 : 2) * ny), rng(workspace, need)};
   const Range ins[7] = {rng(x, x ? 2 * na : 0),
                         rng(a_scales, a_scales ? na / 32 : 0),
                         rng(a_codes, a_codes ? code_bytes(fmt, na) : 0),
@@ -109,13 +109,13 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
   }
   const bool rounds = linear && trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0);
   const trace_host::MxProductArgs p{rounds ? x : nullptr, a_codes, a_scales, row_index, (uint64_t)src_rows, (uint64_t)rows,
-                                    offsets, (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y};
+                                    offsets, (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y, f32};
   return launch_status(trace_host::launch_mx_product(fmt, p, s));
 }
 
 trace_status grad_input(const uint16_t* grad_y, int64_t rows, const int64_t* offsets, int64_t groups,
                         const uint8_t* w_scales, const uint8_t* w_codes, int64_t n, int64_t k, const uint8_t* mask,
-                        uint16_t* grad_x, void* stream) {
+                        void* grad_x, bool f32, void* stream) {
   int64_t weights = 0;
   if (trace_status st = product_groups(offsets, groups, &weights)) return st;
   if (trace_status st = product_sizes(rows, rows, weights, n, k)) return st;
@@ -124,12 +124,12 @@ trace_status grad_input(const uint16_t* grad_y, int64_t rows, const int64_t* off
   const uint64_t ny = (uint64_t)rows * (uint64_t)n, nx = (uint64_t)rows * (uint64_t)k;
   if (!grad_x || (n > 0 && (!grad_y || !w_scales || !w_codes))) return TRACE_E_NULL;
   if (!aligned(grad_y, 16) || !aligned(w_codes, 16) || !aligned(grad_x, 16) || !aligned(mask, 2)) return TRACE_E_ALIGN;
-  const Range outs[1] = {rng(grad_x, 2 * nx)};
+  const Range outs[1] = {rng(grad_x, (f32 ? 4 : 2) * nx)};
   const Range ins[5] = {rng(grad_y, 2 * ny), rng(w_scales, nw / 32), rng(w_codes, nw / 2),
                         rng(mask, mask ? nx / 8 : 0), rng(offsets, offsets ? 8 * ((uint64_t)weights + 1) : 0)};
   if (trace_status st = check_alias(outs, 1, ins, 5)) return st;
   const trace_host::MxGradArgs p{grad_y, (uint64_t)rows, offsets, (uint32_t)weights, w_codes, w_scales, nullptr,
-                                 (uint64_t)rows, (uint32_t)n, (uint32_t)k, mask, grad_x, nullptr};
+                                 (uint64_t)rows, (uint32_t)n, (uint32_t)k, mask, grad_x, f32, nullptr};
   return launch_status(trace_host::launch_mx_grad_input(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -168,7 +168,7 @@ trace_status grad_weight(MxFormat fmt, const uint16_t* grad_y, int64_t rows, con
                         rng(offsets, offsets ? 8 * ((uint64_t)weights + 1) : 0)};
   if (trace_status st = check_alias(outs, 2, ins, 6)) return st;
   const trace_host::MxGradArgs p{grad_y, (uint64_t)rows, offsets, (uint32_t)weights, a_codes, a_scales, row_index,
-                                 (uint64_t)src_rows, (uint32_t)n, (uint32_t)k, mask, grad_w,
+                                 (uint64_t)src_rows, (uint32_t)n, (uint32_t)k, mask, grad_w, false,
                                  static_cast<float*>(workspace)};
   return launch_status(trace_host::launch_mx_grad_weight(fmt, p, static_cast<hipStream_t>(stream)));
 }
@@ -193,13 +193,13 @@ trace_status trace_mx8_quantize(const uint16_t* x, int64_t rows, int64_t cols, u
 trace_status trace_mx_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t rows, const uint8_t* w_scales,
                              const uint8_t* w_codes, int64_t n, int64_t k, uint16_t* y, void* stream) {
   return product(kE2M1, nullptr, nullptr, 0, a_scales, a_codes, rows, nullptr, rows, nullptr, 0, w_scales, w_codes, n,
-                 k, false, y, stream);
+                 k, false, y, false, stream);
 }
 
 trace_status trace_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t rows, const uint8_t* w_scales,
                               const uint8_t* w_codes, int64_t n, int64_t k, uint16_t* y, void* stream) {
   return product(kE4M3, nullptr, nullptr, 0, a_scales, a_codes, rows, nullptr, rows, nullptr, 0, w_scales, w_codes, n,
-                 k, false, y, stream);
+                 k, false, y, false, stream);
 }
 
 trace_status trace_grouped_mx_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
@@ -208,7 +208,7 @@ trace_status trace_grouped_mx_matmul(const uint8_t* a_scales, const uint8_t* a_c
                                      void* stream) {
   if (!offsets) return TRACE_E_NULL;
   return product(kE2M1, nullptr, nullptr, 0, a_scales, a_codes, src_rows, row_index, rows, offsets, groups, w_scales,
-                 w_codes, n, k, false, y, stream);
+                 w_codes, n, k, false, y, false, stream);
 }
 
 trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
@@ -217,7 +217,7 @@ trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const uint8_t* a_
                                       uint16_t* y, void* stream) {
   if (!offsets) return TRACE_E_NULL;
   return product(kE4M3, nullptr, nullptr, 0, a_scales, a_codes, src_rows, row_index, rows, offsets, groups, w_scales,
-                 w_codes, n, k, false, y, stream);
+                 w_codes, n, k, false, y, false, stream);
 }
 
 size_t trace_mx_linear_workspace_bytes(int64_t src_rows, int64_t rows, int64_t groups, int64_t k) {
@@ -233,7 +233,7 @@ trace_status trace_mx_linear(const uint16_t* x, int64_t src_rows, const int64_t*
                              int64_t n, int64_t k, void* workspace, size_t workspace_bytes, uint16_t* y,
                              void* stream) {
   return product(kE2M1, x, workspace, workspace_bytes, nullptr, nullptr, src_rows, row_index, rows, offsets, groups,
-                 w_scales, w_codes, n, k, true, y, stream);
+                 w_scales, w_codes, n, k, true, y, false, stream);
 }
 
 trace_status trace_mx8_linear(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
@@ -241,13 +241,57 @@ trace_status trace_mx8_linear(const uint16_t* x, int64_t src_rows, const int64_t
                               int64_t n, int64_t k, void* workspace, size_t workspace_bytes, uint16_t* y,
                               void* stream) {
   return product(kE4M3, x, workspace, workspace_bytes, nullptr, nullptr, src_rows, row_index, rows, offsets, groups,
-                 w_scales, w_codes, n, k, true, y, stream);
+                 w_scales, w_codes, n, k, true, y, false, stream);
+}
+
+trace_status trace_grouped_mx_matmul_f32(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                         const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                         int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes, int64_t n,
+                                         int64_t k, float* y, void* stream) {
+  if (!offsets) return TRACE_E_NULL;
+  return product(kE2M1, nullptr, nullptr, 0, a_scales, a_codes, src_rows, row_index, rows, offsets, groups, w_scales,
+                 w_codes, n, k, false, y, true, stream);
+}
+
+trace_status trace_grouped_mx_linear_f32(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
+                                         const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
+                                         const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,
+                                         size_t workspace_bytes, float* y, void* stream) {
+  if (!offsets) return TRACE_E_NULL;
+  return product(kE2M1, x, workspace, workspace_bytes, nullptr, nullptr, src_rows, row_index, rows, offsets, groups,
+                 w_scales, w_codes, n, k, true, y, true, stream);
+}
+
+trace_status trace_grouped_mx8_matmul_f32(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                          const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                          int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes, int64_t n,
+                                          int64_t k, float* y, void* stream) {
+  if (!offsets) return TRACE_E_NULL;
+  return product(kE4M3, nullptr, nullptr, 0, a_scales, a_codes, src_rows, row_index, rows, offsets, groups, w_scales,
+                 w_codes, n, k, false, y, true, stream);
+}
+
+trace_status trace_grouped_mx8_linear_f32(const uint16_t* x, int64_t src_rows, const int64_t* row_index, int64_t rows,
+                                          const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
+                                          const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,
+                                          size_t workspace_bytes, float* y, void* stream) {
+  if (!offsets) return TRACE_E_NULL;
+  return product(kE4M3, x, workspace, workspace_bytes, nullptr, nullptr, src_rows, row_index, rows, offsets, groups,
+                 w_scales, w_codes, n, k, true, y, true, stream);
 }
 
 trace_status trace_mx_matmul_bwd_input(const uint16_t* grad_y, int64_t rows, const int64_t* offsets, int64_t groups,
                                        const uint8_t* w_scales, const uint8_t* w_codes, int64_t n, int64_t k,
                                        const uint8_t* mask, uint16_t* grad_x, void* stream) {
-  return grad_input(grad_y, rows, offsets, groups, w_scales, w_codes, n, k, mask, grad_x, stream);
+  return grad_input(grad_y, rows, offsets, groups, w_scales, w_codes, n, k, mask, grad_x, false, stream);
+}
+
+trace_status trace_grouped_mx_matmul_bwd_input_f32(const uint16_t* grad_y, int64_t rows, const int64_t* offsets,
+                                                   int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                                   int64_t n, int64_t k, const uint8_t* mask, float* grad_x,
+                                                   void* stream) {
+  if (!offsets) return TRACE_E_NULL;
+  return grad_input(grad_y, rows, offsets, groups, w_scales, w_codes, n, k, mask, grad_x, true, stream);
 }
 
 size_t trace_mx_matmul_bwd_weight_workspace_bytes(int64_t rows, int64_t groups, int64_t n, int64_t k) {
@@ -319,8 +363,8 @@ trace_status trace_expert_dispatch(const uint16_t* x, int64_t tokens, int64_t co
                                                        out, static_cast<hipStream_t>(stream)));
 }
 
-trace_status trace_expert_combine(const uint16_t* y, int64_t rows, int64_t cols, const int64_t* slot,
-                                  const float* weights, int64_t tokens, int64_t topk, uint16_t* out, void* stream) {
+static trace_status combine(const void* y, bool f32, int64_t rows, int64_t cols, const int64_t* slot, const float* weights,
+                            int64_t tokens, int64_t topk, uint16_t* out, void* stream) {
   uint64_t ny = 0, n = 0;
   if (trace_status st = site_size(rows, cols, &ny)) return st;
   if (trace_status st = site_size(tokens, cols, &n)) return st;
@@ -330,11 +374,22 @@ trace_status trace_expert_combine(const uint16_t* y, int64_t rows, int64_t cols,
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(slot, 8) || !aligned(weights, 4)) return TRACE_E_ALIGN;
   const uint64_t pairs = (uint64_t)(tokens * topk);
   const Range outs[1] = {rng(out, 2 * n)};
-  const Range ins[3] = {rng(y, 2 * ny), rng(slot, 8 * pairs), rng(weights, weights ? 4 * pairs : 0)};
+  const Range ins[3] = {rng(y, (f32 ? 4 : 2) * ny), rng(slot, 8 * pairs), rng(weights, weights ? 4 * pairs : 0)};
   if (trace_status st = check_alias(outs, 1, ins, 3)) return st;
-  return hip_status(trace_host::launch_expert_combine(y, (uint64_t)rows, (uint64_t)cols, slot, weights,
+  return hip_status(trace_host::launch_expert_combine(y, f32, (uint64_t)rows, (uint64_t)cols, slot, weights,
                                                       (uint64_t)tokens, (uint32_t)topk, out,
                                                       static_cast<hipStream_t>(stream)));
+}
+
+trace_status trace_expert_combine(const uint16_t* y, int64_t rows, int64_t cols, const int64_t* slot,
+                                  const float* weights, int64_t tokens, int64_t topk, uint16_t* out, void* stream) {
+  return combine(y, false, rows, cols, slot, weights, tokens, topk, out, stream);
+}
+
+trace_status trace_expert_combine_f32(const float* y, int64_t rows, int64_t cols, const int64_t* slot,
+                                      const float* weights, int64_t tokens, int64_t topk, uint16_t* out,
+                                      void* stream) {
+  return combine(y, true, rows, cols, slot, weights, tokens, topk, out, stream);
 }
 
 trace_status trace_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t rows, int64_t cols,

@@ -248,11 +248,18 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], const uint4& v, floa
   }
 }
 
+__device__ __forceinline__ void add_scaled(float (&acc)[8], const uint4& lo, const uint4& hi, float w) {
+  const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, __uint_as_float(u[i]), acc[i]);
+}
+
 // out[t] = sum over j of weights[t][j] * y[slot[t][j]] in fp32, j ascending;
-// slots outside [0, rows) are left out.  One lane per 8-element vector.  kNT: y
+// slots outside [0, rows) are left out.  One lane per 8-element vector, of y in
+// bf16 or (kF32) fp32.  kNT: y
 // is past the last-level cache (131072 rows of 2048, half of them named: 40 us
 // against 62).
-template <bool kNT>
+template <bool kF32, bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* __restrict__ y, uint64_t rows,
                                                                   uint32_t row_vecs, const int64_t* __restrict__ slot,
                                                                   const float* __restrict__ weights, uint32_t topk,
@@ -266,7 +273,13 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
     for (uint32_t j = 0; j < topk; ++j) {
       const int64_t s = slot[t * topk + j];
       const float w = weights ? weights[t * topk + j] : 1.f;
-      if (s >= 0 && s < (int64_t)rows) add_scaled(acc, load_vec<kNT>(&y[(uint64_t)s * row_vecs + c]), w);
+      if (s >= 0 && s < (int64_t)rows) {
+        const uint64_t at = (uint64_t)s * row_vecs + c;
+        if constexpr (kF32)
+          add_scaled(acc, load_vec<kNT>(&y[2 * at]), load_vec<kNT>(&y[2 * at + 1]), w);
+        else
+          add_scaled(acc, load_vec<kNT>(&y[at]), w);
+      }
     }
     out[g] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
                         pack_bf16(acc[6], acc[7]));
@@ -395,13 +408,15 @@ hipError_t launch_expert_dispatch(const uint16_t* x, uint64_t tokens, uint64_t c
   return hipGetLastError();
 }
 
-hipError_t launch_expert_combine(const uint16_t* y, uint64_t rows, uint64_t cols, const int64_t* slot,
+hipError_t launch_expert_combine(const void* y, bool f32, uint64_t rows, uint64_t cols, const int64_t* slot,
                                  const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
                                  hipStream_t stream) {
   const uint64_t nvec = tokens * (cols / 8);
-  const auto kernel = past_cache(2 * rows * cols) ? expert_combine_kernel<true> : expert_combine_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, reinterpret_cast<const uint4*>(y), rows, (uint32_t)(cols / 8), slot, weights, topk, nvec,
-                     reinterpret_cast<uint4*>(out));
+  const bool nt = past_cache((f32 ? 4 : 2) * rows * cols);
+  const auto kernel = f32 ? (nt ? expert_combine_kernel<true, true> : expert_combine_kernel<true, false>)
+                          : (nt ? expert_combine_kernel<false, true> : expert_combine_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, static_cast<const uint4*>(y),
+                     rows, (uint32_t)(cols / 8), slot, weights, topk, nvec, reinterpret_cast<uint4*>(out));
   return hipGetLastError();
 }
 

@@ -24,7 +24,8 @@ struct MxProductArgs {
   const uint8_t* w_codes;   // [groups, n, k]
   const uint8_t* w_scales;  // [groups, n, k / 32]
   uint32_t n, k;
-  uint16_t* y;  // [rows, n]
+  void* y;   // [rows, n] in bf16, or
+  bool f32;  // in fp32 (grouped products)
   bool stream_out = false;  // y is past the last-level cache: the launcher's
 };
 
@@ -40,7 +41,8 @@ struct MxGradArgs {
   uint64_t src_rows;
   uint32_t n, k;
   const uint8_t* mask;  // clip mask of the gradient's own tensor, or nullptr
-  uint16_t* grad;       // [rows, k], or [groups, n, k]
+  void* grad;           // [rows, k], or [groups, n, k], in bf16, or
+  bool f32;             // in fp32 (grouped, to the activations)
   float* partial;       // workspace of the split contraction, or nullptr
   bool stream_out = false;  // grad is past the last-level cache: the launcher's
 };
@@ -67,7 +69,8 @@ hipError_t launch_expert_sort(const int64_t* ids, uint64_t pairs, uint32_t topk,
                               int64_t* offsets, int64_t* row_index, int64_t* slot, hipStream_t stream);
 hipError_t launch_expert_dispatch(const uint16_t* x, uint64_t tokens, uint64_t cols, const int64_t* row_index,
                                   uint64_t rows, uint16_t* out, hipStream_t stream);
-hipError_t launch_expert_combine(const uint16_t* y, uint64_t rows, uint64_t cols, const int64_t* slot,
+// y: bf16, or fp32 where f32.
+hipError_t launch_expert_combine(const void* y, bool f32, uint64_t rows, uint64_t cols, const int64_t* slot,
                                  const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
                                  hipStream_t stream);
 hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, uint64_t rows, uint64_t cols,

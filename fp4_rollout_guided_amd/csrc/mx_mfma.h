@@ -59,11 +59,19 @@ struct RowBlock {
   }
 };
 
+// Eight consecutive results of a row in fp32: pieces `piece` and the next.
+__device__ __forceinline__ void put_f32(const RowBlock<16>& block, uint32_t row, uint32_t piece, const float (&v)[8]) {
+  uint4 u[2];
+  __builtin_memcpy(u, v, sizeof(u));
+  block.put(row, piece, u[0]);
+  block.put(row, piece + 1, u[1]);
+}
+
 // 16 bytes of a result.  One larger than the last-level cache (past_cache)
 // goes past it, since its reader will not find it there: the weights' gradient
 // of 128 x 1536 x 2048, 805 MB, took 494 us against 570, the product's 537 MB
 // of 131072 x 2048 x 768 205 against 265.
-__device__ __forceinline__ void store_result(uint16_t* at, uint4 v, bool stream) {
+__device__ __forceinline__ void store_result(void* at, uint4 v, bool stream) {
   if (stream)
     store_vec<true>(reinterpret_cast<uint4*>(at), v);
   else

@@ -86,9 +86,10 @@ __device__ __forceinline__ v8bf transposed(const char* at, uint32_t pitch) {
 // multiple of 256 apart, so that the four rows that 32 lanes read transposed
 // lie in different banks.  gy is [c][p] likewise for gw; for gx it is [p][c]
 // with its pieces permuted by the row's bits.
+// kF32: results in fp32 (gx of packed rows, which are summed further).
 // parts > 1 (kWeight, one group only): the contraction's part blockIdx.y, as
 // fp32 to p.partial.
-template <bool kWeight, int kFmt, bool kGather, int kKF, int kPF, int kPerCu>
+template <bool kWeight, int kFmt, bool kGather, bool kF32, int kKF, int kPF, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGradArgs p, uint32_t k_tiles,
                                                               uint32_t p_tiles, uint32_t parts) {
   constexpr bool kFp4 = kFmt == trace_host::kE2M1;
@@ -337,6 +338,31 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
     return;
   }
   // every wave has passed the barrier after its last LDS read
+  if constexpr (kF32) {  // 64 columns at a time
+    const RowBlock<16> block{q_buf[0] + 512 * 16 * wave};
+    static_assert(4 * 512 * 16 <= 2 * kQBytes && kKF % 2 == 0 && !kWeight, "four waves' blocks fit the tiles' buffers");
+#pragma unroll
+    for (int b = 0; b < kPF; ++b) {
+#pragma unroll
+      for (int a0 = 0; a0 < kKF; a0 += 2) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            const uint32_t bits = keep[b][a0 + a] >> (2 * e + 8 * h);
+            float v[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) v[d] = (bits >> d) & 1 ? acc[a0 + a][b][e + d] : 0.f;
+            put_f32(block, r, 8 * a + e / 2 + 2 * h, v);
+          }
+        block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+          const uint32_t pp = wp + 32 * b + row, k = k0 + wk + 32 * a0 + 4 * piece;
+          if (k < p.k && pp < t.count) store_result(static_cast<float*>(p.grad) + (t.first + pp) * p.k + k, v, p.stream_out);
+        });
+      }
+    }
+    return;
+  }
   const RowBlock<4 * kKF> block{q_buf[0] + 512 * 4 * kKF * wave};
   static_assert(4 * 512 * 4 * kKF <= 2 * kQBytes, "four waves' blocks fit the tiles' buffers");
 #pragma unroll
@@ -360,7 +386,7 @@ __global__ __launch_bounds__(256, kPerCu) void mx_grad_kernel(trace_host::MxGrad
       const uint32_t pp = wp + 32 * b + row, k = k0 + wk + 8 * piece;
       if (k < p.k && (kWeight ? p0 + pp < p.n : pp < t.count)) {
         const uint64_t to = kWeight ? (uint64_t)t.group * p.n + p0 + pp : t.first + pp;
-        store_result(p.grad + to * p.k + k, v, p.stream_out);
+        store_result(static_cast<uint16_t*>(p.grad) + to * p.k + k, v, p.stream_out);
       }
     });
   }
@@ -401,21 +427,22 @@ using namespace trace_dev;
 // against 393 in tiles of 64 x 128).
 static bool big_tiles(uint64_t p, uint32_t k) { return (p + 127) / 128 * ((k + 255) / 256) >= 512; }
 
-template <int kKF, int kPF, int kPerCu>
+template <bool kF32, int kKF, int kPF, int kPerCu>
 static hipError_t grad_input(const MxGradArgs& p, hipStream_t stream) {
   const uint32_t k_tiles = (p.k + 64 * kKF - 1) / (64 * kKF);
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 64 * kPF) : (p.rows + 64 * kPF - 1) / (64 * kPF);
   const uint64_t grid = (row_tiles * k_tiles + 7) / 8 * 8;
   if (grid * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((mx_grad_kernel<false, kE2M1, false, kKF, kPF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream,
+  hipLaunchKernelGGL((mx_grad_kernel<false, kE2M1, false, kF32, kKF, kPF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream,
                      p, k_tiles, 1u, 1u);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_grad_input(const MxGradArgs& args, hipStream_t stream) {
   MxGradArgs p = args;
-  p.stream_out = past_cache(2 * p.rows * p.k);
-  return big_tiles(p.rows, p.k) ? grad_input<4, 2, 2>(p, stream) : grad_input<2, 1, 2>(p, stream);
+  p.stream_out = past_cache((p.f32 ? 4 : 2) * p.rows * p.k);
+  if (p.f32) return big_tiles(p.rows, p.k) ? grad_input<true, 4, 2, 2>(p, stream) : grad_input<true, 2, 1, 2>(p, stream);
+  return big_tiles(p.rows, p.k) ? grad_input<false, 4, 2, 2>(p, stream) : grad_input<false, 2, 1, 2>(p, stream);
 }
 
 // Tiles and parts of a weight's gradient.  Tiles of 128 x 256 where, with the
@@ -452,9 +479,9 @@ static hipError_t grad_weight(const MxGradArgs& p, uint32_t parts, hipStream_t s
   if (tiles * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)tiles, parts), block(256);
   if (p.row_index)
-    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, true, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
+    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, true, false, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
   else
-    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, false, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
+    hipLaunchKernelGGL((mx_grad_kernel<true, kFmt, false, false, kKF, kPF, kPerCu>), grid, block, 0, stream, p, k_tiles, p_tiles, parts);
   return hipGetLastError();
 }
 
@@ -467,7 +494,7 @@ static hipError_t grad_weight(const MxGradArgs& p, hipStream_t stream) {
   const uint64_t nvec = (uint64_t)p.n * p.k / 8;
   const uint64_t g = (nvec + kThreads - 1) / kThreads;
   hipLaunchKernelGGL(mx_grad_join_kernel, dim3((unsigned)(g < kMaxGroups ? g : kMaxGroups)), dim3(kThreads), 0, stream,
-                     p.partial, parts, nvec, p.mask, reinterpret_cast<uint4*>(p.grad));
+                     p.partial, parts, nvec, p.mask, static_cast<uint4*>(p.grad));
   return hipGetLastError();
 }
 

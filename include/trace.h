@@ -591,6 +591,18 @@ TRACE_API trace_status trace_grouped_mx8_matmul(const uint8_t* a_scales, const u
                                                 int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
                                                 int64_t n, int64_t k, uint16_t* y, void* stream);
 
+/* Grouped products with their sums left in fp32, y : fp32[rows*n], 16-byte
+ * aligned, for packed rows that trace_expert_combine_f32 sums further: bf16
+ * rows are each rounded once more on the way (by up to 2^-8 of their size). */
+TRACE_API trace_status trace_grouped_mx_matmul_f32(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                                   const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                                   int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                                   int64_t n, int64_t k, float* y, void* stream);
+TRACE_API trace_status trace_grouped_mx8_matmul_f32(const uint8_t* a_scales, const uint8_t* a_codes, int64_t src_rows,
+                                                    const int64_t* row_index, int64_t rows, const int64_t* offsets,
+                                                    int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
+                                                    int64_t n, int64_t k, float* y, void* stream);
+
 /* The product on bf16 activations x [src_rows, k]: trace_mx_quantize (mx8:
  * trace_mx8_quantize) followed by the product, with the same result.  The
  * ungrouped forms take offsets = row_index = NULL, groups = 0 and
@@ -609,6 +621,17 @@ TRACE_API trace_status trace_mx8_linear(const uint16_t* x, int64_t src_rows, con
                                         const int64_t* offsets, int64_t groups, const uint8_t* w_scales,
                                         const uint8_t* w_codes, int64_t n, int64_t k, void* workspace,
                                         size_t workspace_bytes, uint16_t* y, void* stream);
+/* The grouped forms with y : fp32[rows*n] (16-byte aligned). */
+TRACE_API trace_status trace_grouped_mx_linear_f32(const uint16_t* x, int64_t src_rows, const int64_t* row_index,
+                                                   int64_t rows, const int64_t* offsets, int64_t groups,
+                                                   const uint8_t* w_scales, const uint8_t* w_codes, int64_t n,
+                                                   int64_t k, void* workspace, size_t workspace_bytes, float* y,
+                                                   void* stream);
+TRACE_API trace_status trace_grouped_mx8_linear_f32(const uint16_t* x, int64_t src_rows, const int64_t* row_index,
+                                                    int64_t rows, const int64_t* offsets, int64_t groups,
+                                                    const uint8_t* w_scales, const uint8_t* w_codes, int64_t n,
+                                                    int64_t k, void* workspace, size_t workspace_bytes, float* y,
+                                                    void* stream);
 
 /* Gradient of the product to the activations, grad_x = (grad_y W) where mask
  * is 1 and +0 elsewhere (the straight-through estimator of A's rounding):
@@ -619,6 +642,13 @@ TRACE_API trace_status trace_mx_matmul_bwd_input(const uint16_t* grad_y, int64_t
                                                  int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
                                                  int64_t n, int64_t k, const uint8_t* mask, uint16_t* grad_x,
                                                  void* stream);
+/* The grouped form with grad_x : fp32[rows*k] (16-byte aligned), for rows that
+ * trace_expert_combine_f32 sums to the tokens. */
+TRACE_API trace_status trace_grouped_mx_matmul_bwd_input_f32(const uint16_t* grad_y, int64_t rows,
+                                                             const int64_t* offsets, int64_t groups,
+                                                             const uint8_t* w_scales, const uint8_t* w_codes,
+                                                             int64_t n, int64_t k, const uint8_t* mask, float* grad_x,
+                                                             void* stream);
 
 /* Gradient of the product to the weight(s), grad_w = (grad_y^T A) where mask
  * is 1 and +0 elsewhere (the straight-through estimator of W's rounding):
@@ -677,6 +707,10 @@ TRACE_API trace_status trace_expert_dispatch(const uint16_t* x, int64_t tokens, 
 TRACE_API trace_status trace_expert_combine(const uint16_t* y, int64_t rows, int64_t cols, const int64_t* slot,
                                             const float* weights, int64_t tokens, int64_t topk, uint16_t* out,
                                             void* stream);
+/* The same on y : fp32[rows*cols] (16-byte aligned). */
+TRACE_API trace_status trace_expert_combine_f32(const float* y, int64_t rows, int64_t cols, const int64_t* slot,
+                                                const float* weights, int64_t tokens, int64_t topk, uint16_t* out,
+                                                void* stream);
 
 /* Gradients of trace_expert_combine:
  *   grad_y[slot[t][j]] = bf16_RNE(weights[t][j] * grad_out[t]),
