@@ -335,10 +335,11 @@ def _calls(s):
         return out | {"y": linear(s["x"], offsets, s["w_scales"], s["w_codes"], n, row_index=row_index)}
     if kind == "down":
         linear = tr.grouped_mx_linear if mx else tr.grouped_mx8_linear
-        y = linear(s["x"], s["offsets"], s["w_scales"], s["w_codes"], n)
+        y = linear(s["x"], s["offsets"], s["w_scales"], s["w_codes"], n, dtype=torch.float32)
         return {"out": tr.expert_combine(y, s["slot"], s["weights"])}
     if kind == "up_bwd":
-        gr = tr.grouped_mx_matmul_bwd_input(s["grad_y"], s["offsets"], s["w_scales"], s["w_codes"], k)
+        gr = tr.grouped_mx_matmul_bwd_input(s["grad_y"], s["offsets"], s["w_scales"], s["w_codes"], k,
+                                            dtype=torch.float32)
         gx = tr.ste_bwd(tr.expert_combine(gr, s["slot"]), s["mask"])
         bwd_weight = tr.grouped_mx_matmul_bwd_weight if mx else tr.grouped_mx8_matmul_bwd_weight
         gw = bwd_weight(s["grad_y"], s["offsets"], s["a_scales"], s["a_codes"], k, row_index=s["row_index"],
