@@ -1,0 +1,212 @@
+"""The microscaled products and their gradients past the sizes and values of
+test_gpu_mx_product.py: contractions that a wave of the few-row kernels walks
+in several turns, every tile of groups of few rows, rounded tokens against the
+same tokens rounded first, and the ends of the scale and code ranges.
+
+Sums are fp32 (product_util.close); an MXFP8 product's terms are cut as
+described at CUT."""
+import sys
+import zlib
+
+import pytest
+import torch
+
+from tests.product_util import close, groups_of, random_record, values
+
+pytestmark = pytest.mark.gpu
+
+# The matrix instruction cuts the products of eight neighbouring k of an MXFP8
+# operand to multiples of 2^-13 of the largest one's power of two: seven terms,
+# each off by less than 2^-13 of a term.
+CUT = {"mx": 0.0, "mx8": 7 * 2.0 ** -13}
+
+
+def _say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def _gen(device, *key):
+    g = torch.Generator(device=device)
+    g.manual_seed(zlib.crc32(repr(key).encode()))
+    return g
+
+
+def _bf16(rows, cols, g, dev, scale=1.0):
+    return (torch.randn(rows, cols, generator=g, device=dev) * scale).to(torch.bfloat16)
+
+
+def _check(fmt, y, a, w):
+    want, size = a @ w.T.contiguous(), a.abs() @ w.abs().T.contiguous()
+    close(y, want, size, 1, product=a.shape[1] * 2.0 ** -24 + CUT[fmt])
+
+
+def _ops(fmt):
+    import fp4_rollout_guided_amd as tr
+    if fmt == "mx":
+        return tr.mx_quantize, tr.mx_matmul, tr.mx_linear, tr.grouped_mx_matmul, tr.mx_matmul_bwd_weight
+    return tr.mx8_quantize, tr.mx8_matmul, tr.mx8_linear, tr.grouped_mx8_matmul, tr.mx8_matmul_bwd_weight
+
+
+# ---------------------------------------------------------------------------
+# long contractions, every tile
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", [(1, 2048, 7168), (2, 528, 7200), (3, 64, 8224), (16, 4112, 4128), (37, 2048, 7168),
+                                      (100, 2048, 4096), (130, 1040, 4128), (300, 1024, 4128), (1, 64, 16384)])
+def test_matmul_of_long_rows(device, fmt, rows, n, k):
+    _say("case long", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "long")
+    sa, ca = random_record(fmt, rows, k, g, device)
+    sw, cw = random_record("mx", n, k, g, device)
+    y = _ops(fmt)[1](sa, ca, sw, cw, n, k)
+    _check(fmt, y, values(fmt, sa, ca, k), values("mx", sw, cw, k))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("groups,each,n,k", [(4, 5, 64, 4128), (4, 25, 64, 4128), (7, 12, 112, 2080), (64, 20, 1040, 160),
+                                             (64, 20, 1040, 1056), (100, 9, 176, 4128), (3, 31, 48, 8224)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_matmul_of_few_rows_each(device, fmt, groups, each, n, k, gather):
+    _say("case few rows each", fmt, groups, each, n, k, gather)
+    g = _gen(device, fmt, groups, each, n, k, gather)
+    rows = groups * each
+    cuts = torch.randint(0, rows + 1, (groups - 1,), generator=g, device=device).sort().values
+    off = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), rows)])
+    src = rows // 3 + 1 if gather else rows
+    sa, ca = random_record(fmt, src, k, g, device)
+    sw, cw = random_record("mx", groups * n, k, g, device)
+    index = torch.randint(-1, src + 1, (rows,), generator=g, device=device) if gather else None
+    y = _ops(fmt)[3](sa, ca, off, sw, cw, n, k, row_index=index)
+    a, w = values(fmt, sa, ca, k), values("mx", sw, cw, k).view(groups, n, k)
+    if gather:
+        a = a[index.clamp(0, src - 1)] * ((index >= 0) & (index < src)).unsqueeze(1)
+    for e, (lo, hi) in enumerate(groups_of(off, rows)):
+        if lo < hi:
+            _check(fmt, y[lo:hi], a[lo:hi], w[e])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", [(1, 16, 32), (1, 48, 160), (1, 2048, 4096), (1, 1024, 7168), (1, 96, 16384), (2, 4112, 8192),
+                                      (5, 272, 1056), (16, 528, 1024), (16, 80, 992), (17, 80, 992), (40, 1040, 2080)])
+def test_linear_against_its_own_rounding(device, fmt, rows, n, k):
+    """Every row of the product that rounds its tokens: finite ones, the last
+    one, and, in a row of their own, a NaN and an infinity, whose codes are
+    +0 and the largest magnitude of a block of zeros beside them."""
+    _say("case linear rounding", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "rounding")
+    quantize, _, linear, _, _ = _ops(fmt)
+    x = _bf16(rows, k, g, device)
+    if rows > 1:
+        x[rows // 2, 0] = float("nan")
+        x[rows // 2, k - 1] = float("-inf")
+    sw, cw = random_record("mx", n, k, g, device, 110, 124)
+    sa, ca, _ = quantize(x)
+    a = values(fmt, sa, ca, k)
+    assert a.isfinite().all()
+    _check(fmt, linear(x, sw, cw, n), a, values("mx", sw, cw, k))
+
+
+# ---------------------------------------------------------------------------
+# ends of the ranges
+# ---------------------------------------------------------------------------
+
+# few rows with a short row of scales, few rows, many rows (MXFP4: 128 x 128 and 128 x 256 tiles)
+RANGE_SHAPES = [(37, 48, 256), (37, 48, 544), (37, 64, 2592), (600, 2064, 544), (16390, 1040, 544)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", RANGE_SHAPES)
+def test_matmul_at_the_ends_of_the_scales(device, fmt, rows, n, k):
+    """Scale bytes 0 to 2 against 252 to 254, either way round."""
+    _say("case scale ends", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "ends")
+    for low_a in (True, False):
+        la, lw = ((0, 3), (252, 255)) if low_a else ((252, 255), (0, 3))
+        sa, ca = random_record(fmt, rows, k, g, device, *la)
+        sw, cw = random_record("mx", n, k, g, device, *lw)
+        _check(fmt, _ops(fmt)[1](sa, ca, sw, cw, n, k), values(fmt, sa, ca, k), values("mx", sw, cw, k))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", RANGE_SHAPES)
+def test_nan_scales_and_codes_stay_in_their_rows(device, fmt, rows, n, k):
+    _say("case NaN", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "nan")
+    sa, ca = random_record(fmt, rows, k, g, device)
+    sw, cw = random_record("mx", n, k, g, device)
+    blocks = k // 32
+    bad_rows, bad_cols = {3: 0, 11: blocks - 1, rows - 1: blocks // 2}, {0: blocks - 1, 17: 0, n - 1: blocks // 2}
+    for m, b in bad_rows.items():
+        sa.view(rows, -1)[m, b] = 255
+        ca.view(rows, -1)[m] = 0
+    for c, b in bad_cols.items():
+        sw.view(n, -1)[c, b] = 255
+        cw.view(n, -1)[c] = 0
+    if fmt == "mx8":  # NaN codes, at the row's ends and beside zeros
+        for m, j, code in ((5, 0, 0x7F), (6, k - 1, 0xFF), (7, k // 2 + 1, 0x7F)):
+            ca.view(rows, k)[m, j] = code
+            bad_rows[m] = 0
+    y = _ops(fmt)[1](sa, ca, sw, cw, n, k)
+    want = torch.zeros(rows, n, dtype=torch.bool, device=device)
+    want[list(bad_rows)] = True
+    want[:, list(bad_cols)] = True
+    assert torch.equal(y.isnan(), want)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", [(33, 48, 96), (300, 528, 1056)])
+@pytest.mark.parametrize("lo,hi,scale", [(0, 4, 2.0 ** 80), (240, 247, 2.0 ** -100), (246, 253, 2.0 ** -100)])
+def test_gradients_at_the_ends_of_the_scales(device, fmt, rows, n, k, lo, hi, scale):
+    """Scale bytes from 0 to the largest that a finite tensor's quantisation
+    writes (246 for MXFP8, 252 for MXFP4).  A code's value under bf16's
+    smallest step 2^-133 is off by at most half of it."""
+    import fp4_rollout_guided_amd as tr
+    _say("case gradients at the ends", fmt, rows, n, k, lo, hi)
+    g = _gen(device, fmt, rows, n, k, lo)
+    gy = _bf16(rows, n, g, device, scale)
+    gd = gy.double()
+    if fmt == "mx":  # the gradient to the activations reads the MXFP4 weight alone
+        sw, cw = random_record("mx", n, k, g, device, lo, hi)
+        w = values("mx", sw, cw, k)
+        close(tr.mx_matmul_bwd_input(gy, sw, cw, k), gd @ w, gd.abs() @ w.abs(), n)
+    if fmt == "mx8" and hi > 247:
+        return
+    sa, ca = random_record(fmt, rows, k, g, device, lo, hi)
+    a = values(fmt, sa, ca, k)
+    gt = gd.T.contiguous()
+    want, size = gt @ a, gt.abs() @ a.abs()
+    small = gt.abs().sum(1, keepdim=True) * 2.0 ** -134 if fmt == "mx8" else torch.zeros_like(want)
+    got = _ops(fmt)[4](gy, sa, ca, k).double()
+    tol = rows * 2.0 ** -24 * size + small
+    assert ((got - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", [(33, 48, 96), (300, 528, 1056)])
+def test_gradients_of_nan_scales_and_codes(device, fmt, rows, n, k):
+    """A NaN of W or A is a NaN in every result that its value enters, and in no other."""
+    import fp4_rollout_guided_amd as tr
+    _say("case gradients of NaN", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "nan gradients")
+    gy = _bf16(rows, n, g, device)
+    blocks = k // 32
+    if fmt == "mx":
+        sw, cw = random_record("mx", n, k, g, device)
+        want = torch.zeros(rows, k, dtype=torch.bool, device=device)
+        for c, b in ((0, 0), (17, blocks - 1)):
+            sw.view(n, -1)[c, b] = 255
+            want[:, 32 * b:32 * b + 32] = True
+        cw.view(n, -1)[17] = 0
+        assert torch.equal(tr.mx_matmul_bwd_input(gy, sw, cw, k).isnan(), want)
+    sa, ca = random_record(fmt, rows, k, g, device)
+    want = torch.zeros(n, k, dtype=torch.bool, device=device)
+    for m, b in ((1, 1), (rows - 1, blocks - 1)):
+        sa.view(rows, -1)[m, b] = 255
+        want[:, 32 * b:32 * b + 32] = True
+    ca.view(rows, -1)[1] = 0
+    if fmt == "mx8":
+        for m, j, code in ((2, 0, 0x7F), (7, 31, 0xFF)):
+            ca.view(rows, k)[m, j] = code
+            want[:, j] = True
+    assert torch.equal(_ops(fmt)[4](gy, sa, ca, k).isnan(), want)
