@@ -622,6 +622,14 @@ static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Whether a product's activations are few enough to be rounded in its own LDS.
+// Stored ones so few take the same tiles, at any n: the sums' order, and with it
+// the result, is that of the product that rounds them (stored, MXFP4, us against
+// the larger tiles that their n would allow: 1 x 32768 x 4096 14.8 and 24.2, 4 x
+// 131072 x 4096 54 and 59, 16 x 32768 x 1024 7.6 and 8.7, 16 x 131072 x 1024 25
+// and 19).
+static bool few_activations(uint64_t rows, uint64_t k) { return rows <= 16 && rows * k <= kRoundMax; }
+
 // One weight: the smallest tile that gives each CU at most one workgroup, since
 // a larger one leaves CUs idle and a smaller one reads its operands more often
 // (rows x n x k, MXFP4, us: 16 x 2048 x 4096 4.5 with 16 x 16, 5.5 with 16 x 32;
@@ -636,7 +644,7 @@ static hipError_t launch_few_rows(const MxProductArgs& p, hipStream_t stream) {
     return (p.rows + rows - 1) / rows * ((p.n + cols - 1) / cols);
   };
   if (tiles(16, 16) <= kCUs) return launch_skinny<kFmt, kRound, 1, 1, 8, 2>(p, stream);
-  if (kRound || tiles(16, 32) <= kCUs) return launch_skinny<kFmt, kRound, 1, 2, 8, 2>(p, stream);
+  if (few_activations(p.rows, p.k) || tiles(16, 32) <= kCUs) return launch_skinny<kFmt, kRound, 1, 2, 8, 2>(p, stream);
   if constexpr (!kRound) {
     if (tiles(32, 32) <= kCUs) return launch_skinny<kFmt, false, 2, 2, 4, 2>(p, stream);
     if (tiles(32, 64) <= kCUs) return launch_skinny<kFmt, false, 2, 4, 4, 1>(p, stream);
@@ -668,7 +676,7 @@ static hipError_t launch_few_rows_each(const MxProductArgs& p, hipStream_t strea
 // fill one 16-byte load, and row 0 must exist.
 static bool many_rows(const MxProductArgs& p) {
   if (p.k < 512 || p.src_rows == 0) return false;
-  if (!p.offsets) return (p.rows + 63) / 64 * ((p.n + 63) / 64) > kCUs;
+  if (!p.offsets) return !few_activations(p.rows, p.k) && (p.rows + 63) / 64 * ((p.n + 63) / 64) > kCUs;
   return p.rows >= 32 * (uint64_t)p.groups;
 }
 
@@ -691,7 +699,7 @@ static hipError_t launch_product(const MxProductArgs& p, hipStream_t stream) {
 }
 
 bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped) {
-  return !grouped && rows <= 16 && rows * k <= kRoundMax;
+  return !grouped && few_activations(rows, k);
 }
 
 hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& args, hipStream_t stream) {

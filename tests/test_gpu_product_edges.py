@@ -107,6 +107,23 @@ def test_linear_against_its_own_rounding(device, fmt, rows, n, k):
     _check(fmt, linear(x, sw, cw, n), a, values("mx", sw, cw, k))
 
 
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+@pytest.mark.parametrize("rows,n,k", [(1, 4096, 4096), (1, 16384, 4096), (4, 32768, 4096), (2, 8992, 8192), (1, 32000, 16384),
+                                      (16, 32768, 1024), (16, 16400, 992), (9, 20496, 544)])
+def test_linear_of_few_rows_is_quantize_and_matmul_bit_for_bit(device, fmt, rows, n, k):
+    """The tokens' rounding inside the product and before it give the same
+    sums, also past the n where larger tiles would do for stored operands."""
+    _say("case linear bits", fmt, rows, n, k)
+    g = _gen(device, fmt, rows, n, k, "bits")
+    quantize, matmul, linear, _, _ = _ops(fmt)
+    x = _bf16(rows, k, g, device)
+    sw, cw = random_record("mx", n, k, g, device)
+    sa, ca, _ = quantize(x)
+    y = linear(x, sw, cw, n)
+    assert torch.equal(y.view(torch.int16), matmul(sa, ca, sw, cw, n, k).view(torch.int16))
+    _check(fmt, y[-1:], values(fmt, sa, ca, k)[-1:], values("mx", sw, cw, k))
+
+
 # ---------------------------------------------------------------------------
 # ends of the ranges
 # ---------------------------------------------------------------------------
