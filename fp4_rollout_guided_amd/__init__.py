@@ -1111,9 +1111,9 @@ def expert_combine(y, slot, weights=None, out=None):
 
 def expert_combine_bwd(grad_out, y, slot, weights, offsets=None, grad_y=None, grad_weights=None):
     """Gradients of ``expert_combine``: (grad_y bf16, packed as y; grad_weights
-    fp32 [tokens, topk]).  Rows behind the last group of ``offsets`` become
-    zeros; without offsets, rows that no slot names are zeros in a grad_y made
-    here and are left as they are in one passed in."""
+    fp32 [tokens, topk]).  Rows that no slot names are zeros; without
+    ``offsets`` they are left as they are in a grad_y passed in.  No two slots
+    may name the same row."""
     rows, cols = _matrix(y, "y")
     tokens, topk = _pairs(slot, "slot", y, _I64)
     t, c = _matrix(grad_out, "grad_out")

@@ -415,8 +415,8 @@ trace_status trace_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* 
                         rng(offsets, offsets ? 8 * ((uint64_t)groups + 1) : 0)};
   if (trace_status st = check_alias(outs, 2, ins, 5)) return st;
   return hip_status(trace_host::launch_expert_combine_bwd(grad_out, y, (uint64_t)rows, (uint64_t)cols, slot, weights,
-                                                          (uint64_t)tokens, (uint32_t)topk, offsets, (uint32_t)groups,
-                                                          grad_y, grad_weights, static_cast<hipStream_t>(stream)));
+                                                          (uint64_t)tokens, (uint32_t)topk, offsets != nullptr, grad_y,
+                                                          grad_weights, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -286,26 +286,73 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
   }
 }
 
+// Rows of grad_y that no slot names become zeros.  Up to kScanPairs pairs,
+// workgroups of the gradients' own launch take kScanRows rows each and look
+// through all slots for their rows (192 pairs of 2048: 5.9 us a call, 10.3 with the two
+// launches below; 8192 of 512: 9.6 and 11).  Past them every row's first vector is marked, the gradients
+// overwrite what they name, and the rows that kept the mark are cleared
+// (131072 rows of 2048, all named: 10 us, where clearing all of them first takes
+// 78).  The mark is eight signalling NaNs, which no result can be: rounding to
+// bf16 makes every NaN a quiet one.
+constexpr uint64_t kScanPairs = 8192;
+constexpr uint32_t kScanRows = 8;
+constexpr uint32_t kMark = 0x7f817f81u;
+constexpr uint32_t kClearRows = 16;  // rows to a wave
+
+__global__ __launch_bounds__(kThreads) void expert_mark_kernel(uint64_t rows, uint32_t row_vecs,
+                                                               uint4* __restrict__ grad_y) {
+  const uint64_t stride = (uint64_t)gridDim.x * kThreads;
+  for (uint64_t r = (uint64_t)blockIdx.x * kThreads + threadIdx.x; r < rows; r += stride)
+    grad_y[r * row_vecs] = make_uint4(kMark, kMark, kMark, kMark);
+}
+
+__global__ __launch_bounds__(kThreads) void expert_clear_kernel(uint64_t rows, uint32_t row_vecs,
+                                                                uint4* __restrict__ grad_y) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t stride = (uint64_t)gridDim.x * kSortWaves * kClearRows;
+  for (uint64_t r0 = ((uint64_t)blockIdx.x * kSortWaves + (threadIdx.x >> 6)) * kClearRows; r0 < rows; r0 += stride) {
+    bool marked = false;
+    if (lane < kClearRows && r0 + lane < rows) {
+      const uint4 v = grad_y[(r0 + lane) * row_vecs];
+      marked = v.x == kMark && v.y == kMark && v.z == kMark && v.w == kMark;
+    }
+    for (uint64_t left = __ballot(marked); left; left &= left - 1) {
+      uint4* row = grad_y + (r0 + (uint32_t)__ffsll((long long)left) - 1) * row_vecs;
+      for (uint32_t c = lane; c < row_vecs; c += 64) row[c] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
 // Gradients of the weighted sum, one workgroup per token: grad_y[slot] =
 // bf16(w * grad_out[t]) and grad_weights[t][j] = <grad_out[t], y[slot]> in
 // fp32, summed lane by lane, then over lanes and waves in a fixed order.
-// Workgroups past the tokens clear the rows behind the last group.  kNT: y and
-// grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 241
-// us against 254).
+// `scans` workgroups past the tokens clear rows without a slot.  kNT: y and
+// grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 241 us
+// against 254).
 template <bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
     const uint4* __restrict__ grad_out, const uint4* __restrict__ y, uint64_t rows, uint32_t row_vecs,
     const int64_t* __restrict__ slot, const float* __restrict__ weights, uint64_t tokens, uint32_t topk,
-    const int64_t* __restrict__ offsets, uint32_t groups, uint4* __restrict__ grad_y,
-    float* __restrict__ grad_weights) {
+    uint64_t scans, uint4* __restrict__ grad_y, float* __restrict__ grad_weights) {
+  __shared__ uint32_t named;  // bit r: a slot names row r of the workgroup's
   __shared__ float part[kThreads / 64][trace_host::kMaxTopk];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint64_t units = tokens + (offsets ? rows : 0);
-  for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  for (uint64_t u = blockIdx.x; u < tokens + scans; u += gridDim.x) {
     if (u >= tokens) {
-      const uint64_t r = u - tokens;
-      if ((int64_t)r >= offsets[groups])
-        for (uint32_t c = threadIdx.x; c < row_vecs; c += kThreads) grad_y[r * row_vecs + c] = make_uint4(0, 0, 0, 0);
+      const uint64_t r0 = (u - tokens) * kScanRows;
+      if (threadIdx.x == 0) named = 0;
+      __syncthreads();
+#pragma unroll 8
+      for (uint32_t i = threadIdx.x; i < (uint32_t)tokens * topk; i += kThreads) {
+        const uint64_t at = (uint64_t)slot[i] - r0;  // a negative slot, or one before r0, is past every row
+        if (at < kScanRows) atomicOr(&named, 1u << at);
+      }
+      __syncthreads();
+      for (uint32_t r = 0; r < kScanRows && r0 + r < rows; ++r) {
+        if (named >> r & 1) continue;
+        for (uint32_t c = threadIdx.x; c < row_vecs; c += kThreads) grad_y[(r0 + r) * row_vecs + c] = make_uint4(0, 0, 0, 0);
+      }
+      __syncthreads();
       continue;
     }
     for (uint32_t j = 0; j < topk; ++j) {
@@ -422,14 +469,22 @@ hipError_t launch_expert_combine(const void* y, bool f32, uint64_t rows, uint64_
 
 hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, uint64_t rows, uint64_t cols,
                                      const int64_t* slot, const float* weights, uint64_t tokens, uint32_t topk,
-                                     const int64_t* offsets, uint32_t groups, uint16_t* grad_y, float* grad_weights,
-                                     hipStream_t stream) {
-  const uint64_t units = tokens + (offsets ? rows : 0);
+                                     bool clear, uint16_t* grad_y, float* grad_weights, hipStream_t stream) {
+  const uint32_t row_vecs = (uint32_t)(cols / 8);
+  uint4* gv = reinterpret_cast<uint4*>(grad_y);
+  clear = clear && rows > 0 && row_vecs > 0;
+  const bool scan = clear && tokens * topk <= kScanPairs;
+  const uint64_t scans = scan ? (rows + kScanRows - 1) / kScanRows : 0;
+  if (clear && !scan)
+    hipLaunchKernelGGL(expert_mark_kernel, dim3(rows_grid(rows, kThreads)), dim3(kThreads), 0, stream, rows, row_vecs, gv);
   const auto kernel = past_cache(2 * rows * cols) ? expert_combine_bwd_kernel<true> : expert_combine_bwd_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3(rows_grid(units, 1)), dim3(kThreads), 0, stream,
-                     reinterpret_cast<const uint4*>(grad_out), reinterpret_cast<const uint4*>(y), rows,
-                     (uint32_t)(cols / 8), slot, weights, tokens, topk, offsets, groups,
-                     reinterpret_cast<uint4*>(grad_y), grad_weights);
+  if (tokens + scans > 0)
+    hipLaunchKernelGGL(kernel, dim3(rows_grid(tokens + scans, 1)), dim3(kThreads), 0, stream,
+                       reinterpret_cast<const uint4*>(grad_out), reinterpret_cast<const uint4*>(y), rows, row_vecs, slot,
+                       weights, tokens, topk, scans, gv, grad_weights);
+  if (clear && !scan)
+    hipLaunchKernelGGL(expert_clear_kernel, dim3(rows_grid(rows, kSortWaves * kClearRows)), dim3(kThreads), 0, stream,
+                       rows, row_vecs, gv);
   return hipGetLastError();
 }
 

@@ -73,9 +73,9 @@ hipError_t launch_expert_dispatch(const uint16_t* x, uint64_t tokens, uint64_t c
 hipError_t launch_expert_combine(const void* y, bool f32, uint64_t rows, uint64_t cols, const int64_t* slot,
                                  const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
                                  hipStream_t stream);
+// clear: rows of grad_y that no slot names become zeros.
 hipError_t launch_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, uint64_t rows, uint64_t cols,
                                      const int64_t* slot, const float* weights, uint64_t tokens, uint32_t topk,
-                                     const int64_t* offsets, uint32_t groups, uint16_t* grad_y, float* grad_weights,
-                                     hipStream_t stream);
+                                     bool clear, uint16_t* grad_y, float* grad_weights, hipStream_t stream);
 
 }  // namespace trace_host

@@ -715,8 +715,9 @@ TRACE_API trace_status trace_expert_combine_f32(const float* y, int64_t rows, in
 /* Gradients of trace_expert_combine:
  *   grad_y[slot[t][j]] = bf16_RNE(weights[t][j] * grad_out[t]),
  *   grad_weights[t][j] = sum over c of grad_out[t][c] * y[slot[t][j]][c] (fp32; 0 where the slot is left out).
- * Rows of grad_y that no slot names are written only where offsets is given:
- * rows from offsets[groups] on become zeros (offsets = NULL, groups = 0: none).
+ * Rows of grad_y that no slot names (those from offsets[groups] on, and any whose
+ * pair was dropped from slot) become zeros where the rows' offsets are given, and
+ * are left as they are with offsets = NULL, groups = 0.
  * No two slots may name the same row.
  *   weights NULL: all ones. */
 TRACE_API trace_status trace_expert_combine_bwd(const uint16_t* grad_out, const uint16_t* y, int64_t rows,
