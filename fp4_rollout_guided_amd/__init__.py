@@ -56,6 +56,7 @@ import math
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = [
     "TraceError", "LIB_PATH", "SMALLGRID_LIB_PATH", "lib", "load_library", "abi_version", "tensor_scale",
@@ -1160,6 +1161,7 @@ class MxMatmul(torch.autograd.Function):
         return y.view(*x.shape[:-1], n)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         a_scales, a_codes, a_mask, w_scales, w_codes, w_mask, offsets = ctx.saved_tensors
         grad_y = grad_y.contiguous()
@@ -1182,6 +1184,7 @@ class ExpertDispatch(torch.autograd.Function):
         return expert_dispatch(x.contiguous(), row_index)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         (slot,) = ctx.saved_tensors
         return expert_combine(grad.contiguous(), slot).view(ctx.shape), None, None
@@ -1197,6 +1200,7 @@ class ExpertCombine(torch.autograd.Function):
         return expert_combine(y, slot, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         y, slot, weights, offsets = ctx.saved_tensors
         grad_y, grad_weights = expert_combine_bwd(grad_out.contiguous(), y, slot, weights, offsets)
