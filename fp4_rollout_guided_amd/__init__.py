@@ -869,12 +869,14 @@ def mx8_quantize(x, want_mask=False, scales=None, codes=None, mask=None):
     return _quantize("mx8", x, want_mask, scales, codes, mask)
 
 
-def _record(fmt, scales, codes, like, k, prefix):
-    """Rows of a stored operand [rows, k]."""
+def _record(fmt, scales, codes, like, k, prefix, rows):
+    """Rows of a stored operand [rows, k]; with k == 0, which leaves nothing to
+    count them by, the ``rows`` that the caller knows of."""
     _arg(scales, f"{prefix}_scales", like, _U8, 0)
-    if k == 0:
-        raise ValueError("k must be positive")
-    rows = scales.numel() * 32 // k
+    if k > 0:
+        rows = scales.numel() * 32 // k
+    elif rows is None:
+        raise ValueError("k is 0: y must be given, for its rows")
     _fit(scales, f"{prefix}_scales", like, _U8, rows * (k // 32))
     _fit(codes, f"{prefix}_codes", like, _U8, _code_bytes(fmt, rows * k))
     return rows
@@ -890,12 +892,14 @@ def _index(row_index, like):
     return row_index.numel()
 
 
-def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index, y, dtype=torch.bfloat16):
+def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index, y, dtype=torch.bfloat16, rows=None):
     if not isinstance(a_codes, torch.Tensor) or not a_codes.is_cuda:
         raise ValueError("a_codes must be a device tensor")
     _dim(n, "n", 16)
     _dim(k, "k", 32)
-    src_rows = _record(fmt, a_scales, a_codes, a_codes, k, "a")
+    if k == 0 and rows is None:
+        rows = 0 if row_index is not None else y.numel() // n if isinstance(y, torch.Tensor) and n else None
+    src_rows = _record(fmt, a_scales, a_codes, a_codes, k, "a", rows)
     at, groups, weights = _groups(offsets, a_codes)
     _weight(w_scales, w_codes, a_codes, weights, n, k)
     rows = src_rows if row_index is None else _index(row_index, a_codes)
@@ -912,7 +916,8 @@ def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index,
 
 def mx_matmul(a_scales, a_codes, w_scales, w_codes, n, k, y=None):
     """y = A W^T (bf16 [rows, n]) of MXFP4 activations [rows, k] and an MXFP4
-    weight [n, k]; n % 16 == 0, k % 32 == 0."""
+    weight [n, k]; n % 16 == 0, k % 32 == 0.  k == 0 gives zeros in the y
+    passed in."""
     return _matmul("mx", a_scales, a_codes, None, w_scales, w_codes, n, k, None, y)
 
 
@@ -1012,7 +1017,7 @@ def _bwd_weight(fmt, grad_y, offsets, a_scales, a_codes, k, row_index, mask, gra
     rows, n = _matrix(grad_y, "grad_y")
     _dim(k, "k", 32)
     at, groups, weights = _groups(offsets, grad_y)
-    src_rows = _record(fmt, a_scales, a_codes, grad_y, k, "a")
+    src_rows = _record(fmt, a_scales, a_codes, grad_y, k, "a", rows)
     if row_index is not None:
         _fit(row_index, "row_index", grad_y, _I64, rows)
     elif src_rows != rows:
@@ -1157,7 +1162,7 @@ class MxMatmul(torch.autograd.Function):
         w_scales, w_codes, w_mask = mx_quantize(w, want_mask=True)
         ctx.save_for_backward(a_scales, a_codes, a_mask, w_scales, w_codes, w_mask, offsets)
         ctx.fmt, ctx.k = fmt, k
-        y = _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, None, None)
+        y = _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, None, None, rows=math.prod(x.shape[:-1]))
         return y.view(*x.shape[:-1], n)
 
     @staticmethod

@@ -1,5 +1,5 @@
-"""The autograd functions of the products and the routed rows at the edges of
-what they take."""
+"""The autograd functions of the products and the routed rows, and the products
+of empty contractions, at the edges of what they take."""
 import zlib
 
 import pytest
@@ -37,3 +37,31 @@ def test_second_derivatives_are_refused(device, which):
     gx, = torch.autograd.grad(out, x, torch.ones_like(out).requires_grad_(), create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         gx.float().sum().backward()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "mx8"])
+def test_empty_contractions(device, fmt):
+    """k == 0: sums of nothing, as the C entry points give them."""
+    import fp4_rollout_guided_amd as tr
+    matmul, grouped, bwd_weight, grouped_bwd = (
+        (tr.mx_matmul, tr.grouped_mx_matmul, tr.mx_matmul_bwd_weight, tr.grouped_mx_matmul_bwd_weight) if fmt == "mx" else
+        (tr.mx8_matmul, tr.grouped_mx8_matmul, tr.mx8_matmul_bwd_weight, tr.grouped_mx8_matmul_bwd_weight))
+    none = torch.empty(0, dtype=torch.uint8, device=device)
+    off = torch.tensor([0, 2, 4], device=device)
+    y = torch.full((5, 32), 7.0, device=device).bfloat16()
+    assert matmul(none, none, none, none, 32, 0, y=y) is y and (y == 0).all()
+    y.fill_(7)
+    assert (grouped(none, none, off, none, none, 32, 0, y=y) == 0).all()
+    got = grouped(none, none, off, none, none, 32, 0, row_index=torch.zeros(5, dtype=torch.int64, device=device))
+    assert got.shape == (5, 32) and (got == 0).all()
+    with pytest.raises(ValueError, match="y must be given"):
+        matmul(none, none, none, none, 32, 0)
+    gy = torch.ones(5, 32, dtype=torch.bfloat16, device=device)
+    assert bwd_weight(gy, none, none, 0).shape == (32, 0)
+    assert grouped_bwd(gy, off, none, none, 0).shape == (2, 32, 0)
+    x = torch.empty(2, 3, 0, dtype=torch.bfloat16, device=device, requires_grad=True)
+    w = torch.empty(32, 0, dtype=torch.bfloat16, device=device, requires_grad=True)
+    out = tr.MxMatmul.apply(x, w, None, fmt)
+    assert out.shape == (2, 3, 32) and (out == 0).all()
+    out.backward(torch.ones_like(out))
+    assert x.grad.shape == x.shape and w.grad.shape == w.shape
