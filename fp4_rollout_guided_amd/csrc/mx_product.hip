@@ -598,6 +598,18 @@ namespace trace_host {
 
 using namespace trace_dev;
 
+// Whether a product's activations are few enough to be rounded in its own LDS.
+// Stored ones so few take the same tiles, at any n: the sums' order, and with it
+// the result, is that of the product that rounds them (stored, MXFP4, us against
+// the larger tiles that their n would allow: 1 x 32768 x 4096 14.8 and 24.2, 4 x
+// 131072 x 4096 54 and 59, 16 x 32768 x 1024 7.6 and 8.7, 16 x 131072 x 1024 25
+// and 19).
+static bool few_activations(uint64_t rows, uint64_t k) { return rows <= 16 && rows * k <= kRoundMax; }
+
+// Least k of the tiles of many rows: a row's scales fill one 16-byte load and its
+// codes two stages.
+constexpr uint32_t kManyRowsK = 512;
+
 template <int kFmt, bool kRound, int kMF, int kNF, int kWaves, int kSteps>
 static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
   const uint32_t cols = (p.n + 16 * kNF - 1) / (16 * kNF);
@@ -610,6 +622,8 @@ static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
 
 template <int kFmt, bool kF32, int kMF, int kNF, int kPerCu>
 static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
+  // scale_at and a stage's first loads count on these
+  if (p.k < kManyRowsK || p.src_rows == 0) return hipErrorInvalidValue;
   constexpr uint32_t kRows = 64 * kMF, kCols = 64 * kNF;
   const uint32_t cols = (p.n + kCols - 1) / kCols;
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, kRows) : (p.rows + kRows - 1) / kRows;
@@ -621,14 +635,6 @@ static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL((mx_tile_kernel<kFmt, false, kF32, kMF, kNF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
   return hipGetLastError();
 }
-
-// Whether a product's activations are few enough to be rounded in its own LDS.
-// Stored ones so few take the same tiles, at any n: the sums' order, and with it
-// the result, is that of the product that rounds them (stored, MXFP4, us against
-// the larger tiles that their n would allow: 1 x 32768 x 4096 14.8 and 24.2, 4 x
-// 131072 x 4096 54 and 59, 16 x 32768 x 1024 7.6 and 8.7, 16 x 131072 x 1024 25
-// and 19).
-static bool few_activations(uint64_t rows, uint64_t k) { return rows <= 16 && rows * k <= kRoundMax; }
 
 // One weight: the smallest tile that gives each CU at most one workgroup, since
 // a larger one leaves CUs idle and a smaller one reads its operands more often
@@ -672,10 +678,9 @@ static hipError_t launch_few_rows_each(const MxProductArgs& p, hipStream_t strea
 // Whether the rows are many: past the grids of launch_few_rows for one weight,
 // from 32 rows each for groups (128 groups, 1536 x 2048, MXFP4, us in tiles of
 // few and of many rows: 16 rows each 54 and 60, 32 each 76 and 63; 16 groups: 16
-// each 9.3 and 13, 32 each 14 and 14, 64 each 17 and 14).  A row's scales must
-// fill one 16-byte load, and row 0 must exist.
+// each 9.3 and 13, 32 each 14 and 14, 64 each 17 and 14).  Row 0 must exist.
 static bool many_rows(const MxProductArgs& p) {
-  if (p.k < 512 || p.src_rows == 0) return false;
+  if (p.k < kManyRowsK || p.src_rows == 0) return false;
   if (!p.offsets) return !few_activations(p.rows, p.k) && (p.rows + 63) / 64 * ((p.n + 63) / 64) > kCUs;
   return p.rows >= 32 * (uint64_t)p.groups;
 }
@@ -705,6 +710,8 @@ bool mx_product_rounds(uint64_t rows, uint64_t k, bool grouped) {
 hipError_t launch_mx_product(MxFormat fmt, const MxProductArgs& args, hipStream_t stream) {
   MxProductArgs p = args;
   p.stream_out = past_cache((p.f32 ? 4 : 2) * p.rows * p.n);
+  // activations to round: all of them in each workgroup's LDS
+  if (p.x && (p.offsets || p.row_index || !few_activations(p.rows, p.k))) return hipErrorInvalidValue;
   if (p.x) return fmt == kE2M1 ? launch_few_rows<kE2M1, true>(p, stream) : launch_few_rows<kE4M3, true>(p, stream);
   return fmt == kE2M1 ? launch_product<kE2M1>(p, stream) : launch_product<kE4M3>(p, stream);
 }
