@@ -97,19 +97,21 @@ trace_status product(MxFormat fmt, const uint16_t* x, void* workspace, size_t wo
                         rng(offsets, offsets ? 8 * ((uint64_t)weights + 1) : 0)};
   if (trace_status st = check_alias(outs, 2, ins, 7)) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* const codes = static_cast<uint8_t*>(workspace);  // of the rounded activations, where need > 0
+  uint8_t* const scales = need > 0 ? codes + code_bytes(fmt, na) : nullptr;
+  const bool rounds = linear && trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0);
+  trace_host::MxProductArgs p{rounds ? x : nullptr, need > 0 ? codes : a_codes, need > 0 ? scales : a_scales, row_index,
+                              (uint64_t)src_rows, (uint64_t)rows, offsets, (uint32_t)weights, w_codes, w_scales,
+                              (uint32_t)n, (uint32_t)k, y, f32};
   if (need > 0) {
-    uint8_t* codes = static_cast<uint8_t*>(workspace);
-    uint8_t* scales = codes + code_bytes(fmt, na);
+    p.plan_only = true;  // sizes that are refused are refused before anything is enqueued
+    if (trace_status st = launch_status(trace_host::launch_mx_product(fmt, p, s))) return st;
+    p.plan_only = false;
     const int64_t* used = offsets && !row_index ? offsets + groups : nullptr;  // rows behind the last group are not read
     if (trace_status st = hip_status(trace_host::launch_mx_quantize(fmt, x, na / 32, scales, codes, nullptr, used,
                                                                     (uint32_t)(k / 32), s)))
       return st;
-    a_codes = codes;
-    a_scales = scales;
   }
-  const bool rounds = linear && trace_host::mx_product_rounds((uint64_t)rows, (uint64_t)k, groups > 0);
-  const trace_host::MxProductArgs p{rounds ? x : nullptr, a_codes, a_scales, row_index, (uint64_t)src_rows, (uint64_t)rows,
-                                    offsets, (uint32_t)weights, w_codes, w_scales, (uint32_t)n, (uint32_t)k, y, f32};
   return launch_status(trace_host::launch_mx_product(fmt, p, s));
 }
 

@@ -27,6 +27,7 @@ struct MxProductArgs {
   void* y;   // [rows, n] in bf16, or
   bool f32;  // in fp32 (grouped products)
   bool stream_out = false;  // y is past the last-level cache: the launcher's
+  bool plan_only = false;   // check the grid, launch nothing
 };
 
 // The gradients: grad_y W (to the activations) or grad_y^T A (to the weights).

@@ -615,6 +615,7 @@ static hipError_t launch_skinny(const MxProductArgs& p, hipStream_t stream) {
   const uint32_t cols = (p.n + 16 * kNF - 1) / (16 * kNF);
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, 16 * kMF) : (p.rows + 16 * kMF - 1) / (16 * kMF);
   if (row_tiles * cols * (64 * kWaves) > 0xffffffffull) return hipErrorInvalidConfiguration;
+  if (p.plan_only) return hipSuccess;
   hipLaunchKernelGGL((mx_skinny_kernel<kFmt, kRound, kMF, kNF, kWaves, kSteps>), dim3((unsigned)(row_tiles * cols)),
                      dim3(64 * kWaves), 0, stream, p, cols);
   return hipGetLastError();
@@ -629,6 +630,7 @@ static hipError_t launch_tile(const MxProductArgs& p, hipStream_t stream) {
   const uint64_t row_tiles = p.offsets ? max_row_tiles(p.rows, p.groups, kRows) : (p.rows + kRows - 1) / kRows;
   const uint64_t grid = (row_tiles * cols + 7) / 8 * 8;
   if (grid * 256 > 0xffffffffull) return hipErrorInvalidConfiguration;
+  if (p.plan_only) return hipSuccess;
   if (p.row_index)
     hipLaunchKernelGGL((mx_tile_kernel<kFmt, true, kF32, kMF, kNF, kPerCu>), dim3((unsigned)grid), dim3(256), 0, stream, p, cols);
   else

@@ -1,6 +1,6 @@
-"""Refusals of the entry points on fp32 packed rows, on the CPU: every bad
-argument is turned down before any HIP call (the device addresses below are
-never dereferenced)."""
+"""Refusals of the entry points on fp32 packed rows, and of sizes past one
+launch, on the CPU: every bad argument is turned down before any HIP call (the
+device addresses below are never dereferenced)."""
 import pytest
 import torch
 
@@ -68,3 +68,17 @@ def test_binding():
         tr.expert_combine(torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int64))
     with pytest.raises(TypeError, match="y must be bf16"):
         tr.expert_combine(torch.zeros(4, 64, dtype=torch.float16), torch.zeros(4, 2, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("fn", ["trace_mx_linear", "trace_mx8_linear", "trace_grouped_mx_linear_f32",
+                                "trace_grouped_mx8_linear_f32"])
+def test_sizes_past_one_launch_are_refused_before_the_rounding(fn):
+    """Without a GPU, a launch would answer TRACE_E_HIP."""
+    rows = (1 << 31) - 1
+    at = [(1 << 46) + (i << 42) for i in range(6)]
+    grouped = fn.endswith("_f32")
+    for k in (32, 512):
+        need = getattr(L, fn.replace("grouped_", "").replace("_f32", "") + "_workspace_bytes")(rows, rows, int(grouped), k)
+        n = 16 if k == 32 else 1024
+        assert getattr(L, fn)(at[0], rows, None, rows, at[1] if grouped else None, int(grouped), at[2], at[3], n, k, at[4],
+                              need, at[5], None) == E_SHAPE, k
