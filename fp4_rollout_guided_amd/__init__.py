@@ -59,7 +59,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 __all__ = [
-    "TraceError", "LIB_PATH", "SMALLGRID_LIB_PATH", "lib", "load_library", "abi_version", "tensor_scale",
+    "TraceError", "LIB_PATH", "SMALLGRID_LIB_PATH", "lib", "load_library", "abi_version", "abi_revision", "tensor_scale",
     "tensor_scale_noalloc", "capture",
     "guided_fakequant_fwd", "rne_fakequant_fwd", "full_info_fakequant_fwd", "ste_bwd", "gather_records",
     "gathered_guided_fakequant_fwd", "gathered_rne_fakequant_fwd", "gathered_full_info_fakequant_fwd",
@@ -103,6 +103,7 @@ def load_library(path):
     p, i64, st, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     sig = {
         "trace_abi_version": ([], ctypes.c_int),
+        "trace_abi_revision": ([], ctypes.c_int),
         "trace_status_string": ([st], ctypes.c_char_p),
         "trace_last_hip_error": ([], ctypes.c_int),
         "trace_tensor_scale_workspace_bytes": ([i64], sz),
@@ -170,6 +171,11 @@ lib = load_library(LIB_PATH)
 
 def abi_version() -> int:
     return lib.trace_abi_version()
+
+
+def abi_revision() -> int:
+    """Additions within ``abi_version``: 1 has the products and the routed rows."""
+    return lib.trace_abi_revision()
 
 
 # --------------------------------------------------------------------------

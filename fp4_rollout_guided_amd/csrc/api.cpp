@@ -30,6 +30,8 @@ extern "C" {
 
 int trace_abi_version(void) { return TRACE_ABI_VERSION; }
 
+int trace_abi_revision(void) { return TRACE_ABI_REVISION; }
+
 const char* trace_status_string(trace_status s) {
   switch (s) {
     case TRACE_OK: return "TRACE_OK";

@@ -74,6 +74,12 @@ extern "C" {
 #endif
 
 #define TRACE_ABI_VERSION 10
+/* Entry points added within a version: 1 = the products of microscaled operands
+ * and the routed rows.  A caller that needs them asks for
+ * trace_abi_version() == TRACE_ABI_VERSION and
+ * trace_abi_revision() >= TRACE_ABI_REVISION; a library from before them has no
+ * trace_abi_revision. */
+#define TRACE_ABI_REVISION 1
 
 #if defined(__GNUC__)
 #define TRACE_API __attribute__((visibility("default")))
@@ -97,6 +103,8 @@ enum {
 
 /* TRACE_ABI_VERSION of the built library. */
 TRACE_API int trace_abi_version(void);
+/* TRACE_ABI_REVISION of the built library. */
+TRACE_API int trace_abi_revision(void);
 
 /* Static, human-readable name of a status code (never NULL). */
 TRACE_API const char* trace_status_string(trace_status status);
