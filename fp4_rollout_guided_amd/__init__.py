@@ -1186,7 +1186,10 @@ class MxMatmul(torch.autograd.Function):
 
 class ExpertDispatch(torch.autograd.Function):
     """``expert_dispatch`` of the packed rows of ``expert_sort``'s (row_index,
-    slot); the gradient sums a token's packed rows."""
+    slot); the gradient sums a token's packed rows.  They arrive in bf16, as
+    torch hands every gradient on in its tensor's type: each is rounded once
+    before the sum (``grouped_mx_matmul_bwd_input`` with dtype torch.float32 and
+    ``expert_combine`` leave that out)."""
 
     @staticmethod
     def forward(ctx, x, row_index, slot):
@@ -1202,11 +1205,14 @@ class ExpertDispatch(torch.autograd.Function):
 
 
 class ExpertCombine(torch.autograd.Function):
-    """``expert_combine`` with gradients to the packed rows and the weights."""
+    """``expert_combine`` of bf16 rows with gradients to the rows and the
+    weights (None: ones).  As for ``expert_combine_bwd``, no two slots may name
+    the same row."""
 
     @staticmethod
     def forward(ctx, y, slot, weights, offsets):
-        y, weights = _bf16(y.contiguous(), "y"), weights.contiguous()  # the gradients' type too
+        y = _bf16(y.contiguous(), "y")  # the gradients' type too
+        weights = None if weights is None else weights.contiguous()
         ctx.save_for_backward(y, slot, weights, offsets)
         return expert_combine(y, slot, weights)
 
@@ -1215,4 +1221,4 @@ class ExpertCombine(torch.autograd.Function):
     def backward(ctx, grad_out):
         y, slot, weights, offsets = ctx.saved_tensors
         grad_y, grad_weights = expert_combine_bwd(grad_out.contiguous(), y, slot, weights, offsets)
-        return grad_y, None, grad_weights, None
+        return grad_y, None, None if weights is None else grad_weights, None

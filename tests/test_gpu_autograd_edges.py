@@ -65,3 +65,18 @@ def test_empty_contractions(device, fmt):
     assert out.shape == (2, 3, 32) and (out == 0).all()
     out.backward(torch.ones_like(out))
     assert x.grad.shape == x.shape and w.grad.shape == w.shape
+
+
+def test_combine_without_weights(device):
+    import fp4_rollout_guided_amd as tr
+    g = _gen(device, "no weights")
+    ids = torch.randint(0, 4, (10, 3), generator=g, device=device)
+    off, _, slot = tr.expert_sort(ids, 3)
+    y, go = _bf16(30, 64, g, device).requires_grad_(), _bf16(10, 64, g, device)
+    out = tr.ExpertCombine.apply(y, slot, None, off)
+    assert torch.equal(out, tr.expert_combine(y.detach(), slot))
+    out.backward(go)
+    want = go.new_zeros(30, 64)
+    t, j = (slot >= 0).nonzero(as_tuple=True)
+    want[slot[t, j]] = go[t]
+    assert torch.equal(y.grad, want)
