@@ -256,9 +256,9 @@ __device__ __forceinline__ void add_scaled(float (&acc)[8], const uint4& lo, con
 
 // out[t] = sum over j of weights[t][j] * y[slot[t][j]] in fp32, j ascending;
 // slots outside [0, rows) are left out.  One lane per 8-element vector, of y in
-// bf16 or (kF32) fp32.  kNT: y
-// is past the last-level cache (131072 rows of 2048, half of them named: 40 us
-// against 62).
+// bf16 or (kF32) fp32.  kNT: y in bf16 is past the last-level cache (131072 rows
+// of 2048: 116 us against 125; fp32 rows, 1.07 GB of them, take 217 us without
+// the hint and 230 with it).
 template <bool kF32, bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* __restrict__ y, uint64_t rows,
                                                                   uint32_t row_vecs, const int64_t* __restrict__ slot,
@@ -459,8 +459,8 @@ hipError_t launch_expert_combine(const void* y, bool f32, uint64_t rows, uint64_
                                  const float* weights, uint64_t tokens, uint32_t topk, uint16_t* out,
                                  hipStream_t stream) {
   const uint64_t nvec = tokens * (cols / 8);
-  const bool nt = past_cache((f32 ? 4 : 2) * rows * cols);
-  const auto kernel = f32 ? (nt ? expert_combine_kernel<true, true> : expert_combine_kernel<true, false>)
+  const bool nt = past_cache(2 * rows * cols);
+  const auto kernel = f32 ? expert_combine_kernel<true, false>
                           : (nt ? expert_combine_kernel<false, true> : expert_combine_kernel<false, false>);
   hipLaunchKernelGGL(kernel, dim3(rows_grid(nvec, kThreads)), dim3(kThreads), 0, stream, static_cast<const uint4*>(y),
                      rows, (uint32_t)(cols / 8), slot, weights, topk, nvec, reinterpret_cast<uint4*>(out));
