@@ -15,10 +15,10 @@
 //
 // Dispatch, combine and combine's gradients move rows and are bound by
 // memory: 16 bytes per lane, sums in fp32 in the order of a token's pairs.
-// 16384 tokens of 2048, 8 experts each: dispatch 142 us (537 MB written and,
+// 16384 tokens of 2048, 8 experts each: dispatch 144 us (537 MB written and,
 // since a token's rows lie far apart, as much read, most of it from the
-// last-level cache: 7.5 TB/s), combine 124 us (4.9 TB/s), its gradients 238 us
-// (4.8 TB/s).
+// last-level cache: 7.5 TB/s), combine 116 us (5.2 TB/s; of fp32 rows 217, 5.3
+// TB/s), its gradients 220 us (5.2 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -288,12 +288,12 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
 
 // Rows of grad_y that no slot names become zeros.  Up to kScanPairs pairs,
 // workgroups of the gradients' own launch take kScanRows rows each and look
-// through all slots for their rows (192 pairs of 2048: 5.9 us a call, 10.3 with the two
-// launches below; 8192 of 512: 9.6 and 11).  Past them every row's first vector is marked, the gradients
-// overwrite what they name, and the rows that kept the mark are cleared
-// (131072 rows of 2048, all named: 10 us, where clearing all of them first takes
-// 78).  The mark is eight signalling NaNs, which no result can be: rounding to
-// bf16 makes every NaN a quiet one.
+// through all slots for their rows (192 pairs of 2048: 5.9 us a call, 10.3 with
+// the two launches below; 8192 of 512: 9.6 and 11).  Past them every row's first
+// vector is marked, the gradients overwrite what they name, and the rows that
+// kept the mark are cleared (131072 rows of 2048, all named: 10 us, where
+// clearing all of them first takes 78).  The mark is eight signalling NaNs, which
+// no result can be: rounding to bf16 makes every NaN a quiet one.
 constexpr uint64_t kScanPairs = 8192;
 constexpr uint32_t kScanRows = 8;
 constexpr uint32_t kMark = 0x7f817f81u;
@@ -327,8 +327,8 @@ __global__ __launch_bounds__(kThreads) void expert_clear_kernel(uint64_t rows, u
 // bf16(w * grad_out[t]) and grad_weights[t][j] = <grad_out[t], y[slot]> in
 // fp32, summed lane by lane, then over lanes and waves in a fixed order.
 // `scans` workgroups past the tokens clear rows without a slot.  kNT: y and
-// grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 241 us
-// against 254).
+// grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 220 us
+// against 239).
 template <bool kNT>
 __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
     const uint4* __restrict__ grad_out, const uint4* __restrict__ y, uint64_t rows, uint32_t row_vecs,

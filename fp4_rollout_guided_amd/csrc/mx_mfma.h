@@ -69,8 +69,8 @@ __device__ __forceinline__ void put_f32(const RowBlock<16>& block, uint32_t row,
 
 // 16 bytes of a result.  One larger than the last-level cache (past_cache)
 // goes past it, since its reader will not find it there: the weights' gradient
-// of 128 x 1536 x 2048, 805 MB, took 494 us against 570, the product's 537 MB
-// of 131072 x 2048 x 768 205 against 265.
+// of 128 x 1536 x 2048, 805 MB, takes 521 us against 607, the product's 537 MB
+// of 131072 x 2048 x 768 211 against 259.
 __device__ __forceinline__ void store_result(void* at, uint4 v, bool stream) {
   if (stream)
     store_vec<true>(reinterpret_cast<uint4*>(at), v);

@@ -6,9 +6,11 @@
 //
 // W and A are the codes' values; the rounding that made them passes the
 // gradient straight through inside its clip range, so each result is zeroed
-// where its tensor's clip mask is 0.  gy is bf16 and the codes' values from
-// 2^-130 up are exact in bf16, so both run on the bf16 matrix instructions with
-// fp32 sums, rounded once.
+// where its tensor's clip mask is 0.  gy is bf16 and the codes' values are exact
+// in bf16 from 2^-130 up to its largest, 2^128 (past that they are infinite; no
+// finite tensor's rounding writes such), so both run on the bf16 matrix
+// instructions with fp32 sums, rounded once or, for packed rows that are summed
+// further, left as they are.
 //
 // Both are one kernel: D[p, k] = sum over c of G(p, c) Q[c, k], where Q's
 // codes lie row by row along k and are turned into bf16 on the way into LDS.
@@ -17,11 +19,12 @@
 // (ds_read_b64_tr_b16: 16 lanes read four rows of 16 values, lane i gets
 // column i).  Q is the first operand: a lane's results are consecutive k.
 //
-// Measured: 16384 x 4096 x 2048 at 1.07 PFLOP/s (gx 258 us, gw 254 us), the
-// matrix units busy 55% of the time and LDS half of it: writing the decoded
-// tiles and reading them back transposed take as long as the arithmetic and
-// are under it only in part.  Experts' weights (128 of 1536 x 2048, 512 rows
-// each) take 494 us, a quarter of it their 805 MB.
+// Measured: 16384 x 4096 x 2048 at 1.07 PFLOP/s (gx 259 us, gw and the sum of its
+// two parts 253 us), the matrix units busy 55% of the time and LDS half of it:
+// writing the decoded tiles and reading them back transposed take as long as the
+// arithmetic and are under it only in part.  Experts' weights (128 of 1536 x
+// 2048, 512 rows each) take 515 us alone and 640 behind the other kernels of a
+// backward pass, a quarter of it their 805 MB.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -546,7 +546,7 @@ TRACE_API trace_status trace_mx8_full_info_fakequant_fwd(const uint16_t* x_train
  * with fp32 sums whose order depends on the sizes alone.  MXFP4 products are
  * exact; with MXFP8 activations the matrix instruction cuts the products of
  * eight neighbouring j to multiples of 2^-13 of the largest one's power of two
- * before it adds them.
+ * before it adds them (some 2^-16 of a long sum of random terms).
  * Unlike the fake-quant forwards, a scale byte of 0xFF is the NaN of the MX
  * specification here (the library's quantisers never write one), and E4M3
  * NaN codes are NaN.
@@ -645,7 +645,10 @@ TRACE_API trace_status trace_grouped_mx8_linear_f32(const uint16_t* x, int64_t s
  * is 1 and +0 elsewhere (the straight-through estimator of A's rounding):
  *   grad_y : bf16[rows*n]; mask : u8[rows*k/8], the clip mask of the packed
  *   rows' own rounding, or NULL for all ones; grad_x : bf16[rows*k].
- * The same for both activation formats.  offsets = NULL, groups = 0: one weight. */
+ * The same for both activation formats.  offsets = NULL, groups = 0: one weight.
+ * The gradients hold W's and A's values in bf16: exact from 2^-130 to bf16's
+ * largest, and infinite past it (scale bytes past 252 in MXFP4, 246 in MXFP8,
+ * which a finite tensor's rounding never writes). */
 TRACE_API trace_status trace_mx_matmul_bwd_input(const uint16_t* grad_y, int64_t rows, const int64_t* offsets,
                                                  int64_t groups, const uint8_t* w_scales, const uint8_t* w_codes,
                                                  int64_t n, int64_t k, const uint8_t* mask, uint16_t* grad_x,
