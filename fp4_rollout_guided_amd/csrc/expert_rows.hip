@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_kernel(const uint4* _
 // Rows of grad_y that no slot names become zeros.  Up to kScanPairs pairs,
 // workgroups of the gradients' own launch take kScanRows rows each and look
 // through all slots for their rows (192 pairs of 2048: 5.9 us a call, 10.3 with
-// the two launches below; 8192 of 512: 9.6 and 11).  Past them every row's first
+// the two launches below; 8192 of 512: 9.0 and 11).  Past them every row's first
 // vector is marked, the gradients overwrite what they name, and the rows that
 // kept the mark are cleared (131072 rows of 2048, all named: 10 us, where
 // clearing all of them first takes 78).  The mark is eight signalling NaNs, which
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void expert_clear_kernel(uint64_t rows, u
 // Gradients of the weighted sum, one workgroup per token: grad_y[slot] =
 // bf16(w * grad_out[t]) and grad_weights[t][j] = <grad_out[t], y[slot]> in
 // fp32, summed lane by lane, then over lanes and waves in a fixed order.
-// `scans` workgroups past the tokens clear rows without a slot.  kNT: y and
+// `scans` workgroups before the tokens' clear rows without a slot.  kNT: y and
 // grad_y are past the last-level cache (16384 tokens, 8 rows of 2048 each: 220 us
 // against 239).
 template <bool kNT>
@@ -337,9 +337,9 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
   __shared__ uint32_t named;  // bit r: a slot names row r of the workgroup's
   __shared__ float part[kThreads / 64][trace_host::kMaxTopk];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint64_t u = blockIdx.x; u < tokens + scans; u += gridDim.x) {
-    if (u >= tokens) {
-      const uint64_t r0 = (u - tokens) * kScanRows;
+  for (uint64_t unit = blockIdx.x; unit < scans + tokens; unit += gridDim.x) {
+    if (unit < scans) {
+      const uint64_t r0 = unit * kScanRows;
       if (threadIdx.x == 0) named = 0;
       __syncthreads();
 #pragma unroll 8
@@ -355,6 +355,7 @@ __global__ __launch_bounds__(kThreads) void expert_combine_bwd_kernel(
       __syncthreads();
       continue;
     }
+    const uint64_t u = unit - scans;
     for (uint32_t j = 0; j < topk; ++j) {
       const int64_t s = slot[u * topk + j];
       const float w = weights ? weights[u * topk + j] : 1.f;
