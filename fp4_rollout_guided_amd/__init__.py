@@ -59,8 +59,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 __all__ = [
-    "TraceError", "LIB_PATH", "SMALLGRID_LIB_PATH", "lib", "load_library", "abi_version", "abi_revision", "tensor_scale",
-    "tensor_scale_noalloc", "capture",
+    "TraceError", "LIB_PATH", "SMALLGRID_LIB_PATH", "lib", "load_library", "abi_version", "abi_revision",
+    "tensor_scale", "tensor_scale_noalloc", "capture",
     "guided_fakequant_fwd", "rne_fakequant_fwd", "full_info_fakequant_fwd", "ste_bwd", "gather_records",
     "gathered_guided_fakequant_fwd", "gathered_rne_fakequant_fwd", "gathered_full_info_fakequant_fwd",
     "grouped_tensor_scale", "grouped_capture", "grouped_guided_fakequant_fwd", "grouped_rne_fakequant_fwd",
@@ -915,8 +915,8 @@ def _matmul(fmt, a_scales, a_codes, offsets, w_scales, w_codes, n, k, row_index,
         _launch(f"trace_{fmt}_matmul", a_codes, _addr(a_scales), _addr(a_codes), rows, _addr(w_scales), _addr(w_codes),
                 n, k, _addr(y))
     else:
-        _launch(f"trace_grouped_{fmt}_matmul{rows_type}", a_codes, _addr(a_scales), _addr(a_codes), src_rows, _addr(row_index),
-                rows, at, groups, _addr(w_scales), _addr(w_codes), n, k, _addr(y))
+        _launch(f"trace_grouped_{fmt}_matmul{rows_type}", a_codes, _addr(a_scales), _addr(a_codes), src_rows,
+                _addr(row_index), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k, _addr(y))
     return y
 
 
@@ -965,8 +965,9 @@ def _linear(fmt, x, offsets, w_scales, w_codes, n, row_index, workspace, y, dtyp
     rows_type = _rows_type(dtype)
     y = _out(y, "y", x, shape, dtype)
     workspace = _workspace(workspace, x, getattr(lib, f"trace_{fmt}_linear_workspace_bytes")(src_rows, rows, groups, k))
-    _launch(f"trace_grouped_{fmt}_linear_f32" if rows_type else f"trace_{fmt}_linear", x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales),
-            _addr(w_codes), n, k, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(y))
+    name = f"trace_grouped_{fmt}_linear_f32" if rows_type else f"trace_{fmt}_linear"
+    _launch(name, x, _addr(x), src_rows, _addr(row_index), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k,
+            _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(y))
     return y
 
 
@@ -1001,8 +1002,9 @@ def _bwd_input(grad_y, offsets, w_scales, w_codes, k, mask, grad_x, dtype=torch.
         _arg(mask, "mask", grad_y, _U8, rows * k // 8)
     rows_type = _rows_type(dtype)
     grad_x = _out(grad_x, "grad_x", grad_y, (*grad_y.shape[:-1], k), dtype)
-    _launch("trace_grouped_mx_matmul_bwd_input_f32" if rows_type else "trace_mx_matmul_bwd_input", grad_y, _addr(grad_y), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k,
-            _addr(mask), _addr(grad_x))
+    name = "trace_grouped_mx_matmul_bwd_input_f32" if rows_type else "trace_mx_matmul_bwd_input"
+    _launch(name, grad_y, _addr(grad_y), rows, at, groups, _addr(w_scales), _addr(w_codes), n, k, _addr(mask),
+            _addr(grad_x))
     return grad_x
 
 
@@ -1117,7 +1119,8 @@ def expert_combine(y, slot, weights=None, out=None):
     if weights is not None:
         _fit(weights, "weights", y, _F32, tokens * topk)
     out = _out(out, "out", y, (tokens, cols), torch.bfloat16)
-    _launch("trace_expert_combine_f32" if f32 else "trace_expert_combine", y, _addr(y), rows, cols, _addr(slot), _addr(weights), tokens, topk, _addr(out))
+    name = "trace_expert_combine_f32" if f32 else "trace_expert_combine"
+    _launch(name, y, _addr(y), rows, cols, _addr(slot), _addr(weights), tokens, topk, _addr(out))
     return out
 
 
@@ -1150,7 +1153,8 @@ class MxMatmul(torch.autograd.Function):
     x: bf16 [rows, k]; w: bf16 [n, k], or [groups, n, k] with ``offsets`` (the
     packed rows' groups).  fmt: "mx" (MXFP4 activations) or "mx8" (MXFP8).
     scales, bits: the rollout's record of x in that format; x is then rounded
-    by the rollout-guided rule instead of to nearest."""
+    by the rollout-guided rule instead of to nearest.  y and both gradients are
+    bf16; the grouped functions themselves also give fp32 rows."""
 
     @staticmethod
     def forward(ctx, x, w, offsets=None, fmt="mx", scales=None, bits=None):
