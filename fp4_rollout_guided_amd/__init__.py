@@ -48,12 +48,25 @@ routed rows (the groups of the grouped_ forms):
                                                         products with dtype=torch.float32)
     expert_combine_bwd(grad_out, y, slot, weights, offsets=None) -> (grad_y, grad_weights)
 
-and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch`` and ``ExpertCombine``
-wrap the forward/backward pairs as autograd functions.
+the rest of a policy's training step:
+
+    expert_route(logits, topk, renormalize=True, valid=None) -> (ids, weights, counts, probs, balance): the router's
+                                                        choices for expert_sort and expert_combine, the balance loss
+    expert_route_bwd(grad_weights, grad_balance, logits, ids, weights, counts) -> grad_logits
+    linear_cross_entropy(x, w, targets, scale=1.0)   -> (loss, lse) of the logits scale * x W^T, which are not kept
+    linear_cross_entropy_bwd(grad_loss, x, w, targets, lse, scale=1.0) -> (grad_x, grad_w)
+    adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr) -> one AdamW step over many tensors, in place, states
+                                                        in fp32 or as MXFP8 records
+
+and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch``, ``ExpertCombine``,
+``ExpertRoute`` and ``LinearCrossEntropy`` wrap the forward/backward pairs as
+autograd functions; ``AdamW`` keeps the optimiser's states.
 """
 import ctypes
 import math
+import operator
 import os
+from array import array
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -73,6 +86,8 @@ __all__ = [
     "mx_matmul_bwd_weight", "mx8_matmul_bwd_weight", "grouped_mx_matmul_bwd_weight", "grouped_mx8_matmul_bwd_weight",
     "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_bwd", "MxMatmul", "ExpertDispatch",
     "ExpertCombine", "MAX_EXPERTS", "MAX_TOPK", "MAX_PRODUCT_GROUPS",
+    "expert_route", "expert_route_bwd", "ExpertRoute", "linear_cross_entropy", "linear_cross_entropy_bwd",
+    "LinearCrossEntropy", "adamw_step", "AdamW", "step_revision",
     "STATUS",
 ]
 
@@ -151,14 +166,24 @@ def load_library(path):
         "trace_expert_dispatch": ([p, i64, i64, p, i64, p, p], st),
         "trace_expert_combine": ([p, i64, i64, p, p, i64, i64, p, p], st),
         "trace_expert_combine_bwd": ([p, p, i64, i64, p, p, i64, i64, p, i64, p, p, p], st),
+        "trace_step_revision": ([], ctypes.c_int),
+        "trace_linear_cross_entropy_workspace_bytes": ([i64, i64, i64], sz),
+        "trace_linear_cross_entropy": ([p, p, p, i64, i64, i64, ctypes.c_float, p, sz, p, p, p], st),
+        "trace_linear_cross_entropy_bwd_workspace_bytes": ([i64, i64, i64], sz),
+        "trace_linear_cross_entropy_bwd": ([p, p, p, p, p, i64, i64, i64, ctypes.c_float, p, sz, p, p, p], st),
+        "trace_expert_route_workspace_bytes": ([i64, i64], sz),
+        "trace_expert_route": ([p, p, i64, i64, i64, ctypes.c_int, p, sz, p, p, p, p, p, p], st),
+        "trace_expert_route_bwd": ([p, p, p, p, p, p, i64, i64, i64, ctypes.c_int, p, p], st),
+        "trace_adamw_step": ([p, ctypes.c_int32, p, p, p], st),
     }
     for name in ("quantize", "matmul", "linear_workspace_bytes", "linear", "matmul_bwd_weight"):
         sig["trace_mx8_" + name] = sig["trace_mx_" + name]
     sig["trace_grouped_mx8_matmul"] = sig["trace_grouped_mx_matmul"]
     for name, like in (("grouped_mx_matmul", "grouped_mx_matmul"), ("grouped_mx8_matmul", "grouped_mx_matmul"),
                        ("grouped_mx_linear", "mx_linear"), ("grouped_mx8_linear", "mx_linear"),
-                       ("grouped_mx_matmul_bwd_input", "mx_matmul_bwd_input"), ("expert_combine", "expert_combine")):
-        sig[f"trace_{name}_f32"] = sig["trace_" + like]  # the same on fp32 packed rows
+                       ("grouped_mx_matmul_bwd_input", "mx_matmul_bwd_input"), ("expert_combine", "expert_combine"),
+                       ("expert_route", "expert_route"), ("expert_route_bwd", "expert_route_bwd")):
+        sig[f"trace_{name}_f32"] = sig["trace_" + like]  # the same on fp32 rows
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
         fn.argtypes = args
@@ -176,6 +201,11 @@ def abi_version() -> int:
 def abi_revision() -> int:
     """Additions within ``abi_version``: 1 has the products and the routed rows."""
     return lib.trace_abi_revision()
+
+
+def step_revision() -> int:
+    """1: the library has the router, the vocabulary loss and the optimiser step."""
+    return lib.trace_step_revision()
 
 
 # --------------------------------------------------------------------------
@@ -1226,3 +1256,353 @@ class ExpertCombine(torch.autograd.Function):
         y, slot, weights, offsets = ctx.saved_tensors
         grad_y, grad_weights = expert_combine_bwd(grad_out.contiguous(), y, slot, weights, offsets)
         return grad_y, None, None if weights is None else grad_weights, None
+
+
+# --------------------------------------------------------------------------
+# the router
+# --------------------------------------------------------------------------
+
+def _router(logits, topk):
+    """(suffix of the entry points, tokens, experts) of router logits."""
+    f32 = isinstance(logits, torch.Tensor) and logits.dtype == torch.float32
+    tokens, experts = _matrix(logits, "logits", _F32 if f32 else _BF16)
+    if not 1 <= experts <= MAX_EXPERTS:
+        raise ValueError(f"experts must be 1 to {MAX_EXPERTS}, got {experts}")
+    if isinstance(topk, bool) or not isinstance(topk, int) or not 1 <= topk <= min(MAX_TOPK, experts):
+        raise ValueError(f"topk must be 1 to {min(MAX_TOPK, experts)}, got {topk!r}")
+    return "_f32" if f32 else "", tokens, experts
+
+
+def expert_route(logits, topk, renormalize=True, valid=None, ids=None, weights=None, counts=None, probs=None,
+                 balance=None, workspace=None):
+    """Each row's topk experts by its router logits (bf16 or fp32
+    [..., experts]; ties go to the lowest index, NaN is above all, -infinity is
+    never taken).  valid: bool or uint8, one per row; rows where it is 0 are
+    left out.  Returns
+
+    ids int64 [tokens, topk]: what ``expert_sort`` takes; -1 for rows left out;
+    weights fp32 [tokens, topk]: the softmax at ids, divided by its sum over
+    them with ``renormalize``; what ``expert_combine`` takes;
+    counts int64 [experts + 1]: the experts' pairs, then the rows routed;
+    probs fp32 [experts]: the softmaxes summed over the rows routed;
+    balance fp32 [1]: experts * sum of (counts / their sum) * (probs / rows)."""
+    suffix, tokens, experts = _router(logits, topk)
+    if valid is not None:
+        _fit(valid, "valid", logits, (torch.bool, torch.uint8), tokens)
+    ids = _out(ids, "ids", logits, (tokens, topk), torch.int64)
+    weights = _out(weights, "weights", logits, (tokens, topk), torch.float32)
+    counts = _out(counts, "counts", logits, (experts + 1,), torch.int64)
+    probs = _out(probs, "probs", logits, (experts,), torch.float32)
+    balance = _out(balance, "balance", logits, (1,), torch.float32)
+    workspace = _workspace(workspace, logits, lib.trace_expert_route_workspace_bytes(tokens, experts))
+    _launch("trace_expert_route" + suffix, logits, _addr(logits), _addr(valid), tokens, experts, topk,
+            int(bool(renormalize)), _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(ids),
+            _addr(weights), _addr(counts), _addr(probs), _addr(balance))
+    return ids, weights, counts, probs, balance
+
+
+def expert_route_bwd(grad_weights, grad_balance, logits, ids, weights, counts, renormalize=True, grad_logits=None):
+    """The gradient to the logits, of their type, from those of the weights
+    (fp32 [tokens, topk]) and of the balance loss (fp32 [1]); None: zeros.
+    ids, weights: the forward's; counts: the forward's, or summed over ranks.
+    grad_logits may be the logits themselves."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [tokens, topk]")
+    suffix, tokens, experts = _router(logits, ids.shape[1])
+    topk = ids.shape[1]
+    _fit(ids, "ids", logits, _I64, tokens * topk)
+    _fit(weights, "weights", logits, _F32, tokens * topk)
+    _fit(counts, "counts", logits, _I64, experts + 1)
+    if grad_weights is not None:
+        _fit(grad_weights, "grad_weights", logits, _F32, tokens * topk)
+    if grad_balance is not None:
+        _fit(grad_balance, "grad_balance", logits, _F32, 1)
+    grad_logits = _out(grad_logits, "grad_logits", logits, tuple(logits.shape),
+                       torch.float32 if suffix else torch.bfloat16)
+    _launch("trace_expert_route_bwd" + suffix, logits, _addr(grad_weights), _addr(grad_balance), _addr(logits),
+            _addr(ids), _addr(weights), _addr(counts), tokens, experts, topk, int(bool(renormalize)),
+            _addr(grad_logits))
+    return grad_logits
+
+
+class ExpertRoute(torch.autograd.Function):
+    """``expert_route`` as (ids, weights, counts, balance), with gradients from
+    the weights and the balance loss to the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, topk, renormalize=True, valid=None):
+        logits = logits.contiguous()
+        ids, weights, counts, _, balance = expert_route(logits, topk, renormalize, valid)
+        ctx.save_for_backward(logits, ids, weights, counts)
+        ctx.renormalize = renormalize
+        ctx.mark_non_differentiable(ids, counts)
+        ctx.set_materialize_grads(False)
+        return ids, weights, counts, balance
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _ids, grad_weights, _counts, grad_balance):
+        logits, ids, weights, counts = ctx.saved_tensors
+        if grad_weights is not None:
+            grad_weights = grad_weights.contiguous()
+        if grad_balance is not None:
+            grad_balance = grad_balance.contiguous()
+        return expert_route_bwd(grad_weights, grad_balance, logits, ids, weights, counts, ctx.renormalize), None, None, None
+
+
+# --------------------------------------------------------------------------
+# the loss over the vocabulary
+# --------------------------------------------------------------------------
+
+def _logits_of(x, w, targets):
+    """(tokens, vocab, k) of the logits x W^T."""
+    tokens, k = _matrix(x, "x")
+    _bf16(w, "w")
+    if w.device != x.device or w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"w must be [vocab, {k}] on {x.device}, got {tuple(w.shape)} on {w.device}")
+    if k == 0 or k % 32:
+        raise ValueError(f"rows must be a multiple of 32 long, got {k}")
+    if w.shape[0] == 0:
+        raise ValueError("the vocabulary is empty")
+    _fit(targets, "targets", x, _I64, tokens)
+    return tokens, w.shape[0], k
+
+
+def linear_cross_entropy(x, w, targets, scale=1.0, loss=None, lse=None, workspace=None):
+    """Softmax cross entropy of the logits scale * x W^T over the vocabulary,
+    without keeping them: (loss, lse), fp32, one per token.  x: bf16 [..., k];
+    w: bf16 [vocab, k], k % 32 == 0; targets: int64, one per token.  loss is
+    minus the target's log-probability; tokens whose target lies outside
+    [0, vocab) are ignored, with loss and lse 0."""
+    tokens, vocab, k = _logits_of(x, w, targets)
+    loss = _out(loss, "loss", x, tuple(x.shape[:-1]), torch.float32)
+    lse = _out(lse, "lse", x, tuple(x.shape[:-1]), torch.float32)
+    workspace = _workspace(workspace, x, lib.trace_linear_cross_entropy_workspace_bytes(tokens, vocab, k))
+    _launch("trace_linear_cross_entropy", x, _addr(x), _addr(w), _addr(targets), tokens, vocab, k, scale,
+            _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(loss), _addr(lse))
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(grad_loss, x, w, targets, lse, scale=1.0, grad_x=None, grad_w=None, workspace=None,
+                             want_x=True, want_w=True):
+    """Gradients of ``linear_cross_entropy``'s loss, the logits computed again a
+    slice of the vocabulary at a time: (grad_x as x, grad_w as w, in bf16; None
+    where not wanted).  grad_loss: fp32, one per token, not read where the token
+    is ignored; lse: the forward's."""
+    tokens, vocab, k = _logits_of(x, w, targets)
+    _fit(grad_loss, "grad_loss", x, _F32, tokens)
+    _fit(lse, "lse", x, _F32, tokens)
+    grad_x = _out(grad_x, "grad_x", x, tuple(x.shape), torch.bfloat16) if want_x else None
+    grad_w = _out(grad_w, "grad_w", x, tuple(w.shape), torch.bfloat16) if want_w else None
+    workspace = _workspace(workspace, x, lib.trace_linear_cross_entropy_bwd_workspace_bytes(tokens, vocab, k))
+    _launch("trace_linear_cross_entropy_bwd", x, _addr(grad_loss), _addr(x), _addr(w), _addr(targets), _addr(lse),
+            tokens, vocab, k, scale, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(grad_x),
+            _addr(grad_w))
+    return grad_x, grad_w
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """``linear_cross_entropy``'s loss per token, with gradients to x and w."""
+
+    @staticmethod
+    def forward(ctx, x, w, targets, scale=1.0):
+        x, w, targets = x.contiguous(), w.contiguous(), targets.contiguous()
+        loss, lse = linear_cross_entropy(x, w, targets, scale)
+        ctx.save_for_backward(x, w, targets, lse)
+        ctx.scale = scale
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss):
+        x, w, targets, lse = ctx.saved_tensors
+        grad_x, grad_w = linear_cross_entropy_bwd(grad_loss.contiguous(), x, w, targets, lse, ctx.scale,
+                                                  want_x=ctx.needs_input_grad[0], want_w=ctx.needs_input_grad[1])
+        return grad_x, grad_w, None, None
+
+
+# --------------------------------------------------------------------------
+# the optimiser step
+# --------------------------------------------------------------------------
+
+class _AdamwOptions(ctypes.Structure):
+    """trace_adamw_options of include/trace.h."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)] + [
+        (n, ctypes.c_int32) for n in ("param_bf16", "grad_bf16", "states_mx8", "randomly")]
+
+
+_TENSOR_WORDS = 8  # of trace_adamw_tensor: param, grad, avg, sq, avg_scales, sq_scales, copy, n
+_dtype_of = operator.attrgetter("dtype")
+_F32_OR_BF16 = (torch.float32, torch.bfloat16)
+
+
+def _tensors(ts, name, dtypes, device, numels=None):
+    """Check a list of tensors as ``_arg`` does one: all of one type.  The list
+    is walked by C calls: a step has hundreds of them."""
+    try:
+        found = set(map(_dtype_of, ts))
+        devices = set(map(torch.Tensor.get_device, ts))
+        whole = all(map(torch.Tensor.is_contiguous, ts))
+    except (AttributeError, TypeError):
+        raise TypeError(f"{name} must be tensors") from None
+    if len(found) > 1 or not found <= set(dtypes):
+        raise TypeError(f"{name} must all be {' or all '.join(map(str, dtypes))}, got {sorted(map(str, found))}")
+    if devices - {device} or device < 0:
+        raise ValueError(f"{name} must be on one device, the parameters'")
+    if not whole:
+        raise ValueError(f"{name} must be contiguous")
+    got = list(map(torch.Tensor.numel, ts))
+    if numels is not None and got != numels:
+        raise ValueError(f"{name} must hold as many elements as the parameters' {'blocks' if 'scales' in name else 'own'}")
+    return got
+
+
+def _states(avgs, sqs, numels, device):
+    """Whether the states are 8-bit records, after their checks."""
+    if len(avgs) != len(numels) or len(sqs) != len(numels):
+        raise ValueError("one state of each kind per parameter is required")
+    mx8 = bool(numels) and isinstance(avgs[0], (tuple, list))
+    for states, name in ((avgs, "exp_avgs"), (sqs, "exp_avg_sqs")):
+        if mx8:
+            if not all(isinstance(s, (tuple, list)) and len(s) == 2 for s in states):
+                raise TypeError(f"{name} must all be (scales, codes)")
+            _tensors([s[0] for s in states], name + " scales", _U8, device, [(n + 31) // 32 for n in numels])
+            _tensors([s[1] for s in states], name + " codes", _U8, device, numels)
+        else:
+            _tensors(states, name, _F32, device, numels)
+    return mx8
+
+
+def _state_words(words, avgs, sqs, mx8):
+    """Addresses of the states into the tensors' words."""
+    ptr = torch.Tensor.data_ptr
+    if mx8:
+        for at, states, part in ((2, avgs, 1), (3, sqs, 1), (4, avgs, 0), (5, sqs, 0)):
+            words[at::_TENSOR_WORDS] = array("Q", [s[part].data_ptr() for s in states])
+    else:
+        words[2::_TENSOR_WORDS] = array("Q", map(ptr, avgs))
+        words[3::_TENSOR_WORDS] = array("Q", map(ptr, sqs))
+
+
+def _adamw(words, params, grads, copies, numels, mx8, device, step, lr, betas, eps, weight_decay, grad_scale, seed):
+    """The call, once params and states have been checked; words: the states'."""
+    if grad_scale is not None:
+        _fit(grad_scale, "grad_scale", params[0], _F32, 1)
+    if len(grads) != len(params):
+        raise ValueError("one gradient per parameter is required")
+    _tensors(grads, "grads", _F32_OR_BF16, device, numels)
+    ptr = torch.Tensor.data_ptr
+    words[0::_TENSOR_WORDS] = array("Q", map(ptr, params))
+    words[1::_TENSOR_WORDS] = array("Q", map(ptr, grads))
+    words[7::_TENSOR_WORDS] = array("Q", numels)
+    param_bf16 = params[0].dtype == torch.bfloat16
+    if copies is not None:
+        if param_bf16:
+            raise ValueError("copies are for fp32 parameters")
+        if len(copies) != len(params):
+            raise ValueError("one copy per parameter is required")
+        _tensors(copies, "copies", (torch.bfloat16,), device, numels)
+        words[6::_TENSOR_WORDS] = array("Q", map(ptr, copies))
+    if mx8 and seed is None:
+        raise ValueError("8-bit states are rounded at random: seed is required")
+    if seed is not None and (isinstance(seed, bool) or not isinstance(seed, int) or not 0 <= seed < 1 << 64):
+        raise ValueError(f"seed must be an integer of 64 bits, got {seed!r}")
+    options = _AdamwOptions(lr, betas[0], betas[1], eps, weight_decay, step, seed or 0, param_bf16,
+                            grads[0].dtype == torch.bfloat16, mx8, seed is not None)
+    _launch("trace_adamw_step", params[0], words.buffer_info()[0], len(params), ctypes.addressof(options),
+            _addr(grad_scale))
+    torch.autograd.graph.increment_version(params)
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+               grad_scale=None, copies=None, seed=None):
+    """One AdamW step over lists of tensors, in place, in fp32 throughout.
+
+    params: all fp32 or all bf16; grads: likewise, independently.  exp_avgs,
+    exp_avg_sqs: fp32 tensors, or MXFP8 records (scales u8[ceil(n/32)], codes
+    u8[n]) of the first moment and of the second one's square root, zeros to
+    begin with.  step: 1 for the first.  grad_scale: fp32[1] on the device, a
+    factor of every gradient (clipping, unscaling).  copies: bf16 tensors that
+    fp32 parameters are rounded into (the forward's weights).  seed: random
+    roundings of the records and of bf16 parameters, which keep their means;
+    another one for each step.  Without it bf16 parameters go to nearest, and
+    records are refused: rounded to nearest they would stand still.
+
+    The numbers are those of the call: a captured graph replays them."""
+    params, grads = list(params), list(grads)
+    if not params:
+        return
+    device = params[0].get_device() if isinstance(params[0], torch.Tensor) else -1
+    numels = _tensors(params, "params", _F32_OR_BF16, device)
+    mx8 = _states(exp_avgs, exp_avg_sqs, numels, device)
+    words = array("Q", bytes(8 * _TENSOR_WORDS * len(params)))
+    _state_words(words, exp_avgs, exp_avg_sqs, mx8)
+    _adamw(words, params, grads, copies, numels, mx8, device, step, lr, betas, eps, weight_decay, grad_scale, seed)
+
+
+class AdamW:
+    """``adamw_step`` with the states of its parameters: fp32 (states="fp32") or
+    MXFP8 records (states="mx8").  The random bits of step t are those of seed
+    + t; seed None: fp32 states, bf16 parameters rounded to nearest.  lr, betas,
+    eps and weight_decay are plain attributes, read at each step.  copies: as for
+    ``adamw_step``."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="fp32", copies=None,
+                 seed=None):
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.weight_decay, self.copies = lr, betas, eps, weight_decay, copies
+        self.steps, self.seed = 0, seed
+        if states not in ("fp32", "mx8"):
+            raise ValueError(f'states must be "fp32" or "mx8", got {states!r}')
+        if states == "mx8" and seed is None:
+            raise ValueError("8-bit states are rounded at random: seed is required")
+        if not self.params:
+            raise ValueError("no parameters")
+        self._device = self.params[0].get_device() if isinstance(self.params[0], torch.Tensor) else -1
+        self._numels = _tensors(self.params, "params", _F32_OR_BF16, self._device)
+        self._mx8 = states == "mx8"
+
+        def zeros(p):
+            if not self._mx8:
+                return torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            n = p.numel()
+            return (torch.zeros((n + 31) // 32, dtype=torch.uint8, device=p.device),
+                    torch.zeros(n, dtype=torch.uint8, device=p.device))
+
+        self._avgs, self._sqs = [zeros(p) for p in self.params], [zeros(p) for p in self.params]
+        self._words = array("Q", bytes(8 * _TENSOR_WORDS * len(self.params)))
+        _state_words(self._words, self._avgs, self._sqs, self._mx8)
+
+    def step(self, grads=None, grad_scale=None):
+        """One step with these gradients, or the parameters' own .grad."""
+        params = self.params
+        if grads is None:
+            grads = [p.grad for p in params]
+            if any(g is None for g in grads):
+                raise ValueError("a parameter has no gradient")
+        _tensors(params, "params", _F32_OR_BF16, self._device, self._numels)  # again: their storage may be another one
+        t = self.steps + 1
+        seed = None if self.seed is None else (self.seed + t) % (1 << 64)
+        _adamw(self._words, params, list(grads), self.copies, self._numels, self._mx8, self._device, t, self.lr,
+               self.betas, self.eps, self.weight_decay, grad_scale, seed)
+        self.steps = t
+
+    def zero_grad(self):
+        for p in self.params:
+            p.grad = None
+
+    def state_dict(self):
+        """The states themselves, not copies."""
+        return {"steps": self.steps, "seed": self.seed, "exp_avgs": list(self._avgs), "exp_avg_sqs": list(self._sqs)}
+
+    def load_state_dict(self, state):
+        """Copies states of the same kind and sizes into these."""
+        avgs, sqs = state["exp_avgs"], state["exp_avg_sqs"]
+        if _states(avgs, sqs, self._numels, self._device) != self._mx8:
+            raise TypeError("the states are of the other kind")
+        for mine, theirs in ((self._avgs, avgs), (self._sqs, sqs)):
+            for to, of in zip(mine, theirs):
+                for a, b in zip(to, of) if self._mx8 else ((to, of),):
+                    a.copy_(b.view(a.shape))
+        self.steps, self.seed = state["steps"], state["seed"]

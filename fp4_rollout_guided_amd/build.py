@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtrace.so")
 SOURCES = ["kernels.hip", "mx_kernels.hip", "mx8_kernels.hip", "diag_kernels.hip", "mx_quantize.hip", "mx_product.hip",
-           "mx_product_bwd.hip", "expert_rows.hip", "api.cpp", "api_mx_product.cpp"]
+           "mx_product_bwd.hip", "expert_rows.hip", "cross_entropy.hip", "expert_route.hip", "adamw.hip", "api.cpp",
+           "api_mx_product.cpp", "api_step.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,712 @@
+// libtrace softmax cross entropy over a large vocabulary for gfx950, and its
+// gradients, without keeping the logits:
+//
+//   z[t, v] = scale * sum over k of x[t, k] w[v, k]
+//   lse[t] = log(sum over v of exp(z[t, v])),  loss[t] = lse[t] - z[t, target[t]]
+//   P[t, v] = scale * grad_loss[t] * (exp(z[t, v] - lse[t]) - (v == target[t]))
+//   grad_x = P W,  grad_w = P^T X
+//
+// Forward: each tile of logits leaves the maximum and the sum of its columns for
+// every token, and the target's logit where it has it; one more launch joins the
+// tiles.  Backward: a slice of the vocabulary at a time, the logits are computed
+// again and P is written in bf16 to the workspace; then the slice's part of
+// grad_x is added to fp32 sums, and its rows of grad_w are finished.
+//
+// Tokens without a target (prompts, padding) are taken out before: the rows
+// that remain are listed, and for the backward pass packed, so that ignored rows
+// are neither read nor paid for.
+//
+// P is rounded to bf16 for the matrix instructions.  Its entries are divided by
+// the largest |grad_loss| first, which is multiplied back in fp32: equal gradients
+// (a mean) then leave the target's entry, close to one, nearly unrounded, where
+// they would otherwise round all of a batch's rows the same way.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bf16_tile.h"
+#include "device_math.h"
+#include "fp4_block.h"
+#include "launch.h"
+#include "launch_step.h"
+
+namespace trace_dev {
+
+using trace_host::CrossEntropyArgs;
+
+constexpr uint32_t kTileT = 256;  // tokens and vocabulary of the largest tile
+constexpr uint32_t kPlanThreads = 1024;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// What the kernels of a call pass on in its workspace.
+struct CrossEntropyPlan {
+  uint32_t count;     // tokens with a target
+  float grad_top;     // the largest finite |grad_loss| among them, or 1 where that is 0
+  uint32_t pad[14];
+  uint32_t zeros[16];  // what a copy past the end of k reads
+};
+static_assert(sizeof(CrossEntropyPlan) == 128, "two lines");
+
+__device__ __forceinline__ uint32_t tiles_of(uint32_t n, uint32_t each) { return (n + each - 1) / each; }
+
+// list[i]: the i-th token with a target; at[t]: the place of token t, or -1.
+__global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const int64_t* __restrict__ targets,
+                                                                          const float* __restrict__ grad_loss,
+                                                                          uint32_t tokens, uint32_t vocab,
+                                                                          CrossEntropyPlan* plan, int32_t* list,
+                                                                          int32_t* at) {
+  constexpr uint32_t kWaves = kPlanThreads / 64, kEach = 8;
+  __shared__ uint32_t part[kWaves];
+  __shared__ uint32_t tops[kWaves];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t before = 0, top = 0;
+  for (uint64_t t0 = 0; t0 < tokens; t0 += kPlanThreads * kEach) {
+    // a wave's kEach * 64 tokens follow each other
+    bool has[kEach];
+    uint64_t mask[kEach];
+    uint32_t mine = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint64_t t = t0 + (wave * kEach + i) * 64 + lane;
+      has[i] = false;
+      if (t < tokens) {
+        const int64_t v = targets[t];
+        has[i] = v >= 0 && v < (int64_t)vocab;
+        if (grad_loss && has[i]) {
+          const uint32_t g = __float_as_uint(grad_loss[t]) & 0x7fffffffu;
+          if (g < 0x7f800000u) top = g > top ? g : top;
+        }
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      mask[i] = __ballot(has[i]);
+      mine += (uint32_t)__popcll(mask[i]);
+    }
+    __syncthreads();
+    if (lane == 0) part[wave] = mine;
+    __syncthreads();
+    uint32_t place = before;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) {
+      place += w < wave ? part[w] : 0u;
+      before += part[w];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const uint64_t t = t0 + (wave * kEach + i) * 64 + lane;
+      const uint32_t p = place + (uint32_t)__popcll(mask[i] & ((1ull << lane) - 1));
+      if (t < tokens) {
+        at[t] = has[i] ? (int32_t)p : -1;
+        if (has[i]) list[p] = (int32_t)t;
+      }
+      place += (uint32_t)__popcll(mask[i]);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
+    top = o > top ? o : top;
+  }
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (uint32_t w = 1; w < kWaves; ++w) top = tops[w] > top ? tops[w] : top;
+    plan->count = before;
+    plan->grad_top = top ? __uint_as_float(top) : 1.f;
+  }
+  if (threadIdx.x < 16) plan->zeros[threadIdx.x] = 0;
+}
+
+// The backward pass's rows: x packed (zeros up to the next multiple of kTileT),
+// and for each the gradient over grad_top, lse in powers of two and the target.
+struct PackedRow {
+  float grad;
+  float lse2;
+  int32_t target;
+  int32_t pad;
+};
+__global__ __launch_bounds__(256) void cross_entropy_pack_kernel(CrossEntropyArgs p, const float* __restrict__ grad_loss,
+                                                                 const float* __restrict__ lse,
+                                                                 const CrossEntropyPlan* __restrict__ plan,
+                                                                 const int32_t* __restrict__ list, uint4* rows,
+                                                                 PackedRow* about) {
+  const uint32_t vecs = p.k / 8, count = plan->count;
+  const uint64_t all = (uint64_t)tiles_of(count, kTileT) * kTileT * vecs;
+  const uint64_t stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
+    const uint32_t r = (uint32_t)(i / vecs), c = (uint32_t)(i - (uint64_t)r * vecs);
+    const int64_t t = r < count ? list[r] : -1;
+    rows[i] = t >= 0 ? reinterpret_cast<const uint4*>(p.x)[(uint64_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
+    if (c == 0) {
+      PackedRow a{0.f, 0.f, -1, 0};
+      if (t >= 0) a = PackedRow{grad_loss[t] / plan->grad_top, lse[t] * kLog2e, (int32_t)p.targets[t], 0};
+      about[r] = a;
+    }
+  }
+}
+
+__device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// A maximum and the sum of 2^(value - maximum); an empty one is (-infinity, 0).
+struct TopSum {
+  float top, sum;
+};
+__device__ __forceinline__ TopSum join(TopSum a, TopSum b) {
+  const float top = fmaxf(a.top, b.top);
+  if (top == -__builtin_inff()) return TopSum{top, a.sum + b.sum};
+  return TopSum{top, a.sum * exp2_of(a.top - top) + b.sum * exp2_of(b.top - top)};
+}
+
+// The logits' tile: rows i of the vocabulary from v0 (v_end: past the slice),
+// columns j of tokens.  kPacked: tokens are rows of the packed x.
+// Forward: part[tile of v][token], hit[token].  Backward: P.
+struct LogitsArgs {
+  CrossEntropyArgs p;
+  const CrossEntropyPlan* plan;  // nullptr: every token, in its own place
+  const int32_t* list;           // forward: the tokens' rows
+  TopSum* part;                  // [tiles of v][pitch]
+  float* hit;
+  uint64_t pitch;           // of part, tokens
+  const uint16_t* rows;     // backward: packed x
+  const PackedRow* about;
+  uint16_t* probs;          // P of the slice, [tokens rounded up][slice]
+  uint32_t v0, slice;       // slice: a multiple of kTileT
+};
+
+template <class T, bool kBackward, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(LogitsArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  const CrossEntropyArgs& p = a.p;
+  const uint32_t count = a.plan ? a.plan->count : (uint32_t)p.tokens;
+  const uint32_t v_end = p.vocab - a.v0 < a.slice ? p.vocab : a.v0 + a.slice;
+  const uint32_t tiles_v = tiles_of(v_end - a.v0, T::kRowsI), tiles_t = tiles_of(count, T::kRowsJ);
+  const uint64_t tiles = (uint64_t)tiles_v * tiles_t;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  // eight tiles of tokens at a time: an XCD's tiles share rows of both operands
+  constexpr uint32_t kGroup = 8;
+  const uint32_t group = (uint32_t)(tile / ((uint64_t)kGroup * tiles_v));
+  const uint32_t in = (uint32_t)(tile - (uint64_t)group * kGroup * tiles_v);
+  const uint32_t wide = tiles_t - group * kGroup < kGroup ? tiles_t - group * kGroup : kGroup;
+  const uint32_t tile_v = in / wide, tile_t = group * kGroup + in % wide;
+  const uint32_t v0 = a.v0 + tile_v * T::kRowsI, t0 = tile_t * T::kRowsJ;
+  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wi = T::wave_i(), wj = T::wave_j();
+
+  const char *from_i[T::I::kCopies], *from_j[T::J::kCopies];
+  uint32_t col_i[T::I::kCopies], col_j[T::J::kCopies];
+#pragma unroll
+  for (uint32_t n = 0; n < T::I::kCopies; ++n) {
+    uint32_t row;
+    T::I::place(wave, n, row, col_i[n]);
+    const uint32_t v = v0 + row < p.vocab ? v0 + row : p.vocab - 1;  // past the last one: any, left out below
+    from_i[n] = reinterpret_cast<const char*>(p.w + (uint64_t)v * p.k + col_i[n]);
+  }
+#pragma unroll
+  for (uint32_t n = 0; n < T::J::kCopies; ++n) {
+    uint32_t row;
+    T::J::place(wave, n, row, col_j[n]);
+    uint64_t t = t0 + row;
+    if (!kBackward) {
+      t = t < count ? t : count - 1;
+      if (a.plan) t = (uint32_t)a.list[t];
+    }
+    from_j[n] = reinterpret_cast<const char*>((kBackward ? a.rows : p.x) + t * p.k + col_j[n]);
+  }
+  // k is a multiple of 32: in a last half stage the pieces past it are zeros in both operands
+  const uint32_t stages = tiles_of(p.k, kStageC), whole = p.k / kStageC;
+  const char* zeros = reinterpret_cast<const char*>(a.plan ? a.plan->zeros : static_cast<CrossEntropyPlan*>(p.workspace)->zeros);
+  v16f acc[T::kI][T::kJ] = {};
+  T::multiply(
+      ring, stages,
+      [&](uint32_t n, uint32_t st) {
+        const char* at = from_i[n] + 2 * kStageC * st;
+        return st < whole || col_i[n] < kStageC / 2 ? at : zeros;
+      },
+      [&](uint32_t n, uint32_t st) {
+        const char* at = from_j[n] + 2 * kStageC * st;
+        return st < whole || col_j[n] < kStageC / 2 ? at : zeros;
+      },
+      acc);
+
+  // register e of block (i, j): v = wi + 32 i + 16 (e / 8) + 8 h + e % 8, token wj + 32 j + r
+  const float to_log2 = p.scale * kLog2e;
+  const bool ends = v0 + T::kRowsI > v_end;
+#pragma unroll
+  for (int j = 0; j < T::kJ; ++j) {
+    const uint32_t t = t0 + wj + 32 * j + r;
+    int32_t target = -1;  // within this lane's rows: v - v0 - wi - 8 h
+    PackedRow about{0.f, 0.f, -1, 0};
+    if (kBackward) {
+      about = a.about[t];
+      target = about.target;
+    } else if (t < count) {
+      const int64_t v = p.targets[a.plan ? (uint32_t)a.list[t] : t];
+      target = v >= 0 && v < (int64_t)p.vocab ? (int32_t)v : -1;
+    }
+    target -= (int32_t)(v0 + wi);  // a target of -1 is below every row
+    const bool hits = __ballot(target >= 0 && target < 32 * T::kI) != 0;
+    if constexpr (!kBackward) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t row = 32 * i + 16 * (e / 8) + 8 * h + e % 8;
+          if (hits && target == (int32_t)row) a.hit[t] = acc[i][j][e] * p.scale;
+          float z = acc[i][j][e] * to_log2;
+          if (ends && v0 + wi + row >= v_end) z = -__builtin_inff();
+          acc[i][j][e] = z;
+          top = fmaxf(top, z);
+        }
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float from = top == -__builtin_inff() ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += exp2_of(acc[i][j][e] - from);
+      sum += __shfl_xor(sum, 32);
+      if (h == 0) reinterpret_cast<TopSum*>(ring)[wi / (32 * T::kI) * T::kRowsJ + wj + 32 * j + r] = TopSum{top, sum};
+    } else {
+      static_assert(!kBackward || T::kI == 4, "a wave's rows are 256 bytes of P");
+      const RowBlock<16> block{ring + 512 * 16 * wave};
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float d[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t row = 32 * i + 16 * q + 8 * h + e;
+            float v = exp2_of(acc[i][j][8 * q + e] * to_log2 - about.lse2);
+            if (hits && target == (int32_t)row) v -= 1.f;
+            d[e] = ends && v0 + wi + row >= v_end ? 0.f : v * about.grad;
+          }
+          uint32_t u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bf16x2 two = __builtin_convertvector((f32x2){d[2 * e], d[2 * e + 1]}, bf16x2);
+            __builtin_memcpy(&u[e], &two, 4);
+          }
+          block.put(r, 4 * i + 2 * q + h, make_uint4(u[0], u[1], u[2], u[3]));
+        }
+      block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+        const uint64_t at = (uint64_t)(t0 + wj + 32 * j + row) * a.slice + (v0 - a.v0) + wi + 8 * piece;
+        *reinterpret_cast<uint4*>(a.probs + at) = v;
+      });
+    }
+  }
+  if constexpr (!kBackward) {
+    __syncthreads();
+    for (uint32_t j = threadIdx.x; j < T::kRowsJ; j += 256) {
+      TopSum s = reinterpret_cast<const TopSum*>(ring)[j];
+#pragma unroll
+      for (int w = 1; w < T::kWI; ++w) s = join(s, reinterpret_cast<const TopSum*>(ring)[w * T::kRowsJ + j]);
+      if (t0 + j < count) a.part[(uint64_t)tile_v * a.pitch + t0 + j] = s;
+    }
+  }
+}
+
+// Joins the tiles: 16 tokens to a workgroup, 64 lanes to each.
+__global__ __launch_bounds__(1024) void cross_entropy_join_kernel(CrossEntropyArgs p, const int32_t* __restrict__ at,
+                                                                  const TopSum* __restrict__ part, uint64_t pitch,
+                                                                  uint32_t tiles, const float* __restrict__ hit,
+                                                                  float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ TopSum sums[1024];
+  const uint32_t j = threadIdx.x % 16, share = threadIdx.x / 16;
+  const uint64_t t = (uint64_t)blockIdx.x * 16 + j;
+  bool has = t < p.tokens;
+  uint64_t place = t;
+  if (has) {
+    if (at) {
+      has = at[t] >= 0;
+      place = has ? (uint32_t)at[t] : 0;
+    } else {
+      const int64_t v = p.targets[t];
+      has = v >= 0 && v < (int64_t)p.vocab;
+    }
+  }
+  TopSum s{-__builtin_inff(), 0.f};
+  if (has) {
+#pragma unroll 4
+    for (uint32_t i = share; i < tiles; i += 64) s = join(s, part[i * pitch + place]);
+  }
+  sums[threadIdx.x] = s;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t d = 32; d >= 1; d >>= 1) {
+    if (share < d) sums[threadIdx.x] = join(sums[threadIdx.x], sums[threadIdx.x + 16 * d]);
+    __syncthreads();
+  }
+  if (share == 0 && t < p.tokens) {
+    const TopSum all = sums[j];
+    const float l = has ? all.top * kLn2 + logf(all.sum) : 0.f;
+    lse[t] = l;
+    loss[t] = has ? l - hit[place] : 0.f;
+  }
+}
+
+// grad_x's sums over a slice of the vocabulary: i along k, j the packed tokens.
+struct GradRowsArgs {
+  CrossEntropyArgs p;
+  const CrossEntropyPlan* plan;
+  const uint16_t* probs;
+  uint32_t v0, slice, parts;
+  bool first;     // of the slices
+  float* sums;    // [parts][pitch][k]
+  uint64_t pitch;
+};
+template <class T, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(GradRowsArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  const CrossEntropyArgs& p = a.p;
+  const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_t = tiles_of(a.plan->count, T::kRowsJ);
+  const uint64_t tiles = (uint64_t)tiles_k * tiles_t * a.parts;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const uint32_t part = (uint32_t)(tile / ((uint64_t)tiles_k * tiles_t));
+  const uint32_t in = (uint32_t)(tile - (uint64_t)part * tiles_k * tiles_t);
+  const uint32_t k0 = in % tiles_k * T::kRowsI, t0 = in / tiles_k * T::kRowsJ;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t all = tiles_of(p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice, kStageC);
+  const uint32_t begin = (uint32_t)((uint64_t)all * part / a.parts), end = (uint32_t)((uint64_t)all * (part + 1) / a.parts);
+  const uint32_t left = p.vocab - a.v0;  // rows of w from the slice on; P is zero past them, any row will do
+  uint32_t row_i[T::I::kCopies];
+  const uint16_t* from_i[T::I::kCopies];
+  const uint16_t* from_j[T::J::kCopies];
+#pragma unroll
+  for (uint32_t n = 0; n < T::I::kCopies; ++n) {
+    uint32_t col;
+    T::I::place(wave, n, row_i[n], col);
+    from_i[n] = p.w + (uint64_t)a.v0 * p.k + (k0 + col < p.k ? k0 + col : 0);
+  }
+#pragma unroll
+  for (uint32_t n = 0; n < T::J::kCopies; ++n) {
+    uint32_t row, col;
+    T::J::place(wave, n, row, col);
+    from_j[n] = a.probs + (uint64_t)(t0 + row) * a.slice + col;
+  }
+  v16f acc[T::kI][T::kJ] = {};
+  T::multiply(
+      ring, end - begin,
+      [&](uint32_t n, uint32_t st) {
+        const uint32_t v = (begin + st) * kStageC + row_i[n];
+        return from_i[n] + (uint64_t)(v < left ? v : left - 1) * p.k;
+      },
+      [&](uint32_t n, uint32_t st) { return from_j[n] + (begin + st) * kStageC; }, acc);
+  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const uint32_t wi = T::wave_i(), wj = T::wave_j();
+  const RowBlock<16> block{ring + 512 * 16 * wave};
+#pragma unroll
+  for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+    for (int i = 0; i < T::kI; i += 2) {  // 64 k at a time
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[i + q / 2][j][8 * (q & 1) + e];
+        put_f32(block, r, 4 * q + 2 * h, v);
+      }
+      block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+        const uint32_t k = k0 + wi + 32 * i + 4 * piece;
+        if (k >= p.k) return;
+        float4* at = reinterpret_cast<float4*>(a.sums + (part * a.pitch + t0 + wj + 32 * j + row) * p.k + k);
+        float4 s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+        if (!a.first) {
+          const float4 o = *at;
+          s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+        }
+        *at = s;
+      });
+    }
+}
+
+// grad_x = grad_top * scale * the parts' sums, to the tokens' own rows; zeros for ignored ones.
+__global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p,
+                                                                 const CrossEntropyPlan* __restrict__ plan,
+                                                                 const int32_t* __restrict__ at,
+                                                                 const float* __restrict__ sums, uint32_t parts,
+                                                                 uint64_t pitch, uint16_t* __restrict__ grad_x) {
+  const uint32_t vecs = p.k / 8;
+  const uint64_t all = p.tokens * vecs, stride = (uint64_t)gridDim.x * 256;
+  const float by = plan->grad_top * p.scale;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
+    const uint64_t t = i / vecs, c = i - t * vecs;
+    const int32_t row = at[t];
+    uint32_t u[4] = {0, 0, 0, 0};
+    if (row >= 0) {
+      float v[8] = {};
+      for (uint32_t s = 0; s < parts; ++s) {
+        const float* from = sums + (s * pitch + (uint32_t)row) * p.k + 8 * c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += from[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bf16x2 two = __builtin_convertvector((f32x2){v[2 * e] * by, v[2 * e + 1] * by}, bf16x2);
+        __builtin_memcpy(&u[e], &two, 4);
+      }
+    }
+    reinterpret_cast<uint4*>(grad_x)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// grad_w's rows of a slice: i along k, j the vocabulary.
+struct GradWeightArgs {
+  CrossEntropyArgs p;
+  const CrossEntropyPlan* plan;
+  const uint16_t* rows;
+  const uint16_t* probs;
+  uint32_t v0, slice;
+  uint16_t* grad_w;
+};
+template <class T, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(GradWeightArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  static_assert(T::kI == 4, "a wave's rows are 256 bytes of the result");
+  const CrossEntropyArgs& p = a.p;
+  const uint32_t left = p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice;
+  const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_v = tiles_of(left, T::kRowsJ);
+  const uint64_t tiles = (uint64_t)tiles_k * tiles_v;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  const uint32_t k0 = (uint32_t)(tile % tiles_k) * T::kRowsI, v0 = (uint32_t)(tile / tiles_k) * T::kRowsJ;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint16_t* from_i[T::I::kCopies];
+  const uint16_t* from_j[T::J::kCopies];
+#pragma unroll
+  for (uint32_t n = 0; n < T::I::kCopies; ++n) {
+    uint32_t row, col;
+    T::I::place(wave, n, row, col);
+    from_i[n] = a.rows + (uint64_t)row * p.k + (k0 + col < p.k ? k0 + col : 0);
+  }
+#pragma unroll
+  for (uint32_t n = 0; n < T::J::kCopies; ++n) {
+    uint32_t row, col;
+    T::J::place(wave, n, row, col);
+    from_j[n] = a.probs + (uint64_t)row * a.slice + v0 + col;
+  }
+  v16f acc[T::kI][T::kJ] = {};
+  T::multiply(
+      ring, tiles_of(a.plan->count, kStageC),
+      [&](uint32_t n, uint32_t st) { return from_i[n] + (uint64_t)st * kStageC * p.k; },
+      [&](uint32_t n, uint32_t st) { return from_j[n] + (uint64_t)st * kStageC * a.slice; }, acc);
+  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const uint32_t wi = T::wave_i(), wj = T::wave_j();
+  const float by = a.plan->grad_top * p.scale;
+  const RowBlock<16> block{ring + 512 * 16 * wave};
+#pragma unroll
+  for (int j = 0; j < T::kJ; ++j) {
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bf16x2 two = __builtin_convertvector(
+              (f32x2){acc[i][j][8 * q + 2 * e] * by, acc[i][j][8 * q + 2 * e + 1] * by}, bf16x2);
+          __builtin_memcpy(&u[e], &two, 4);
+        }
+        block.put(r, 4 * i + 2 * q + h, make_uint4(u[0], u[1], u[2], u[3]));
+      }
+    block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+      const uint32_t n = v0 + wj + 32 * j + row, k = k0 + wi + 8 * piece;
+      if (n < left && k < p.k) *reinterpret_cast<uint4*>(a.grad_w + ((uint64_t)a.v0 + n) * p.k + k) = v;
+    });
+  }
+}
+
+// grad_w of no tokens.
+__global__ __launch_bounds__(256) void cross_entropy_clear_kernel(uint4* out, uint64_t nvec) {
+  const uint64_t stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < nvec; i += stride) out[i] = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace trace_dev
+
+namespace trace_host {
+
+using namespace trace_dev;
+
+namespace {
+
+constexpr uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// Tiles of the forward by the tokens: rows of the vocabulary x tokens.
+using Logits256 = Tile<4, 4, 2, 2, false, false, 2>;
+using Logits128 = Tile<4, 2, 2, 2, false, false, 3>;
+using Logits64 = Tile<2, 1, 2, 2, false, false, 3>;
+using Logits32 = Tile<1, 1, 4, 1, false, false, 3>;
+using Probs256 = Tile<4, 4, 2, 2, false, false, 2>;
+using GradRows256 = Tile<4, 4, 2, 2, true, false, 2>;
+using GradWeight256 = Tile<4, 4, 2, 2, true, true, 2>;
+
+// Few tokens are not listed: every one is computed, in its own place.
+constexpr uint64_t kUnlisted = 64;
+
+uint32_t tile_rows_v(uint64_t tokens) { return tokens <= 64 ? 128u : 256u; }
+
+// Workspace of the forward.
+struct ForwardSpace {
+  uint64_t pitch, tiles, list, at, part, hit, bytes;
+  ForwardSpace(uint64_t tokens, uint32_t vocab) {
+    pitch = round_up(tokens, 16);
+    tiles = (vocab + tile_rows_v(tokens) - 1) / tile_rows_v(tokens);
+    const uint64_t lists = tokens > kUnlisted ? 4 * pitch : 0;
+    list = sizeof(CrossEntropyPlan);
+    at = list + lists;
+    hit = at + lists;
+    part = hit + 4 * pitch;
+    bytes = part + tiles * pitch * sizeof(TopSum);
+  }
+};
+
+// Workspace of the backward pass.
+struct BackwardSpace {
+  uint64_t tall;   // tokens rounded up to whole tiles
+  uint32_t slice;  // of the vocabulary
+  uint32_t parts;  // of a slice's contraction for grad_x
+  uint64_t list, at, about, rows, probs, sums, bytes;
+  BackwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
+    tall = round_up(tokens, kTileT);
+    // P of half a gigabyte, but at least 8192 columns, to fill the card with tiles of grad_w
+    uint64_t s = (1ull << 28) / tall / kTileT * kTileT;
+    if (s < 8192) s = 8192;
+    if (s > round_up(vocab, kTileT)) s = round_up(vocab, kTileT);
+    slice = (uint32_t)s;
+    const uint64_t tiles = tall / kTileT * ((k + kTileT - 1) / kTileT);
+    parts = (uint32_t)(1024 / tiles < 1 ? 1 : (1024 / tiles > 16 ? 16 : 1024 / tiles));
+    list = sizeof(CrossEntropyPlan);
+    at = list + 4 * tall;
+    about = at + 4 * tall;
+    rows = about + sizeof(PackedRow) * tall;
+    probs = rows + 2 * tall * k;
+    sums = probs + 2 * tall * slice;
+    bytes = sums + 4 * (uint64_t)parts * tall * k;
+  }
+};
+
+uint32_t xcd_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
+constexpr uint64_t kMostTiles = (1u << 24) - 8;  // a launch counts its work-items in 32 bits
+
+template <class T, int kPerCu>
+hipError_t run_logits(const LogitsArgs& a, uint64_t tokens, hipStream_t stream) {
+  const uint64_t tiles = (uint64_t)((a.p.vocab + T::kRowsI - 1) / T::kRowsI) * ((tokens + T::kRowsJ - 1) / T::kRowsJ);
+  hipLaunchKernelGGL((cross_entropy_logits_kernel<T, false, kPerCu>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t cross_entropy_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t k) {
+  (void)k;
+  return ForwardSpace(tokens, vocab).bytes;
+}
+
+uint64_t cross_entropy_bwd_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t k) {
+  return BackwardSpace(tokens, vocab, k).bytes;
+}
+
+hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* lse, hipStream_t stream) {
+  const ForwardSpace s(p.tokens, p.vocab);
+  if (s.tiles * ((p.tokens + kTileT - 1) / kTileT) > kMostTiles) return hipErrorInvalidConfiguration;
+  char* const at = static_cast<char*>(p.workspace);
+  const bool listed = p.tokens > kUnlisted;
+  LogitsArgs a{};
+  a.p = p;
+  a.part = reinterpret_cast<TopSum*>(at + s.part);
+  a.hit = reinterpret_cast<float*>(at + s.hit);
+  a.pitch = s.pitch;
+  a.slice = (uint32_t)round_up(p.vocab, kTileT);
+  CrossEntropyPlan* const plan = reinterpret_cast<CrossEntropyPlan*>(at);
+  int32_t* const list = reinterpret_cast<int32_t*>(at + s.list);
+  int32_t* const places = listed ? reinterpret_cast<int32_t*>(at + s.at) : nullptr;
+  if (listed || p.k % kStageC) {
+    hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, (const float*)nullptr,
+                       listed ? (uint32_t)p.tokens : 0u, p.vocab, plan, list, places);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (listed) {
+    a.plan = plan;
+    a.list = list;
+  }
+  const hipError_t e = p.tokens <= 32    ? run_logits<Logits32, 2>(a, p.tokens, stream)
+                       : p.tokens <= 64  ? run_logits<Logits64, 2>(a, p.tokens, stream)
+                       : p.tokens <= 128 ? run_logits<Logits128, 1>(a, p.tokens, stream)
+                                         : run_logits<Logits256, 1>(a, p.tokens, stream);
+  if (e) return e;
+  hipLaunchKernelGGL(cross_entropy_join_kernel, dim3((uint32_t)((p.tokens + 15) / 16)), dim3(1024), 0, stream, p, places,
+                     (const TopSum*)a.part, s.pitch, (uint32_t)s.tiles, (const float*)a.hit, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad_loss, const float* lse,
+                                    uint16_t* grad_x, uint16_t* grad_w, hipStream_t stream) {
+  const auto groups = [](uint64_t vecs) {
+    const uint64_t n = (vecs + 255) / 256, most = 8192 < kMaxGroups ? 8192 : kMaxGroups;
+    return dim3((uint32_t)(n < most ? n : most));
+  };
+  if (p.tokens == 0) {
+    const uint64_t vecs = (uint64_t)p.vocab * p.k / 8;
+    hipLaunchKernelGGL(cross_entropy_clear_kernel, groups(vecs), dim3(256), 0, stream, reinterpret_cast<uint4*>(grad_w),
+                       vecs);
+    return hipGetLastError();
+  }
+  const BackwardSpace s(p.tokens, p.vocab, p.k);
+  const uint64_t tiles_t = s.tall / kTileT, tiles_k = (p.k + kTileT - 1) / kTileT;
+  if (s.slice / kTileT * tiles_t > kMostTiles || tiles_t * tiles_k * s.parts > kMostTiles ||
+      s.slice / kTileT * tiles_k > kMostTiles)
+    return hipErrorInvalidConfiguration;
+  char* const at = static_cast<char*>(p.workspace);
+  CrossEntropyPlan* const plan = reinterpret_cast<CrossEntropyPlan*>(at);
+  int32_t* const list = reinterpret_cast<int32_t*>(at + s.list);
+  int32_t* const places = reinterpret_cast<int32_t*>(at + s.at);
+  PackedRow* const about = reinterpret_cast<PackedRow*>(at + s.about);
+  uint16_t* const rows = reinterpret_cast<uint16_t*>(at + s.rows);
+  uint16_t* const probs = reinterpret_cast<uint16_t*>(at + s.probs);
+  float* const sums = reinterpret_cast<float*>(at + s.sums);
+  hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, grad_loss,
+                     (uint32_t)p.tokens, p.vocab, plan, list, places);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL(cross_entropy_pack_kernel, groups(s.tall * (p.k / 8)), dim3(256), 0, stream, p, grad_loss, lse,
+                     (const CrossEntropyPlan*)plan, (const int32_t*)list, reinterpret_cast<uint4*>(rows), about);
+  if (hipError_t e = hipGetLastError()) return e;
+  for (uint64_t v0 = 0; v0 < p.vocab; v0 += s.slice) {
+    LogitsArgs a{};
+    a.p = p;
+    a.plan = plan;
+    a.rows = rows;
+    a.about = about;
+    a.probs = probs;
+    a.v0 = (uint32_t)v0;
+    a.slice = s.slice;
+    hipLaunchKernelGGL((cross_entropy_logits_kernel<Probs256, true, 1>), dim3(xcd_grid(s.slice / kTileT * tiles_t)),
+                       dim3(256), 0, stream, a);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (grad_x) {
+      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, s.parts, v0 == 0, sums, s.tall};
+      hipLaunchKernelGGL((cross_entropy_grad_rows_kernel<GradRows256, 1>), dim3(xcd_grid(tiles_t * tiles_k * s.parts)),
+                         dim3(256), 0, stream, g);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (grad_w) {
+      const GradWeightArgs g{p, plan, rows, probs, (uint32_t)v0, s.slice, grad_w};
+      hipLaunchKernelGGL((cross_entropy_grad_weight_kernel<GradWeight256, 1>), dim3(xcd_grid(s.slice / kTileT * tiles_k)),
+                         dim3(256), 0, stream, g);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+  }
+  if (grad_x) {
+    hipLaunchKernelGGL(cross_entropy_rows_kernel, groups(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
+                       (const CrossEntropyPlan*)plan, (const int32_t*)places, (const float*)sums, s.parts, s.tall, grad_x);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace trace_host

@@ -736,6 +736,127 @@ TRACE_API trace_status trace_expert_combine_bwd(const uint16_t* grad_out, const 
                                                 int64_t tokens, int64_t topk, const int64_t* offsets, int64_t groups,
                                                 uint16_t* grad_y, float* grad_weights, void* stream);
 
+/*
+ * The rest of a policy's training step: the loss over the vocabulary, the
+ * router, and the optimiser.  These entry points were added after revision 1 of
+ * this version; trace_step_revision() names them, and a library from before
+ * them has no trace_step_revision.
+ */
+#define TRACE_STEP_REVISION 1
+TRACE_API int trace_step_revision(void);
+
+/* Softmax cross entropy of the logits z = scale * x W^T, which are not kept:
+ *   lse[t]  = log(sum over v of exp(z[t][v])),
+ *   loss[t] = lse[t] - z[t][targets[t]]  (minus the token's log-probability).
+ * A token whose target lies outside [0, vocab) is ignored: its loss and lse are
+ * 0, and nothing depends on its row of x.
+ *   x : bf16[tokens*k]; w : bf16[vocab*k]; targets : int64[tokens]; loss, lse :
+ *   fp32[tokens]; k a multiple of 32, at least 32; vocab at least 1.
+ *   workspace : trace_linear_cross_entropy_workspace_bytes(tokens, vocab, k)
+ *   bytes, 16-byte aligned, contents not preserved.
+ * Products of bf16 are exact in fp32, sums are fp32. */
+TRACE_API size_t trace_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t k);
+TRACE_API trace_status trace_linear_cross_entropy(const uint16_t* x, const uint16_t* w, const int64_t* targets,
+                                                  int64_t tokens, int64_t vocab, int64_t k, float scale,
+                                                  void* workspace, size_t workspace_bytes, float* loss, float* lse,
+                                                  void* stream);
+
+/* Its gradients, from the forward's lse:
+ *   P[t][v] = scale * grad_loss[t] * (exp(z[t][v] - lse[t]) - (v == targets[t])),
+ *   grad_x = P W (bf16[tokens*k]; zeros for ignored tokens, whose grad_loss is
+ *   not read), grad_w = P^T x (bf16[vocab*k]).
+ * grad_x or grad_w may be NULL: that gradient is not computed.  P passes
+ * through the workspace a slice of the vocabulary at a time, rounded to bf16.
+ *   workspace : trace_linear_cross_entropy_bwd_workspace_bytes(tokens, vocab, k)
+ *   bytes, 16-byte aligned. */
+TRACE_API size_t trace_linear_cross_entropy_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t k);
+TRACE_API trace_status trace_linear_cross_entropy_bwd(const float* grad_loss, const uint16_t* x, const uint16_t* w,
+                                                      const int64_t* targets, const float* lse, int64_t tokens,
+                                                      int64_t vocab, int64_t k, float scale, void* workspace,
+                                                      size_t workspace_bytes, uint16_t* grad_x, uint16_t* grad_w,
+                                                      void* stream);
+
+/* The router: each row's topk experts by its logits, their weights, and what the
+ * balance loss needs.
+ *   logits : bf16 (trace_expert_route) or fp32 (trace_expert_route_f32),
+ *            [tokens*experts], any alignment of their type;
+ *   valid  : u8[tokens], 0 for a row that is left out, or NULL;
+ *   ids    : int64[tokens*topk], the experts of the topk largest logits in
+ *            descending order, the lowest index first among equals (NaN above
+ *            all); an expert whose logit is -infinity is never taken: -1 in its
+ *            place, and in all places of a row that is left out;
+ *   weights: fp32[tokens*topk], softmax of the row at ids, divided by the sum
+ *            over the chosen where renormalize is not 0; 0 beside id -1;
+ *   counts : int64[experts + 1], the pairs of each expert, and the rows routed;
+ *   probs  : fp32[experts], the softmaxes summed over the rows routed;
+ *   balance: fp32[1], experts * sum over e of
+ *            (counts[e] / sum of counts) * (probs[e] / counts[experts]), 0 with no rows;
+ *   workspace : trace_expert_route_workspace_bytes(tokens, experts) bytes, 16-byte
+ *            aligned (NULL where that is 0).
+ *   1 <= topk <= min(64, experts), experts <= 1024, tokens*topk below 2^31. */
+TRACE_API size_t trace_expert_route_workspace_bytes(int64_t tokens, int64_t experts);
+TRACE_API trace_status trace_expert_route(const uint16_t* logits, const uint8_t* valid, int64_t tokens,
+                                          int64_t experts, int64_t topk, int renormalize, void* workspace,
+                                          size_t workspace_bytes, int64_t* ids, float* weights, int64_t* counts,
+                                          float* probs, float* balance, void* stream);
+TRACE_API trace_status trace_expert_route_f32(const float* logits, const uint8_t* valid, int64_t tokens,
+                                              int64_t experts, int64_t topk, int renormalize, void* workspace,
+                                              size_t workspace_bytes, int64_t* ids, float* weights, int64_t* counts,
+                                              float* probs, float* balance, void* stream);
+
+/* The gradient to the logits, of their type, from those of the weights
+ * (fp32[tokens*topk], not read beside id -1) and of the balance loss (fp32[1], on
+ * the device); either may be NULL for zeros.  ids, weights : the forward's.
+ * counts : the forward's, or their sums over several ranks, whose balance loss is
+ * then the gradient's (grad_balance with all ranks' rows in it).  Rows whose ids
+ * are all -1 get zeros. */
+TRACE_API trace_status trace_expert_route_bwd(const float* grad_weights, const float* grad_balance,
+                                              const uint16_t* logits, const int64_t* ids, const float* weights,
+                                              const int64_t* counts, int64_t tokens, int64_t experts, int64_t topk,
+                                              int renormalize, uint16_t* grad_logits, void* stream);
+TRACE_API trace_status trace_expert_route_bwd_f32(const float* grad_weights, const float* grad_balance,
+                                                  const float* logits, const int64_t* ids, const float* weights,
+                                                  const int64_t* counts, int64_t tokens, int64_t experts,
+                                                  int64_t topk, int renormalize, float* grad_logits, void* stream);
+
+/* One AdamW step over many tensors, in place, in fp32, each operation rounded by
+ * itself:
+ *   g = grad * *grad_scale (fp32[1] on the device; NULL: 1)
+ *   m = m * beta1 + g * (1 - beta1),  v = v * beta2 + (g * g) * (1 - beta2)
+ *   param = param * (1 - lr * weight_decay)
+ *           - (m / (sqrt(v) * (1 / sqrt(1 - beta2^step)) + eps)) * (lr / (1 - beta1^step))
+ * with the factors in parentheses computed in fp64 and rounded to fp32.
+ *   param  : fp32 or bf16 (param_bf16), n elements; grad likewise (grad_bf16);
+ *   avg, sq: m and v in fp32; or, with states_mx8, the E4M3 codes (u8[n]) of m and
+ *            of sqrt(v), whose E8M0 bytes are avg_scales and sq_scales
+ *            (u8[ceil(n / 32)], one per 32 elements, the last of them perhaps
+ *            fewer).  All bytes 0: zeros.  A block with an infinity or a NaN gets
+ *            byte 255 and is NaN from then on;
+ *   copy   : bf16[n], param rounded to nearest (fp32 params), or NULL.
+ * 8-bit states, and bf16 params with `randomly` not 0, are rounded to one of
+ * their two neighbours at random, so that the mean is kept, by bits of `seed`
+ * and the element's place in the list; other roundings are to nearest.
+ * The tensors are the same in type.  Data 16-byte aligned (codes 4-byte,
+ * scale bytes any).  No element may belong to two tensors. */
+typedef struct trace_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* avg;
+  void* sq;
+  uint8_t* avg_scales;
+  uint8_t* sq_scales;
+  uint16_t* copy;
+  int64_t n;
+} trace_adamw_tensor;
+typedef struct trace_adamw_options {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step; /* 1 for the first */
+  uint64_t seed;
+  int32_t param_bf16, grad_bf16, states_mx8, randomly;
+} trace_adamw_options;
+TRACE_API trace_status trace_adamw_step(const trace_adamw_tensor* tensors, int32_t count,
+                                        const trace_adamw_options* options, const float* grad_scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
