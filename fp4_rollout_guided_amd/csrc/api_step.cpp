@@ -16,7 +16,7 @@ using namespace trace_api;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
-constexpr int64_t kMaxDim = (int64_t)1 << 24;
+constexpr int64_t kMaxDim = (int64_t)1 << 20;  // a tile's rows are addressed in 32 bits
 
 trace_status launch_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? TRACE_E_SHAPE : hip_status(e); }
 

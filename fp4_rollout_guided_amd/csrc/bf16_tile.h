@@ -1,19 +1,24 @@
 // Tiles of bf16 products with fp32 sums (gfx950), for the loss over the
 // vocabulary and its gradients:  D[i, j] = sum over c of I(i, c) J(j, c).
 //
-// A workgroup of four waves, kWI x kWJ of them, owns 32 kWI kI results i times
-// 32 kWJ kJ results j, each wave kI x kJ blocks of the 32x32x16 instruction.  A
-// lane holds one j and, in consecutive registers, eight consecutive i at a time.
+// A workgroup of four waves, kWI x kWJ of them, owns 16 kWI kI results i times
+// 16 kWJ kJ results j, each wave kI x kJ blocks of the 16x16x32 instruction.  A
+// lane holds one j and, in the registers of two neighbouring blocks, eight
+// consecutive i.
 //
 // Each operand lies in memory either along c (rows i or j of consecutive c) or
 // across it (rows c of consecutive i or j).  Stages of 64 c are copied straight
-// to LDS, 1 KiB (64 lanes' 16 bytes) per instruction, kRing stages in turn, one
-// barrier per stage; the copies run kRing - 1 stages ahead of the arithmetic.
-// Place i of a copy's KiB belongs to lane i, so the lanes choose which 16 bytes
-// they fetch: pieces are permuted by their row's bits, so that the rows that are
-// read together lie in different banks.  Operands across c are read back
-// transposed (ds_read_b64_tr_b16: 16 lanes read four rows of 16 values, lane i
-// gets column i).
+// to LDS, 1 KiB (64 lanes' 16 bytes) per instruction, a few stages in turn, one
+// barrier per stage.  Place i of a copy's KiB belongs to lane i, so the lanes
+// choose which 16 bytes they fetch: pieces are permuted by their row's bits, so
+// that the rows that are read together lie in different banks.  Operands across c
+// are read back transposed (ds_read_b64_tr_b16: 16 lanes read four rows of 16
+// values, lane i gets column i).
+//
+// What bounds the largest tile (256 x 256) is power: at full use of the matrix
+// units the clock falls from 2.4 to some 1.8 GHz.  The 16x16x32 instruction does
+// 1.67 PFLOP/s alone where 32x32x16 does 1.51 (it moves fewer bytes of sums for a
+// product), and 1.40 against 1.30 with the reads of LDS under it.
 //
 // The copies are written as assembly: the compiler would wait for all of them
 // before each read of LDS.  They have no result registers; the barrier below waits
@@ -22,6 +27,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device_math.h"
 #include "fp4_block.h"
@@ -35,19 +42,53 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 
 constexpr uint32_t kStageC = 64;  // c of a stage
 
+// This lane's number in its wave, by a value that is not known before this point:
+// or what a tile's end computes from it would fill registers throughout its loop.
+__device__ __forceinline__ uint32_t late_lane() {
+  uint32_t lane = threadIdx.x & 63;
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(lane));
+#endif
+  return lane;
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
 
-// Copies 16 bytes per lane to lds + 16 * lane.
-__device__ __forceinline__ void copy_to_lds(const void* from, uint32_t lds) {
+// Where the next copies go in LDS: lds + 16 * lane, and kAt bytes on below.
+__device__ __forceinline__ void copies_to(uint32_t lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds));
+#endif
+}
+// Copies 16 bytes per lane from base + off + kAt, in the lanes that `lanes` has:
+// all of them or none (all are active here).
+template <uint32_t kAt>
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint64_t lanes) {
+  static_assert(kAt < 4096, "the instruction's offset");
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%2\n\ts_mov_b64 exec, -1" ::"v"(off),
+               "s"(base), "n"(kAt), "s"(lanes));
 #endif
 }
 
-// All but the last kLeft copies of this wave have arrived and its LDS reads are
-// done; meet the workgroup's other waves.
+// A loop whose index is a constant.
+template <uint32_t kFrom, uint32_t kTo, class F>
+__device__ __forceinline__ void unrolled(const F& f) {
+  if constexpr (kFrom < kTo) {
+    f(std::integral_constant<uint32_t, kFrom>());
+    unrolled<kFrom + 1, kTo>(f);
+  }
+}
+
+// This wave's LDS reads are done (and, of its copies, all but the last kLeft);
+// meet the workgroup's other waves.
+__device__ __forceinline__ void reads_barrier() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#endif
+}
 template <uint32_t kLeft>
 __device__ __forceinline__ void stage_barrier() {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -64,27 +105,33 @@ struct TileOperand {
   static constexpr uint32_t kCopies = kBytes / 4096;  // per wave
   static constexpr uint32_t kPitch = kAcross ? 2 * kRows : 128;
 
-  // What this lane fetches with copy n of its wave: the row of the operand in
-  // memory and its first of eight columns.
-  static __device__ __forceinline__ void place(uint32_t wave, uint32_t n, uint32_t& row, uint32_t& col) {
-    const uint32_t at = 1024 * (wave * kCopies + n) + 16 * (threadIdx.x & 63);
-    row = at / kPitch;
-    const uint32_t piece = at % kPitch / 16;
-    col = 8 * (kAcross ? piece ^ ((row & 3) << 2) : piece ^ ((row >> 1) & 7));
+  // How a row's pieces are permuted.  Along c, 16 lanes read one piece of 16 rows
+  // that differ in bits 0 to 3, or 0, 1, 3 and 4 (kPairs below), two rows to 256
+  // bytes; across it 32 bytes of four rows.
+  static __device__ __forceinline__ uint32_t swap(uint32_t row) {
+    return kAcross ? (row & 3) << 2 : ((row >> 1) & 1) | ((row >> 2) & 2) | (((row ^ (row >> 2)) & 4));
   }
 
-  // Operand registers of k-step kk, rows first + 32 f + (lane % 32).  kSwap:
-  // rows 4..7 and 8..11 of every 16 trade places (a lane's eight consecutive
-  // results are then eight consecutive i).
-  template <bool kSwap>
+  // What this lane fetches with copy n of its wave: the row of the operand in
+  // memory and its first of eight columns.
+  static __device__ __forceinline__ void place(uint32_t wave, uint32_t lane, uint32_t n, uint32_t& row, uint32_t& col) {
+    const uint32_t at = 1024 * (wave * kCopies + n) + 16 * lane;
+    row = at / kPitch;
+    col = 8 * ((at % kPitch / 16) ^ swap(row));
+  }
+
+  // Operand registers of k-step kk (32 c): block f, 16 rows from first + 16 f,
+  // this lane's (lane % 16).  kPairs: blocks 2 q and 2 q + 1 share 32 rows, the
+  // first with those whose bit 2 is 0 (a lane's results in both are then eight
+  // consecutive ones).
+  template <bool kPairs>
   static __device__ __forceinline__ v8bf read(const char* stage, uint32_t first, uint32_t f, uint32_t kk) {
-    const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+    const uint32_t lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
     if constexpr (kAcross) {
-      const uint32_t j = lane & 15, half = (lane >> 4) & 1;
-      const uint32_t quad = kSwap ? ((j & 1) << 1) | ((j >> 1) & 1) : j & 3;
-      const uint32_t row = 8 * h + (j >> 2);  // and four rows on, whose low bits are the same
-      const uint32_t piece = first / 8 + 4 * f + 2 * half + (quad >> 1);
-      const char* at = stage + (16 * kk + row) * kPitch + 16 * (piece ^ ((row & 3) << 2)) + 8 * (quad & 1);
+      const uint32_t row = 8 * g + (q >> 2), run = q & 3;  // and four rows on, whose low bits are the same
+      const uint32_t piece = first / 8 + (kPairs ? 4 * (f / 2) + run : 2 * f + (run >> 1));
+      const uint32_t half = kPairs ? f & 1 : run & 1;
+      const char* at = stage + (32 * kk + row) * kPitch + 16 * (piece ^ swap(row)) + 8 * half;
       const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
       const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * kPitch));
       v8bf out;
@@ -92,8 +139,8 @@ struct TileOperand {
       __builtin_memcpy(reinterpret_cast<char*>(&out) + 8, &hi, 8);
       return out;
     } else {
-      const uint32_t row = first + 32 * f + (kSwap ? (r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1) : r);
-      return *reinterpret_cast<const v8bf*>(stage + row * kPitch + 16 * ((2 * kk + h) ^ ((row >> 1) & 7)));
+      const uint32_t row = first + (kPairs ? 32 * (f / 2) + 8 * (q >> 2) + 4 * (f & 1) + (q & 3) : 16 * f + q);
+      return *reinterpret_cast<const v8bf*>(stage + row * kPitch + 16 * ((4 * kk + g) ^ swap(row)));
     }
   }
 };
@@ -101,77 +148,155 @@ struct TileOperand {
 template <int kI_, int kJ_, int kWI_, int kWJ_, bool kAcrossI, bool kAcrossJ, int kRing_>
 struct Tile {
   static constexpr int kI = kI_, kJ = kJ_, kWI = kWI_, kWJ = kWJ_;
-  static constexpr uint32_t kRing = kRing_;
-  static constexpr uint32_t kRowsI = 32 * kI * kWI, kRowsJ = 32 * kJ * kWJ;
+  static constexpr uint32_t kRing = kRing_;  // stages in LDS
+  static constexpr uint32_t kRowsI = 16 * kI * kWI, kRowsJ = 16 * kJ * kWJ;
   using I = TileOperand<kRowsI, kAcrossI>;
   using J = TileOperand<kRowsJ, kAcrossJ>;
-  static constexpr uint32_t kStageBytes = I::kBytes + J::kBytes;
-  static constexpr uint32_t kLds = kRing * kStageBytes;
+  static constexpr uint32_t kStageBytes = I::kBytes + J::kBytes, kLds = kRing * kStageBytes;
   static constexpr uint32_t kCopies = I::kCopies + J::kCopies;
-  static_assert(kWI * kWJ == 4, "four waves");
-  static_assert(kCopies * (kRing - 2) < 64, "copies that the wait can count");
+  static_assert(kWI * kWJ == 4 && kI % 2 == 0 && kRing >= 2, "four waves, pairs of blocks");
+  static_assert(kCopies * (kRing - 1) < 64 && kLds <= 163840, "what the wait can count; LDS");
 
   // This wave's first row of the tile's I and J.
   static __device__ __forceinline__ uint32_t wave_i() {
-    return 32 * kI * (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWJ);
+    return 16 * kI * (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWJ);
   }
   static __device__ __forceinline__ uint32_t wave_j() {
-    return 32 * kJ * (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWJ);
+    return 16 * kJ * (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWJ);
   }
 
-  // from_i(n, stage), from_j(n, stage): where this lane's 16 bytes of copy n of a
-  // stage lie.  Leaves every wave past its last read of the ring.
-  template <class FromI, class FromJ>
-  static __device__ __forceinline__ void multiply(char* ring, uint32_t stages, FromI from_i, FromJ from_j,
-                                                  v16f (&acc)[kI][kJ]) {
+  // Where an operand's copies come from: base + stage * step, the same for all
+  // lanes, and each lane's place in a stage for each of its wave's copies.
+  template <class Operand>
+  struct Source {
+    const char* base;
+    uint64_t step;
+    uint32_t off[Operand::kCopies];
+  };
+
+  // Sums of `stages` stages.  From stage `whole` on (the last one, or none) lanes
+  // would pass an operand's end: before its copies shorten(from_i, from_j) moves
+  // their places.  half: of the last stage only the first k-step counts.  Leaves
+  // every wave past its last read of the ring that matters.
+  //
+  // A stage is two k-steps; under the arithmetic of each the next one's operands
+  // are read.  Half way through the first, when all waves have read the stage's
+  // second half, its slot is free, and the copies of the stage kRing on go there:
+  // they have more than kRing - 1 stages' time.  The order is the program's own
+  // (sched_barrier): the compiler would gather the reads before their use,
+  // where they are waited for.  There is one copy of the arithmetic, since branches
+  // around products would move their sums between registers; past the last stage
+  // the copies run with no lanes, and the reads find an old stage.
+  template <class Shorten>
+  static __device__ __forceinline__ void multiply(char* ring, uint32_t stages, uint32_t whole, bool half,
+                                                  Source<I>& from_i, Source<J>& from_j, Shorten shorten,
+                                                  v4f (&acc)[kI][kJ]) {
+    constexpr uint32_t kProducts = kI * kJ, kFragments = kI + kJ;
+    constexpr uint32_t kHalf = (kProducts + 1) / 2, kReadsEach = (kFragments + kHalf - 1) / kHalf;
+    // the product after which a slot is free, products to a copy and copies to a product after that
+    constexpr uint32_t kRead = (kFragments + kReadsEach - 1) / kReadsEach - 1;  // the last product that reads follow
+    constexpr uint32_t kFree = kRead > kProducts * 5 / 16 ? kRead : kProducts * 5 / 16, kLeft = kProducts - kFree;
+    constexpr uint32_t kEvery = kLeft / kCopies < 1 ? 1 : (kLeft / kCopies > 2 ? 2 : kLeft / kCopies);
+    constexpr uint32_t kAtOnce = kLeft / kCopies < 1 ? (kCopies + kLeft - 1) / kLeft : 1;
+    if (stages == 0) return;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t base = __builtin_amdgcn_readfirstlane(lds_address(ring));
-    const auto fetch = [&](uint32_t st, uint32_t slot) {
-      const uint32_t to = base + slot * kStageBytes;
+    // this wave's part of slot 0 of either operand
+    const uint32_t to_i = __builtin_amdgcn_readfirstlane(lds_address(ring)) + 1024 * I::kCopies * wave;
+    const uint32_t to_j = __builtin_amdgcn_readfirstlane(lds_address(ring)) + I::kBytes + 1024 * J::kCopies * wave;
+    // the instruction's offset moves the place in memory too
 #pragma unroll
-      for (uint32_t n = 0; n < I::kCopies; ++n) copy_to_lds(from_i(n, st), to + 1024 * (wave * I::kCopies + n));
+    for (uint32_t n = 0; n < I::kCopies; ++n) from_i.off[n] += 4096 - 1024 * (n % 4);
 #pragma unroll
-      for (uint32_t n = 0; n < J::kCopies; ++n)
-        copy_to_lds(from_j(n, st), to + I::kBytes + 1024 * (wave * J::kCopies + n));
+    for (uint32_t n = 0; n < J::kCopies; ++n) from_j.off[n] += 4096 - 1024 * (n % 4);
+    const char* next_i = from_i.base - 4096;
+    const char* next_j = from_j.base - 4096;
+    uint64_t lanes = ~0ull;
+    const auto copy = [&](auto n, uint32_t slot) {
+      constexpr uint32_t kN = decltype(n)::value;
+      if constexpr (kN < J::kCopies) {
+        if constexpr (kN % 4 == 0) copies_to(to_j + slot * kStageBytes + 1024 * kN);
+        copy_to_lds<1024 * (kN % 4)>(next_j, from_j.off[kN], lanes);
+      } else if constexpr (kN < kCopies) {
+        constexpr uint32_t kM = kN - J::kCopies;
+        if constexpr (kM % 4 == 0) copies_to(to_i + slot * kStageBytes + 1024 * kM);
+        copy_to_lds<1024 * (kM % 4)>(next_i, from_i.off[kM], lanes);
+      }
     };
     const uint32_t wi = wave_i(), wj = wave_j();
     v8bf fi[2][kI], fj[2][kJ];
-    const auto read = [&](uint32_t slot, uint32_t kk, v8bf(&a)[kI], v8bf(&b)[kJ]) {
+    // fragment f of a k-step, in the order of their first use
+    const auto read = [&](auto f, uint32_t slot, uint32_t kk) {
+      constexpr uint32_t kF = decltype(f)::value;
       const char* from = ring + slot * kStageBytes;
-#pragma unroll
-      for (uint32_t f = 0; f < kI; ++f) a[f] = I::template read<true>(from, wi, f, kk);
-#pragma unroll
-      for (uint32_t f = 0; f < kJ; ++f) b[f] = J::template read<false>(from + I::kBytes, wj, f, kk);
+      if constexpr (kF == 0 || (kF > kJ && kF < kFragments))
+        fi[kk][kF == 0 ? 0 : kF - kJ] = I::template read<true>(from, wi, kF == 0 ? 0 : kF - kJ, kk);
+      else if constexpr (kF <= kJ)
+        fj[kk][kF - 1] = J::template read<false>(from + I::kBytes, wj, kF - 1, kk);
     };
-    const auto multiply_step = [&](const v8bf(&a)[kI], const v8bf(&b)[kJ]) {
-#pragma unroll
-      for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    // k-step kk; under it `under` is called after each product
+    const auto products = [&](uint32_t kk, const auto& under) {
+      unrolled<0, kProducts>([&](auto m) {
+        constexpr uint32_t kM = decltype(m)::value;
+        acc[kM / kJ][kM % kJ] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fi[kk][kM / kJ], fj[kk][kM % kJ], acc[kM / kJ][kM % kJ], 0, 0, 0);
+        under(m);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     };
-    if (stages == 0) return;
+    const auto read_under = [&](auto m, uint32_t slot, uint32_t kk) {
+      constexpr uint32_t kM = decltype(m)::value;
+      unrolled<kM * kReadsEach, (kM + 1) * kReadsEach>([&](auto f) { read(f, slot, kk); });
+    };
 #pragma unroll
-    for (uint32_t s = 0; s < kRing - 1; ++s)
-      if (s < stages) fetch(s, s);
+    for (uint32_t s = 0; s < kRing; ++s) {
+      if (s >= stages) continue;
+      if (s == whole) shorten(from_i, from_j);
+      unrolled<0, kCopies>([&](auto n) { copy(n, s); });
+      next_i += from_i.step;
+      next_j += from_j.step;
+    }
     stage_barrier<0>();
-    read(0, 0, fi[0], fj[0]);
+    unrolled<0, kFragments>([&](auto f) { read(f, 0, 0); });
     uint32_t slot = 0;
+#pragma unroll 1
     for (uint32_t st = 0; st < stages; ++st) {
-      const uint32_t ahead = slot == 0 ? kRing - 1 : slot - 1;  // the slot of stage st - 1, free since the last barrier
-      const bool more = st + kRing - 1 < stages;
-      if (more) fetch(st + kRing - 1, ahead);
-#pragma unroll
-      for (uint32_t kk = 0; kk < 3; ++kk) {
-        read(slot, kk + 1, fi[(kk + 1) & 1], fj[(kk + 1) & 1]);
-        multiply_step(fi[kk & 1], fj[kk & 1]);
+      if (st + kRing >= whole) {
+        if (st + kRing >= stages)
+          lanes = 0;
+        else
+          shorten(from_i, from_j);
       }
-      slot = slot + 1 == kRing ? 0 : slot + 1;
-      if (more)
-        stage_barrier<kCopies * (kRing - 2)>();
+      products(0, [&](auto m) {
+        constexpr uint32_t kM = decltype(m)::value;
+        read_under(m, slot, 1);
+        if constexpr (kM == kFree) reads_barrier();
+        if constexpr (kM >= kFree && (kM - kFree) % kEvery == 0)
+          unrolled<(kM - kFree) / kEvery * kAtOnce, (kM - kFree) / kEvery * kAtOnce + kAtOnce>(
+              [&](auto n) { copy(n, slot); });
+      });
+      if (st + kRing < stages)
+        stage_barrier<kCopies * (kRing - 1)>();
       else
         stage_barrier<0>();
-      if (st + 1 < stages) read(slot, 0, fi[0], fj[0]);
-      multiply_step(fi[1], fj[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      next_i += from_i.step;
+      next_j += from_j.step;
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      if (half && st + 1 == stages) {
+#pragma unroll
+        for (int f = 0; f < kI; ++f) fi[1][f] = v8bf{};
+#pragma unroll
+        for (int f = 0; f < kJ; ++f) fj[1][f] = v8bf{};
+      }
+      products(1, [&](auto m) { read_under(m, slot, 0); });
+#ifdef __HIP_DEVICE_COMPILE__
+      // sums that fill half of the registers stay in that half, whatever follows the loop
+      if constexpr (kProducts == 64)
+#pragma unroll
+        for (int i = 0; i < kI; ++i)
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+#endif
     }
   }
 };

@@ -42,10 +42,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 struct CrossEntropyPlan {
   uint32_t count;     // tokens with a target
   float grad_top;     // the largest finite |grad_loss| among them, or 1 where that is 0
-  uint32_t pad[14];
-  uint32_t zeros[16];  // what a copy past the end of k reads
+  uint32_t pad[30];
 };
-static_assert(sizeof(CrossEntropyPlan) == 128, "two lines");
+static_assert(sizeof(CrossEntropyPlan) == 128, "a line of its own");
 
 __device__ __forceinline__ uint32_t tiles_of(uint32_t n, uint32_t each) { return (n + each - 1) / each; }
 
@@ -115,11 +114,11 @@ __global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const 
     plan->count = before;
     plan->grad_top = top ? __uint_as_float(top) : 1.f;
   }
-  if (threadIdx.x < 16) plan->zeros[threadIdx.x] = 0;
 }
 
-// The backward pass's rows: x packed (zeros up to the next multiple of kTileT),
-// and for each the gradient over grad_top, lse in powers of two and the target.
+// The rows with a target: x packed (zeros up to the next multiple of kTileT), and
+// for the backward pass the gradient over grad_top, lse in powers of two and the
+// target of each.
 struct PackedRow {
   float grad;
   float lse2;
@@ -138,12 +137,19 @@ __global__ __launch_bounds__(256) void cross_entropy_pack_kernel(CrossEntropyArg
     const uint32_t r = (uint32_t)(i / vecs), c = (uint32_t)(i - (uint64_t)r * vecs);
     const int64_t t = r < count ? list[r] : -1;
     rows[i] = t >= 0 ? reinterpret_cast<const uint4*>(p.x)[(uint64_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
-    if (c == 0) {
+    if (about && c == 0) {
       PackedRow a{0.f, 0.f, -1, 0};
       if (t >= 0) a = PackedRow{grad_loss[t] / plan->grad_top, lse[t] * kLog2e, (int32_t)p.targets[t], 0};
       about[r] = a;
     }
   }
+}
+
+__device__ __forceinline__ uint32_t two_bf16(float a, float b) {
+  const bf16x2 p = __builtin_convertvector((f32x2){a, b}, bf16x2);
+  uint32_t u;
+  __builtin_memcpy(&u, &p, 4);
+  return u;
 }
 
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -159,16 +165,16 @@ __device__ __forceinline__ TopSum join(TopSum a, TopSum b) {
 }
 
 // The logits' tile: rows i of the vocabulary from v0 (v_end: past the slice),
-// columns j of tokens.  kPacked: tokens are rows of the packed x.
+// columns j of tokens.
 // Forward: part[tile of v][token], hit[token].  Backward: P.
 struct LogitsArgs {
   CrossEntropyArgs p;
   const CrossEntropyPlan* plan;  // nullptr: every token, in its own place
-  const int32_t* list;           // forward: the tokens' rows
+  const int32_t* list;           // forward: the packed rows' tokens
   TopSum* part;                  // [tiles of v][pitch]
   float* hit;
   uint64_t pitch;           // of part, tokens
-  const uint16_t* rows;     // backward: packed x
+  const uint16_t* rows;     // packed x, where there is a plan
   const PackedRow* about;
   uint16_t* probs;          // P of the slice, [tokens rounded up][slice]
   uint32_t v0, slice;       // slice: a multiple of kTileT
@@ -191,53 +197,56 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
   const uint32_t wide = tiles_t - group * kGroup < kGroup ? tiles_t - group * kGroup : kGroup;
   const uint32_t tile_v = in / wide, tile_t = group * kGroup + in % wide;
   const uint32_t v0 = a.v0 + tile_v * T::kRowsI, t0 = tile_t * T::kRowsJ;
-  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t wi = T::wave_i(), wj = T::wave_j();
 
-  const char *from_i[T::I::kCopies], *from_j[T::J::kCopies];
-  uint32_t col_i[T::I::kCopies], col_j[T::J::kCopies];
+  typename T::template Source<typename T::I> from_i;
+  typename T::template Source<typename T::J> from_j;
+  from_i.base = reinterpret_cast<const char*>(p.w + (uint64_t)v0 * p.k);
+  from_j.base = reinterpret_cast<const char*>((a.plan ? a.rows : p.x) + (uint64_t)t0 * p.k);
+  from_i.step = from_j.step = 2 * kStageC;
 #pragma unroll
   for (uint32_t n = 0; n < T::I::kCopies; ++n) {
-    uint32_t row;
-    T::I::place(wave, n, row, col_i[n]);
-    const uint32_t v = v0 + row < p.vocab ? v0 + row : p.vocab - 1;  // past the last one: any, left out below
-    from_i[n] = reinterpret_cast<const char*>(p.w + (uint64_t)v * p.k + col_i[n]);
+    uint32_t row, col;
+    T::I::place(wave, threadIdx.x & 63, n, row, col);
+    // rows past the last one: the tile's first, left out below
+    from_i.off[n] = 2 * ((v0 + row < p.vocab ? row : 0) * p.k + col);
   }
 #pragma unroll
   for (uint32_t n = 0; n < T::J::kCopies; ++n) {
-    uint32_t row;
-    T::J::place(wave, n, row, col_j[n]);
-    uint64_t t = t0 + row;
-    if (!kBackward) {
-      t = t < count ? t : count - 1;
-      if (a.plan) t = (uint32_t)a.list[t];
-    }
-    from_j[n] = reinterpret_cast<const char*>((kBackward ? a.rows : p.x) + t * p.k + col_j[n]);
+    uint32_t row, col;
+    T::J::place(wave, threadIdx.x & 63, n, row, col);
+    from_j.off[n] = 2 * ((a.plan || t0 + row < count ? row : 0) * p.k + col);  // packed rows fill their tiles
   }
-  // k is a multiple of 32: in a last half stage the pieces past it are zeros in both operands
-  const uint32_t stages = tiles_of(p.k, kStageC), whole = p.k / kStageC;
-  const char* zeros = reinterpret_cast<const char*>(a.plan ? a.plan->zeros : static_cast<CrossEntropyPlan*>(p.workspace)->zeros);
-  v16f acc[T::kI][T::kJ] = {};
+  // k is a multiple of 32: of a last half stage only the first k-step counts, and
+  // the lanes past its end read its own columns again
+  v4f acc[T::kI][T::kJ] = {};
   T::multiply(
-      ring, stages,
-      [&](uint32_t n, uint32_t st) {
-        const char* at = from_i[n] + 2 * kStageC * st;
-        return st < whole || col_i[n] < kStageC / 2 ? at : zeros;
-      },
-      [&](uint32_t n, uint32_t st) {
-        const char* at = from_j[n] + 2 * kStageC * st;
-        return st < whole || col_j[n] < kStageC / 2 ? at : zeros;
+      ring, tiles_of(p.k, kStageC), p.k / kStageC, p.k % kStageC != 0, from_i, from_j,
+      [&](auto& i, auto& j) {
+        const uint32_t lane = late_lane();
+        uint32_t row, col;
+#pragma unroll
+        for (uint32_t n = 0; n < T::I::kCopies; ++n) {
+          T::I::place(wave, lane, n, row, col);
+          i.off[n] -= col < kStageC / 2 ? 0 : kStageC;
+        }
+#pragma unroll
+        for (uint32_t n = 0; n < T::J::kCopies; ++n) {
+          T::J::place(wave, lane, n, row, col);
+          j.off[n] -= col < kStageC / 2 ? 0 : kStageC;
+        }
       },
       acc);
 
-  // register e of block (i, j): v = wi + 32 i + 16 (e / 8) + 8 h + e % 8, token wj + 32 j + r
+  const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
+  // blocks 2 q and 2 q + 1: v = wi + 32 q + 8 g + 0 .. 7; block j: token wj + 16 j + r
   const float to_log2 = p.scale * kLog2e;
   const bool ends = v0 + T::kRowsI > v_end;
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j) {
-    const uint32_t t = t0 + wj + 32 * j + r;
-    int32_t target = -1;  // within this lane's rows: v - v0 - wi - 8 h
+    const uint32_t t = t0 + wj + 16 * j + r;
+    int32_t target = -1;
     PackedRow about{0.f, 0.f, -1, 0};
     if (kBackward) {
       about = a.about[t];
@@ -246,57 +255,58 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
       const int64_t v = p.targets[a.plan ? (uint32_t)a.list[t] : t];
       target = v >= 0 && v < (int64_t)p.vocab ? (int32_t)v : -1;
     }
+    __builtin_amdgcn_sched_barrier(0);  // a block's values at a time: all of them would not fit the registers
     target -= (int32_t)(v0 + wi);  // a target of -1 is below every row
-    const bool hits = __ballot(target >= 0 && target < 32 * T::kI) != 0;
+    const bool hits = __ballot(target >= 0 && target < 16 * T::kI) != 0;
     if constexpr (!kBackward) {
       float top = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t row = 32 * i + 16 * (e / 8) + 8 * h + e % 8;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t row = 32 * (i / 2) + 8 * g + 4 * (i & 1) + e;
           if (hits && target == (int32_t)row) a.hit[t] = acc[i][j][e] * p.scale;
           float z = acc[i][j][e] * to_log2;
           if (ends && v0 + wi + row >= v_end) z = -__builtin_inff();
           acc[i][j][e] = z;
           top = fmaxf(top, z);
         }
+      top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float from = top == -__builtin_inff() ? 0.f : top;
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum += exp2_of(acc[i][j][e] - from);
+        for (int e = 0; e < 4; ++e) sum += exp2_of(acc[i][j][e] - from);
+      sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (h == 0) reinterpret_cast<TopSum*>(ring)[wi / (32 * T::kI) * T::kRowsJ + wj + 32 * j + r] = TopSum{top, sum};
+      if (g == 0) reinterpret_cast<TopSum*>(ring)[wi / (16 * T::kI) * T::kRowsJ + wj + 16 * j + r] = TopSum{top, sum};
     } else {
-      static_assert(!kBackward || T::kI == 4, "a wave's rows are 256 bytes of P");
+      static_assert(!kBackward || (T::kI == 8 && T::kJ % 2 == 0), "a wave's rows are 256 bytes of P, 32 at a time");
       const RowBlock<16> block{ring + 512 * 16 * wave};
 #pragma unroll
-      for (int i = 0; i < T::kI; ++i)
+      for (int q = 0; q < T::kI / 2; ++q) {
+        uint32_t u[4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float d[8];
+        for (int e = 0; e < 8; e += 2) {
+          float d[2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t row = 32 * i + 16 * q + 8 * h + e;
-            float v = exp2_of(acc[i][j][8 * q + e] * to_log2 - about.lse2);
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t row = 32 * q + 8 * g + e + o;
+            float v = exp2_of(acc[2 * q + e / 4][j][e % 4 + o] * to_log2 - about.lse2);
             if (hits && target == (int32_t)row) v -= 1.f;
-            d[e] = ends && v0 + wi + row >= v_end ? 0.f : v * about.grad;
+            d[o] = ends && v0 + wi + row >= v_end ? 0.f : v * about.grad;
           }
-          uint32_t u[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bf16x2 two = __builtin_convertvector((f32x2){d[2 * e], d[2 * e + 1]}, bf16x2);
-            __builtin_memcpy(&u[e], &two, 4);
-          }
-          block.put(r, 4 * i + 2 * q + h, make_uint4(u[0], u[1], u[2], u[3]));
+          u[e / 2] = two_bf16(d[0], d[1]);
         }
-      block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
-        const uint64_t at = (uint64_t)(t0 + wj + 32 * j + row) * a.slice + (v0 - a.v0) + wi + 8 * piece;
-        *reinterpret_cast<uint4*>(a.probs + at) = v;
-      });
+        block.put(16 * (j & 1) + r, 4 * q + g, make_uint4(u[0], u[1], u[2], u[3]));
+      }
+      if (j & 1)
+        block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+          const uint64_t at = (uint64_t)(t0 + wj + 16 * (j - 1) + row) * a.slice + (v0 - a.v0) + wi + 8 * piece;
+          *reinterpret_cast<uint4*>(a.probs + at) = v;
+        });
     }
   }
   if constexpr (!kBackward) {
@@ -374,58 +384,57 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
   const uint32_t all = tiles_of(p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice, kStageC);
   const uint32_t begin = (uint32_t)((uint64_t)all * part / a.parts), end = (uint32_t)((uint64_t)all * (part + 1) / a.parts);
   const uint32_t left = p.vocab - a.v0;  // rows of w from the slice on; P is zero past them, any row will do
-  uint32_t row_i[T::I::kCopies];
-  const uint16_t* from_i[T::I::kCopies];
-  const uint16_t* from_j[T::J::kCopies];
+  typename T::template Source<typename T::I> from_i;
+  typename T::template Source<typename T::J> from_j;
+  from_i.base = reinterpret_cast<const char*>(p.w + ((uint64_t)a.v0 + begin * kStageC) * p.k + k0);
+  from_i.step = 2 * kStageC * (uint64_t)p.k;
+  from_j.base = reinterpret_cast<const char*>(a.probs + (uint64_t)t0 * a.slice + begin * kStageC);
+  from_j.step = 2 * kStageC;
 #pragma unroll
   for (uint32_t n = 0; n < T::I::kCopies; ++n) {
-    uint32_t col;
-    T::I::place(wave, n, row_i[n], col);
-    from_i[n] = p.w + (uint64_t)a.v0 * p.k + (k0 + col < p.k ? k0 + col : 0);
+    uint32_t row, col;
+    T::I::place(wave, threadIdx.x & 63, n, row, col);
+    from_i.off[n] = 2 * (row * p.k + (k0 + col < p.k ? col : 0));
   }
 #pragma unroll
   for (uint32_t n = 0; n < T::J::kCopies; ++n) {
     uint32_t row, col;
-    T::J::place(wave, n, row, col);
-    from_j[n] = a.probs + (uint64_t)(t0 + row) * a.slice + col;
+    T::J::place(wave, threadIdx.x & 63, n, row, col);
+    from_j.off[n] = 2 * (row * a.slice + col);
   }
-  v16f acc[T::kI][T::kJ] = {};
+  v4f acc[T::kI][T::kJ] = {};
   T::multiply(
-      ring, end - begin,
-      [&](uint32_t n, uint32_t st) {
-        const uint32_t v = (begin + st) * kStageC + row_i[n];
-        return from_i[n] + (uint64_t)(v < left ? v : left - 1) * p.k;
+      ring, end - begin, end * kStageC <= left ? end - begin : end - 1 - begin, false, from_i, from_j,
+      [&](auto& i, auto&) {
+        const uint32_t there = left - (end - 1) * kStageC, lane = late_lane();  // rows of the last stage
+        uint32_t row, col;
+#pragma unroll
+        for (uint32_t n = 0; n < T::I::kCopies; ++n) {
+          T::I::place(wave, lane, n, row, col);
+          i.off[n] -= 2 * p.k * (row - (row < there ? row : there - 1));
+        }
       },
-      [&](uint32_t n, uint32_t st) { return from_j[n] + (begin + st) * kStageC; }, acc);
-  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+      acc);
+  const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
   const uint32_t wi = T::wave_i(), wj = T::wave_j();
-  const RowBlock<16> block{ring + 512 * 16 * wave};
+  float* const sums = a.sums + (part * a.pitch + t0 + wj) * p.k + k0 + wi;
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j)
 #pragma unroll
-    for (int i = 0; i < T::kI; i += 2) {  // 64 k at a time
+    for (int q = 0; q < T::kI / 2; ++q) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (k0 + wi + 32 * q >= p.k) continue;  // k is a multiple of 32
+      float* const at = sums + ((16 * j + r) * p.k + 32 * q + 8 * g);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = acc[i + q / 2][j][8 * (q & 1) + e];
-        put_f32(block, r, 4 * q + 2 * h, v);
+      for (int o = 0; o < 2; ++o) {
+        v4f v = acc[2 * q + o][j] * p.scale;
+        if (!a.first) v += reinterpret_cast<const v4f*>(at)[o];
+        reinterpret_cast<v4f*>(at)[o] = v;
       }
-      block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
-        const uint32_t k = k0 + wi + 32 * i + 4 * piece;
-        if (k >= p.k) return;
-        float4* at = reinterpret_cast<float4*>(a.sums + (part * a.pitch + t0 + wj + 32 * j + row) * p.k + k);
-        float4 s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-        if (!a.first) {
-          const float4 o = *at;
-          s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
-        }
-        *at = s;
-      });
     }
 }
 
-// grad_x = grad_top * scale * the parts' sums, to the tokens' own rows; zeros for ignored ones.
+// grad_x = grad_top * the parts' sums, to the tokens' own rows; zeros for ignored ones.
 __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p,
                                                                  const CrossEntropyPlan* __restrict__ plan,
                                                                  const int32_t* __restrict__ at,
@@ -433,7 +442,7 @@ __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArg
                                                                  uint64_t pitch, uint16_t* __restrict__ grad_x) {
   const uint32_t vecs = p.k / 8;
   const uint64_t all = p.tokens * vecs, stride = (uint64_t)gridDim.x * 256;
-  const float by = plan->grad_top * p.scale;
+  const float by = plan->grad_top;
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
     const uint64_t t = i / vecs, c = i - t * vecs;
     const int32_t row = at[t];
@@ -446,10 +455,7 @@ __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArg
         for (int e = 0; e < 8; ++e) v[e] += from[e];
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bf16x2 two = __builtin_convertvector((f32x2){v[2 * e] * by, v[2 * e + 1] * by}, bf16x2);
-        __builtin_memcpy(&u[e], &two, 4);
-      }
+      for (int e = 0; e < 4; ++e) u[e] = two_bf16(v[2 * e] * by, v[2 * e + 1] * by);
     }
     reinterpret_cast<uint4*>(grad_x)[i] = make_uint4(u[0], u[1], u[2], u[3]);
   }
@@ -467,7 +473,7 @@ struct GradWeightArgs {
 template <class T, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(GradWeightArgs a) {
   __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
-  static_assert(T::kI == 4, "a wave's rows are 256 bytes of the result");
+  static_assert(T::kI == 8 && T::kJ % 2 == 0, "a wave's rows are 256 bytes of the result, 32 at a time");
   const CrossEntropyArgs& p = a.p;
   const uint32_t left = p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice;
   const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_v = tiles_of(left, T::kRowsJ);
@@ -476,48 +482,47 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(
   if (tile >= tiles) return;
   const uint32_t k0 = (uint32_t)(tile % tiles_k) * T::kRowsI, v0 = (uint32_t)(tile / tiles_k) * T::kRowsJ;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint16_t* from_i[T::I::kCopies];
-  const uint16_t* from_j[T::J::kCopies];
+  typename T::template Source<typename T::I> from_i;
+  typename T::template Source<typename T::J> from_j;
+  from_i.base = reinterpret_cast<const char*>(a.rows + k0);
+  from_i.step = 2 * kStageC * (uint64_t)p.k;
+  from_j.base = reinterpret_cast<const char*>(a.probs + v0);
+  from_j.step = 2 * kStageC * (uint64_t)a.slice;
 #pragma unroll
   for (uint32_t n = 0; n < T::I::kCopies; ++n) {
     uint32_t row, col;
-    T::I::place(wave, n, row, col);
-    from_i[n] = a.rows + (uint64_t)row * p.k + (k0 + col < p.k ? k0 + col : 0);
+    T::I::place(wave, threadIdx.x & 63, n, row, col);
+    from_i.off[n] = 2 * (row * p.k + (k0 + col < p.k ? col : 0));
   }
 #pragma unroll
   for (uint32_t n = 0; n < T::J::kCopies; ++n) {
     uint32_t row, col;
-    T::J::place(wave, n, row, col);
-    from_j[n] = a.probs + (uint64_t)row * a.slice + v0 + col;
+    T::J::place(wave, threadIdx.x & 63, n, row, col);
+    from_j.off[n] = 2 * (row * a.slice + col);
   }
-  v16f acc[T::kI][T::kJ] = {};
-  T::multiply(
-      ring, tiles_of(a.plan->count, kStageC),
-      [&](uint32_t n, uint32_t st) { return from_i[n] + (uint64_t)st * kStageC * p.k; },
-      [&](uint32_t n, uint32_t st) { return from_j[n] + (uint64_t)st * kStageC * a.slice; }, acc);
-  const uint32_t lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  v4f acc[T::kI][T::kJ] = {};
+  const uint32_t stages = tiles_of(a.plan->count, kStageC);  // the packed rows and P fill whole ones
+  T::multiply(ring, stages, stages, false, from_i, from_j, [](auto&, auto&) {}, acc);
+  const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
   const uint32_t wi = T::wave_i(), wj = T::wave_j();
   const float by = a.plan->grad_top * p.scale;
   const RowBlock<16> block{ring + 512 * 16 * wave};
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < T::kI; ++i)
+    for (int q = 0; q < T::kI / 2; ++q) {
+      uint32_t u[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bf16x2 two = __builtin_convertvector(
-              (f32x2){acc[i][j][8 * q + 2 * e] * by, acc[i][j][8 * q + 2 * e + 1] * by}, bf16x2);
-          __builtin_memcpy(&u[e], &two, 4);
-        }
-        block.put(r, 4 * i + 2 * q + h, make_uint4(u[0], u[1], u[2], u[3]));
-      }
-    block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
-      const uint32_t n = v0 + wj + 32 * j + row, k = k0 + wi + 8 * piece;
-      if (n < left && k < p.k) *reinterpret_cast<uint4*>(a.grad_w + ((uint64_t)a.v0 + n) * p.k + k) = v;
-    });
+      for (int e = 0; e < 8; e += 2)
+        u[e / 2] = two_bf16(acc[2 * q + e / 4][j][e % 4] * by, acc[2 * q + e / 4][j][e % 4 + 1] * by);
+      block.put(16 * (j & 1) + r, 4 * q + g, make_uint4(u[0], u[1], u[2], u[3]));
+    }
+    if (j & 1)
+      block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
+        const uint32_t n = v0 + wj + 16 * (j - 1) + row, k = k0 + wi + 8 * piece;
+        if (n < left && k < p.k) *reinterpret_cast<uint4*>(a.grad_w + ((uint64_t)a.v0 + n) * p.k + k) = v;
+      });
   }
 }
 
@@ -538,13 +543,13 @@ namespace {
 constexpr uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // Tiles of the forward by the tokens: rows of the vocabulary x tokens.
-using Logits256 = Tile<4, 4, 2, 2, false, false, 2>;
-using Logits128 = Tile<4, 2, 2, 2, false, false, 3>;
-using Logits64 = Tile<2, 1, 2, 2, false, false, 3>;
-using Logits32 = Tile<1, 1, 4, 1, false, false, 3>;
-using Probs256 = Tile<4, 4, 2, 2, false, false, 2>;
-using GradRows256 = Tile<4, 4, 2, 2, true, false, 2>;
-using GradWeight256 = Tile<4, 4, 2, 2, true, true, 2>;
+using Logits256 = Tile<8, 8, 2, 2, false, false, 2>;
+using Logits128 = Tile<8, 4, 2, 2, false, false, 3>;
+using Logits64 = Tile<4, 2, 2, 2, false, false, 3>;
+using Logits32 = Tile<2, 2, 4, 1, false, false, 3>;
+using Probs256 = Tile<8, 8, 2, 2, false, false, 2>;
+using GradRows256 = Tile<8, 8, 2, 2, true, false, 2>;
+using GradWeight256 = Tile<8, 8, 2, 2, true, true, 2>;
 
 // Few tokens are not listed: every one is computed, in its own place.
 constexpr uint64_t kUnlisted = 64;
@@ -553,14 +558,15 @@ uint32_t tile_rows_v(uint64_t tokens) { return tokens <= 64 ? 128u : 256u; }
 
 // Workspace of the forward.
 struct ForwardSpace {
-  uint64_t pitch, tiles, list, at, part, hit, bytes;
-  ForwardSpace(uint64_t tokens, uint32_t vocab) {
+  uint64_t pitch, tiles, list, at, rows, part, hit, bytes;
+  ForwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
     pitch = round_up(tokens, 16);
     tiles = (vocab + tile_rows_v(tokens) - 1) / tile_rows_v(tokens);
     const uint64_t lists = tokens > kUnlisted ? 4 * pitch : 0;
     list = sizeof(CrossEntropyPlan);
     at = list + lists;
-    hit = at + lists;
+    rows = at + lists;
+    hit = rows + (tokens > kUnlisted ? 2 * round_up(tokens, kTileT) * k : 0);
     part = hit + 4 * pitch;
     bytes = part + tiles * pitch * sizeof(TopSum);
   }
@@ -591,6 +597,11 @@ struct BackwardSpace {
   }
 };
 
+dim3 vector_grid(uint64_t vecs) {
+  const uint64_t n = (vecs + 255) / 256, most = 8192 < kMaxGroups ? 8192 : kMaxGroups;
+  return dim3((uint32_t)(n < most ? n : most));
+}
+
 uint32_t xcd_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 constexpr uint64_t kMostTiles = (1u << 24) - 8;  // a launch counts its work-items in 32 bits
 
@@ -604,8 +615,7 @@ hipError_t run_logits(const LogitsArgs& a, uint64_t tokens, hipStream_t stream) 
 }  // namespace
 
 uint64_t cross_entropy_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t k) {
-  (void)k;
-  return ForwardSpace(tokens, vocab).bytes;
+  return ForwardSpace(tokens, vocab, k).bytes;
 }
 
 uint64_t cross_entropy_bwd_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t k) {
@@ -613,7 +623,7 @@ uint64_t cross_entropy_bwd_workspace_bytes(uint64_t tokens, uint32_t vocab, uint
 }
 
 hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* lse, hipStream_t stream) {
-  const ForwardSpace s(p.tokens, p.vocab);
+  const ForwardSpace s(p.tokens, p.vocab, p.k);
   if (s.tiles * ((p.tokens + kTileT - 1) / kTileT) > kMostTiles) return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
   const bool listed = p.tokens > kUnlisted;
@@ -626,14 +636,18 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
   CrossEntropyPlan* const plan = reinterpret_cast<CrossEntropyPlan*>(at);
   int32_t* const list = reinterpret_cast<int32_t*>(at + s.list);
   int32_t* const places = listed ? reinterpret_cast<int32_t*>(at + s.at) : nullptr;
-  if (listed || p.k % kStageC) {
-    hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, (const float*)nullptr,
-                       listed ? (uint32_t)p.tokens : 0u, p.vocab, plan, list, places);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
   if (listed) {
+    hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, (const float*)nullptr,
+                       (uint32_t)p.tokens, p.vocab, plan, list, places);
+    if (hipError_t e = hipGetLastError()) return e;
+    uint16_t* const rows = reinterpret_cast<uint16_t*>(at + s.rows);
+    hipLaunchKernelGGL(cross_entropy_pack_kernel, vector_grid(round_up(p.tokens, kTileT) * (p.k / 8)), dim3(256), 0,
+                       stream, p, (const float*)nullptr, (const float*)nullptr, (const CrossEntropyPlan*)plan,
+                       (const int32_t*)list, reinterpret_cast<uint4*>(rows), (PackedRow*)nullptr);
+    if (hipError_t e = hipGetLastError()) return e;
     a.plan = plan;
     a.list = list;
+    a.rows = rows;
   }
   const hipError_t e = p.tokens <= 32    ? run_logits<Logits32, 2>(a, p.tokens, stream)
                        : p.tokens <= 64  ? run_logits<Logits64, 2>(a, p.tokens, stream)
@@ -647,13 +661,9 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
 
 hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad_loss, const float* lse,
                                     uint16_t* grad_x, uint16_t* grad_w, hipStream_t stream) {
-  const auto groups = [](uint64_t vecs) {
-    const uint64_t n = (vecs + 255) / 256, most = 8192 < kMaxGroups ? 8192 : kMaxGroups;
-    return dim3((uint32_t)(n < most ? n : most));
-  };
   if (p.tokens == 0) {
     const uint64_t vecs = (uint64_t)p.vocab * p.k / 8;
-    hipLaunchKernelGGL(cross_entropy_clear_kernel, groups(vecs), dim3(256), 0, stream, reinterpret_cast<uint4*>(grad_w),
+    hipLaunchKernelGGL(cross_entropy_clear_kernel, vector_grid(vecs), dim3(256), 0, stream, reinterpret_cast<uint4*>(grad_w),
                        vecs);
     return hipGetLastError();
   }
@@ -673,7 +683,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, grad_loss,
                      (uint32_t)p.tokens, p.vocab, plan, list, places);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(cross_entropy_pack_kernel, groups(s.tall * (p.k / 8)), dim3(256), 0, stream, p, grad_loss, lse,
+  hipLaunchKernelGGL(cross_entropy_pack_kernel, vector_grid(s.tall * (p.k / 8)), dim3(256), 0, stream, p, grad_loss, lse,
                      (const CrossEntropyPlan*)plan, (const int32_t*)list, reinterpret_cast<uint4*>(rows), about);
   if (hipError_t e = hipGetLastError()) return e;
   for (uint64_t v0 = 0; v0 < p.vocab; v0 += s.slice) {
@@ -702,7 +712,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     }
   }
   if (grad_x) {
-    hipLaunchKernelGGL(cross_entropy_rows_kernel, groups(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
+    hipLaunchKernelGGL(cross_entropy_rows_kernel, vector_grid(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
                        (const CrossEntropyPlan*)plan, (const int32_t*)places, (const float*)sums, s.parts, s.tall, grad_x);
     if (hipError_t e = hipGetLastError()) return e;
   }

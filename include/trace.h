@@ -751,7 +751,7 @@ TRACE_API int trace_step_revision(void);
  * A token whose target lies outside [0, vocab) is ignored: its loss and lse are
  * 0, and nothing depends on its row of x.
  *   x : bf16[tokens*k]; w : bf16[vocab*k]; targets : int64[tokens]; loss, lse :
- *   fp32[tokens]; k a multiple of 32, at least 32; vocab at least 1.
+ *   fp32[tokens]; k a multiple of 32, from 32 to 2^20 - 32; vocab at least 1.
  *   workspace : trace_linear_cross_entropy_workspace_bytes(tokens, vocab, k)
  *   bytes, 16-byte aligned, contents not preserved.
  * Products of bf16 are exact in fp32, sums are fp32. */
