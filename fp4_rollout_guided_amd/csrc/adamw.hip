@@ -32,8 +32,7 @@ using trace_host::AdamwScalars;
 using trace_host::AdamwTensor;
 
 constexpr uint32_t kAdamThreads = 256;
-constexpr uint32_t kAdamRounds = 4;
-constexpr uint32_t kAdamChunk = kAdamThreads * 4 * kAdamRounds;
+constexpr uint32_t kAdamChunk = 4096;
 // Tensors of a launch: their descriptors are kernel arguments, 4 KiB at most.
 constexpr uint32_t kAdamTensors = 48;
 
@@ -44,6 +43,8 @@ struct AdamwBatch {
   uint32_t count;
 };
 static_assert(sizeof(AdamwBatch) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // A 32-bit integer to another one, each bit of which depends on all of its
 // bits: shifts and products with odd numbers, the fractions of the square roots
@@ -56,48 +57,53 @@ __host__ __device__ inline uint32_t mix_bits(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// Four consecutive elements at element i, of which `left` exist.
-template <bool kBf16, bool kNT>
-struct Four {
-  uint32_t raw[kBf16 ? 2 : 4];
-  __device__ __forceinline__ void load(const void* from, uint64_t i, uint32_t left) {
-    if (left >= 4) {
-      if constexpr (kBf16) {
+// kPer consecutive elements of a tensor in fp32 or bf16, raw, at element i of
+// `from`; kWhole: all of them exist, otherwise the first `left` do.
+template <bool kBf16, bool kNT, int kPer>
+struct Elements {
+  static constexpr int kDwords = kBf16 ? kPer / 2 : kPer;
+  uint32_t raw[kDwords];
+  template <bool kWhole>
+  __device__ __forceinline__ void load(const void* from, uint32_t i, uint32_t left) {
+    if constexpr (kWhole) {
+      if constexpr (kDwords == 2) {
         const u32x2* at = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(from) + i);
         const u32x2 v = kNT ? __builtin_nontemporal_load(at) : *at;
         raw[0] = v[0], raw[1] = v[1];
       } else {
-        const uint4 v = load_vec<kNT>(reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(from) + i));
-        raw[0] = v.x, raw[1] = v.y, raw[2] = v.z, raw[3] = v.w;
+#pragma unroll
+        for (int d = 0; d < kDwords; d += 4) {
+          const uint4 v = load_vec<kNT>(
+              reinterpret_cast<const uint4*>(static_cast<const char*>(from) + (uint64_t)i * (kBf16 ? 2 : 4)) + d / 4);
+          raw[d] = v.x, raw[d + 1] = v.y, raw[d + 2] = v.z, raw[d + 3] = v.w;
+        }
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (uint32_t j = 0; j < (kBf16 ? 2 : 4); ++j) raw[j] = 0;
+      for (int d = 0; d < kDwords; ++d) raw[d] = 0;
 #pragma unroll
-    for (uint32_t j = 0; j < 3; ++j) {
-      if (j >= left) continue;
-      if constexpr (kBf16)
-        raw[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(from)[i + j] << (16 * (j & 1));
-      else
-        raw[j] = static_cast<const uint32_t*>(from)[i + j];
+      for (uint32_t j = 0; j < kPer; ++j) {
+        if (j >= left) continue;
+        if constexpr (kBf16)
+          raw[j >> 1] |= (uint32_t)static_cast<const uint16_t*>(from)[i + j] << (16 * (j & 1));
+        else
+          raw[j] = static_cast<const uint32_t*>(from)[i + j];
+      }
     }
   }
-  __device__ __forceinline__ void values(float (&v)[4]) const {
+  __device__ __forceinline__ void values(float (&v)[kPer]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kPer; ++j) {
       if constexpr (kBf16)
         v[j] = (j & 1) ? bf16_hi(raw[j >> 1]) : bf16_lo(raw[j >> 1]);
       else
         v[j] = __uint_as_float(raw[j]);
     }
   }
-  __device__ __forceinline__ void store(void* to, uint64_t i, uint32_t left) const {
-    if (left >= 4) {
-      if constexpr (kBf16) {
+  template <bool kWhole>
+  __device__ __forceinline__ void store(void* to, uint32_t i, uint32_t left) const {
+    if constexpr (kWhole) {
+      if constexpr (kDwords == 2) {
         u32x2* at = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(to) + i);
         const u32x2 v = {raw[0], raw[1]};
         if (kNT)
@@ -105,44 +111,50 @@ struct Four {
         else
           *at = v;
       } else {
-        store_vec<kNT>(reinterpret_cast<uint4*>(static_cast<uint32_t*>(to) + i),
-                       make_uint4(raw[0], raw[1], raw[2], raw[3]));
-      }
-      return;
-    }
 #pragma unroll
-    for (uint32_t j = 0; j < 3; ++j) {
-      if (j >= left) continue;
-      if constexpr (kBf16)
-        static_cast<uint16_t*>(to)[i + j] = (uint16_t)(raw[j >> 1] >> (16 * (j & 1)));
-      else
-        static_cast<uint32_t*>(to)[i + j] = raw[j];
+        for (int d = 0; d < kDwords; d += 4)
+          store_vec<kNT>(reinterpret_cast<uint4*>(static_cast<char*>(to) + (uint64_t)i * (kBf16 ? 2 : 4)) + d / 4,
+                         make_uint4(raw[d], raw[d + 1], raw[d + 2], raw[d + 3]));
+      }
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < kPer; ++j) {
+        if (j >= left) continue;
+        if constexpr (kBf16)
+          static_cast<uint16_t*>(to)[i + j] = (uint16_t)(raw[j >> 1] >> (16 * (j & 1)));
+        else
+          static_cast<uint32_t*>(to)[i + j] = raw[j];
+      }
     }
   }
 };
 
-// Four code bytes likewise.
-template <bool kNT>
-__device__ __forceinline__ uint32_t load_codes(const void* from, uint64_t i, uint32_t left) {
-  if (left >= 4) {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(from) + i);
+// Eight code bytes likewise.
+template <bool kWhole, bool kNT>
+__device__ __forceinline__ u32x2 load_codes(const void* from, uint32_t i, uint32_t left) {
+  u32x2 v = {0, 0};
+  if constexpr (kWhole) {
+    const u32x2* at = reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(from) + i);
     return kNT ? __builtin_nontemporal_load(at) : *at;
   }
-  uint32_t v = 0;
-  for (uint32_t j = 0; j < left; ++j) v |= (uint32_t)static_cast<const uint8_t*>(from)[i + j] << (8 * j);
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j)
+    if (j < left) v[j >> 2] |= (uint32_t)static_cast<const uint8_t*>(from)[i + j] << (8 * (j & 3));
   return v;
 }
-template <bool kNT>
-__device__ __forceinline__ void store_codes(void* to, uint64_t i, uint32_t left, uint32_t v) {
-  if (left >= 4) {
-    uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(to) + i);
+template <bool kWhole, bool kNT>
+__device__ __forceinline__ void store_codes(void* to, uint32_t i, uint32_t left, u32x2 v) {
+  if constexpr (kWhole) {
+    u32x2* at = reinterpret_cast<u32x2*>(static_cast<uint8_t*>(to) + i);
     if (kNT)
       __builtin_nontemporal_store(v, at);
     else
       *at = v;
     return;
   }
-  for (uint32_t j = 0; j < left; ++j) static_cast<uint8_t*>(to)[i + j] = (uint8_t)(v >> (8 * j));
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j)
+    if (j < left) static_cast<uint8_t*>(to)[i + j] = (uint8_t)(v[j >> 2] >> (8 * (j & 3)));
 }
 
 // 2^(b - 127), b in 0 .. 254, and NaN for 255.
@@ -150,48 +162,57 @@ __device__ __forceinline__ float e8m0_value(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : (b == 255 ? 0x7fc00000u : b << 23));
 }
 
-__device__ __forceinline__ void decode_codes(uint32_t c, uint32_t scale, float (&v)[4]) {
+__device__ __forceinline__ void decode_codes(u32x2 c, uint32_t scale, float (&v)[8]) {
   const float s = e8m0_value(scale);
-  v[0] = __builtin_amdgcn_cvt_f32_fp8((int)c, 0) * s;
-  v[1] = __builtin_amdgcn_cvt_f32_fp8((int)c, 1) * s;
-  v[2] = __builtin_amdgcn_cvt_f32_fp8((int)c, 2) * s;
-  v[3] = __builtin_amdgcn_cvt_f32_fp8((int)c, 3) * s;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    v[4 * d + 0] = __builtin_amdgcn_cvt_f32_fp8((int)c[d], 0) * s;
+    v[4 * d + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[d], 1) * s;
+    v[4 * d + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[d], 2) * s;
+    v[4 * d + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[d], 3) * s;
+  }
 }
 
-// The larger of the values of lanes 8 i .. 8 i + 7, in all of them.
-__device__ __forceinline__ uint32_t max_of_eight(uint32_t v) {
+// The largest of the values of lanes 4 i .. 4 i + 3, in all of them.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t v) {
   const auto with = [&](uint32_t o) { v = v > o ? v : o; };
-  with((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // lanes 1 0 3 2
-  with((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // lanes 2 3 0 1
-  with((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));  // eight lanes mirrored
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));  // lanes 1 0 3 2
+  with((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
   return v;
 }
 
-// A block's E8M0 byte and its elements' codes; u: 16 random bits each.  A block
-// with an infinity or NaN gets byte 255.
-__device__ __forceinline__ uint32_t encode_codes(const float (&v)[4], const uint32_t (&u)[4], uint32_t& codes) {
+// A block's E8M0 byte and this lane's codes; u(j): 16 random bits.  A block with
+// an infinity or NaN gets byte 255.  Below 2^-6 the codes' steps are all 2^-9:
+// with 2^-6 added the same bits of the sum count them.
+template <class Bits>
+__device__ __forceinline__ uint32_t encode_codes(const float (&v)[8], const Bits& u, u32x2& codes) {
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 8; ++j) {
     const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
     top = a > top ? a : top;
   }
-  top = max_of_eight(top);
+  top = max_of_four(top);
   // the smallest e with top <= 448 * 2^e, 448 = 1.75 * 2^8; subnormal tops: -127
-  const int e8 = (int)(top >> 23) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0) - 8;
-  const uint32_t byte = top >= 0x7f800000u ? 255u : (uint32_t)(e8 > 0 ? e8 : 0);
-  const float inv = __uint_as_float(byte >= 254 ? 0x00400000u : (254u - byte) << 23);
-  codes = 0;
+  const int e8 = (int)((top + 0x1fffffu) >> 23) - 8;  // carries where the fraction passes 0.75
+  const bool bad = top >= 0x7f800000u;
+  const uint32_t byte = bad ? 255u : (uint32_t)(e8 > 0 ? e8 : 0);
+  const float inv = __uint_as_float(bad ? 0x00400000u : (254u - byte) << 23);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float z = fabsf(v[j]) * inv;
-    uint32_t c;
-    if (z < 0x1p-6f)
-      c = (uint32_t)floorf(z * 512.f + (float)u[j] * 0x1p-16f);
-    else
-      c = ((__float_as_uint(z) + (u[j] << 4)) >> 20) - (120u << 3);
-    c = byte == 255u ? 0x7fu : c;
-    codes |= (c | (__float_as_uint(v[j]) >> 31 << 7)) << (8 * j);
+  for (int d = 0; d < 2; ++d) {
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+      const float z = fabsf(v[4 * d + j]) * inv;
+      const bool low = z < 0x1p-6f;
+      const float y = low ? z + 0x1p-6f : z;
+      const uint32_t c = ((__float_as_uint(y) + (u(4 * d + j) << 4)) >> 20) - (low ? 121u << 3 : 120u << 3);
+      all = all << 8 | c;
+    }
+    uint32_t signs = 0;
+#pragma unroll
+    for (int j = 3; j >= 0; --j) signs = signs >> 8 | (__float_as_uint(v[4 * d + 3 - j]) & 0x80000000u);
+    codes[d] = (bad ? 0x7f7f7f7fu : all) | signs;
   }
   return byte;
 }
@@ -206,6 +227,121 @@ __device__ __forceinline__ uint32_t bf16_nearest(float p) {
   return p != p ? (b >> 16 | 0x40u) : bf16_rne_bits(p);
 }
 
+// One workgroup's elements; kWhole: all of its chunk exist.
+template <bool kParamBf16, bool kGradBf16, bool kMx8, bool kNT, bool kWhole>
+__device__ __forceinline__ void adamw_chunk(const AdamwTensor& all, uint64_t chunk, uint64_t first_place,
+                                            const AdamwScalars& s, float gs, bool random) {
+  constexpr int kPer = kMx8 ? 8 : 4;  // to a lane: a block of 32 is four lanes
+  constexpr uint32_t kRounds = kAdamChunk / (kAdamThreads * kPer);
+  // the chunk's own tensors: places within it take 32 bits
+  char* const param = static_cast<char*>(all.param) + chunk * (kParamBf16 ? 2 : 4);
+  const char* const grad = static_cast<const char*>(all.grad) + chunk * (kGradBf16 ? 2 : 4);
+  char* const avg = static_cast<char*>(all.avg) + chunk * (kMx8 ? 1 : 4);
+  char* const sq = static_cast<char*>(all.sq) + chunk * (kMx8 ? 1 : 4);
+  uint8_t* const avg_scales = all.avg_scales + chunk / 32;
+  uint8_t* const sq_scales = all.sq_scales + chunk / 32;
+  uint16_t* const copy = all.copy ? all.copy + chunk : nullptr;
+  const uint32_t n = kWhole ? kAdamChunk : (uint32_t)(all.n - chunk);
+  Elements<kParamBf16, kNT, kPer> p[kRounds];
+  Elements<kGradBf16, kNT, kPer> g[kRounds];
+  Elements<false, kNT, kPer> m[kRounds], v[kRounds];
+  u32x2 mc[kRounds], rc[kRounds];
+  uint32_t ms[kRounds], rs[kRounds];
+  const auto left_of = [&](uint32_t i) -> uint32_t {
+    return kWhole ? kPer : (i >= n ? 0u : (n - i < kPer ? n - i : (uint32_t)kPer));
+  };
+#pragma unroll
+  for (uint32_t k = 0; k < kRounds; ++k) {
+    const uint32_t i = (k * kAdamThreads + threadIdx.x) * kPer, left = left_of(i);
+    if (!kWhole && left == 0) continue;
+    p[k].template load<kWhole>(param, i, left);
+    g[k].template load<kWhole>(grad, i, left);
+    if constexpr (kMx8) {
+      mc[k] = load_codes<kWhole, kNT>(avg, i, left);
+      rc[k] = load_codes<kWhole, kNT>(sq, i, left);
+      ms[k] = avg_scales[i / 32];
+      rs[k] = sq_scales[i / 32];
+    } else {
+      m[k].template load<kWhole>(avg, i, left);
+      v[k].template load<kWhole>(sq, i, left);
+    }
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kRounds; ++k) {
+    const uint32_t i = (k * kAdamThreads + threadIdx.x) * kPer, left = left_of(i);
+    // a block's lanes stay together: those past the end hold zeros
+    if (!kWhole && i / 32 * 32 >= n) continue;
+    float pv[kPer] = {}, gv[kPer] = {}, mv[kPer] = {}, vv[kPer] = {}, rv[kPer];
+    if (kWhole || left) {
+      p[k].values(pv);
+      g[k].values(gv);
+      if constexpr (kMx8) {
+        decode_codes(mc[k], ms[k], mv);
+        decode_codes(rc[k], rs[k], rv);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) vv[j] = rv[j] * rv[j];
+      } else {
+        m[k].values(mv);
+        v[k].values(vv);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float gj = gv[j] * gs;
+      mv[j] = mv[j] * s.beta1 + gj * s.rest1;
+      vv[j] = vv[j] * s.beta2 + (gj * gj) * s.rest2;
+      rv[j] = sqrtf(vv[j]);
+      pv[j] = pv[j] * s.decay - (mv[j] / (rv[j] * s.root + s.eps)) * s.rate;
+      if (kMx8 && !kWhole && (uint32_t)j >= left) mv[j] = rv[j] = 0.f;  // the block's other elements alone choose its scale
+    }
+    uint32_t bits[kPer] = {};
+    if (kMx8 || (kParamBf16 && random)) {
+      const uint64_t place = first_place + chunk;  // of the chunk, a multiple of 32
+      const uint32_t low = (uint32_t)place + i;
+      const uint32_t key = mix_bits(s.key + (uint32_t)((place + i) >> 32));
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) bits[j] = mix_bits(mix_bits(low + j) + key);
+    }
+    if (kWhole || left) {
+      Elements<kParamBf16, kNT, kPer> out;
+      if constexpr (kParamBf16) {
+        uint32_t h[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) h[j] = random ? bf16_random(pv[j], mix_bits(bits[j]) >> 16) : bf16_nearest(pv[j]);
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) out.raw[j / 2] = h[j] | h[j + 1] << 16;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) out.raw[j] = __float_as_uint(pv[j]);
+        if (copy) {
+          Elements<true, kNT, kPer> c;
+#pragma unroll
+          for (int j = 0; j < kPer; j += 2) c.raw[j / 2] = bf16_nearest(pv[j]) | bf16_nearest(pv[j + 1]) << 16;
+          c.template store<kWhole>(copy, i, left);
+        }
+      }
+      out.template store<kWhole>(param, i, left);
+    }
+    if constexpr (kMx8) {
+      u32x2 codes;
+      uint32_t byte = encode_codes(mv, [&](int j) { return bits[j] & 0xffffu; }, codes);
+      if (kWhole || left) store_codes<kWhole, kNT>(avg, i, left, codes);
+      if ((threadIdx.x & 3) == 0) avg_scales[i / 32] = (uint8_t)byte;
+      byte = encode_codes(rv, [&](int j) { return bits[j] >> 16; }, codes);
+      if (kWhole || left) store_codes<kWhole, kNT>(sq, i, left, codes);
+      if ((threadIdx.x & 3) == 0) sq_scales[i / 32] = (uint8_t)byte;
+    } else if (kWhole || left) {
+      Elements<false, kNT, kPer> o;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o.raw[j] = __float_as_uint(mv[j]);
+      o.template store<kWhole>(avg, i, left);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o.raw[j] = __float_as_uint(vv[j]);
+      o.template store<kWhole>(sq, i, left);
+    }
+  }
+}
+
 template <bool kParamBf16, bool kGradBf16, bool kMx8, bool kNT>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamwBatch batch, AdamwScalars s,
                                                              const float* __restrict__ grad_scale, bool random) {
@@ -213,105 +349,12 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamwBatch batch, A
   const uint32_t lane = threadIdx.x & 63;
   const uint64_t hit = __ballot(lane < batch.count && batch.first[lane < batch.count ? lane : 0] <= blockIdx.x);
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(63 - __builtin_clzll(hit)));
-  const AdamwTensor t = batch.t[at];
   const uint64_t chunk = (uint64_t)(blockIdx.x - batch.first[at]) * kAdamChunk;
   const float gs = grad_scale ? *grad_scale : 1.f;
-  Four<kParamBf16, kNT> p[kAdamRounds];
-  Four<kGradBf16, kNT> g[kAdamRounds];
-  Four<false, kNT> m[kAdamRounds], v[kAdamRounds];
-  uint32_t mc[kAdamRounds], rc[kAdamRounds], ms[kAdamRounds], rs[kAdamRounds];
-#pragma unroll
-  for (uint32_t k = 0; k < kAdamRounds; ++k) {
-    const uint64_t i = chunk + (k * kAdamThreads + threadIdx.x) * 4;
-    if (i >= t.n) continue;
-    const uint32_t left = t.n - i < 4 ? (uint32_t)(t.n - i) : 4u;
-    p[k].load(t.param, i, left);
-    g[k].load(t.grad, i, left);
-    if constexpr (kMx8) {
-      mc[k] = load_codes<kNT>(t.avg, i, left);
-      rc[k] = load_codes<kNT>(t.sq, i, left);
-      ms[k] = t.avg_scales[i / 32];
-      rs[k] = t.sq_scales[i / 32];
-    } else {
-      m[k].load(t.avg, i, left);
-      v[k].load(t.sq, i, left);
-    }
-  }
-#pragma unroll
-  for (uint32_t k = 0; k < kAdamRounds; ++k) {
-    const uint64_t i = chunk + (k * kAdamThreads + threadIdx.x) * 4;
-    // a block's eight lanes stay together: those past the end hold zeros
-    if (i / 32 * 32 >= t.n) continue;
-    const uint32_t left = i >= t.n ? 0u : (t.n - i < 4 ? (uint32_t)(t.n - i) : 4u);
-    float pv[4] = {0, 0, 0, 0}, gv[4] = {0, 0, 0, 0}, mv[4] = {0, 0, 0, 0}, vv[4] = {0, 0, 0, 0}, rv[4];
-    if (left) {
-      p[k].values(pv);
-      g[k].values(gv);
-      if constexpr (kMx8) {
-        decode_codes(mc[k], ms[k], mv);
-        decode_codes(rc[k], rs[k], rv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vv[j] = rv[j] * rv[j];
-      } else {
-        m[k].values(mv);
-        v[k].values(vv);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float gj = gv[j] * gs;
-      mv[j] = mv[j] * s.beta1 + gj * s.rest1;
-      vv[j] = vv[j] * s.beta2 + (gj * gj) * s.rest2;
-      rv[j] = sqrtf(vv[j]);
-      pv[j] = pv[j] * s.decay - (mv[j] / (rv[j] * s.root + s.eps)) * s.rate;
-      if (kMx8 && (uint32_t)j >= left) mv[j] = rv[j] = 0.f;  // the block's other elements alone choose its scale
-    }
-    uint32_t bits[4] = {0, 0, 0, 0};
-    if (kMx8 || (kParamBf16 && random)) {
-      const uint64_t place = batch.place[at] + i;
-      const uint32_t key = mix_bits(s.key + (uint32_t)(place >> 32));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bits[j] = mix_bits(mix_bits((uint32_t)place + j) + key);  // place is a multiple of 4
-    }
-    if (left) {
-      Four<kParamBf16, kNT> out;
-      if constexpr (kParamBf16) {
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = random ? bf16_random(pv[j], mix_bits(bits[j]) >> 16) : bf16_nearest(pv[j]);
-        out.raw[0] = h[0] | h[1] << 16, out.raw[1] = h[2] | h[3] << 16;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out.raw[j] = __float_as_uint(pv[j]);
-        if (t.copy) {
-          Four<true, kNT> c;
-          c.raw[0] = bf16_nearest(pv[0]) | bf16_nearest(pv[1]) << 16;
-          c.raw[1] = bf16_nearest(pv[2]) | bf16_nearest(pv[3]) << 16;
-          c.store(t.copy, i, left);
-        }
-      }
-      out.store(t.param, i, left);
-    }
-    if constexpr (kMx8) {
-      uint32_t lo[4], hi[4], codes;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) lo[j] = bits[j] & 0xffffu, hi[j] = bits[j] >> 16;
-      uint32_t byte = encode_codes(mv, lo, codes);
-      if (left) store_codes<kNT>(t.avg, i, left, codes);
-      if ((i & 31) == 0) t.avg_scales[i / 32] = (uint8_t)byte;
-      byte = encode_codes(rv, hi, codes);
-      if (left) store_codes<kNT>(t.sq, i, left, codes);
-      if ((i & 31) == 0) t.sq_scales[i / 32] = (uint8_t)byte;
-    } else if (left) {
-      Four<false, kNT> o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o.raw[j] = __float_as_uint(mv[j]);
-      o.store(t.avg, i, left);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o.raw[j] = __float_as_uint(vv[j]);
-      o.store(t.sq, i, left);
-    }
-  }
+  if (chunk + kAdamChunk <= batch.t[at].n)
+    adamw_chunk<kParamBf16, kGradBf16, kMx8, kNT, true>(batch.t[at], chunk, batch.place[at], s, gs, random);
+  else
+    adamw_chunk<kParamBf16, kGradBf16, kMx8, kNT, false>(batch.t[at], chunk, batch.place[at], s, gs, random);
 }
 
 }  // namespace trace_dev

@@ -137,8 +137,8 @@ trace_status adamw(const trace_adamw_tensor* tensors, int32_t count, const trace
     if (all > (1ull << 48)) return TRACE_E_SHAPE;
     if (!t.param || !t.grad || !t.avg || !t.sq || (mx8 && (!t.avg_scales || !t.sq_scales))) return TRACE_E_NULL;
     if (t.copy && o->param_bf16) return TRACE_E_SHAPE;
-    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.avg, mx8 ? 4 : 16) ||
-        !aligned(t.sq, mx8 ? 4 : 16) || !aligned(t.copy, 16))
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.avg, mx8 ? 8 : 16) ||
+        !aligned(t.sq, mx8 ? 8 : 16) || !aligned(t.copy, 16))
       return TRACE_E_ALIGN;
   }
   if (all == 0) return TRACE_OK;

@@ -3,8 +3,8 @@
 //
 // A workgroup of four waves, kWI x kWJ of them, owns 16 kWI kI results i times
 // 16 kWJ kJ results j, each wave kI x kJ blocks of the 16x16x32 instruction.  A
-// lane holds one j and, in the registers of two neighbouring blocks, eight
-// consecutive i.
+// lane holds one j and four consecutive i, or (I along c, below) in the registers
+// of two neighbouring blocks eight.
 //
 // Each operand lies in memory either along c (rows i or j of consecutive c) or
 // across it (rows c of consecutive i or j).  Stages of 64 c are copied straight
@@ -107,9 +107,10 @@ struct TileOperand {
 
   // How a row's pieces are permuted.  Along c, 16 lanes read one piece of 16 rows
   // that differ in bits 0 to 3, or 0, 1, 3 and 4 (kPairs below), two rows to 256
-  // bytes; across it 32 bytes of four rows.
+  // bytes; across it, 32 lanes read 32 bytes of eight rows that differ in bits 0, 1
+  // and 3.
   static __device__ __forceinline__ uint32_t swap(uint32_t row) {
-    return kAcross ? (row & 3) << 2 : ((row >> 1) & 1) | ((row >> 2) & 2) | (((row ^ (row >> 2)) & 4));
+    return kAcross ? (row & 3) << 2 | ((row >> 2) & 2) : ((row >> 1) & 1) | ((row >> 2) & 2) | (((row ^ (row >> 2)) & 4));
   }
 
   // What this lane fetches with copy n of its wave: the row of the operand in
@@ -123,15 +124,15 @@ struct TileOperand {
   // Operand registers of k-step kk (32 c): block f, 16 rows from first + 16 f,
   // this lane's (lane % 16).  kPairs: blocks 2 q and 2 q + 1 share 32 rows, the
   // first with those whose bit 2 is 0 (a lane's results in both are then eight
-  // consecutive ones).
+  // consecutive ones); across c that would read half of the banks.
   template <bool kPairs>
   static __device__ __forceinline__ v8bf read(const char* stage, uint32_t first, uint32_t f, uint32_t kk) {
     const uint32_t lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
     if constexpr (kAcross) {
-      const uint32_t row = 8 * g + (q >> 2), run = q & 3;  // and four rows on, whose low bits are the same
-      const uint32_t piece = first / 8 + (kPairs ? 4 * (f / 2) + run : 2 * f + (run >> 1));
-      const uint32_t half = kPairs ? f & 1 : run & 1;
-      const char* at = stage + (32 * kk + row) * kPitch + 16 * (piece ^ swap(row)) + 8 * half;
+      static_assert(!kPairs);
+      const uint32_t row = 8 * g + (q >> 2), run = q & 3;  // and four rows on, which are permuted alike
+      const uint32_t piece = first / 8 + 2 * f + (run >> 1);
+      const char* at = stage + (32 * kk + row) * kPitch + 16 * (piece ^ swap(row)) + 8 * (run & 1);
       const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
       const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4 * kPitch));
       v8bf out;
@@ -149,6 +150,7 @@ template <int kI_, int kJ_, int kWI_, int kWJ_, bool kAcrossI, bool kAcrossJ, in
 struct Tile {
   static constexpr int kI = kI_, kJ = kJ_, kWI = kWI_, kWJ = kWJ_;
   static constexpr uint32_t kRing = kRing_;  // stages in LDS
+  static constexpr bool kPairs = !kAcrossI;
   static constexpr uint32_t kRowsI = 16 * kI * kWI, kRowsJ = 16 * kJ * kWJ;
   using I = TileOperand<kRowsI, kAcrossI>;
   using J = TileOperand<kRowsJ, kAcrossJ>;
@@ -229,7 +231,7 @@ struct Tile {
       constexpr uint32_t kF = decltype(f)::value;
       const char* from = ring + slot * kStageBytes;
       if constexpr (kF == 0 || (kF > kJ && kF < kFragments))
-        fi[kk][kF == 0 ? 0 : kF - kJ] = I::template read<true>(from, wi, kF == 0 ? 0 : kF - kJ, kk);
+        fi[kk][kF == 0 ? 0 : kF - kJ] = I::template read<kPairs>(from, wi, kF == 0 ? 0 : kF - kJ, kk);
       else if constexpr (kF <= kJ)
         fj[kk][kF - 1] = J::template read<false>(from + I::kBytes, wj, kF - 1, kk);
     };

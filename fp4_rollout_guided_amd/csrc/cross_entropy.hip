@@ -421,16 +421,13 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j)
 #pragma unroll
-    for (int q = 0; q < T::kI / 2; ++q) {
+    for (int i = 0; i < T::kI; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      if (k0 + wi + 32 * q >= p.k) continue;  // k is a multiple of 32
-      float* const at = sums + ((16 * j + r) * p.k + 32 * q + 8 * g);
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        v4f v = acc[2 * q + o][j] * p.scale;
-        if (!a.first) v += reinterpret_cast<const v4f*>(at)[o];
-        reinterpret_cast<v4f*>(at)[o] = v;
-      }
+      if (k0 + wi + 16 * i >= p.k) continue;  // k is a multiple of 32
+      v4f* const at = reinterpret_cast<v4f*>(sums + ((16 * j + r) * p.k + 16 * i + 4 * g));
+      v4f v = acc[i][j] * p.scale;
+      if (!a.first) v += *at;
+      *at = v;
     }
 }
 
@@ -511,12 +508,10 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(
   for (int j = 0; j < T::kJ; ++j) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < T::kI / 2; ++q) {
-      uint32_t u[4];
-#pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        u[e / 2] = two_bf16(acc[2 * q + e / 4][j][e % 4] * by, acc[2 * q + e / 4][j][e % 4 + 1] * by);
-      block.put(16 * (j & 1) + r, 4 * q + g, make_uint4(u[0], u[1], u[2], u[3]));
+    for (int i = 0; i < T::kI; ++i) {
+      const v4f v = acc[i][j] * by;
+      *reinterpret_cast<uint2*>(block.at(16 * (j & 1) + r, 2 * i + (g >> 1)) + 8 * (g & 1)) =
+          make_uint2(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]));
     }
     if (j & 1)
       block.drain([&](uint32_t row, uint32_t piece, uint4 v) {
