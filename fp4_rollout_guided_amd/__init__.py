@@ -64,7 +64,6 @@ autograd functions; ``AdamW`` keeps the optimiser's states.
 """
 import ctypes
 import math
-import operator
 import os
 from array import array
 
@@ -192,6 +191,10 @@ def load_library(path):
 
 
 lib = load_library(LIB_PATH)
+try:
+    from . import _tensor_lists
+except ImportError as e:
+    raise ImportError(f"{e}: build it with `python fp4_rollout_guided_amd/build.py`") from None
 
 
 def abi_version() -> int:
@@ -1432,87 +1435,65 @@ class _AdamwOptions(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("param_bf16", "grad_bf16", "states_mx8", "randomly")]
 
 
-_TENSOR_WORDS = 8  # of trace_adamw_tensor: param, grad, avg, sq, avg_scales, sq_scales, copy, n
-_dtype_of = operator.attrgetter("dtype")
+# Words of trace_adamw_tensor: param, grad, avg, sq, avg_scales, sq_scales, copy, n
+_TENSOR_WORDS = 8
 _F32_OR_BF16 = (torch.float32, torch.bfloat16)
+_BF16_ONLY = (torch.bfloat16,)
 
 
-def _tensors(ts, name, dtypes, device, numels=None):
-    """Check a list of tensors as ``_arg`` does one: all of one type.  The list
-    is walked by C calls: a step has hundreds of them."""
-    try:
-        found = set(map(_dtype_of, ts))
-        devices = set(map(torch.Tensor.get_device, ts))
-        whole = all(map(torch.Tensor.is_contiguous, ts))
-    except (AttributeError, TypeError):
-        raise TypeError(f"{name} must be tensors") from None
-    if len(found) > 1 or not found <= set(dtypes):
-        raise TypeError(f"{name} must all be {' or all '.join(map(str, dtypes))}, got {sorted(map(str, found))}")
-    if devices - {device} or device < 0:
-        raise ValueError(f"{name} must be on one device, the parameters'")
-    if not whole:
-        raise ValueError(f"{name} must be contiguous")
-    got = list(map(torch.Tensor.numel, ts))
-    if numels is not None and got != numels:
-        raise ValueError(f"{name} must hold as many elements as the parameters' {'blocks' if 'scales' in name else 'own'}")
-    return got
+def _list(ts):
+    return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
-def _states(avgs, sqs, numels, device):
-    """Whether the states are 8-bit records, after their checks."""
-    if len(avgs) != len(numels) or len(sqs) != len(numels):
-        raise ValueError("one state of each kind per parameter is required")
-    mx8 = bool(numels) and isinstance(avgs[0], (tuple, list))
-    for states, name in ((avgs, "exp_avgs"), (sqs, "exp_avg_sqs")):
-        if mx8:
-            if not all(isinstance(s, (tuple, list)) and len(s) == 2 for s in states):
-                raise TypeError(f"{name} must all be (scales, codes)")
-            _tensors([s[0] for s in states], name + " scales", _U8, device, [(n + 31) // 32 for n in numels])
-            _tensors([s[1] for s in states], name + " codes", _U8, device, numels)
-        else:
-            _tensors(states, name, _F32, device, numels)
-    return mx8
+class _Step:
+    """The words of a list of parameters: their checks and addresses, one call
+    for each list."""
 
+    def __init__(self, params):
+        if not isinstance(params[0], torch.Tensor):
+            raise TypeError(f"params[0] must be a tensor, got {type(params[0]).__name__}")
+        self.device = params[0].get_device()
+        if self.device < 0:
+            raise ValueError("params must be device tensors")
+        self.count = len(params)
+        self.numels = array("q", bytes(8 * self.count))
+        self.words = array("q", bytes(8 * _TENSOR_WORDS * self.count))
+        _tensor_lists.check(params, -1, "params", _F32_OR_BF16, self.device, self.numels, None, 0, 0)
+        self.words[7::_TENSOR_WORDS] = self.numels
 
-def _state_words(words, avgs, sqs, mx8):
-    """Addresses of the states into the tensors' words."""
-    ptr = torch.Tensor.data_ptr
-    if mx8:
-        for at, states, part in ((2, avgs, 1), (3, sqs, 1), (4, avgs, 0), (5, sqs, 0)):
-            words[at::_TENSOR_WORDS] = array("Q", [s[part].data_ptr() for s in states])
-    else:
-        words[2::_TENSOR_WORDS] = array("Q", map(ptr, avgs))
-        words[3::_TENSOR_WORDS] = array("Q", map(ptr, sqs))
+    def put(self, ts, column, name, dtypes, part=-1, numels=None):
+        return _tensor_lists.check(ts, part, name, dtypes, self.device, self.numels if numels is None else numels,
+                                   self.words, _TENSOR_WORDS, column)
 
+    def put_states(self, avgs, sqs):
+        self.mx8 = len(avgs) > 0 and isinstance(avgs[0], (tuple, list))
+        if not self.mx8:
+            self.put(avgs, 2, "exp_avgs", _F32)
+            self.put(sqs, 3, "exp_avg_sqs", _F32)
+            return
+        blocks = array("q", [(n + 31) // 32 for n in self.numels])
+        for ts, name, column in ((avgs, "exp_avgs", 2), (sqs, "exp_avg_sqs", 3)):
+            self.put(ts, column, name + " codes", _U8, 1)
+            self.put(ts, column + 2, name + " scales", _U8, 0, blocks)
 
-def _adamw(words, params, grads, copies, numels, mx8, device, step, lr, betas, eps, weight_decay, grad_scale, seed):
-    """The call, once params and states have been checked; words: the states'."""
-    if grad_scale is not None:
-        _fit(grad_scale, "grad_scale", params[0], _F32, 1)
-    if len(grads) != len(params):
-        raise ValueError("one gradient per parameter is required")
-    _tensors(grads, "grads", _F32_OR_BF16, device, numels)
-    ptr = torch.Tensor.data_ptr
-    words[0::_TENSOR_WORDS] = array("Q", map(ptr, params))
-    words[1::_TENSOR_WORDS] = array("Q", map(ptr, grads))
-    words[7::_TENSOR_WORDS] = array("Q", numels)
-    param_bf16 = params[0].dtype == torch.bfloat16
-    if copies is not None:
-        if param_bf16:
-            raise ValueError("copies are for fp32 parameters")
-        if len(copies) != len(params):
-            raise ValueError("one copy per parameter is required")
-        _tensors(copies, "copies", (torch.bfloat16,), device, numels)
-        words[6::_TENSOR_WORDS] = array("Q", map(ptr, copies))
-    if mx8 and seed is None:
-        raise ValueError("8-bit states are rounded at random: seed is required")
-    if seed is not None and (isinstance(seed, bool) or not isinstance(seed, int) or not 0 <= seed < 1 << 64):
-        raise ValueError(f"seed must be an integer of 64 bits, got {seed!r}")
-    options = _AdamwOptions(lr, betas[0], betas[1], eps, weight_decay, step, seed or 0, param_bf16,
-                            grads[0].dtype == torch.bfloat16, mx8, seed is not None)
-    _launch("trace_adamw_step", params[0], words.buffer_info()[0], len(params), ctypes.addressof(options),
-            _addr(grad_scale))
-    torch.autograd.graph.increment_version(params)
+    def run(self, params, grads, copies, step, lr, betas, eps, weight_decay, grad_scale, seed):
+        param = self.put(params, 0, "params", _F32_OR_BF16)
+        grad = self.put(grads, 1, "grads", _F32_OR_BF16)
+        if copies is not None:
+            if param == torch.bfloat16:
+                raise ValueError("copies are for fp32 parameters")
+            self.put(copies, 6, "copies", _BF16_ONLY)
+        if grad_scale is not None:
+            _fit(grad_scale, "grad_scale", params[0], _F32, 1)
+        if self.mx8 and seed is None:
+            raise ValueError("8-bit states are rounded at random: seed is required")
+        if seed is not None and (isinstance(seed, bool) or not isinstance(seed, int) or not 0 <= seed < 1 << 64):
+            raise ValueError(f"seed must be an integer of 64 bits, got {seed!r}")
+        options = _AdamwOptions(lr, betas[0], betas[1], eps, weight_decay, step, seed or 0, param == torch.bfloat16,
+                                grad == torch.bfloat16, self.mx8, seed is not None)
+        _launch("trace_adamw_step", params[0], self.words.buffer_info()[0], self.count, ctypes.addressof(options),
+                _addr(grad_scale))
+        _tensor_lists.changed(params)
 
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
@@ -1530,15 +1511,13 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     records are refused: rounded to nearest they would stand still.
 
     The numbers are those of the call: a captured graph replays them."""
-    params, grads = list(params), list(grads)
-    if not params:
+    params = _list(params)
+    if len(params) == 0:
         return
-    device = params[0].get_device() if isinstance(params[0], torch.Tensor) else -1
-    numels = _tensors(params, "params", _F32_OR_BF16, device)
-    mx8 = _states(exp_avgs, exp_avg_sqs, numels, device)
-    words = array("Q", bytes(8 * _TENSOR_WORDS * len(params)))
-    _state_words(words, exp_avgs, exp_avg_sqs, mx8)
-    _adamw(words, params, grads, copies, numels, mx8, device, step, lr, betas, eps, weight_decay, grad_scale, seed)
+    words = _Step(params)
+    words.put_states(_list(exp_avgs), _list(exp_avg_sqs))
+    words.run(params, _list(grads), None if copies is None else _list(copies), step, lr, betas, eps, weight_decay,
+              grad_scale, seed)
 
 
 class AdamW:
@@ -1559,8 +1538,7 @@ class AdamW:
             raise ValueError("8-bit states are rounded at random: seed is required")
         if not self.params:
             raise ValueError("no parameters")
-        self._device = self.params[0].get_device() if isinstance(self.params[0], torch.Tensor) else -1
-        self._numels = _tensors(self.params, "params", _F32_OR_BF16, self._device)
+        self._words = _Step(self.params)
         self._mx8 = states == "mx8"
 
         def zeros(p):
@@ -1571,8 +1549,7 @@ class AdamW:
                     torch.zeros(n, dtype=torch.uint8, device=p.device))
 
         self._avgs, self._sqs = [zeros(p) for p in self.params], [zeros(p) for p in self.params]
-        self._words = array("Q", bytes(8 * _TENSOR_WORDS * len(self.params)))
-        _state_words(self._words, self._avgs, self._sqs, self._mx8)
+        self._words.put_states(self._avgs, self._sqs)
 
     def step(self, grads=None, grad_scale=None):
         """One step with these gradients, or the parameters' own .grad."""
@@ -1581,11 +1558,10 @@ class AdamW:
             grads = [p.grad for p in params]
             if any(g is None for g in grads):
                 raise ValueError("a parameter has no gradient")
-        _tensors(params, "params", _F32_OR_BF16, self._device, self._numels)  # again: their storage may be another one
         t = self.steps + 1
         seed = None if self.seed is None else (self.seed + t) % (1 << 64)
-        _adamw(self._words, params, list(grads), self.copies, self._numels, self._mx8, self._device, t, self.lr,
-               self.betas, self.eps, self.weight_decay, grad_scale, seed)
+        self._words.run(params, _list(grads), self.copies, t, self.lr, self.betas, self.eps, self.weight_decay,
+                        grad_scale, seed)
         self.steps = t
 
     def zero_grad(self):
@@ -1599,7 +1575,9 @@ class AdamW:
     def load_state_dict(self, state):
         """Copies states of the same kind and sizes into these."""
         avgs, sqs = state["exp_avgs"], state["exp_avg_sqs"]
-        if _states(avgs, sqs, self._numels, self._device) != self._mx8:
+        theirs = _Step(self.params)
+        theirs.put_states(avgs, sqs)  # the checks
+        if theirs.mx8 != self._mx8:
             raise TypeError("the states are of the other kind")
         for mine, theirs in ((self._avgs, avgs), (self._sqs, sqs)):
             for to, of in zip(mine, theirs):

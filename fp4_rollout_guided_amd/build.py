@@ -10,10 +10,12 @@ denormals kept, no fast-math.  Packed-fp32 instructions are disabled.  SLP
 vectorization is off: it turns the per-element flag tests into vector-of-bool
 packing code.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -64,6 +66,19 @@ def _command(out, defines=()):
             *[os.path.join(CSRC, s) for s in SOURCES], "-o", out]
 
 
+# The binding's walk over lists of tensors: a Python module in C++, host code only.
+LISTS_LIB = os.path.join(PKG, "_tensor_lists.so")
+
+
+def _lists_command(out):
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    include, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_lists.cpp"),
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-o", out]
+
+
 # The bench's practical-ceiling probe (plain copy / read / fill streams).
 CEILING_SRC = os.path.join(ROOT, "bench_ceiling.hip")
 CEILING_BIN = os.path.join(ROOT, "_build", "bench_ceiling")
@@ -86,7 +101,8 @@ def build(verbose: bool = False) -> str:
     """Compile every source into fp4_rollout_guided_amd/libtrace.so (and the
     small-grid test build beside it), always rebuilding, and return the
     library's path."""
-    jobs = [(LIB, _command(LIB + ".tmp")), (SMALLGRID_LIB, _command(SMALLGRID_LIB + ".tmp", SMALLGRID_DEFINES))]
+    jobs = [(LIB, _command(LIB + ".tmp")), (SMALLGRID_LIB, _command(SMALLGRID_LIB + ".tmp", SMALLGRID_DEFINES)),
+            (LISTS_LIB, _lists_command(LISTS_LIB + ".tmp"))]
     if os.path.exists(CEILING_SRC):
         os.makedirs(os.path.dirname(CEILING_BIN), exist_ok=True)
         jobs.append((CEILING_BIN, [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17",
@@ -101,7 +117,7 @@ def build(verbose: bool = False) -> str:
         stdout, stderr = p.communicate()
         if p.returncode != 0:
             sys.stderr.write(stdout + stderr)
-            raise RuntimeError(f"hipcc failed with exit code {p.returncode} building {os.path.basename(out)}")
+            raise RuntimeError(f"the compiler failed with exit code {p.returncode} building {os.path.basename(out)}")
         if verbose and stderr.strip():
             # the host pass does not know the packed-fp32 feature flag; that warning is expected
             lines = [l for l in stderr.splitlines() if "packed-fp32-ops" not in l and l.strip()]

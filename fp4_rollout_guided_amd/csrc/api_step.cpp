@@ -106,16 +106,28 @@ struct Span {
   bool written;
 };
 
-// Whether something that is written overlaps anything else.
-bool spans_clash(Span* s, size_t n) {
-  std::sort(s, s + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  uintptr_t any = 0, written = 0;  // how far what came before reaches
-  for (size_t i = 0; i < n; ++i) {
-    if (s[i].lo < written || (s[i].written && s[i].lo < any)) return true;
-    any = std::max(any, s[i].hi);
-    if (s[i].written) written = std::max(written, s[i].hi);
+// Whether something that is written overlaps anything else.  `runs` runs of
+// `each` spans (the tensors' params, their grads, ...), in ascending order as a rule
+// where the tensors are parts of larger ones.
+bool spans_clash(Span* s, size_t runs, size_t each) {
+  const auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  for (size_t r = 0; r < runs; ++r) {
+    Span* const run = s + r * each;
+    if (!std::is_sorted(run, run + each, before)) std::sort(run, run + each, before);
   }
-  return false;
+  uintptr_t any = 0, written = 0;  // how far what came before reaches
+  size_t at[8] = {};
+  for (;;) {
+    size_t best = runs;
+    for (size_t r = 0; r < runs; ++r)
+      if (at[r] < each && (best == runs || s[r * each + at[r]].lo < s[best * each + at[best]].lo)) best = r;
+    if (best == runs) return false;
+    const Span& x = s[best * each + at[best]++];
+    if (x.hi == x.lo) continue;
+    if (x.lo < written || (x.written && x.lo < any)) return true;
+    any = std::max(any, x.hi);
+    if (x.written) written = std::max(written, x.hi);
+  }
 }
 
 trace_status adamw(const trace_adamw_tensor* tensors, int32_t count, const trace_adamw_options* o,
@@ -142,28 +154,30 @@ trace_status adamw(const trace_adamw_tensor* tensors, int32_t count, const trace
       return TRACE_E_ALIGN;
   }
   if (all == 0) return TRACE_OK;
-  Span few[64];
-  const size_t most = 7 * (size_t)count + 1;
-  Span* const many = most > 64 ? new (std::nothrow) Span[most] : few;
-  if (!many) return hip_status(hipErrorOutOfMemory);
-  size_t n = 0;
-  const auto add = [&](const void* p, uint64_t bytes, bool written) {
-    if (p && bytes) many[n++] = Span{(uintptr_t)p, (uintptr_t)p + bytes, written};
-  };
-  add(grad_scale, 4, false);
-  for (int32_t i = 0; i < count; ++i) {
+  constexpr size_t kRuns = 7;
+  Span few[kRuns * 16];
+  const size_t each = (size_t)count;
+  Span* const spans = each > 16 ? new (std::nothrow) Span[kRuns * each] : few;
+  if (!spans) return hip_status(hipErrorOutOfMemory);
+  for (size_t i = 0; i < each; ++i) {
     const trace_adamw_tensor& t = tensors[i];
     const uint64_t e = (uint64_t)t.n;
-    add(t.param, param * e, true);
-    add(t.grad, grad * e, false);
-    add(t.avg, state * e, true);
-    add(t.sq, state * e, true);
-    add(mx8 ? t.avg_scales : nullptr, (e + 31) / 32, true);
-    add(mx8 ? t.sq_scales : nullptr, (e + 31) / 32, true);
-    add(t.copy, 2 * e, true);
+    const auto put = [&](size_t run, const void* p, uint64_t bytes, bool written) {
+      spans[run * each + i] = Span{(uintptr_t)p, p ? (uintptr_t)p + bytes : 0, written};
+    };
+    put(0, t.param, param * e, true);
+    put(1, t.grad, grad * e, false);
+    put(2, t.avg, state * e, true);
+    put(3, t.sq, state * e, true);
+    put(4, t.copy, 2 * e, true);
+    put(5, mx8 ? t.avg_scales : nullptr, (e + 31) / 32, true);
+    put(6, mx8 ? t.sq_scales : nullptr, (e + 31) / 32, true);
   }
-  const bool clash = spans_clash(many, n);
-  if (many != few) delete[] many;
+  bool clash = spans_clash(spans, mx8 ? kRuns : kRuns - 2, each);
+  const uintptr_t scale_at = (uintptr_t)grad_scale;
+  for (size_t i = 0; grad_scale && i < kRuns * each; ++i)
+    clash |= spans[i].written && spans[i].lo < scale_at + 4 && scale_at < spans[i].hi;
+  if (spans != few) delete[] spans;
   if (clash) return TRACE_E_ALIAS;
   const double rest1 = 1 - pow(o->beta1, (double)o->step), rest2 = 1 - pow(o->beta2, (double)o->step);
   trace_host::AdamwScalars s{};
