@@ -283,8 +283,8 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
       sum += __shfl_xor(sum, 32);
       if (g == 0) reinterpret_cast<TopSum*>(ring)[wi / (16 * T::kI) * T::kRowsJ + wj + 16 * j + r] = TopSum{top, sum};
     } else {
-      static_assert(!kBackward || (T::kI == 8 && T::kJ % 2 == 0), "a wave's rows are 256 bytes of P, 32 at a time");
-      const RowBlock<16> block{ring + 512 * 16 * wave};
+      static_assert(!kBackward || T::kJ % 2 == 0, "32 rows of P at a time");
+      const RowBlock<2 * T::kI> block{ring + 1024 * T::kI * wave};
 #pragma unroll
       for (int q = 0; q < T::kI / 2; ++q) {
         uint32_t u[4];
@@ -320,14 +320,16 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
   }
 }
 
-// Joins the tiles: 16 tokens to a workgroup, 64 lanes to each.
-__global__ __launch_bounds__(1024) void cross_entropy_join_kernel(CrossEntropyArgs p, const int32_t* __restrict__ at,
-                                                                  const TopSum* __restrict__ part, uint64_t pitch,
-                                                                  uint32_t tiles, const float* __restrict__ hit,
-                                                                  float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ TopSum sums[1024];
-  const uint32_t j = threadIdx.x % 16, share = threadIdx.x / 16;
-  const uint64_t t = (uint64_t)blockIdx.x * 16 + j;
+// Joins the tiles: kEach tokens to a workgroup, 256 / kEach lanes to each.
+template <uint32_t kEach>
+__global__ __launch_bounds__(256) void cross_entropy_join_kernel(CrossEntropyArgs p, const int32_t* __restrict__ at,
+                                                                 const TopSum* __restrict__ part, uint64_t pitch,
+                                                                 uint32_t tiles, const float* __restrict__ hit,
+                                                                 float* __restrict__ loss, float* __restrict__ lse) {
+  constexpr uint32_t kShares = 256 / kEach, kAtOnce = 8;
+  __shared__ TopSum sums[256];
+  const uint32_t j = threadIdx.x % kEach, share = threadIdx.x / kEach;
+  const uint64_t t = (uint64_t)blockIdx.x * kEach + j;
   bool has = t < p.tokens;
   uint64_t place = t;
   if (has) {
@@ -341,14 +343,23 @@ __global__ __launch_bounds__(1024) void cross_entropy_join_kernel(CrossEntropyAr
   }
   TopSum s{-__builtin_inff(), 0.f};
   if (has) {
-#pragma unroll 4
-    for (uint32_t i = share; i < tiles; i += 64) s = join(s, part[i * pitch + place]);
+    for (uint32_t i0 = share; i0 < tiles; i0 += kShares * kAtOnce) {
+      TopSum v[kAtOnce];
+#pragma unroll
+      for (uint32_t n = 0; n < kAtOnce; ++n) {
+        const uint32_t i = i0 + n * kShares;
+        v[n] = part[(i < tiles ? i : tiles - 1) * pitch + place];
+        if (i >= tiles) v[n] = TopSum{-__builtin_inff(), 0.f};
+      }
+#pragma unroll
+      for (uint32_t n = 0; n < kAtOnce; ++n) s = join(s, v[n]);
+    }
   }
   sums[threadIdx.x] = s;
   __syncthreads();
 #pragma unroll
-  for (uint32_t d = 32; d >= 1; d >>= 1) {
-    if (share < d) sums[threadIdx.x] = join(sums[threadIdx.x], sums[threadIdx.x + 16 * d]);
+  for (uint32_t d = kShares / 2; d >= 1; d >>= 1) {
+    if (share < d) sums[threadIdx.x] = join(sums[threadIdx.x], sums[threadIdx.x + kEach * d]);
     __syncthreads();
   }
   if (share == 0 && t < p.tokens) {
@@ -470,7 +481,7 @@ struct GradWeightArgs {
 template <class T, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(GradWeightArgs a) {
   __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
-  static_assert(T::kI == 8 && T::kJ % 2 == 0, "a wave's rows are 256 bytes of the result, 32 at a time");
+  static_assert(T::kJ % 2 == 0, "32 rows of the result at a time");
   const CrossEntropyArgs& p = a.p;
   const uint32_t left = p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice;
   const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_v = tiles_of(left, T::kRowsJ);
@@ -503,7 +514,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(
   const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
   const uint32_t wi = T::wave_i(), wj = T::wave_j();
   const float by = a.plan->grad_top * p.scale;
-  const RowBlock<16> block{ring + 512 * 16 * wave};
+  const RowBlock<2 * T::kI> block{ring + 1024 * T::kI * wave};
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j) {
     __builtin_amdgcn_sched_barrier(0);
@@ -537,26 +548,39 @@ namespace {
 
 constexpr uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-// Tiles of the forward by the tokens: rows of the vocabulary x tokens.
+// Tiles: vocabulary x tokens, k x tokens, k x vocabulary.
 using Logits256 = Tile<8, 8, 2, 2, false, false, 2>;
-using Logits128 = Tile<8, 4, 2, 2, false, false, 3>;
+using Logits128 = Tile<4, 4, 2, 2, false, false, 2>;
 using Logits64 = Tile<4, 2, 2, 2, false, false, 3>;
 using Logits32 = Tile<2, 2, 4, 1, false, false, 3>;
-using Probs256 = Tile<8, 8, 2, 2, false, false, 2>;
 using GradRows256 = Tile<8, 8, 2, 2, true, false, 2>;
+using GradRows128 = Tile<4, 4, 2, 2, true, false, 2>;
 using GradWeight256 = Tile<8, 8, 2, 2, true, true, 2>;
+using GradWeight128 = Tile<4, 4, 2, 2, true, true, 2>;
+
+constexpr uint64_t tiles_in(uint64_t n, uint64_t m, uint64_t each) { return (n + each - 1) / each * ((m + each - 1) / each); }
+
+// Whether n x m results (times `parts`) are done in tiles of 128 rather than 256.
+// A compute unit holds one tile of 256 or two of 128; a stage of one takes some
+// 1.9 us, of two of the others side by side 1.1.  So tiles of 128 win where those of
+// 256 leave many units idle (in their only, or their last, turn).
+bool small_tiles(uint64_t n, uint64_t m, uint64_t parts = 1) {
+  const uint64_t turns256 = (tiles_in(n, m, 256) * parts + 255) / 256, turns128 = (tiles_in(n, m, 128) * parts + 511) / 512;
+  return 11 * turns128 < 19 * turns256;
+}
 
 // Few tokens are not listed: every one is computed, in its own place.
 constexpr uint64_t kUnlisted = 64;
 
-uint32_t tile_rows_v(uint64_t tokens) { return tokens <= 64 ? 128u : 256u; }
+uint32_t tile_rows_v(uint64_t tokens, uint32_t vocab) { return tokens <= 64 || small_tiles(tokens, vocab) ? 128u : 256u; }
 
 // Workspace of the forward.
 struct ForwardSpace {
   uint64_t pitch, tiles, list, at, rows, part, hit, bytes;
   ForwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
     pitch = round_up(tokens, 16);
-    tiles = (vocab + tile_rows_v(tokens) - 1) / tile_rows_v(tokens);
+    const uint32_t rows_v = tile_rows_v(tokens, vocab);
+    tiles = (vocab + rows_v - 1) / rows_v;
     const uint64_t lists = tokens > kUnlisted ? 4 * pitch : 0;
     list = sizeof(CrossEntropyPlan);
     at = list + lists;
@@ -580,8 +604,11 @@ struct BackwardSpace {
     if (s < 8192) s = 8192;
     if (s > round_up(vocab, kTileT)) s = round_up(vocab, kTileT);
     slice = (uint32_t)s;
-    const uint64_t tiles = tall / kTileT * ((k + kTileT - 1) / kTileT);
+    // of a slice's contraction for grad_x: until its tiles take four turns, but
+    // eight stages at least to each
+    const uint64_t tiles = tiles_in(tall, k, 256), most = (s + 8 * kStageC - 1) / (8 * kStageC);
     parts = (uint32_t)(1024 / tiles < 1 ? 1 : (1024 / tiles > 16 ? 16 : 1024 / tiles));
+    if (parts > most) parts = (uint32_t)most;
     list = sizeof(CrossEntropyPlan);
     at = list + 4 * tall;
     about = at + 4 * tall;
@@ -619,7 +646,7 @@ uint64_t cross_entropy_bwd_workspace_bytes(uint64_t tokens, uint32_t vocab, uint
 
 hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* lse, hipStream_t stream) {
   const ForwardSpace s(p.tokens, p.vocab, p.k);
-  if (s.tiles * ((p.tokens + kTileT - 1) / kTileT) > kMostTiles) return hipErrorInvalidConfiguration;
+  if (tiles_in(p.tokens, p.vocab, 256) > kMostTiles) return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
   const bool listed = p.tokens > kUnlisted;
   LogitsArgs a{};
@@ -646,11 +673,17 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
   }
   const hipError_t e = p.tokens <= 32    ? run_logits<Logits32, 2>(a, p.tokens, stream)
                        : p.tokens <= 64  ? run_logits<Logits64, 2>(a, p.tokens, stream)
-                       : p.tokens <= 128 ? run_logits<Logits128, 1>(a, p.tokens, stream)
-                                         : run_logits<Logits256, 1>(a, p.tokens, stream);
+                       : small_tiles(p.tokens, p.vocab) ? run_logits<Logits128, 2>(a, p.tokens, stream)
+                                                        : run_logits<Logits256, 1>(a, p.tokens, stream);
   if (e) return e;
-  hipLaunchKernelGGL(cross_entropy_join_kernel, dim3((uint32_t)((p.tokens + 15) / 16)), dim3(1024), 0, stream, p, places,
-                     (const TopSum*)a.part, s.pitch, (uint32_t)s.tiles, (const float*)a.hit, loss, lse);
+  const auto join = [&](auto each, auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((p.tokens + each - 1) / each)), dim3(256), 0, stream, p, places,
+                       (const TopSum*)a.part, s.pitch, (uint32_t)s.tiles, (const float*)a.hit, loss, lse);
+  };
+  if (listed)  // neighbouring tokens' parts lie together
+    join(16u, cross_entropy_join_kernel<16>);
+  else
+    join(1u, cross_entropy_join_kernel<1>);
   return hipGetLastError();
 }
 
@@ -663,9 +696,8 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     return hipGetLastError();
   }
   const BackwardSpace s(p.tokens, p.vocab, p.k);
-  const uint64_t tiles_t = s.tall / kTileT, tiles_k = (p.k + kTileT - 1) / kTileT;
-  if (s.slice / kTileT * tiles_t > kMostTiles || tiles_t * tiles_k * s.parts > kMostTiles ||
-      s.slice / kTileT * tiles_k > kMostTiles)
+  if (tiles_in(p.tokens, s.slice, 256) > kMostTiles || tiles_in(p.tokens, p.k, 256) * s.parts > kMostTiles ||
+      tiles_in(s.slice, p.k, 256) > kMostTiles)
     return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
   CrossEntropyPlan* const plan = reinterpret_cast<CrossEntropyPlan*>(at);
@@ -682,6 +714,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
                      (const CrossEntropyPlan*)plan, (const int32_t*)list, reinterpret_cast<uint4*>(rows), about);
   if (hipError_t e = hipGetLastError()) return e;
   for (uint64_t v0 = 0; v0 < p.vocab; v0 += s.slice) {
+    const uint64_t cols = p.vocab - v0 < s.slice ? p.vocab - v0 : s.slice;
     LogitsArgs a{};
     a.p = p;
     a.plan = plan;
@@ -690,19 +723,28 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     a.probs = probs;
     a.v0 = (uint32_t)v0;
     a.slice = s.slice;
-    hipLaunchKernelGGL((cross_entropy_logits_kernel<Probs256, true, 1>), dim3(xcd_grid(s.slice / kTileT * tiles_t)),
-                       dim3(256), 0, stream, a);
+    const auto grid = [&](uint64_t n, uint64_t m, uint64_t parts, bool small) {
+      return dim3(xcd_grid(tiles_in(n, m, small ? 128 : 256) * parts));
+    };
+    bool small = small_tiles(p.tokens, cols);
+    hipLaunchKernelGGL((small ? cross_entropy_logits_kernel<Logits128, true, 2>
+                              : cross_entropy_logits_kernel<Logits256, true, 1>),
+                       grid(p.tokens, cols, 1, small), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (grad_x) {
       const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, s.parts, v0 == 0, sums, s.tall};
-      hipLaunchKernelGGL((cross_entropy_grad_rows_kernel<GradRows256, 1>), dim3(xcd_grid(tiles_t * tiles_k * s.parts)),
-                         dim3(256), 0, stream, g);
+      small = small_tiles(p.tokens, p.k, s.parts);
+      hipLaunchKernelGGL((small ? cross_entropy_grad_rows_kernel<GradRows128, 2>
+                                : cross_entropy_grad_rows_kernel<GradRows256, 1>),
+                         grid(p.tokens, p.k, s.parts, small), dim3(256), 0, stream, g);
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (grad_w) {
       const GradWeightArgs g{p, plan, rows, probs, (uint32_t)v0, s.slice, grad_w};
-      hipLaunchKernelGGL((cross_entropy_grad_weight_kernel<GradWeight256, 1>), dim3(xcd_grid(s.slice / kTileT * tiles_k)),
-                         dim3(256), 0, stream, g);
+      small = small_tiles(cols, p.k);
+      hipLaunchKernelGGL((small ? cross_entropy_grad_weight_kernel<GradWeight128, 2>
+                                : cross_entropy_grad_weight_kernel<GradWeight256, 1>),
+                         grid(cols, p.k, 1, small), dim3(256), 0, stream, g);
       if (hipError_t e = hipGetLastError()) return e;
     }
   }

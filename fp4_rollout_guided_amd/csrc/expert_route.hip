@@ -9,8 +9,8 @@
 //
 // A row of up to 256 experts is held by 16 lanes, so that a wave routes four
 // rows and a maximum takes four DPP moves; more experts take the wave's 64
-// lanes.  Lane l holds experts l, l + 16, ... (loads of neighbouring lanes are
-// neighbours, whatever the row's alignment).  The topk rounds each find
+// lanes.  Lanes hold 16 bytes of neighbouring experts at a time, or, where rows are
+// not whole vectors, single ones.  The topk rounds each find
 // the largest key and then, among the lanes that hold it, the lowest index.
 // Probabilities are summed per lane, then in the order of the waves and of the
 // workgroups (fp64), counts by integer atomics in LDS: no result depends on the
@@ -18,7 +18,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_math.h"
+#include "fp4_block.h"
 #include "launch.h"
 #include "launch_step.h"
 
@@ -72,19 +75,39 @@ __device__ __forceinline__ float row_sum(float v) {
   }));
 }
 
-// Lane l's logits of a row: experts l + kLanes j; -infinity past the last one.
-template <bool kBf16, int kLanes, int kPer>
+// Expert i of lane l: kVec neighbours at a time, the lanes' side by side.
+template <int kLanes, int kVec>
+__device__ __forceinline__ uint32_t expert_of(uint32_t l, int i) {
+  return kVec * l + kLanes * kVec * (i / kVec) + i % kVec;
+}
+
+// Lane l's logits of a row, -infinity past the last one.  kVec > 1: experts is a
+// multiple of it and rows are aligned to kVec logits.
+template <bool kBf16, int kLanes, int kPer, int kVec>
 __device__ __forceinline__ void load_logits(const void* logits, uint64_t row, uint32_t experts, uint32_t l,
                                             float (&z)[kPer]) {
+  constexpr int kDwords = kBf16 ? (kVec + 1) / 2 : kVec;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint32_t e = l + kLanes * j;
-    z[j] = -__builtin_inff();
-    if (e < experts) {
-      if (kBf16)
-        z[j] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[row * experts + e] << 16);
+  for (int i = 0; i < kPer; i += kVec) {
+    const uint32_t e = expert_of<kLanes, kVec>(l, i);
+    const bool in = e < experts;
+    const uint64_t at = row * experts + (in ? e : 0);
+    if constexpr (kVec == 1) {
+      float v;
+      if constexpr (kBf16)
+        v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
       else
-        z[j] = static_cast<const float*>(logits)[row * experts + e];
+        v = static_cast<const float*>(logits)[at];
+      z[i] = in ? v : -__builtin_inff();
+    } else {
+      uint32_t d[kDwords];
+      __builtin_memcpy(d, __builtin_assume_aligned(static_cast<const char*>(logits) + at * (kBf16 ? 2 : 4), 4 * kDwords),
+                       4 * kDwords);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float v = kBf16 ? ((j & 1) ? bf16_hi(d[j / 2]) : bf16_lo(d[j / 2])) : __uint_as_float(d[j]);
+        z[i + j] = in ? v : -__builtin_inff();
+      }
     }
   }
 }
@@ -124,12 +147,20 @@ __device__ __forceinline__ void finish_route(const uint32_t* part_counts, const 
   for (uint32_t e0 = 0; e0 <= experts; e0 += per) {
     const uint32_t e = e0 + threadIdx.x % per, share = threadIdx.x / per;
     double probs = 0, count = 0;
-    if (e <= experts) {
-#pragma unroll 8
-      for (uint32_t b = share; b < blocks; b += wide) {
-        count += part_counts[(uint64_t)b * (experts + 1) + e];
-        if (e < experts) probs += part_probs[(uint64_t)b * experts + e];
+    constexpr uint32_t kAtOnce = 16;  // loads under way: their latency is all that this takes
+    const uint32_t ec = e <= experts ? e : experts, ep = e < experts ? e : experts - 1;
+    for (uint32_t b0 = share; b0 < blocks; b0 += wide * kAtOnce) {
+      uint32_t c[kAtOnce];
+      float f[kAtOnce];
+#pragma unroll
+      for (uint32_t i = 0; i < kAtOnce; ++i) {
+        const uint32_t b = b0 + i * wide < blocks ? b0 + i * wide : blocks - 1;
+        c[i] = part_counts[b * (experts + 1) + ec];
+        f[i] = part_probs[b * experts + ep];
       }
+#pragma unroll
+      for (uint32_t i = 0; i < kAtOnce; ++i)
+        if (b0 + i * wide < blocks) count += c[i], probs += f[i];
     }
     __syncthreads();
     probs_of[threadIdx.x] = probs;
@@ -168,7 +199,7 @@ __device__ __forceinline__ void finish_route(const uint32_t* part_counts, const 
   }
 }
 
-template <bool kBf16, int kLanes, int kPer>
+template <bool kBf16, int kLanes, int kPer, int kVec>
 __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p, const uint8_t* __restrict__ valid,
                                                                      int64_t* __restrict__ ids,
                                                                      float* __restrict__ weights, uint32_t* part_counts,
@@ -186,11 +217,11 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p
     const bool there = row < p.tokens;
     const uint64_t from = there ? row : p.tokens - 1;
     float z[kPer];
-    load_logits<kBf16, kLanes, kPer>(p.logits, from, p.experts, l, z);
+    load_logits<kBf16, kLanes, kPer, kVec>(p.logits, from, p.experts, l, z);
     const bool wanted = there && (!valid || valid[from] != 0);
     uint32_t key[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) key[j] = l + kLanes * j < p.experts ? order_key(z[j]) : 0u;
+    for (int j = 0; j < kPer; ++j) key[j] = expert_of<kLanes, kVec>(l, j) < p.experts ? order_key(z[j]) : 0u;
     const float sum = row_softmax<kLanes, kPer>(z);
     // lane l keeps the pairs l, l + kLanes, ... until all are known
     constexpr uint32_t kKept = (trace_host::kMaxRouted < 64 ? trace_host::kMaxRouted : 64) / kLanes;
@@ -206,19 +237,19 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p
       best = row_max<kLanes>(best);
       uint32_t at = 0xffffffffu;
 #pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) at = key[i] == best ? l + kLanes * i : at;
+      for (int i = kPer - 1; i >= 0; --i) at = key[i] == best ? expert_of<kLanes, kVec>(l, i) : at;
       at = row_min<kLanes>(at);
       const bool found = best > kKeyOfMinusInfinity && wanted;
       float e = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const bool here = at == l + kLanes * i;
+        const bool here = at == expert_of<kLanes, kVec>(l, i);
         e = here ? z[i] : e;
         key[i] = here ? 0u : key[i];
       }
       // the chosen exponential is in one lane: the others add zeros
       e = found ? e : 0.f;
-      e = row_sum<kLanes>(at % kLanes == l ? e : 0.f);
+      e = row_sum<kLanes>(e);
       chosen += e;
       some |= found;
 #pragma unroll
@@ -252,7 +283,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p
       probs[j] += __shfl_xor(probs[j], 16);
       probs[j] += __shfl_xor(probs[j], 32);
     }
-    if (lane < kLanes) sums[wave][l + kLanes * j] = probs[j];
+    if (lane < kLanes) sums[wave][expert_of<kLanes, kVec>(l, j)] = probs[j];
   }
   __syncthreads();
   part_counts += (uint64_t)blockIdx.x * (p.experts + 1);
@@ -283,7 +314,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_finish_kernel(cons
 //   otherwise:    dz[e] -= p[e] s,  dz[ids[j]] += weights[j] grad_weights[j]
 //   balance:      dz[e] += p[e] (c[e] - sum of p c),  c[e] = grad_balance experts counts[e] / (sum of counts * N).
 // Rows without an expert (ids[t, 0] < 0) get zeros.
-template <bool kBf16, int kLanes, int kPer>
+template <bool kBf16, int kLanes, int kPer, int kVec>
 __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, const float* __restrict__ grad_weights,
                                                                const float* __restrict__ grad_balance,
                                                                const int64_t* __restrict__ ids,
@@ -296,7 +327,7 @@ __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, cons
     double pairs = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t e = l + kLanes * j;
+      const uint32_t e = expert_of<kLanes, kVec>(l, j);
       if (e < p.experts) pairs += (double)counts[e];
     }
 #pragma unroll
@@ -305,7 +336,7 @@ __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, cons
     const double each = pairs > 0 && rows > 0 ? (double)*grad_balance * p.experts / (pairs * rows) : 0.0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t e = l + kLanes * j;
+      const uint32_t e = expert_of<kLanes, kVec>(l, j);
       if (e < p.experts) c[j] = (float)(each * (double)counts[e]);
     }
   }
@@ -315,7 +346,7 @@ __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, cons
     const bool there = row < p.tokens;
     const uint64_t from = there ? row : p.tokens - 1;
     float z[kPer], dz[kPer];
-    load_logits<kBf16, kLanes, kPer>(p.logits, from, p.experts, l, z);
+    load_logits<kBf16, kLanes, kPer, kVec>(p.logits, from, p.experts, l, z);
     const bool wanted = ids[from * p.topk] >= 0;
     const float sum = row_softmax<kLanes, kPer>(z);
     float dot = 0.f;
@@ -328,33 +359,66 @@ __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, cons
 #pragma unroll
     for (int j = 0; j < kPer; ++j) dz[j] = z[j] * (c[j] - dot);
     if (grad_weights) {
-      // pairs kLanes at a time, one to a lane; their products' sum first
-      float s = 0.f;
-      for (uint32_t j = l; j < p.topk; j += kLanes)
-        if (ids[from * p.topk + j] >= 0) s += weights[from * p.topk + j] * grad_weights[from * p.topk + j];
+      // lane l holds pairs l, l + kLanes, ..., loaded at once
+      constexpr uint32_t kKept = 64 / kLanes;
+      int32_t id[kKept];
+      float w[kKept], g[kKept], s = 0.f;
+#pragma unroll
+      for (uint32_t i = 0; i < kKept; ++i) {
+        const uint32_t j = l + kLanes * i;
+        id[i] = -1, w[i] = 0.f, g[i] = 0.f;
+        if (j < p.topk) {
+          id[i] = (int32_t)ids[from * p.topk + j];
+          w[i] = weights[from * p.topk + j];
+          g[i] = grad_weights[from * p.topk + j];
+        }
+        if (id[i] >= 0) s += w[i] * g[i];
+      }
       s = row_sum<kLanes>(s);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) dz[i] -= p.renormalize ? 0.f : z[i] * s;
-      for (uint32_t j = 0; j < p.topk; ++j) {
-        const int64_t id = ids[from * p.topk + j];
-        if (id < 0) continue;
-        const float w = weights[from * p.topk + j], g = grad_weights[from * p.topk + j];
-        const float d = w * (p.renormalize ? g - s : g);
+      for (uint32_t i = 0; i < kKept; ++i) w[i] *= p.renormalize ? g[i] - s : g[i];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) dz[i] += id == (int64_t)(l + kLanes * i) ? d : 0.f;
+      for (int i = 0; i < kPer; ++i) dz[i] -= p.renormalize ? 0.f : z[i] * s;
+#pragma unroll
+      for (uint32_t k = 0; k < kKept; ++k) {
+        const uint32_t end = p.topk > kLanes * k ? (p.topk - kLanes * k < kLanes ? p.topk - kLanes * k : kLanes) : 0;
+        for (uint32_t j = 0; j < end; ++j) {
+          const int32_t at = __shfl(id[k], (int)j, kLanes);
+          const float d = __shfl(w[k], (int)j, kLanes);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) dz[i] += at == (int32_t)expert_of<kLanes, kVec>(l, i) ? d : 0.f;
+        }
       }
     }
     if (!there) continue;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t e = l + kLanes * j;
+    for (int i = 0; i < kPer; i += kVec) {
+      const uint32_t e = expert_of<kLanes, kVec>(l, i);
       if (e >= p.experts) continue;
-      const float v = wanted ? dz[j] : 0.f;
-      if (kBf16) {
-        const __bf16 h = (__bf16)v;
-        __builtin_memcpy(static_cast<uint16_t*>(grad_logits) + row * p.experts + e, &h, 2);
+      const uint64_t at = row * p.experts + e;
+      if constexpr (kVec == 1) {
+        const float v = wanted ? dz[i] : 0.f;
+        if constexpr (kBf16) {
+          const __bf16 h = (__bf16)v;
+          __builtin_memcpy(static_cast<uint16_t*>(grad_logits) + at, &h, 2);
+        } else {
+          static_cast<float*>(grad_logits)[at] = v;
+        }
       } else {
-        static_cast<float*>(grad_logits)[row * p.experts + e] = v;
+        constexpr int kDwords = kBf16 ? kVec / 2 : kVec;
+        uint32_t d[kDwords];
+#pragma unroll
+        for (int j = 0; j < kDwords; ++j) {
+          if constexpr (kBf16) {
+            const bf16x2 two = __builtin_convertvector(
+                (f32x2){wanted ? dz[i + 2 * j] : 0.f, wanted ? dz[i + 2 * j + 1] : 0.f}, bf16x2);
+            __builtin_memcpy(&d[j], &two, 4);
+          } else {
+            d[j] = __float_as_uint(wanted ? dz[i + j] : 0.f);
+          }
+        }
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<char*>(grad_logits) + at * (kBf16 ? 2 : 4), 4 * kDwords), d,
+                         4 * kDwords);
       }
     }
   }
@@ -375,18 +439,41 @@ uint32_t route_blocks(uint64_t tokens, uint32_t experts) {
   return (uint32_t)(blocks < most ? blocks : most);
 }
 
-template <bool kBf16, class Run>
-void by_experts(uint32_t experts, const Run& run) {
-  if (experts <= 64)
-    run(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
-  else if (experts <= 128)
-    run(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
-  else if (experts <= 256)
-    run(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
-  else if (experts <= 512)
-    run(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+// Kernels by the number of experts, and vectors of 16 bytes (8 bytes for up to 64
+// experts in bf16) where rows are whole ones: 65573 rows of 256 in bf16, their
+// gradients, 59 us one by one and KVEC_US so.
+template <bool kBf16, int kLanes, int kPer, class Run>
+void by_vectors(bool vectors, const Run& run) {
+  constexpr int kVec = kBf16 && kPer >= 8 ? 8 : 4;
+  constexpr std::integral_constant<bool, kBf16> bf16;
+  constexpr std::integral_constant<int, kLanes> lanes;
+  constexpr std::integral_constant<int, kPer> per;
+  if (vectors)
+    run(bf16, lanes, per, std::integral_constant<int, kVec>());
   else
-    run(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+    run(bf16, lanes, per, std::integral_constant<int, 1>());
+}
+template <bool kBf16, class Run>
+void by_experts(uint32_t experts, uintptr_t where, const Run& run) {
+  const uint32_t vec = kBf16 && experts > 64 ? 8 : 4;
+  const bool vectors = experts % vec == 0 && where % (vec * (kBf16 ? 2 : 4)) == 0;
+  if (experts <= 64)
+    by_vectors<kBf16, 16, 4>(vectors, run);
+  else if (experts <= 128)
+    by_vectors<kBf16, 16, 8>(vectors, run);
+  else if (experts <= 256)
+    by_vectors<kBf16, 16, 16>(vectors, run);
+  else if (experts <= 512)
+    by_vectors<kBf16, 64, 8>(vectors, run);
+  else
+    by_vectors<kBf16, 64, 16>(vectors, run);
+}
+template <class Run>
+void by_kind(const RouteArgs& p, uintptr_t where, const Run& run) {
+  if (p.bf16)
+    by_experts<true>(p.experts, where, run);
+  else
+    by_experts<false>(p.experts, where, run);
 }
 
 }  // namespace
@@ -402,17 +489,11 @@ hipError_t launch_route(const RouteArgs& p, const uint8_t* valid, void* workspac
   float* const part_probs = reinterpret_cast<float*>(part_counts + (uint64_t)blocks * (p.experts + 1));
   const RouteTotals out{counts, probs, balance};
   if (blocks) {
-    const auto run = [&](auto bf16) {
-      constexpr bool kB = decltype(bf16)::value;
-      by_experts<kB>(p.experts, [&](auto lanes, auto per) {
-        hipLaunchKernelGGL((expert_route_kernel<kB, decltype(lanes)::value, decltype(per)::value>), dim3(blocks),
-                           dim3(kRouteThreads), 0, stream, p, valid, ids, weights, part_counts, part_probs, out);
-      });
-    };
-    if (p.bf16)
-      run(std::true_type());
-    else
-      run(std::false_type());
+    by_kind(p, (uintptr_t)p.logits, [&](auto bf16, auto lanes, auto per, auto vec) {
+      hipLaunchKernelGGL((expert_route_kernel<decltype(bf16)::value, decltype(lanes)::value, decltype(per)::value,
+                                              decltype(vec)::value>),
+                         dim3(blocks), dim3(kRouteThreads), 0, stream, p, valid, ids, weights, part_counts, part_probs, out);
+    });
     if (hipError_t e = hipGetLastError()) return e;
     if (blocks == 1) return hipSuccess;
   }
@@ -428,17 +509,11 @@ hipError_t launch_route_bwd(const RouteArgs& p, const float* grad_weights, const
   const uint64_t blocks = (p.tokens + rows - 1) / rows;
   const uint64_t most = 2048 < kMaxGroups ? 2048 : kMaxGroups;
   const uint32_t grid = (uint32_t)(blocks < most ? blocks : most);
-  const auto run = [&](auto bf16) {
-    constexpr bool kB = decltype(bf16)::value;
-    by_experts<kB>(p.experts, [&](auto lanes, auto per) {
-      hipLaunchKernelGGL((expert_route_bwd_kernel<kB, decltype(lanes)::value, decltype(per)::value>), dim3(grid),
-                         dim3(256), 0, stream, p, grad_weights, grad_balance, ids, weights, counts, grad_logits);
-    });
-  };
-  if (p.bf16)
-    run(std::true_type());
-  else
-    run(std::false_type());
+  by_kind(p, (uintptr_t)p.logits | (uintptr_t)grad_logits, [&](auto bf16, auto lanes, auto per, auto vec) {
+    hipLaunchKernelGGL((expert_route_bwd_kernel<decltype(bf16)::value, decltype(lanes)::value, decltype(per)::value,
+                                                decltype(vec)::value>),
+                       dim3(grid), dim3(256), 0, stream, p, grad_weights, grad_balance, ids, weights, counts, grad_logits);
+  });
   return hipGetLastError();
 }
 
