@@ -16,10 +16,13 @@
 // that remain are listed, and for the backward pass packed, so that ignored rows
 // are neither read nor paid for.
 //
-// P is rounded to bf16 for the matrix instructions.  Its entries are divided by
-// the largest |grad_loss| first, which is multiplied back in fp32: equal gradients
-// (a mean) then leave the target's entry, close to one, nearly unrounded, where
-// they would otherwise round all of a batch's rows the same way.
+// The matrix instructions want P in bf16.  Its largest entry in a row as a rule is
+// the target's, p - 1: a rounding there is a factor on the token's whole part of the
+// gradients.  So a row is written over |p - 1|, which leaves the target's entry -1
+// and all others below one, and the factor |p - 1| scale grad_loss goes onto the sums
+// of grad_x in fp32, and for grad_w onto the token's row of x, whose elements
+// are then rounded each by itself.  Against 64 bits grad_x is off by little
+// more than its own rounding to bf16 and grad_w by 1.4 times that.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,7 +44,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // What the kernels of a call pass on in its workspace.
 struct CrossEntropyPlan {
   uint32_t count;     // tokens with a target
-  float grad_top;     // the largest finite |grad_loss| among them, or 1 where that is 0
+  float grad_top;     // the largest finite |grad_loss| among them, or 1 where that is 0: a unit for rows of x
   uint32_t pad[30];
 };
 static_assert(sizeof(CrossEntropyPlan) == 128, "a line of its own");
@@ -116,35 +119,6 @@ __global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const 
   }
 }
 
-// The rows with a target: x packed (zeros up to the next multiple of kTileT), and
-// for the backward pass the gradient over grad_top, lse in powers of two and the
-// target of each.
-struct PackedRow {
-  float grad;
-  float lse2;
-  int32_t target;
-  int32_t pad;
-};
-__global__ __launch_bounds__(256) void cross_entropy_pack_kernel(CrossEntropyArgs p, const float* __restrict__ grad_loss,
-                                                                 const float* __restrict__ lse,
-                                                                 const CrossEntropyPlan* __restrict__ plan,
-                                                                 const int32_t* __restrict__ list, uint4* rows,
-                                                                 PackedRow* about) {
-  const uint32_t vecs = p.k / 8, count = plan->count;
-  const uint64_t all = (uint64_t)tiles_of(count, kTileT) * kTileT * vecs;
-  const uint64_t stride = (uint64_t)gridDim.x * 256;
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
-    const uint32_t r = (uint32_t)(i / vecs), c = (uint32_t)(i - (uint64_t)r * vecs);
-    const int64_t t = r < count ? list[r] : -1;
-    rows[i] = t >= 0 ? reinterpret_cast<const uint4*>(p.x)[(uint64_t)t * vecs + c] : make_uint4(0, 0, 0, 0);
-    if (about && c == 0) {
-      PackedRow a{0.f, 0.f, -1, 0};
-      if (t >= 0) a = PackedRow{grad_loss[t] / plan->grad_top, lse[t] * kLog2e, (int32_t)p.targets[t], 0};
-      about[r] = a;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
   const bf16x2 p = __builtin_convertvector((f32x2){a, b}, bf16x2);
   uint32_t u;
@@ -153,6 +127,82 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
 }
 
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// The rows with a target: x packed, zeros up to the next multiple of kTileT.
+__global__ __launch_bounds__(256) void cross_entropy_pack_kernel(CrossEntropyArgs p,
+                                                                 const CrossEntropyPlan* __restrict__ plan,
+                                                                 const int32_t* __restrict__ list, uint4* rows) {
+  const uint32_t vecs = p.k / 8, count = plan->count;
+  const uint64_t all = (uint64_t)tiles_of(count, kTileT) * kTileT * vecs;
+  const uint64_t stride = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
+    const uint32_t r = (uint32_t)(i / vecs), c = (uint32_t)(i - (uint64_t)r * vecs);
+    rows[i] = r < count ? reinterpret_cast<const uint4*>(p.x)[(uint64_t)list[r] * vecs + c] : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// What the backward pass knows of a packed row: 1 / |p - 1|, lse in powers of two,
+// the target, and the factor |p - 1| scale grad_loss of its gradients.  All zero for
+// rows past the last one.
+struct PackedRow {
+  float over;
+  float lse2;
+  int32_t target;
+  float factor;
+};
+
+// The same for the backward pass, with the rows' facts, and x times factor over
+// grad_top.  A workgroup to a row; p of its target by a product of its own.
+__global__ __launch_bounds__(256) void cross_entropy_pack_bwd_kernel(
+    CrossEntropyArgs p, const float* __restrict__ grad_loss, const float* __restrict__ lse,
+    const CrossEntropyPlan* __restrict__ plan, const int32_t* __restrict__ list, uint4* rows, uint4* scaled,
+    PackedRow* about) {
+  __shared__ float part[2][4];
+  const uint32_t vecs = p.k / 8, count = plan->count, all = tiles_of(count, kTileT) * kTileT;
+  uint32_t turn = 0;
+  for (uint32_t r = blockIdx.x; r < all; r += gridDim.x, turn ^= 1) {
+    uint4* const to = rows + (uint64_t)r * vecs;
+    uint4* const to_scaled = scaled + (uint64_t)r * vecs;
+    if (r >= count) {  // the same for the whole workgroup
+      for (uint32_t c = threadIdx.x; c < vecs; c += 256) to[c] = to_scaled[c] = make_uint4(0, 0, 0, 0);
+      if (threadIdx.x == 0) about[r] = PackedRow{0.f, 0.f, -1, 0.f};
+      continue;
+    }
+    const uint32_t t = (uint32_t)list[r];
+    const int32_t target = (int32_t)p.targets[t];
+    const uint4* const x = reinterpret_cast<const uint4*>(p.x) + (uint64_t)t * vecs;
+    const uint4* const w = reinterpret_cast<const uint4*>(p.w) + (uint64_t)target * vecs;
+    float dot = 0.f;
+    for (uint32_t c = threadIdx.x; c < vecs; c += 256) {
+      const uint4 a = x[c], b = w[c];
+      to[c] = a;
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dot = fmaf(bf16_lo(u[i]), bf16_lo(v[i]), dot);
+        dot = fmaf(bf16_hi(u[i]), bf16_hi(v[i]), dot);
+      }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+    if ((threadIdx.x & 63) == 0) part[turn][threadIdx.x >> 6] = dot;
+    __syncthreads();  // one a row: the next one's parts go to the other half
+    dot = part[turn][0] + part[turn][1] + part[turn][2] + part[turn][3];
+    // p near one: |p - 1| is what the roundings of p leave, and 2^-20 will do
+    const float lse2 = lse[t] * kLog2e, rest = fabsf(1.f - exp2_of(dot * p.scale * kLog2e - lse2));
+    const float over = 1.f / (rest < 0x1p-20f ? 0x1p-20f : rest);  // a NaN stays
+    const float factor = grad_loss[t] * p.scale / over, by = factor / plan->grad_top;
+    if (threadIdx.x == 0) about[r] = PackedRow{over, lse2, target, factor};
+    for (uint32_t c = threadIdx.x; c < vecs; c += 256) {
+      const uint4 a = x[c];
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = two_bf16(bf16_lo(u[i]) * by, bf16_hi(u[i]) * by);
+      to_scaled[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
 
 // A maximum and the sum of 2^(value - maximum); an empty one is (-infinity, 0).
 struct TopSum {
@@ -247,7 +297,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
   for (int j = 0; j < T::kJ; ++j) {
     const uint32_t t = t0 + wj + 16 * j + r;
     int32_t target = -1;
-    PackedRow about{0.f, 0.f, -1, 0};
+    PackedRow about{0.f, 0.f, -1, 0.f};
     if (kBackward) {
       about = a.about[t];
       target = about.target;
@@ -296,7 +346,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
             const uint32_t row = 32 * q + 8 * g + e + o;
             float v = exp2_of(acc[2 * q + e / 4][j][e % 4 + o] * to_log2 - about.lse2);
             if (hits && target == (int32_t)row) v -= 1.f;
-            d[o] = ends && v0 + wi + row >= v_end ? 0.f : v * about.grad;
+            d[o] = ends && v0 + wi + row >= v_end ? 0.f : v * about.over;
           }
           u[e / 2] = two_bf16(d[0], d[1]);
         }
@@ -377,6 +427,7 @@ struct GradRowsArgs {
   const uint16_t* probs;
   uint32_t v0, slice, parts;
   bool first;     // of the slices
+  float one;      // 1: a product takes the sums out of the registers that hold them
   float* sums;    // [parts][pitch][k]
   uint64_t pitch;
 };
@@ -436,34 +487,38 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
       __builtin_amdgcn_sched_barrier(0);
       if (k0 + wi + 16 * i >= p.k) continue;  // k is a multiple of 32
       v4f* const at = reinterpret_cast<v4f*>(sums + ((16 * j + r) * p.k + 16 * i + 4 * g));
-      v4f v = acc[i][j] * p.scale;
+      v4f v = acc[i][j] * a.one;
       if (!a.first) v += *at;
       *at = v;
     }
 }
 
-// grad_x = grad_top * the parts' sums, to the tokens' own rows; zeros for ignored ones.
-__global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p,
-                                                                 const CrossEntropyPlan* __restrict__ plan,
+// grad_x = the rows' factors times the parts' sums, to the tokens' own rows; zeros for ignored ones.
+__global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p, const PackedRow* __restrict__ about,
                                                                  const int32_t* __restrict__ at,
                                                                  const float* __restrict__ sums, uint32_t parts,
                                                                  uint64_t pitch, uint16_t* __restrict__ grad_x) {
   const uint32_t vecs = p.k / 8;
   const uint64_t all = p.tokens * vecs, stride = (uint64_t)gridDim.x * 256;
-  const float by = plan->grad_top;
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
     const uint64_t t = i / vecs, c = i - t * vecs;
     const int32_t row = at[t];
     uint32_t u[4] = {0, 0, 0, 0};
     if (row >= 0) {
-      float v[8] = {};
+      const float by = about[row].factor;
+      v4f lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll 4
       for (uint32_t s = 0; s < parts; ++s) {
-        const float* from = sums + (s * pitch + (uint32_t)row) * p.k + 8 * c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += from[e];
+        const v4f* from = reinterpret_cast<const v4f*>(sums + (s * pitch + (uint32_t)row) * p.k + 8 * c);
+        lo += from[0];
+        hi += from[1];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = two_bf16(v[2 * e] * by, v[2 * e + 1] * by);
+      lo *= by;
+      hi *= by;
+      u[0] = two_bf16(lo[0], lo[1]);
+      u[1] = two_bf16(lo[2], lo[3]);
+      u[2] = two_bf16(hi[0], hi[1]);
+      u[3] = two_bf16(hi[2], hi[3]);
     }
     reinterpret_cast<uint4*>(grad_x)[i] = make_uint4(u[0], u[1], u[2], u[3]);
   }
@@ -473,7 +528,7 @@ __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArg
 struct GradWeightArgs {
   CrossEntropyArgs p;
   const CrossEntropyPlan* plan;
-  const uint16_t* rows;
+  const uint16_t* rows;  // scaled
   const uint16_t* probs;
   uint32_t v0, slice;
   uint16_t* grad_w;
@@ -513,7 +568,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(
   T::multiply(ring, stages, stages, false, from_i, from_j, [](auto&, auto&) {}, acc);
   const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
   const uint32_t wi = T::wave_i(), wj = T::wave_j();
-  const float by = a.plan->grad_top * p.scale;
+  const float by = a.plan->grad_top;
   const RowBlock<2 * T::kI> block{ring + 1024 * T::kI * wave};
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j) {
@@ -596,11 +651,12 @@ struct BackwardSpace {
   uint64_t tall;   // tokens rounded up to whole tiles
   uint32_t slice;  // of the vocabulary
   uint32_t parts;  // of a slice's contraction for grad_x
-  uint64_t list, at, about, rows, probs, sums, bytes;
+  uint64_t list, at, about, rows, scaled, probs, sums, bytes;
   BackwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
     tall = round_up(tokens, kTileT);
-    // P of half a gigabyte, but at least 8192 columns, to fill the card with tiles of grad_w
-    uint64_t s = (1ull << 28) / tall / kTileT * kTileT;
+    // P of a gigabyte, but at least 8192 columns, to fill the card with tiles of grad_w; each
+    // slice reads and writes grad_x's sums once
+    uint64_t s = (1ull << 29) / tall / kTileT * kTileT;
     if (s < 8192) s = 8192;
     if (s > round_up(vocab, kTileT)) s = round_up(vocab, kTileT);
     slice = (uint32_t)s;
@@ -613,7 +669,8 @@ struct BackwardSpace {
     at = list + 4 * tall;
     about = at + 4 * tall;
     rows = about + sizeof(PackedRow) * tall;
-    probs = rows + 2 * tall * k;
+    scaled = rows + 2 * tall * k;
+    probs = scaled + 2 * tall * k;
     sums = probs + 2 * tall * slice;
     bytes = sums + 4 * (uint64_t)parts * tall * k;
   }
@@ -664,8 +721,7 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
     if (hipError_t e = hipGetLastError()) return e;
     uint16_t* const rows = reinterpret_cast<uint16_t*>(at + s.rows);
     hipLaunchKernelGGL(cross_entropy_pack_kernel, vector_grid(round_up(p.tokens, kTileT) * (p.k / 8)), dim3(256), 0,
-                       stream, p, (const float*)nullptr, (const float*)nullptr, (const CrossEntropyPlan*)plan,
-                       (const int32_t*)list, reinterpret_cast<uint4*>(rows), (PackedRow*)nullptr);
+                       stream, p, (const CrossEntropyPlan*)plan, (const int32_t*)list, reinterpret_cast<uint4*>(rows));
     if (hipError_t e = hipGetLastError()) return e;
     a.plan = plan;
     a.list = list;
@@ -705,13 +761,16 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   int32_t* const places = reinterpret_cast<int32_t*>(at + s.at);
   PackedRow* const about = reinterpret_cast<PackedRow*>(at + s.about);
   uint16_t* const rows = reinterpret_cast<uint16_t*>(at + s.rows);
+  uint16_t* const scaled = reinterpret_cast<uint16_t*>(at + s.scaled);
   uint16_t* const probs = reinterpret_cast<uint16_t*>(at + s.probs);
   float* const sums = reinterpret_cast<float*>(at + s.sums);
   hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, grad_loss,
                      (uint32_t)p.tokens, p.vocab, plan, list, places);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL(cross_entropy_pack_kernel, vector_grid(s.tall * (p.k / 8)), dim3(256), 0, stream, p, grad_loss, lse,
-                     (const CrossEntropyPlan*)plan, (const int32_t*)list, reinterpret_cast<uint4*>(rows), about);
+  const uint64_t most = 8192 < kMaxGroups ? 8192 : kMaxGroups;
+  hipLaunchKernelGGL(cross_entropy_pack_bwd_kernel, dim3((uint32_t)(s.tall < most ? s.tall : most)), dim3(256), 0, stream,
+                     p, grad_loss, lse, (const CrossEntropyPlan*)plan, (const int32_t*)list,
+                     reinterpret_cast<uint4*>(rows), reinterpret_cast<uint4*>(scaled), about);
   if (hipError_t e = hipGetLastError()) return e;
   for (uint64_t v0 = 0; v0 < p.vocab; v0 += s.slice) {
     const uint64_t cols = p.vocab - v0 < s.slice ? p.vocab - v0 : s.slice;
@@ -732,7 +791,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
                        grid(p.tokens, cols, 1, small), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (grad_x) {
-      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, s.parts, v0 == 0, sums, s.tall};
+      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, s.parts, v0 == 0, 1.f, sums, s.tall};
       small = small_tiles(p.tokens, p.k, s.parts);
       hipLaunchKernelGGL((small ? cross_entropy_grad_rows_kernel<GradRows128, 2>
                                 : cross_entropy_grad_rows_kernel<GradRows256, 1>),
@@ -740,7 +799,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (grad_w) {
-      const GradWeightArgs g{p, plan, rows, probs, (uint32_t)v0, s.slice, grad_w};
+      const GradWeightArgs g{p, plan, scaled, probs, (uint32_t)v0, s.slice, grad_w};
       small = small_tiles(cols, p.k);
       hipLaunchKernelGGL((small ? cross_entropy_grad_weight_kernel<GradWeight128, 2>
                                 : cross_entropy_grad_weight_kernel<GradWeight256, 1>),
@@ -750,7 +809,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   }
   if (grad_x) {
     hipLaunchKernelGGL(cross_entropy_rows_kernel, vector_grid(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
-                       (const CrossEntropyPlan*)plan, (const int32_t*)places, (const float*)sums, s.parts, s.tall, grad_x);
+                       (const PackedRow*)about, (const int32_t*)places, (const float*)sums, s.parts, s.tall, grad_x);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;

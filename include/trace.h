@@ -766,8 +766,9 @@ TRACE_API trace_status trace_linear_cross_entropy(const uint16_t* x, const uint1
  *   grad_x = P W (bf16[tokens*k]; zeros for ignored tokens, whose grad_loss is
  *   not read), grad_w = P^T x (bf16[vocab*k]).
  * grad_x or grad_w may be NULL: that gradient is not computed.  P passes
- * through the workspace a slice of the vocabulary at a time, rounded to bf16;
- * an entry below 2^-126 of the largest |scale * grad_loss| counts as zero.
+ * through the workspace a slice of the vocabulary at a time, in bf16 over each
+ * row's |p - 1| (p the target's probability), which the sums are multiplied by; an
+ * entry below 2^-126 of that counts as zero.
  *   workspace : trace_linear_cross_entropy_bwd_workspace_bytes(tokens, vocab, k)
  *   bytes, 16-byte aligned. */
 TRACE_API size_t trace_linear_cross_entropy_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t k);

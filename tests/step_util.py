@@ -60,22 +60,22 @@ STEP = 2.0 ** -8  # half a step of bf16
 def gradients_close(got, want, size, terms, x, w, scale, ctx):
     """bf16 gradients.  Each of P's entries is off by the logit's error (relative,
     as above, k + 3 + 4 steps of the largest logit's size), by 8 roundings of its
-    own arithmetic and by half a step of bf16, 2^-8; their sum by `terms`
-    additions; the result by half a step.  An entry of P over the largest |grad_loss|
-    that is below 2^-126 counts as zero (the exponential gives no subnormal numbers,
-    the matrix instruction takes none), and one above may lose that much in
-    its two factors: 2^-125 of the largest gradient for each term, which `size` has
-    in it, over the 2^-8 below."""
+    own arithmetic and by half a step of bf16, 2^-8; for grad_w x times the row's
+    factor is rounded by half a step too; their sum by `terms` additions; the result
+    by half a step.  An entry of P over |p - 1| that is below 2^-126 counts as zero
+    (the exponential gives no subnormal numbers, the matrix instruction takes none), a
+    product of two factors near it as well: 2^-125 of the largest gradient for each
+    term, which `size` has in it, over the 2^-8 below."""
     k = x.shape[1]
     largest = float((x.double().abs().nan_to_num(0, 0, 0) @ w.double().abs().t().contiguous()).max()) * abs(scale)
-    each = STEP + 8 * 2.0 ** -24 + (k + 7) * 2.0 ** -24 * largest + largest * 2.0 ** -21
+    each = (2 if ctx[-1] == "grad_w" else 1) * STEP + 12 * 2.0 ** -24 + (k + 7) * 2.0 ** -24 * largest + largest * 2.0 ** -21
     tol = size * (each + terms * 2.0 ** -24)
     tol = tol + STEP * (want.abs() + tol) + 2.0 ** -133
     bad = ~((got.double() - want).abs() <= tol)
     if bad.any():
         i = tuple(bad.nonzero()[0].tolist())
         raise AssertionError((ctx, int(bad.sum()), i, got[i].item(), want[i].item(), tol[i].item()))
-    # and as a whole: independent roundings of P and of the result, 2^-9 of each at most on average
+    # as a whole: the result's rounding, at most 2^-8, and for grad_w as much again from x, independent of each other
     rel = float((got.double() - want).norm() / want.norm().clamp(min=1e-300))
     assert rel < 2.0 ** -7.5, (ctx, rel)
 

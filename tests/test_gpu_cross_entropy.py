@@ -100,9 +100,10 @@ def test_equal_gradients(device):
         _, lse = tr.linear_cross_entropy(x, w, targets)
         gx, gw = tr.linear_cross_entropy_bwd(grad, x, w, targets, lse)
         wx, ww, _, _ = U.loss_gradients(grad, x, w, targets)
-        # the result's own rounding is 2^-8 / sqrt(3) of a value at most on average; P's entries stay below as much again
-        for got, want in ((gx, wx), (gw, ww)):
-            assert float((got.double() - want).norm() / want.norm()) < 1.5 * 2.0 ** -8 / 3 ** 0.5, g
+        # the result's own rounding is 2^-8 / sqrt(3) of a value at most on average, with x's as much again for grad_w; P's
+        # entries add a little
+        for got, want, most in ((gx, wx, 1.1), (gw, ww, 1.5)):
+            assert float((got.double() - want).norm() / want.norm()) < most * 2.0 ** -8 / 3 ** 0.5, g
     zero = torch.zeros(700, device=device)
     gx, gw = tr.linear_cross_entropy_bwd(zero, x, w, targets, lse)
     assert (gx == 0).all() and (gw == 0).all()
@@ -221,8 +222,8 @@ def test_autograd(device):
     assert loss.shape == (2, 65)
     (loss * weight.view(2, 65)).sum().backward()
     wx, ww, sx, sw = U.loss_gradients(weight, x, w, t, 0.9)
-    U.gradients_close(xs.grad.reshape(130, 64), wx, sx, 333, x, w, 0.9, "x")
-    U.gradients_close(ws.grad, ww, sw, 138, x, w, 0.9, "w")
+    U.gradients_close(xs.grad.reshape(130, 64), wx, sx, 333, x, w, 0.9, ("autograd", "grad_x"))
+    U.gradients_close(ws.grad, ww, sw, 138, x, w, 0.9, ("autograd", "grad_w"))
     only = x.detach().requires_grad_(True)
     tr.LinearCrossEntropy.apply(only, w, t).sum().backward()  # a frozen weight
     assert only.grad is not None
@@ -247,8 +248,8 @@ def test_gradient_against_differences(device):
                             (gw, sw, lambda d, s: (x.double(), w.double() + s * h * d))):
         d = torch.randn(got.shape, device=device, dtype=torch.float64)
         slope = (f(*move(d, 1)) - f(*move(d, -1))) / (2 * h)
-        # each element's rounding, 2^-8 of itself, and P's, 2^-8 of the sum's size, with random signs: the sums of their
-        # sizes bound them, and a sixth of that is already out of reach
+        # each element's roundings, 2^-8 of itself or of the sum's size, have random signs: the sums of their sizes bound
+        # them, and a sixth of that is already out of reach
         assert abs(float((got.double() * d).sum()) - slope) <= float((size * d.abs()).sum()) * 2.0 ** -8 / 6 + 1e-6
 
 
