@@ -63,13 +63,18 @@ __device__ __forceinline__ void copies_to(uint32_t lds) {
 #endif
 }
 // Copies 16 bytes per lane from base + off + kAt, in the lanes that `lanes` has:
-// all of them or none (all are active here).
-template <uint32_t kAt>
+// all of them or none (all are active here).  kStream: past the caches, for what
+// is read once.
+template <uint32_t kAt, bool kStream>
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint64_t lanes) {
   static_assert(kAt < 4096, "the instruction's offset");
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%2\n\ts_mov_b64 exec, -1" ::"v"(off),
-               "s"(base), "n"(kAt), "s"(lanes));
+  if constexpr (kStream)
+    asm volatile("s_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%2 nt\n\ts_mov_b64 exec, -1" ::"v"(off),
+                 "s"(base), "n"(kAt), "s"(lanes));
+  else
+    asm volatile("s_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%2\n\ts_mov_b64 exec, -1" ::"v"(off),
+                 "s"(base), "n"(kAt), "s"(lanes));
 #endif
 }
 
@@ -146,17 +151,22 @@ struct TileOperand {
   }
 };
 
-template <int kI_, int kJ_, int kWI_, int kWJ_, bool kAcrossI, bool kAcrossJ, int kRing_>
+template <int kI_, int kJ_, int kWI_, int kWJ_, bool kAcrossI, bool kAcrossJ, int kRing_, bool kStreamI = false>
 struct Tile {
   static constexpr int kI = kI_, kJ = kJ_, kWI = kWI_, kWJ = kWJ_;
   static constexpr uint32_t kRing = kRing_;  // stages in LDS
-  static constexpr bool kPairs = !kAcrossI;
+  static constexpr bool kPairs = !kAcrossI && kI % 2 == 0;
+
+  // The wave's row i of element e of block b, in lane group g (lane / 16).
+  static __device__ __forceinline__ uint32_t row_of(uint32_t b, uint32_t g, uint32_t e) {
+    return kPairs ? 32 * (b / 2) + 8 * g + 4 * (b & 1) + e : 16 * b + 4 * g + e;
+  }
   static constexpr uint32_t kRowsI = 16 * kI * kWI, kRowsJ = 16 * kJ * kWJ;
   using I = TileOperand<kRowsI, kAcrossI>;
   using J = TileOperand<kRowsJ, kAcrossJ>;
   static constexpr uint32_t kStageBytes = I::kBytes + J::kBytes, kLds = kRing * kStageBytes;
   static constexpr uint32_t kCopies = I::kCopies + J::kCopies;
-  static_assert(kWI * kWJ == 4 && kI % 2 == 0 && kRing >= 2, "four waves, pairs of blocks");
+  static_assert(kWI * kWJ == 4 && kRing >= 2, "four waves");
   static_assert(kCopies * (kRing - 1) < 64 && kLds <= 163840, "what the wait can count; LDS");
 
   // This wave's first row of the tile's I and J.
@@ -217,11 +227,11 @@ struct Tile {
       constexpr uint32_t kN = decltype(n)::value;
       if constexpr (kN < J::kCopies) {
         if constexpr (kN % 4 == 0) copies_to(to_j + slot * kStageBytes + 1024 * kN);
-        copy_to_lds<1024 * (kN % 4)>(next_j, from_j.off[kN], lanes);
+        copy_to_lds<1024 * (kN % 4), false>(next_j, from_j.off[kN], lanes);
       } else if constexpr (kN < kCopies) {
         constexpr uint32_t kM = kN - J::kCopies;
         if constexpr (kM % 4 == 0) copies_to(to_i + slot * kStageBytes + 1024 * kM);
-        copy_to_lds<1024 * (kM % 4)>(next_i, from_i.off[kM], lanes);
+        copy_to_lds<1024 * (kM % 4), kStreamI>(next_i, from_i.off[kM], lanes);
       }
     };
     const uint32_t wi = wave_i(), wj = wave_j();

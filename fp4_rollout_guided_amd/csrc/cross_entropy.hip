@@ -219,58 +219,42 @@ __device__ __forceinline__ TopSum join(TopSum a, TopSum b) {
 // Forward: part[tile of v][token], hit[token].  Backward: P.
 struct LogitsArgs {
   CrossEntropyArgs p;
-  const CrossEntropyPlan* plan;  // nullptr: every token, in its own place
-  const int32_t* list;           // forward: the packed rows' tokens
-  TopSum* part;                  // [tiles of v][pitch]
+  const CrossEntropyPlan* plan;
+  const int32_t* list;  // forward: the packed rows' tokens
+  TopSum* part;         // [tiles of v, or shares][pitch]
   float* hit;
   uint64_t pitch;           // of part, tokens
-  const uint16_t* rows;     // packed x, where there is a plan
+  const uint16_t* rows;     // packed x
   const PackedRow* about;
   uint16_t* probs;          // P of the slice, [tokens rounded up][slice]
   uint32_t v0, slice;       // slice: a multiple of kTileT
 };
 
-template <class T, bool kBackward, int kPerCu>
-__global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(LogitsArgs a) {
-  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
-  const CrossEntropyArgs& p = a.p;
-  const uint32_t count = a.plan ? a.plan->count : (uint32_t)p.tokens;
-  const uint32_t v_end = p.vocab - a.v0 < a.slice ? p.vocab : a.v0 + a.slice;
-  const uint32_t tiles_v = tiles_of(v_end - a.v0, T::kRowsI), tiles_t = tiles_of(count, T::kRowsJ);
-  const uint64_t tiles = (uint64_t)tiles_v * tiles_t;
-  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
-  if (tile >= tiles) return;
-  // eight tiles of tokens at a time: an XCD's tiles share rows of both operands
-  constexpr uint32_t kGroup = 8;
-  const uint32_t group = (uint32_t)(tile / ((uint64_t)kGroup * tiles_v));
-  const uint32_t in = (uint32_t)(tile - (uint64_t)group * kGroup * tiles_v);
-  const uint32_t wide = tiles_t - group * kGroup < kGroup ? tiles_t - group * kGroup : kGroup;
-  const uint32_t tile_v = in / wide, tile_t = group * kGroup + in % wide;
-  const uint32_t v0 = a.v0 + tile_v * T::kRowsI, t0 = tile_t * T::kRowsJ;
+// acc = the products of w's rows from v0 on and of `tokens` rows x (packed ones
+// fill their tile).  Rows from v_end on, and past the tokens, are the tile's first
+// again: their results are left out.  k is a multiple of 32: of a last half stage only the
+// first k-step counts, and the lanes past its end read its own columns again.
+template <class T>
+__device__ __forceinline__ void logits_tile(char* ring, const CrossEntropyArgs& p, uint32_t v0, uint32_t v_end,
+                                            const uint16_t* x, uint32_t tokens, v4f (&acc)[T::kI][T::kJ]) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t wi = T::wave_i(), wj = T::wave_j();
-
   typename T::template Source<typename T::I> from_i;
   typename T::template Source<typename T::J> from_j;
   from_i.base = reinterpret_cast<const char*>(p.w + (uint64_t)v0 * p.k);
-  from_j.base = reinterpret_cast<const char*>((a.plan ? a.rows : p.x) + (uint64_t)t0 * p.k);
+  from_j.base = reinterpret_cast<const char*>(x);
   from_i.step = from_j.step = 2 * kStageC;
 #pragma unroll
   for (uint32_t n = 0; n < T::I::kCopies; ++n) {
     uint32_t row, col;
     T::I::place(wave, threadIdx.x & 63, n, row, col);
-    // rows past the last one: the tile's first, left out below
-    from_i.off[n] = 2 * ((v0 + row < p.vocab ? row : 0) * p.k + col);
+    from_i.off[n] = 2 * ((v0 + row < v_end ? row : 0) * p.k + col);
   }
 #pragma unroll
   for (uint32_t n = 0; n < T::J::kCopies; ++n) {
     uint32_t row, col;
     T::J::place(wave, threadIdx.x & 63, n, row, col);
-    from_j.off[n] = 2 * ((a.plan || t0 + row < count ? row : 0) * p.k + col);  // packed rows fill their tiles
+    from_j.off[n] = 2 * ((row < tokens ? row : 0) * p.k + col);
   }
-  // k is a multiple of 32: of a last half stage only the first k-step counts, and
-  // the lanes past its end read its own columns again
-  v4f acc[T::kI][T::kJ] = {};
   T::multiply(
       ring, tiles_of(p.k, kStageC), p.k / kStageC, p.k % kStageC != 0, from_i, from_j,
       [&](auto& i, auto& j) {
@@ -288,53 +272,129 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
         }
       },
       acc);
+}
 
+// The maximum and sum of a tile's column for each token, one per wave and token to
+// sums[wave's rows][token]; the targets' logits to hit.  target_of(t), t from t0 on:
+// the token's target below v_end, or -1.  Rows from v_end on are left out.
+template <class T, class TargetOf>
+__device__ __forceinline__ void column_sums(v4f (&acc)[T::kI][T::kJ], float scale, uint32_t v0, uint32_t v_end, uint32_t t0,
+                                            TargetOf target_of, float* hit, TopSum* sums) {
   const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
-  // blocks 2 q and 2 q + 1: v = wi + 32 q + 8 g + 0 .. 7; block j: token wj + 16 j + r
-  const float to_log2 = p.scale * kLog2e;
+  const uint32_t wi = T::wave_i(), wj = T::wave_j();
+  const float to_log2 = scale * kLog2e;
   const bool ends = v0 + T::kRowsI > v_end;
 #pragma unroll
   for (int j = 0; j < T::kJ; ++j) {
     const uint32_t t = t0 + wj + 16 * j + r;
-    int32_t target = -1;
-    PackedRow about{0.f, 0.f, -1, 0.f};
-    if (kBackward) {
-      about = a.about[t];
-      target = about.target;
-    } else if (t < count) {
-      const int64_t v = p.targets[a.plan ? (uint32_t)a.list[t] : t];
-      target = v >= 0 && v < (int64_t)p.vocab ? (int32_t)v : -1;
-    }
+    int32_t target = target_of(t);
     __builtin_amdgcn_sched_barrier(0);  // a block's values at a time: all of them would not fit the registers
-    target -= (int32_t)(v0 + wi);  // a target of -1 is below every row
+    target -= (int32_t)(v0 + wi);       // a target of -1 is below every row
     const bool hits = __ballot(target >= 0 && target < 16 * T::kI) != 0;
-    if constexpr (!kBackward) {
-      float top = -__builtin_inff();
+    float top = -__builtin_inff();
 #pragma unroll
-      for (int i = 0; i < T::kI; ++i)
+    for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t row = 32 * (i / 2) + 8 * g + 4 * (i & 1) + e;
-          if (hits && target == (int32_t)row) a.hit[t] = acc[i][j][e] * p.scale;
-          float z = acc[i][j][e] * to_log2;
-          if (ends && v0 + wi + row >= v_end) z = -__builtin_inff();
-          acc[i][j][e] = z;
-          top = fmaxf(top, z);
-        }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float from = top == -__builtin_inff() ? 0.f : top;
-      float sum = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t row = T::row_of(i, g, e);
+        if (hits && target == (int32_t)row) hit[t] = acc[i][j][e] * scale;
+        float z = acc[i][j][e] * to_log2;
+        if (ends && v0 + wi + row >= v_end) z = -__builtin_inff();
+        acc[i][j][e] = z;
+        top = fmaxf(top, z);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float from = top == -__builtin_inff() ? 0.f : top;
+    float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < T::kI; ++i)
+    for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += exp2_of(acc[i][j][e] - from);
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (g == 0) reinterpret_cast<TopSum*>(ring)[wi / (16 * T::kI) * T::kRowsJ + wj + 16 * j + r] = TopSum{top, sum};
-    } else {
-      static_assert(!kBackward || T::kJ % 2 == 0, "32 rows of P at a time");
-      const RowBlock<2 * T::kI> block{ring + 1024 * T::kI * wave};
+      for (int e = 0; e < 4; ++e) sum += exp2_of(acc[i][j][e] - from);
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (g == 0) sums[wi / (16 * T::kI) * T::kRowsJ + wj + 16 * j + r] = TopSum{top, sum};
+  }
+}
+
+// Few tokens: bound by w's bytes, which stream past the caches.  Each workgroup takes
+// an equal share of w's rows, whatever their number (whole tiles would leave the last
+// turn's units idle: 100003 rows in tiles of 128 are one and a half turns), a tile's
+// rows at a time, and leaves one sum.  The tokens' rows come from the caches once for
+// each tile, so that 64 tokens go with 128 rows (61 x 100003 x 7168: 244 us, 5.9 TB/s;
+// with 64 rows 284).  32 tokens go with 64, four workgroups to a compute unit, which
+// cover each other's ends (16 x 131072 x 2048: 97 us; two deeper ones 108).
+template <class T, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_few_kernel(LogitsArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  const CrossEntropyArgs& p = a.p;
+  const uint64_t shares = tiles_of(p.vocab, 16);
+  const uint32_t first = (uint32_t)(blockIdx.x * shares / gridDim.x) * 16;
+  const uint64_t past = ((uint64_t)blockIdx.x + 1) * shares / gridDim.x * 16;
+  const uint32_t end = past < p.vocab ? (uint32_t)past : p.vocab, count = (uint32_t)p.tokens;
+  TopSum all{-__builtin_inff(), 0.f};  // of token threadIdx.x
+  for (uint32_t v0 = first; v0 < end; v0 += T::kRowsI) {
+    v4f acc[T::kI][T::kJ] = {};
+    logits_tile<T>(ring, p, v0, end, p.x, count, acc);
+    TopSum* const sums = reinterpret_cast<TopSum*>(ring);
+    column_sums<T>(
+        acc, p.scale, v0, end, 0,
+        [&](uint32_t t) -> int32_t {
+          const int64_t v = t < count ? p.targets[t] : -1;
+          return v >= 0 && v < (int64_t)end ? (int32_t)v : -1;
+        },
+        a.hit, sums);
+    __syncthreads();
+    if (threadIdx.x < T::kRowsJ) {
+#pragma unroll
+      for (int w = 0; w < T::kWI; ++w) all = join(all, sums[w * T::kRowsJ + threadIdx.x]);
+    }
+    __syncthreads();  // the next tile's copies go there
+  }
+  if (threadIdx.x < count) a.part[blockIdx.x * a.pitch + threadIdx.x] = all;
+}
+
+template <class T, bool kBackward, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(LogitsArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  const CrossEntropyArgs& p = a.p;
+  const uint32_t count = a.plan->count;
+  const uint32_t v_end = p.vocab - a.v0 < a.slice ? p.vocab : a.v0 + a.slice;
+  const uint32_t tiles_v = tiles_of(v_end - a.v0, T::kRowsI), tiles_t = tiles_of(count, T::kRowsJ);
+  const uint64_t tiles = (uint64_t)tiles_v * tiles_t;
+  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  if (tile >= tiles) return;
+  // eight tiles of tokens at a time: an XCD's tiles share rows of both operands
+  constexpr uint32_t kGroup = 8;
+  const uint32_t group = (uint32_t)(tile / ((uint64_t)kGroup * tiles_v));
+  const uint32_t in = (uint32_t)(tile - (uint64_t)group * kGroup * tiles_v);
+  const uint32_t wide = tiles_t - group * kGroup < kGroup ? tiles_t - group * kGroup : kGroup;
+  const uint32_t tile_v = in / wide, tile_t = group * kGroup + in % wide;
+  const uint32_t v0 = a.v0 + tile_v * T::kRowsI, t0 = tile_t * T::kRowsJ;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  v4f acc[T::kI][T::kJ] = {};
+  logits_tile<T>(ring, p, v0, p.vocab, a.rows + (uint64_t)t0 * p.k, T::kRowsJ, acc);
+
+  if constexpr (!kBackward) {
+    column_sums<T>(
+        acc, p.scale, v0, v_end, t0,
+        [&](uint32_t t) -> int32_t { return t < count ? (int32_t)p.targets[(uint32_t)a.list[t]] : -1; }, a.hit,
+        reinterpret_cast<TopSum*>(ring));
+  } else {
+    // blocks 2 q and 2 q + 1: v = wi + 32 q + 8 g + 0 .. 7; block j: token wj + 16 j + r
+    const uint32_t lane = late_lane(), g = lane >> 4, r = lane & 15;
+    const uint32_t wi = T::wave_i(), wj = T::wave_j();
+    const float to_log2 = p.scale * kLog2e;
+    const bool ends = v0 + T::kRowsI > v_end;
+    static_assert(T::kPairs && T::kJ % 2 == 0, "32 rows of P at a time");
+    const RowBlock<2 * T::kI> block{ring + 1024 * T::kI * wave};
+#pragma unroll
+    for (int j = 0; j < T::kJ; ++j) {
+      const PackedRow about = a.about[t0 + wj + 16 * j + r];
+      __builtin_amdgcn_sched_barrier(0);  // a block's values at a time: all of them would not fit the registers
+      const int32_t target = about.target - (int32_t)(v0 + wi);
+      const bool hits = __ballot(target >= 0 && target < 16 * T::kI) != 0;
 #pragma unroll
       for (int q = 0; q < T::kI / 2; ++q) {
         uint32_t u[4];
@@ -606,8 +666,8 @@ constexpr uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to 
 // Tiles: vocabulary x tokens, k x tokens, k x vocabulary.
 using Logits256 = Tile<8, 8, 2, 2, false, false, 2>;
 using Logits128 = Tile<4, 4, 2, 2, false, false, 2>;
-using Logits64 = Tile<4, 2, 2, 2, false, false, 3>;
-using Logits32 = Tile<2, 2, 4, 1, false, false, 3>;
+using Few64 = Tile<2, 4, 4, 1, false, false, 3, true>;
+using Few32 = Tile<1, 2, 4, 1, false, false, 3, true>;
 using GradRows256 = Tile<8, 8, 2, 2, true, false, 2>;
 using GradRows128 = Tile<4, 4, 2, 2, true, false, 2>;
 using GradWeight256 = Tile<8, 8, 2, 2, true, true, 2>;
@@ -625,22 +685,27 @@ bool small_tiles(uint64_t n, uint64_t m, uint64_t parts = 1) {
 }
 
 // Few tokens are not listed: every one is computed, in its own place.
-constexpr uint64_t kUnlisted = 64;
+constexpr uint64_t kFew = 64;
+constexpr uint32_t kFewGroups = 1024;  // workgroups for them, of 64 rows of w at least
 
-uint32_t tile_rows_v(uint64_t tokens, uint32_t vocab) { return tokens <= 64 || small_tiles(tokens, vocab) ? 128u : 256u; }
+// Sums that the forward leaves for each token.
+uint32_t logits_parts(uint64_t tokens, uint32_t vocab) {
+  if (tokens > kFew) return (uint32_t)tiles_in(vocab, 1, small_tiles(tokens, vocab) ? 128 : 256);
+  const uint32_t shares = (vocab + 63) / 64;
+  return shares < kFewGroups ? shares : kFewGroups;
+}
 
 // Workspace of the forward.
 struct ForwardSpace {
   uint64_t pitch, tiles, list, at, rows, part, hit, bytes;
   ForwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
     pitch = round_up(tokens, 16);
-    const uint32_t rows_v = tile_rows_v(tokens, vocab);
-    tiles = (vocab + rows_v - 1) / rows_v;
-    const uint64_t lists = tokens > kUnlisted ? 4 * pitch : 0;
+    tiles = logits_parts(tokens, vocab);
+    const uint64_t lists = tokens > kFew ? 4 * pitch : 0;
     list = sizeof(CrossEntropyPlan);
     at = list + lists;
     rows = at + lists;
-    hit = rows + (tokens > kUnlisted ? 2 * round_up(tokens, kTileT) * k : 0);
+    hit = rows + (tokens > kFew ? 2 * round_up(tokens, kTileT) * k : 0);
     part = hit + 4 * pitch;
     bytes = part + tiles * pitch * sizeof(TopSum);
   }
@@ -684,13 +749,6 @@ dim3 vector_grid(uint64_t vecs) {
 uint32_t xcd_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 constexpr uint64_t kMostTiles = (1u << 24) - 8;  // a launch counts its work-items in 32 bits
 
-template <class T, int kPerCu>
-hipError_t run_logits(const LogitsArgs& a, uint64_t tokens, hipStream_t stream) {
-  const uint64_t tiles = (uint64_t)((a.p.vocab + T::kRowsI - 1) / T::kRowsI) * ((tokens + T::kRowsJ - 1) / T::kRowsJ);
-  hipLaunchKernelGGL((cross_entropy_logits_kernel<T, false, kPerCu>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, a);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 uint64_t cross_entropy_workspace_bytes(uint64_t tokens, uint32_t vocab, uint32_t k) {
@@ -705,7 +763,7 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
   const ForwardSpace s(p.tokens, p.vocab, p.k);
   if (tiles_in(p.tokens, p.vocab, 256) > kMostTiles) return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
-  const bool listed = p.tokens > kUnlisted;
+  const bool listed = p.tokens > kFew;
   LogitsArgs a{};
   a.p = p;
   a.part = reinterpret_cast<TopSum*>(at + s.part);
@@ -727,11 +785,16 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
     a.list = list;
     a.rows = rows;
   }
-  const hipError_t e = p.tokens <= 32    ? run_logits<Logits32, 2>(a, p.tokens, stream)
-                       : p.tokens <= 64  ? run_logits<Logits64, 2>(a, p.tokens, stream)
-                       : small_tiles(p.tokens, p.vocab) ? run_logits<Logits128, 2>(a, p.tokens, stream)
-                                                        : run_logits<Logits256, 1>(a, p.tokens, stream);
-  if (e) return e;
+  if (!listed) {
+    hipLaunchKernelGGL((p.tokens <= 32 ? cross_entropy_few_kernel<Few32, 4> : cross_entropy_few_kernel<Few64, 2>),
+                       dim3((uint32_t)s.tiles), dim3(256), 0, stream, a);
+  } else {
+    const bool small = small_tiles(p.tokens, p.vocab);
+    hipLaunchKernelGGL((small ? cross_entropy_logits_kernel<Logits128, false, 2>
+                              : cross_entropy_logits_kernel<Logits256, false, 1>),
+                       dim3(xcd_grid(tiles_in(p.tokens, p.vocab, small ? 128 : 256))), dim3(256), 0, stream, a);
+  }
+  if (hipError_t e = hipGetLastError()) return e;
   const auto join = [&](auto each, auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((uint32_t)((p.tokens + each - 1) / each)), dim3(256), 0, stream, p, places,
                        (const TopSum*)a.part, s.pitch, (uint32_t)s.tiles, (const float*)a.hit, loss, lse);
