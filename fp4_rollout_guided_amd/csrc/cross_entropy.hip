@@ -699,14 +699,14 @@ uint32_t logits_parts(uint64_t tokens, uint32_t vocab) {
 struct ForwardSpace {
   uint64_t pitch, tiles, list, at, rows, part, hit, bytes;
   ForwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
-    pitch = round_up(tokens, 16);
+    pitch = tokens > kFew ? round_up(tokens, 16) : tokens;
     tiles = logits_parts(tokens, vocab);
     const uint64_t lists = tokens > kFew ? 4 * pitch : 0;
     list = sizeof(CrossEntropyPlan);
     at = list + lists;
     rows = at + lists;
     hit = rows + (tokens > kFew ? 2 * round_up(tokens, kTileT) * k : 0);
-    part = hit + 4 * pitch;
+    part = hit + round_up(4 * pitch, 16);
     bytes = part + tiles * pitch * sizeof(TopSum);
   }
 };
