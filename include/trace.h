@@ -794,7 +794,7 @@ TRACE_API trace_status trace_linear_cross_entropy_bwd(const float* grad_loss, co
  *   balance: fp32[1], experts * sum over e of
  *            (counts[e] / sum of counts) * (probs[e] / counts[experts]), 0 with no rows;
  *   workspace : trace_expert_route_workspace_bytes(tokens, experts) bytes, 16-byte
- *            aligned (NULL where that is 0).
+ *            aligned.
  *   1 <= topk <= min(64, experts), experts <= 1024, tokens*topk below 2^31. */
 TRACE_API size_t trace_expert_route_workspace_bytes(int64_t tokens, int64_t experts);
 TRACE_API trace_status trace_expert_route(const uint16_t* logits, const uint8_t* valid, int64_t tokens,
