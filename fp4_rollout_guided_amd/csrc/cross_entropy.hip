@@ -45,18 +45,46 @@ constexpr float kLn2 = 0.69314718055994530942f;
 struct CrossEntropyPlan {
   uint32_t count;     // tokens with a target
   float grad_top;     // the largest finite |grad_loss| among them, or 1 where that is 0: a unit for rows of x
-  uint32_t pad[30];
+  uint32_t parts;     // of grad_x's contraction
+  uint32_t pad[29];
 };
 static_assert(sizeof(CrossEntropyPlan) == 128, "a line of its own");
 
-__device__ __forceinline__ uint32_t tiles_of(uint32_t n, uint32_t each) { return (n + each - 1) / each; }
+__host__ __device__ inline uint32_t tiles_of(uint32_t n, uint32_t each) { return (n + each - 1) / each; }
+
+// The time of a stage of `tiles` tiles of 256 or (small) 128, in units of 0.05 us.  A
+// compute unit holds one tile of 256 at a time (1.65 us), one of 128 (0.5) or two of
+// them (0.9).  So tiles of 128 win where those of 256 leave many units idle, in their
+// only or their last turn: grad_w of 1000 x 10007 x 1056, 5 us of 135.
+__host__ __device__ inline uint64_t stage_time(uint64_t tiles, bool small) {
+  if (!small) return (tiles + 255) / 256 * 33;
+  const uint32_t rest = tiles % 512;
+  return tiles / 512 * 18 + (rest == 0 ? 0 : (rest <= 256 ? 10 : 18));
+}
+
+// grad_x's contraction over a slice goes in parts, to fill the card, whose sums are
+// written and read again.  Its time in `parts`, in units of 0.05 us: the stages, 3 us to
+// start and end a turn, and 7 TB/s for `sums` elements of a part.  2000 tokens of k = 2048 go
+// in 4 parts of one turn rather than in 16 of four: 840 -> 736 us with the rest of the
+// gradients; 509 of k = 1056 in 7 of tiles of 128 rather than in 16 of 256: 94 -> 82.
+__host__ __device__ inline uint64_t parts_time(uint64_t tiles, uint32_t parts, uint32_t stages, uint64_t sums, bool small) {
+  const uint64_t turn = small ? 512 : 256;
+  return stage_time(tiles * parts, small) * tiles_of(stages, parts) + (tiles * parts + turn - 1) / turn * 60 +
+         parts * sums / 43750;
+}
+struct PartsRule {
+  uint32_t most;    // parts, up to 64; 0: none are wanted
+  uint32_t stages;  // of a slice
+  uint32_t k;
+  bool small;
+};
 
 // list[i]: the i-th token with a target; at[t]: the place of token t, or -1.
 __global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const int64_t* __restrict__ targets,
                                                                           const float* __restrict__ grad_loss,
                                                                           uint32_t tokens, uint32_t vocab,
-                                                                          CrossEntropyPlan* plan, int32_t* list,
-                                                                          int32_t* at) {
+                                                                          PartsRule rule, CrossEntropyPlan* plan,
+                                                                          int32_t* list, int32_t* at) {
   constexpr uint32_t kWaves = kPlanThreads / 64, kEach = 8;
   __shared__ uint32_t part[kWaves];
   __shared__ uint32_t tops[kWaves];
@@ -67,18 +95,18 @@ __global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const 
     bool has[kEach];
     uint64_t mask[kEach];
     uint32_t mine = 0;
+    int64_t v[kEach];
+    uint32_t g[kEach];
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {  // all loads under way at once
+      const uint64_t t = t0 + (wave * kEach + i) * 64 + lane;
+      v[i] = t < tokens ? targets[t] : -1;
+      g[i] = t < tokens && grad_loss ? __float_as_uint(grad_loss[t]) & 0x7fffffffu : 0u;
+    }
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
-      const uint64_t t = t0 + (wave * kEach + i) * 64 + lane;
-      has[i] = false;
-      if (t < tokens) {
-        const int64_t v = targets[t];
-        has[i] = v >= 0 && v < (int64_t)vocab;
-        if (grad_loss && has[i]) {
-          const uint32_t g = __float_as_uint(grad_loss[t]) & 0x7fffffffu;
-          if (g < 0x7f800000u) top = g > top ? g : top;
-        }
-      }
+      has[i] = v[i] >= 0 && v[i] < (int64_t)vocab;
+      if (has[i] && g[i] < 0x7f800000u) top = g[i] > top ? g[i] : top;
     }
 #pragma unroll
     for (uint32_t i = 0; i < kEach; ++i) {
@@ -111,6 +139,19 @@ __global__ __launch_bounds__(kPlanThreads) void cross_entropy_plan_kernel(const 
     top = o > top ? o : top;
   }
   if (lane == 0) tops[wave] = top;
+  if (wave == 0 && rule.most) {  // a lane to a number of parts
+    const uint32_t edge = rule.small ? 128 : 256;
+    const uint64_t tiles = (uint64_t)tiles_of(before, edge) * tiles_of(rule.k, edge);
+    uint64_t best = ~0ull;
+    if (lane < rule.most)
+      best = parts_time(tiles, lane + 1, rule.stages, (uint64_t)tiles_of(before, edge) * edge * rule.k, rule.small) << 6 | lane;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const uint64_t o = __shfl_xor(best, d);
+      best = o < best ? o : best;
+    }
+    if (lane == 0) plan->parts = (uint32_t)(best & 63) + 1;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     for (uint32_t w = 1; w < kWaves; ++w) top = tops[w] > top ? tops[w] : top;
@@ -485,7 +526,7 @@ struct GradRowsArgs {
   CrossEntropyArgs p;
   const CrossEntropyPlan* plan;
   const uint16_t* probs;
-  uint32_t v0, slice, parts;
+  uint32_t v0, slice;
   bool first;     // of the slices
   float one;      // 1: a product takes the sums out of the registers that hold them
   float* sums;    // [parts][pitch][k]
@@ -496,7 +537,8 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
   __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
   const CrossEntropyArgs& p = a.p;
   const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_t = tiles_of(a.plan->count, T::kRowsJ);
-  const uint64_t tiles = (uint64_t)tiles_k * tiles_t * a.parts;
+  const uint32_t parts = a.plan->parts;
+  const uint64_t tiles = (uint64_t)tiles_k * tiles_t * parts;
   const uint64_t tile = xcd_tile(blockIdx.x, tiles);
   if (tile >= tiles) return;
   const uint32_t part = (uint32_t)(tile / ((uint64_t)tiles_k * tiles_t));
@@ -504,7 +546,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
   const uint32_t k0 = in % tiles_k * T::kRowsI, t0 = in / tiles_k * T::kRowsJ;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t all = tiles_of(p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice, kStageC);
-  const uint32_t begin = (uint32_t)((uint64_t)all * part / a.parts), end = (uint32_t)((uint64_t)all * (part + 1) / a.parts);
+  const uint32_t begin = (uint32_t)((uint64_t)all * part / parts), end = (uint32_t)((uint64_t)all * (part + 1) / parts);
   const uint32_t left = p.vocab - a.v0;  // rows of w from the slice on; P is zero past them, any row will do
   typename T::template Source<typename T::I> from_i;
   typename T::template Source<typename T::J> from_j;
@@ -556,9 +598,10 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
 // grad_x = the rows' factors times the parts' sums, to the tokens' own rows; zeros for ignored ones.
 __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p, const PackedRow* __restrict__ about,
                                                                  const int32_t* __restrict__ at,
-                                                                 const float* __restrict__ sums, uint32_t parts,
+                                                                 const float* __restrict__ sums,
+                                                                 const CrossEntropyPlan* __restrict__ plan,
                                                                  uint64_t pitch, uint16_t* __restrict__ grad_x) {
-  const uint32_t vecs = p.k / 8;
+  const uint32_t vecs = p.k / 8, parts = plan->parts;
   const uint64_t all = p.tokens * vecs, stride = (uint64_t)gridDim.x * 256;
   for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += stride) {
     const uint64_t t = i / vecs, c = i - t * vecs;
@@ -675,13 +718,13 @@ using GradWeight128 = Tile<4, 4, 2, 2, true, true, 2>;
 
 constexpr uint64_t tiles_in(uint64_t n, uint64_t m, uint64_t each) { return (n + each - 1) / each * ((m + each - 1) / each); }
 
-// Whether n x m results (times `parts`) are done in tiles of 128 rather than 256.
-// A compute unit holds one tile of 256 or two of 128; a stage of one takes some
-// 1.9 us, of two of the others side by side 1.1.  So tiles of 128 win where those of
-// 256 leave many units idle (in their only, or their last, turn).
-bool small_tiles(uint64_t n, uint64_t m, uint64_t parts = 1) {
-  const uint64_t turns256 = (tiles_in(n, m, 256) * parts + 255) / 256, turns128 = (tiles_in(n, m, 128) * parts + 511) / 512;
-  return 11 * turns128 < 19 * turns256;
+constexpr uint64_t kMostTiles = (1u << 24) - 8;  // a launch counts its work-items in 32 bits
+
+// Whether n x m results are done in tiles of 128 rather than 256: they read the
+// operands twice as often, and have to be a tenth better for it.
+bool small_tiles(uint64_t n, uint64_t m) {
+  const uint64_t small = tiles_in(n, m, 128);
+  return small <= kMostTiles && 10 * stage_time(small, true) < 9 * stage_time(tiles_in(n, m, 256), false);
 }
 
 // Few tokens are not listed: every one is computed, in its own place.
@@ -715,7 +758,7 @@ struct ForwardSpace {
 struct BackwardSpace {
   uint64_t tall;   // tokens rounded up to whole tiles
   uint32_t slice;  // of the vocabulary
-  uint32_t parts;  // of a slice's contraction for grad_x
+  PartsRule parts;  // of a slice's contraction for grad_x
   uint64_t list, at, about, rows, scaled, probs, sums, bytes;
   BackwardSpace(uint64_t tokens, uint32_t vocab, uint32_t k) {
     tall = round_up(tokens, kTileT);
@@ -725,11 +768,20 @@ struct BackwardSpace {
     if (s < 8192) s = 8192;
     if (s > round_up(vocab, kTileT)) s = round_up(vocab, kTileT);
     slice = (uint32_t)s;
-    // of a slice's contraction for grad_x: until its tiles take four turns, but
-    // eight stages at least to each
-    const uint64_t tiles = tiles_in(tall, k, 256), most = (s + 8 * kStageC - 1) / (8 * kStageC);
-    parts = (uint32_t)(1024 / tiles < 1 ? 1 : (1024 / tiles > 16 ? 16 : 1024 / tiles));
-    if (parts > most) parts = (uint32_t)most;
+    // as many as all tokens could want, eight stages at least to each; the ones of a
+    // call are chosen when the tokens with a target are known
+    parts = PartsRule{0, (uint32_t)(s / kStageC), k, false};
+    uint64_t best = ~0ull;
+    for (const bool small : {false, true})
+      for (uint32_t n = 1; n <= 16 && (n == 1 || 8 * n <= parts.stages); ++n) {
+        const uint64_t time =
+            (small ? 10 : 9) * parts_time(tiles_in(tokens, k, small ? 128 : 256), n, parts.stages, tall * k, small);
+        if (time < best && (!small || tiles_in(tokens, k, 128) * 16 <= kMostTiles)) best = time, parts.small = small;
+      }
+    // fewer tokens fill fewer tiles, and want more parts: up to four turns
+    const uint64_t tiles = tiles_in(tokens, k, parts.small ? 128 : 256), turns = (parts.small ? 2048 : 1024) / tiles;
+    parts.most = (uint32_t)(turns < 1 ? 1 : (turns > 16 ? 16 : turns));
+    if (8 * parts.most > parts.stages) parts.most = parts.stages < 8 ? 1 : parts.stages / 8;
     list = sizeof(CrossEntropyPlan);
     at = list + 4 * tall;
     about = at + 4 * tall;
@@ -737,7 +789,7 @@ struct BackwardSpace {
     scaled = rows + 2 * tall * k;
     probs = scaled + 2 * tall * k;
     sums = probs + 2 * tall * slice;
-    bytes = sums + 4 * (uint64_t)parts * tall * k;
+    bytes = sums + 4 * (uint64_t)parts.most * tall * k;
   }
 };
 
@@ -747,7 +799,6 @@ dim3 vector_grid(uint64_t vecs) {
 }
 
 uint32_t xcd_grid(uint64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
-constexpr uint64_t kMostTiles = (1u << 24) - 8;  // a launch counts its work-items in 32 bits
 
 }  // namespace
 
@@ -775,7 +826,7 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
   int32_t* const places = listed ? reinterpret_cast<int32_t*>(at + s.at) : nullptr;
   if (listed) {
     hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, (const float*)nullptr,
-                       (uint32_t)p.tokens, p.vocab, plan, list, places);
+                       (uint32_t)p.tokens, p.vocab, PartsRule{}, plan, list, places);
     if (hipError_t e = hipGetLastError()) return e;
     uint16_t* const rows = reinterpret_cast<uint16_t*>(at + s.rows);
     hipLaunchKernelGGL(cross_entropy_pack_kernel, vector_grid(round_up(p.tokens, kTileT) * (p.k / 8)), dim3(256), 0,
@@ -815,7 +866,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     return hipGetLastError();
   }
   const BackwardSpace s(p.tokens, p.vocab, p.k);
-  if (tiles_in(p.tokens, s.slice, 256) > kMostTiles || tiles_in(p.tokens, p.k, 256) * s.parts > kMostTiles ||
+  if (tiles_in(p.tokens, s.slice, 256) > kMostTiles || tiles_in(p.tokens, p.k, s.parts.small ? 128 : 256) * s.parts.most > kMostTiles ||
       tiles_in(s.slice, p.k, 256) > kMostTiles)
     return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
@@ -828,7 +879,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   uint16_t* const probs = reinterpret_cast<uint16_t*>(at + s.probs);
   float* const sums = reinterpret_cast<float*>(at + s.sums);
   hipLaunchKernelGGL(cross_entropy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p.targets, grad_loss,
-                     (uint32_t)p.tokens, p.vocab, plan, list, places);
+                     (uint32_t)p.tokens, p.vocab, s.parts, plan, list, places);
   if (hipError_t e = hipGetLastError()) return e;
   const uint64_t most = 8192 < kMaxGroups ? 8192 : kMaxGroups;
   hipLaunchKernelGGL(cross_entropy_pack_bwd_kernel, dim3((uint32_t)(s.tall < most ? s.tall : most)), dim3(256), 0, stream,
@@ -854,11 +905,11 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
                        grid(p.tokens, cols, 1, small), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (grad_x) {
-      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, s.parts, v0 == 0, 1.f, sums, s.tall};
-      small = small_tiles(p.tokens, p.k, s.parts);
+      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, v0 == 0, 1.f, sums, s.tall};
+      small = s.parts.small;
       hipLaunchKernelGGL((small ? cross_entropy_grad_rows_kernel<GradRows128, 2>
                                 : cross_entropy_grad_rows_kernel<GradRows256, 1>),
-                         grid(p.tokens, p.k, s.parts, small), dim3(256), 0, stream, g);
+                         grid(p.tokens, p.k, s.parts.most, small), dim3(256), 0, stream, g);
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (grad_w) {
@@ -872,7 +923,7 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   }
   if (grad_x) {
     hipLaunchKernelGGL(cross_entropy_rows_kernel, vector_grid(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
-                       (const PackedRow*)about, (const int32_t*)places, (const float*)sums, s.parts, s.tall, grad_x);
+                       (const PackedRow*)about, (const int32_t*)places, (const float*)sums, (const CrossEntropyPlan*)plan, s.tall, grad_x);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
