@@ -805,6 +805,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel()
+
+
 # A device's current stream as an integer.  A Stream object for each call would
 # take a microsecond of the ten that a small product's call takes.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -860,6 +864,18 @@ def _out(t, name, like, shape, dtype):
     if t is None:
         return like.new_empty(shape, dtype=dtype)
     return _arg(t, name, like, _BF16 if dtype == torch.bfloat16 else (dtype,), n)
+
+
+def _outs(like, workspace_bytes, workspace, *outs):
+    """Several outputs, each (given, name, shape, dtype), and the workspace
+    after them: those that were given checked, the others made at once."""
+    if workspace is None and all(o[0] is None for o in outs):
+        wanted = []
+        for _, _, shape, dtype in outs:
+            wanted += (shape, dtype)
+        return _tensor_lists.empties(like, *wanted, workspace_bytes, torch.uint8)
+    return (*(_out(t, name, like, shape, dtype) for t, name, shape, dtype in outs),
+            _workspace(workspace, like, workspace_bytes))
 
 
 def _rows_type(dtype):
@@ -1292,15 +1308,14 @@ def expert_route(logits, topk, renormalize=True, valid=None, ids=None, weights=N
     suffix, tokens, experts = _router(logits, topk)
     if valid is not None:
         _fit(valid, "valid", logits, (torch.bool, torch.uint8), tokens)
-    ids = _out(ids, "ids", logits, (tokens, topk), torch.int64)
-    weights = _out(weights, "weights", logits, (tokens, topk), torch.float32)
-    counts = _out(counts, "counts", logits, (experts + 1,), torch.int64)
-    probs = _out(probs, "probs", logits, (experts,), torch.float32)
-    balance = _out(balance, "balance", logits, (1,), torch.float32)
-    workspace = _workspace(workspace, logits, lib.trace_expert_route_workspace_bytes(tokens, experts))
+    ids, weights, counts, probs, balance, workspace = _outs(
+        logits, lib.trace_expert_route_workspace_bytes(tokens, experts), workspace,
+        (ids, "ids", (tokens, topk), torch.int64), (weights, "weights", (tokens, topk), torch.float32),
+        (counts, "counts", (experts + 1,), torch.int64), (probs, "probs", (experts,), torch.float32),
+        (balance, "balance", (1,), torch.float32))
     _launch("trace_expert_route" + suffix, logits, _addr(logits), _addr(valid), tokens, experts, topk,
-            int(bool(renormalize)), _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(ids),
-            _addr(weights), _addr(counts), _addr(probs), _addr(balance))
+            int(bool(renormalize)), _addr(workspace), _bytes(workspace), _addr(ids), _addr(weights), _addr(counts),
+            _addr(probs), _addr(balance))
     return ids, weights, counts, probs, balance
 
 
@@ -1313,15 +1328,22 @@ def expert_route_bwd(grad_weights, grad_balance, logits, ids, weights, counts, r
         raise ValueError("ids must be [tokens, topk]")
     suffix, tokens, experts = _router(logits, ids.shape[1])
     topk = ids.shape[1]
-    _fit(ids, "ids", logits, _I64, tokens * topk)
-    _fit(weights, "weights", logits, _F32, tokens * topk)
-    _fit(counts, "counts", logits, _I64, experts + 1)
-    if grad_weights is not None:
-        _fit(grad_weights, "grad_weights", logits, _F32, tokens * topk)
-    if grad_balance is not None:
-        _fit(grad_balance, "grad_balance", logits, _F32, 1)
-    grad_logits = _out(grad_logits, "grad_logits", logits, tuple(logits.shape),
-                       torch.float32 if suffix else torch.bfloat16)
+    pairs = tokens * topk
+    if weights is None or counts is None or not _tensor_lists.fits(  # otherwise: which one, and why
+            logits, ids, torch.int64, pairs, weights, torch.float32, pairs, counts, torch.int64, experts + 1,
+            grad_weights, torch.float32, pairs, grad_balance, torch.float32, 1):
+        _fit(ids, "ids", logits, _I64, pairs)
+        _fit(weights, "weights", logits, _F32, pairs)
+        _fit(counts, "counts", logits, _I64, experts + 1)
+        if grad_weights is not None:
+            _fit(grad_weights, "grad_weights", logits, _F32, pairs)
+        if grad_balance is not None:
+            _fit(grad_balance, "grad_balance", logits, _F32, 1)
+    dtype = torch.float32 if suffix else torch.bfloat16
+    if grad_logits is None:
+        grad_logits, = _tensor_lists.empties(logits, tuple(logits.shape), dtype)
+    else:
+        _out(grad_logits, "grad_logits", logits, tuple(logits.shape), dtype)
     _launch("trace_expert_route_bwd" + suffix, logits, _addr(grad_weights), _addr(grad_balance), _addr(logits),
             _addr(ids), _addr(weights), _addr(counts), tokens, experts, topk, int(bool(renormalize)),
             _addr(grad_logits))
@@ -1378,11 +1400,11 @@ def linear_cross_entropy(x, w, targets, scale=1.0, loss=None, lse=None, workspac
     minus the target's log-probability; tokens whose target lies outside
     [0, vocab) are ignored, with loss and lse 0."""
     tokens, vocab, k = _logits_of(x, w, targets)
-    loss = _out(loss, "loss", x, tuple(x.shape[:-1]), torch.float32)
-    lse = _out(lse, "lse", x, tuple(x.shape[:-1]), torch.float32)
-    workspace = _workspace(workspace, x, lib.trace_linear_cross_entropy_workspace_bytes(tokens, vocab, k))
+    shape = tuple(x.shape[:-1])
+    loss, lse, workspace = _outs(x, lib.trace_linear_cross_entropy_workspace_bytes(tokens, vocab, k), workspace,
+                                 (loss, "loss", shape, torch.float32), (lse, "lse", shape, torch.float32))
     _launch("trace_linear_cross_entropy", x, _addr(x), _addr(w), _addr(targets), tokens, vocab, k, scale,
-            _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(loss), _addr(lse))
+            _addr(workspace), _bytes(workspace), _addr(loss), _addr(lse))
     return loss, lse
 
 
@@ -1399,7 +1421,7 @@ def linear_cross_entropy_bwd(grad_loss, x, w, targets, lse, scale=1.0, grad_x=No
     grad_w = _out(grad_w, "grad_w", x, tuple(w.shape), torch.bfloat16) if want_w else None
     workspace = _workspace(workspace, x, lib.trace_linear_cross_entropy_bwd_workspace_bytes(tokens, vocab, k))
     _launch("trace_linear_cross_entropy_bwd", x, _addr(grad_loss), _addr(x), _addr(w), _addr(targets), _addr(lse),
-            tokens, vocab, k, scale, _addr(workspace), 0 if workspace is None else workspace.numel(), _addr(grad_x),
+            tokens, vocab, k, scale, _addr(workspace), _bytes(workspace), _addr(grad_x),
             _addr(grad_w))
     return grad_x, grad_w
 

@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_math.h"
 #include "fp4_block.h"
 #include "launch.h"
@@ -33,16 +35,30 @@ using trace_host::AdamwTensor;
 
 constexpr uint32_t kAdamThreads = 256;
 constexpr uint32_t kAdamChunk = 4096;
-// Tensors of a launch: their descriptors are kernel arguments, 4 KiB at most.
-constexpr uint32_t kAdamTensors = 48;
-
+// A launch's tensors are kernel arguments, 4 KiB at most: without the addresses of
+// scales a wave's lanes' number of them.
+struct AdamwPlain {
+  explicit AdamwPlain(const AdamwTensor& t) : param(t.param), grad(t.grad), avg(t.avg), sq(t.sq), copy(t.copy), n(t.n) {}
+  AdamwPlain() = default;
+  void* param;
+  const void* grad;
+  void* avg;
+  void* sq;
+  uint16_t* copy;
+  uint64_t n;
+  static constexpr uint8_t *avg_scales = nullptr, *sq_scales = nullptr;
+};
+template <bool kMx8>
 struct AdamwBatch {
-  AdamwTensor t[kAdamTensors];
-  uint32_t first[kAdamTensors];  // the tensor's first workgroup
-  uint64_t place[kAdamTensors];  // of its first element among all tensors' elements, each tensor filled up to 32
+  static constexpr uint32_t kMost = kMx8 ? 48 : 64;
+  using Tensor = std::conditional_t<kMx8, AdamwTensor, AdamwPlain>;
+  Tensor t[kMost];
+  uint64_t place[kMost];  // of its first element among all tensors' elements, each tensor filled up to 32
+  uint32_t first[kMost];  // the tensor's first workgroup
   uint32_t count;
 };
-static_assert(sizeof(AdamwBatch) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
+static_assert(sizeof(AdamwBatch<true>) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
+static_assert(sizeof(AdamwBatch<false>) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -229,8 +245,8 @@ __device__ __forceinline__ uint32_t bf16_nearest(float p) {
 
 // One workgroup's elements; kWhole: all of its chunk exist.
 template <bool kParamBf16, bool kGradBf16, bool kMx8, bool kNT, bool kWhole>
-__device__ __forceinline__ void adamw_chunk(const AdamwTensor& all, uint64_t chunk, uint64_t first_place,
-                                            const AdamwScalars& s, float gs, bool random) {
+__device__ __forceinline__ void adamw_chunk(const typename AdamwBatch<kMx8>::Tensor& all, uint64_t chunk,
+                                            uint64_t first_place, const AdamwScalars& s, float gs, bool random) {
   constexpr int kPer = kMx8 ? 8 : 4;  // to a lane: a block of 32 is four lanes
   constexpr uint32_t kRounds = kAdamChunk / (kAdamThreads * kPer);
   // the chunk's own tensors: places within it take 32 bits
@@ -343,7 +359,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwTensor& all, uint64_t chu
 }
 
 template <bool kParamBf16, bool kGradBf16, bool kMx8, bool kNT>
-__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamwBatch batch, AdamwScalars s,
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamwBatch<kMx8> batch, AdamwScalars s,
                                                              const float* __restrict__ grad_scale, bool random) {
   // the tensor of this workgroup: the last one that starts at or before it
   const uint32_t lane = threadIdx.x & 63;
@@ -363,28 +379,20 @@ namespace trace_host {
 
 using namespace trace_dev;
 
-hipError_t launch_adamw(const AdamwTensor* tensors, uint32_t count, const AdamwTypes& types, const AdamwScalars& s,
-                        const float* grad_scale, hipStream_t stream) {
-  const uint64_t each = (types.param_bf16 ? 4 : 8) + (types.grad_bf16 ? 2 : 4) + (types.mx8 ? 4 : 16);
-  uint64_t all = 0;
-  for (uint32_t i = 0; i < count; ++i) all += tensors[i].n;
-  const bool nt = past_cache(all * each);
+namespace {
+
+template <bool kParamBf16, bool kGradBf16, bool kMx8>
+hipError_t run_adamw(const AdamwTensor* tensors, uint32_t count, bool nt, const AdamwScalars& s, const float* grad_scale,
+                     bool random, hipStream_t stream) {
   constexpr uint32_t kMostGroups = 0xffffffffu / kAdamThreads;  // a launch counts its work-items in 32 bits
-  const auto kernel = [&](auto pb, auto gb, auto mx) {
-    constexpr bool kP = decltype(pb)::value, kG = decltype(gb)::value, kM = decltype(mx)::value;
-    return nt ? adamw_kernel<kP, kG, kM, true> : adamw_kernel<kP, kG, kM, false>;
-  };
-  constexpr std::integral_constant<bool, true> yes;
-  constexpr std::integral_constant<bool, false> no;
-  const auto of = [&](auto pb, auto gb) { return types.mx8 ? kernel(pb, gb, yes) : kernel(pb, gb, no); };
-  const auto run = types.param_bf16 ? (types.grad_bf16 ? of(yes, yes) : of(yes, no))
-                                    : (types.grad_bf16 ? of(no, yes) : of(no, no));
-  AdamwBatch b;
+  using Batch = AdamwBatch<kMx8>;
+  Batch b;
   b.count = 0;
   uint64_t groups = 0, place = 0;
   const auto flush = [&]() -> hipError_t {
     if (b.count == 0) return hipSuccess;
-    hipLaunchKernelGGL(run, dim3((uint32_t)groups), dim3(kAdamThreads), 0, stream, b, s, grad_scale, types.random);
+    hipLaunchKernelGGL((nt ? adamw_kernel<kParamBf16, kGradBf16, kMx8, true> : adamw_kernel<kParamBf16, kGradBf16, kMx8, false>),
+                       dim3((uint32_t)groups), dim3(kAdamThreads), 0, stream, b, s, grad_scale, random);
     b.count = 0;
     groups = 0;
     return hipGetLastError();
@@ -393,9 +401,9 @@ hipError_t launch_adamw(const AdamwTensor* tensors, uint32_t count, const AdamwT
     const AdamwTensor& t = tensors[i];
     if (t.n == 0) continue;
     const uint64_t need = (t.n + kAdamChunk - 1) / kAdamChunk;
-    if (b.count == kAdamTensors || groups + need > kMostGroups)
+    if (b.count == Batch::kMost || groups + need > kMostGroups)
       if (hipError_t e = flush()) return e;
-    b.t[b.count] = t;
+    b.t[b.count] = typename Batch::Tensor(t);
     b.first[b.count] = (uint32_t)groups;
     b.place[b.count] = place;
     ++b.count;
@@ -403,6 +411,24 @@ hipError_t launch_adamw(const AdamwTensor* tensors, uint32_t count, const AdamwT
     place += (t.n + 31) / 32 * 32;
   }
   return flush();
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwTensor* tensors, uint32_t count, const AdamwTypes& types, const AdamwScalars& s,
+                        const float* grad_scale, hipStream_t stream) {
+  const uint64_t each = (types.param_bf16 ? 4 : 8) + (types.grad_bf16 ? 2 : 4) + (types.mx8 ? 4 : 16);
+  uint64_t all = 0;
+  for (uint32_t i = 0; i < count; ++i) all += tensors[i].n;
+  const bool nt = past_cache(all * each);
+  const auto of = [&](auto pb, auto gb) {
+    constexpr bool kP = decltype(pb)::value, kG = decltype(gb)::value;
+    return types.mx8 ? run_adamw<kP, kG, true>(tensors, count, nt, s, grad_scale, types.random, stream)
+                     : run_adamw<kP, kG, false>(tensors, count, nt, s, grad_scale, types.random, stream);
+  };
+  constexpr std::integral_constant<bool, true> yes;
+  constexpr std::integral_constant<bool, false> no;
+  return types.param_bf16 ? (types.grad_bf16 ? of(yes, yes) : of(yes, no)) : (types.grad_bf16 ? of(no, yes) : of(no, no));
 }
 
 }  // namespace trace_host
