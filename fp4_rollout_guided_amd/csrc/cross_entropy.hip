@@ -395,6 +395,10 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_few_kernel(LogitsAr
   if (threadIdx.x < count) a.part[blockIdx.x * a.pitch + threadIdx.x] = all;
 }
 
+//
+// Bound by the tile loop (matrix units busy 52%): 5734 tokens of 131072 x 2048 in 2.74
+// ms, 1.13 PFLOP/s, of the library's products of this shape 1.27 to 1.51, which leave their
+// logits in memory; the backward pass's 65536 columns at a time in 1.37 ms, 1.13 PFLOP/s.
 template <class T, bool kBackward, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(LogitsArgs a) {
   __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
@@ -522,6 +526,7 @@ __global__ __launch_bounds__(256) void cross_entropy_join_kernel(CrossEntropyArg
 }
 
 // grad_x's sums over a slice of the vocabulary: i along k, j the packed tokens.
+// 5734 tokens, 2048, 65536 columns: 1.43 ms, 1.08 PFLOP/s, bound by the tile loop.
 struct GradRowsArgs {
   CrossEntropyArgs p;
   const CrossEntropyPlan* plan;
@@ -627,7 +632,8 @@ __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArg
   }
 }
 
-// grad_w's rows of a slice: i along k, j the vocabulary.
+// grad_w's rows of a slice: i along k, j the vocabulary.  5734 tokens, 2048, 65536
+// columns: 1.29 ms, 1.19 PFLOP/s, where a library product of these layouts does 1.01 to 1.13.
 struct GradWeightArgs {
   CrossEntropyArgs p;
   const CrossEntropyPlan* plan;
