@@ -18,8 +18,8 @@
 // Bound by memory: each element's bytes once in, once out, 16 bytes per lane of
 // an fp32 tensor.  A workgroup owns 4096 consecutive elements of one tensor and
 // loads all of them before the first arithmetic.  94 million elements with fp32 states
-// and bf16 gradients and copies: 0.45 ms, 6.1 TB/s.  With 8-bit states and bf16 parameters the
-// arithmetic counts (two records, random bits, exact root and quotient): 0.24 ms, 4.1 TB/s.
+// and bf16 gradients and copies: 0.45 ms, 5.8 TB/s.  With 8-bit states and bf16 parameters the
+// arithmetic counts (two records, random bits, exact root and quotient): 0.24 ms, 4.0 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -74,6 +74,24 @@ def test_several_slices(device, vocab):
     check(tr, *inputs(32768 + 40, vocab, 64, device, ignored=0.5), 1.0, vocab)
 
 
+# up to 64 tokens: more rows of w to a workgroup than a tile's, and shares that end inside one
+@pytest.mark.parametrize("tokens,vocab,k", [(5, 200003, 32), (32, 65536 + 197, 96), (33, 131072 + 77, 64), (50, 300007, 32),
+                                            (64, 65, 64), (64, 1024 * 64 + 1, 32)])
+def test_few_tokens_and_long_vocabularies(device, tokens, vocab, k):
+    import fp4_rollout_guided_amd as tr
+    _say("case few tokens", tokens, vocab, k)
+    check(tr, *inputs(tokens, vocab, k, device, ignored=0.2), 0.9, (tokens, vocab, k))
+
+
+# grad_x's parts go by the tokens that have targets: few of many, one, all, and a last slice shorter than the parts
+@pytest.mark.parametrize("tokens,vocab,k,ignored", [(2000, 9000, 256, 0.6), (700, 20000, 96, 0.97), (1000, 10007, 288, 0.0),
+                                                    (300, 5000, 64, 0.996), (66000, 8192 + 70, 32, 0.999)])
+def test_parts(device, tokens, vocab, k, ignored):
+    import fp4_rollout_guided_amd as tr
+    _say("case parts", tokens, vocab, k, ignored)
+    check(tr, *inputs(tokens, vocab, k, device, ignored=ignored), 1.0, (tokens, vocab, k))
+
+
 def test_long_rows(device):
     """k past the tiles, the largest hidden size of the workloads."""
     import fp4_rollout_guided_amd as tr

@@ -136,6 +136,29 @@ def test_nan_and_infinity(device):
     assert probs.isnan().all() and balance.isnan() and int(counts[-1]) == 40
 
 
+def test_pairs_that_the_forward_does_not_make(device):
+    """ids past the last expert are passed over, the same expert twice gets both gradients."""
+    import fp4_rollout_guided_amd as tr
+    _say("case odd pairs")
+    z = logits(30, 40, torch.float32, device)
+    ids, weights, counts, _, _ = tr.expert_route(z, 4)
+    gw = torch.randn(30, 4, device=device)
+    odd = ids.clone()
+    odd[:10, 1], odd[10:20, 2], odd[20:, 3] = 40, 2 ** 40 + 3, odd[20:, 1]
+    for renormalize in (True, False):
+        g = tr.expert_route_bwd(gw, None, z, odd, weights, counts, renormalize=renormalize)
+        w, d, p = weights.double(), gw.double(), torch.softmax(z.double(), 1)
+        s = (w * d).sum(1, keepdim=True)
+        add = w * (d - s) if renormalize else w * d
+        want = torch.zeros_like(p) if renormalize else -p * s
+        there = odd < 40
+        want.scatter_add_(1, torch.where(there, odd, 0), torch.where(there, add, 0.0))
+        # products and sums of a few fp32 terms of their sizes
+        size = p * (w * d.abs()).sum(1, keepdim=True)
+        size.scatter_add_(1, torch.where(there, odd, 0), w * (d.abs() + (w * d.abs()).sum(1, keepdim=True)))
+        assert ((g.double() - want).abs() <= 2.0 ** -18 * size + 2.0 ** -126).all()
+
+
 def test_no_rows(device):
     import fp4_rollout_guided_amd as tr
     _say("case no rows")
