@@ -537,14 +537,13 @@ struct GradRowsArgs {
   float* sums;    // [parts][pitch][k]
   uint64_t pitch;
 };
-template <class T, int kPerCu>
-__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(GradRowsArgs a) {
-  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+template <class T>
+__device__ __forceinline__ void grad_rows_tile(char* ring, const GradRowsArgs& a, uint32_t group) {
   const CrossEntropyArgs& p = a.p;
   const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_t = tiles_of(a.plan->count, T::kRowsJ);
   const uint32_t parts = a.plan->parts;
   const uint64_t tiles = (uint64_t)tiles_k * tiles_t * parts;
-  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  const uint64_t tile = xcd_tile(group, tiles);
   if (tile >= tiles) return;
   const uint32_t part = (uint32_t)(tile / ((uint64_t)tiles_k * tiles_t));
   const uint32_t in = (uint32_t)(tile - (uint64_t)part * tiles_k * tiles_t);
@@ -599,6 +598,11 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(Gr
       *at = v;
     }
 }
+template <class T, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_rows_kernel(GradRowsArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  grad_rows_tile<T>(ring, a, blockIdx.x);
+}
 
 // grad_x = the rows' factors times the parts' sums, to the tokens' own rows; zeros for ignored ones.
 __global__ __launch_bounds__(256) void cross_entropy_rows_kernel(CrossEntropyArgs p, const PackedRow* __restrict__ about,
@@ -642,15 +646,14 @@ struct GradWeightArgs {
   uint32_t v0, slice;
   uint16_t* grad_w;
 };
-template <class T, int kPerCu>
-__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(GradWeightArgs a) {
-  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+template <class T>
+__device__ __forceinline__ void grad_weight_tile(char* ring, GradWeightArgs a, uint32_t group) {
   static_assert(T::kJ % 2 == 0, "32 rows of the result at a time");
   const CrossEntropyArgs& p = a.p;
   const uint32_t left = p.vocab - a.v0 < a.slice ? p.vocab - a.v0 : a.slice;
   const uint32_t tiles_k = tiles_of(p.k, T::kRowsI), tiles_v = tiles_of(left, T::kRowsJ);
   const uint64_t tiles = (uint64_t)tiles_k * tiles_v;
-  const uint64_t tile = xcd_tile(blockIdx.x, tiles);
+  const uint64_t tile = xcd_tile(group, tiles);
   if (tile >= tiles) return;
   const uint32_t k0 = (uint32_t)(tile % tiles_k) * T::kRowsI, v0 = (uint32_t)(tile / tiles_k) * T::kRowsJ;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -694,6 +697,25 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(
         if (n < left && k < p.k) *reinterpret_cast<uint4*>(a.grad_w + ((uint64_t)a.v0 + n) * p.k + k) = v;
       });
   }
+}
+
+template <class T, int kPerCu>
+__global__ __launch_bounds__(256, kPerCu) void cross_entropy_grad_weight_kernel(GradWeightArgs a) {
+  __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
+  grad_weight_tile<T>(ring, a, blockIdx.x);
+}
+
+// Both, where tiles of 128 do for both: neither fills the card to its end, and the
+// one's tiles run beside the other's.  The first `rows` workgroups (the longer tiles
+// as a rule) do grad_x.
+template <class TRows, class TWeight>
+__global__ __launch_bounds__(256, 2) void cross_entropy_grads_kernel(GradRowsArgs a, GradWeightArgs b, uint32_t rows) {
+  static_assert(TRows::kLds == TWeight::kLds, "one ring for either");
+  __shared__ __attribute__((aligned(1024))) char ring[TRows::kLds];
+  if (blockIdx.x < rows)
+    grad_rows_tile<TRows>(ring, a, blockIdx.x);
+  else
+    grad_weight_tile<TWeight>(ring, b, blockIdx.x - rows);
 }
 
 // grad_w of no tokens.
@@ -905,25 +927,31 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     const auto grid = [&](uint64_t n, uint64_t m, uint64_t parts, bool small) {
       return dim3(xcd_grid(tiles_in(n, m, small ? 128 : 256) * parts));
     };
-    bool small = small_tiles(p.tokens, cols);
+    const bool small = small_tiles(p.tokens, cols);
     hipLaunchKernelGGL((small ? cross_entropy_logits_kernel<Logits128, true, 2>
                               : cross_entropy_logits_kernel<Logits256, true, 1>),
                        grid(p.tokens, cols, 1, small), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError()) return e;
+    const GradRowsArgs of_x{p, plan, probs, (uint32_t)v0, s.slice, v0 == 0, 1.f, sums, s.tall};
+    const GradWeightArgs of_w{p, plan, scaled, probs, (uint32_t)v0, s.slice, grad_w};
+    const bool small_x = s.parts.small, small_w = small_tiles(cols, p.k);
+    const dim3 grid_x = grid(p.tokens, p.k, s.parts.most, small_x), grid_w = grid(cols, p.k, 1, small_w);
+    if (grad_x && grad_w && small_x && small_w && (uint64_t)grid_x.x + grid_w.x <= kMostTiles) {
+      hipLaunchKernelGGL((cross_entropy_grads_kernel<GradRows128, GradWeight128>), dim3(grid_x.x + grid_w.x), dim3(256), 0,
+                         stream, of_x, of_w, grid_x.x);
+      if (hipError_t e = hipGetLastError()) return e;
+      continue;
+    }
     if (grad_x) {
-      const GradRowsArgs g{p, plan, probs, (uint32_t)v0, s.slice, v0 == 0, 1.f, sums, s.tall};
-      small = s.parts.small;
-      hipLaunchKernelGGL((small ? cross_entropy_grad_rows_kernel<GradRows128, 2>
-                                : cross_entropy_grad_rows_kernel<GradRows256, 1>),
-                         grid(p.tokens, p.k, s.parts.most, small), dim3(256), 0, stream, g);
+      hipLaunchKernelGGL((small_x ? cross_entropy_grad_rows_kernel<GradRows128, 2>
+                                  : cross_entropy_grad_rows_kernel<GradRows256, 1>),
+                         grid_x, dim3(256), 0, stream, of_x);
       if (hipError_t e = hipGetLastError()) return e;
     }
     if (grad_w) {
-      const GradWeightArgs g{p, plan, scaled, probs, (uint32_t)v0, s.slice, grad_w};
-      small = small_tiles(cols, p.k);
-      hipLaunchKernelGGL((small ? cross_entropy_grad_weight_kernel<GradWeight128, 2>
-                                : cross_entropy_grad_weight_kernel<GradWeight256, 1>),
-                         grid(cols, p.k, 1, small), dim3(256), 0, stream, g);
+      hipLaunchKernelGGL((small_w ? cross_entropy_grad_weight_kernel<GradWeight128, 2>
+                                  : cross_entropy_grad_weight_kernel<GradWeight256, 1>),
+                         grid_w, dim3(256), 0, stream, of_w);
       if (hipError_t e = hipGetLastError()) return e;
     }
   }
