@@ -155,6 +155,7 @@ template <int kI_, int kJ_, int kWI_, int kWJ_, bool kAcrossI, bool kAcrossJ, in
 struct Tile {
   static constexpr int kI = kI_, kJ = kJ_, kWI = kWI_, kWJ = kWJ_;
   static constexpr uint32_t kRing = kRing_;  // stages in LDS
+  static constexpr bool kStreams = kStreamI;
   static constexpr bool kPairs = !kAcrossI && kI % 2 == 0;
 
   // The wave's row i of element e of block b, in lane group g (lane / 16).
@@ -188,7 +189,8 @@ struct Tile {
 
   // Sums of `stages` stages.  From stage `whole` on (the last one, or none) lanes
   // would pass an operand's end: before its copies shorten(from_i, from_j) moves
-  // their places.  half: of the last stage only the first k-step counts.  Leaves
+  // their places.  half: of the last stage only the first k-step counts.  first
+  // (with kStreamI): the stage to begin with, then on to `whole` and round.  Leaves
   // every wave past its last read of the ring that matters.
   //
   // A stage is two k-steps; under the arithmetic of each the next one's operands
@@ -202,7 +204,7 @@ struct Tile {
   template <class Shorten>
   static __device__ __forceinline__ void multiply(char* ring, uint32_t stages, uint32_t whole, bool half,
                                                   Source<I>& from_i, Source<J>& from_j, Shorten shorten,
-                                                  v4f (&acc)[kI][kJ]) {
+                                                  v4f (&acc)[kI][kJ], uint32_t first = 0) {
     constexpr uint32_t kProducts = kI * kJ, kFragments = kI + kJ;
     constexpr uint32_t kHalf = (kProducts + 1) / 2, kReadsEach = (kFragments + kHalf - 1) / kHalf;
     // the product after which a slot is free, products to a copy and copies to a product after that
@@ -220,8 +222,25 @@ struct Tile {
     for (uint32_t n = 0; n < I::kCopies; ++n) from_i.off[n] += 4096 - 1024 * (n % 4);
 #pragma unroll
     for (uint32_t n = 0; n < J::kCopies; ++n) from_j.off[n] += 4096 - 1024 * (n % 4);
-    const char* next_i = from_i.base - 4096;
-    const char* next_j = from_j.base - 4096;
+    const char* next_i = from_i.base - 4096 + (kStreamI ? first * from_i.step : 0);
+    const char* next_j = from_j.base - 4096 + (kStreamI ? first * from_j.step : 0);
+    uint32_t place = first;
+    const auto advance = [&]() {
+      next_i += from_i.step;
+      next_j += from_j.step;
+      if (kStreamI && ++place == whole) {
+        next_i -= whole * from_i.step;
+        next_j -= whole * from_j.step;
+        place = 0;
+      }
+    };
+    const auto to_last = [&]() {
+      shorten(from_i, from_j);
+      if (kStreamI) {
+        next_i = from_i.base - 4096 + whole * from_i.step;
+        next_j = from_j.base - 4096 + whole * from_j.step;
+      }
+    };
     uint64_t lanes = ~0ull;
     const auto copy = [&](auto n, uint32_t slot) {
       constexpr uint32_t kN = decltype(n)::value;
@@ -262,10 +281,9 @@ struct Tile {
 #pragma unroll
     for (uint32_t s = 0; s < kRing; ++s) {
       if (s >= stages) continue;
-      if (s == whole) shorten(from_i, from_j);
+      if (s == whole) to_last();
       unrolled<0, kCopies>([&](auto n) { copy(n, s); });
-      next_i += from_i.step;
-      next_j += from_j.step;
+      advance();
     }
     stage_barrier<0>();
     unrolled<0, kFragments>([&](auto f) { read(f, 0, 0); });
@@ -276,7 +294,7 @@ struct Tile {
         if (st + kRing >= stages)
           lanes = 0;
         else
-          shorten(from_i, from_j);
+          to_last();
       }
       products(0, [&](auto m) {
         constexpr uint32_t kM = decltype(m)::value;
@@ -291,8 +309,7 @@ struct Tile {
       else
         stage_barrier<0>();
       __builtin_amdgcn_sched_barrier(0);
-      next_i += from_i.step;
-      next_j += from_j.step;
+      advance();
       slot = slot + 1 == kRing ? 0 : slot + 1;
       if (half && st + 1 == stages) {
 #pragma unroll

@@ -366,6 +366,11 @@ struct LogitsArgs {
 // fill their tile).  Rows from v_end on, and past the tokens, are the tile's first
 // again: their results are left out.  k is a multiple of 32: of a last half stage only the
 // first k-step counts, and the lanes past its end read its own columns again.
+//
+// Rows at multiples of 4 KiB lie alike over the memory's channels, and workgroups in
+// step with each other would all ask the same ones: of few tokens each begins at a place of its
+// own in k (4 x 32000 x 8192: 118 -> 87 us, 1 x 32768 x 2048: 36 -> 30; with rows of
+// other lengths it costs up to 3%).
 template <class T>
 __device__ __forceinline__ void logits_tile(char* ring, const CrossEntropyArgs& p, uint32_t v0, uint32_t v_end,
                                             const uint16_t* x, uint32_t tokens, v4f (&acc)[T::kI][T::kJ]) {
@@ -403,7 +408,7 @@ __device__ __forceinline__ void logits_tile(char* ring, const CrossEntropyArgs& 
           j.off[n] -= col < kStageC / 2 ? 0 : kStageC;
         }
       },
-      acc);
+      acc, T::kStreams && p.k % 2048 == 0 ? blockIdx.x * 5 % (p.k / kStageC) : 0);
 }
 
 // The maximum and sum of a tile's column for each token, one per wave and token to
@@ -455,7 +460,7 @@ __device__ __forceinline__ void column_sums(v4f (&acc)[T::kI][T::kJ], float scal
 // rows at a time, and leaves one sum.  The tokens' rows come from the caches once for
 // each tile, so that 64 tokens go with 128 rows (61 x 100003 x 7168: 244 us, 5.9 TB/s;
 // with 64 rows 284).  32 tokens go with 64, four workgroups to a compute unit, which
-// cover each other's ends (16 x 131072 x 2048: 97 us; two deeper ones 108).
+// cover each other's ends (16 x 131072 x 2048: 93 us; two deeper ones took 108 where four took 97).
 template <class T, int kPerCu>
 __global__ __launch_bounds__(256, kPerCu) void cross_entropy_few_kernel(LogitsArgs a) {
   __shared__ __attribute__((aligned(1024))) char ring[T::kLds];
