@@ -997,8 +997,8 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
     return hipGetLastError();
   }
   const BackwardSpace s(p.tokens, p.vocab, p.k);
-  if (tiles_in(p.tokens, s.slice, 256) > kMostTiles || tiles_in(p.tokens, p.k, s.parts.small ? 128 : 256) * s.parts.most > kMostTiles ||
-      tiles_in(s.slice, p.k, 256) > kMostTiles)
+  if (tiles_in(p.tokens, s.slice, 256) > kMostTiles || tiles_in(s.slice, p.k, 256) > kMostTiles ||
+      tiles_in(p.tokens, p.k, s.parts.small ? 128 : 256) * s.parts.most > kMostTiles)
     return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
   CrossEntropyPlan* const plan = reinterpret_cast<CrossEntropyPlan*>(at);
@@ -1065,7 +1065,8 @@ hipError_t launch_cross_entropy_bwd(const CrossEntropyArgs& p, const float* grad
   }
   if (grad_x) {
     hipLaunchKernelGGL(cross_entropy_rows_kernel, vector_grid(p.tokens * (p.k / 8)), dim3(256), 0, stream, p,
-                       (const PackedRow*)about, (const int32_t*)places, (const float*)sums, (const CrossEntropyPlan*)plan, s.tall, grad_x);
+                       (const PackedRow*)about, (const int32_t*)places, (const float*)sums,
+                       (const CrossEntropyPlan*)plan, s.tall, grad_x);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
