@@ -313,6 +313,33 @@ def test_graph_replays_and_streams(device):
     del graph
 
 
+@pytest.mark.parametrize("tokens,vocab,k", [(20, 70000, 96), (700, 5000, 64), (1500, 3001, 64)])
+def test_replays_with_other_targets(device, tokens, vocab, k):
+    """What a captured pass lists, packs and splits is the replay's own: as many targets as it finds."""
+    import fp4_rollout_guided_amd as tr
+    _say("case replays with other targets", tokens)
+    x, w, t, g = inputs(tokens, vocab, k, device)
+
+    def run():
+        loss, lse = tr.linear_cross_entropy(x, w, t)
+        return loss, lse, *tr.linear_cross_entropy_bwd(g, x, w, t, lse)
+    stream = torch.cuda.Stream(device=device)
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    first = t.clone()
+    for keep in (tokens, 1, tokens // 2, 0, tokens):
+        t.copy_(torch.where(torch.arange(tokens, device=device) < keep, first.clamp(0, vocab - 1), -1))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in out]
+        assert all(torch.equal(a, b) for a, b in zip(run(), got)), keep
+    del graph
+
+
 def test_binding_refusals(device):
     import fp4_rollout_guided_amd as tr
     _say("case refusals")
