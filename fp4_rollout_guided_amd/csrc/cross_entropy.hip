@@ -412,8 +412,9 @@ __device__ __forceinline__ void logits_tile(char* ring, const CrossEntropyArgs& 
 }
 
 // The maximum and sum of a tile's column for each token, one per wave and token to
-// sums[wave's rows][token]; the targets' logits to hit.  target_of(t), t from t0 on:
-// the token's target below v_end, or -1.  Rows from v_end on are left out.
+// sums[wave's rows][token]; the targets' logits to hit, in powers of two as the
+// maxima are.  target_of(t), t from t0 on: the token's target below v_end, or -1.
+// Rows from v_end on are left out.
 template <class T, class TargetOf>
 __device__ __forceinline__ void column_sums(v4f (&acc)[T::kI][T::kJ], float scale, uint32_t v0, uint32_t v_end, uint32_t t0,
                                             TargetOf target_of, float* hit, TopSum* sums) {
@@ -434,8 +435,8 @@ __device__ __forceinline__ void column_sums(v4f (&acc)[T::kI][T::kJ], float scal
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t row = T::row_of(i, g, e);
-        if (hits && target == (int32_t)row) hit[t] = acc[i][j][e] * scale;
         float z = acc[i][j][e] * to_log2;
+        if (hits && target == (int32_t)row) hit[t] = z;
         if (ends && v0 + wi + row >= v_end) z = -__builtin_inff();
         acc[i][j][e] = z;
         top = fmaxf(top, z);
@@ -615,9 +616,11 @@ __global__ __launch_bounds__(256) void cross_entropy_join_kernel(CrossEntropyArg
   }
   if (share == 0 && t < p.tokens) {
     const TopSum all = sums[j];
-    const float l = has ? all.top * kLn2 + logf(all.sum) : 0.f;
-    lse[t] = l;
-    loss[t] = has ? l - hit[place] : 0.f;
+    // the target's logit is one of those that the maximum was taken from and the sum is one at least: no loss is
+    // below zero, and a confident token's keeps nothing of its logit's roundings
+    const float log_sum = has ? logf(all.sum) : 0.f;
+    lse[t] = has ? all.top * kLn2 + log_sum : 0.f;
+    loss[t] = has ? (all.top - hit[place]) * kLn2 + log_sum : 0.f;
   }
 }
 

@@ -1,0 +1,42 @@
+"""The loss over the vocabulary where roundings and fillers could show: very
+confident tokens, vocabulary rows of -infinity, and the tiles of the largest calls."""
+import sys
+
+import pytest
+import torch
+
+from tests import step_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+def _say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.mark.parametrize("tokens,vocab,scale", [(40, 500, 1.0), (64, 9000, 0.7), (300, 500, 1.25), (1500, 3001, 1.0)])
+def test_confident_tokens_lose_nothing(device, tokens, vocab, scale):
+    """No log-probability is above zero.  Where the target's logit is the largest, the loss is the logarithm of one and
+    the other exponentials' sum: each of them off by the two logits' errors (step_util.loss_tolerance), the sum by 2^-24
+    for each addition, and nothing of the logit's own size."""
+    import fp4_rollout_guided_amd as tr
+    _say("case confident tokens", tokens, vocab, scale)
+    g = torch.Generator(device=device)
+    g.manual_seed(tokens)
+    k = 128
+    w = (torch.randn(vocab, k, generator=g, device=device) / k ** 0.5).to(torch.bfloat16)
+    targets = torch.randint(0, vocab, (tokens,), generator=g, device=device)
+    lean = 1 + 79 * torch.rand(tokens, 1, generator=g, device=device) / scale
+    x = (lean * w[targets].float()).to(torch.bfloat16)
+    loss, lse = tr.linear_cross_entropy(x, w, targets, scale)
+    want, want_lse, has = U.loss(x, w, targets, scale)
+    z = U.logits(x, w, scale)
+    tol = U.loss_tolerance(x, w, has, scale, want_lse)
+    assert ((lse.double() - want_lse).abs() <= tol).all()
+    assert (loss >= 0).all(), float(loss.min())
+    largest = z.gather(1, targets.unsqueeze(1)).squeeze(1) >= z.amax(1)
+    assert int(largest.sum()) > tokens // 2
+    size = (x.double().abs() @ w.double().abs().t().contiguous()).amax(1) * scale
+    each = torch.expm1(2 * size * ((k + 3) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -21)
+    near = want * each + (100 + vocab / 64) * 2.0 ** -24 + want * 2.0 ** -22
+    assert ((loss.double() - want).abs() <= near)[largest].all()
