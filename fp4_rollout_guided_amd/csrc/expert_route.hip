@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p
 //   renormalised: dz[ids[j]] += weights[j] (grad_weights[j] - s)   (the softmax of the chosen logits alone)
 //   otherwise:    dz[e] -= p[e] s,  dz[ids[j]] += weights[j] grad_weights[j]
 //   balance:      dz[e] += p[e] (c[e] - sum of p c),  c[e] = grad_balance experts counts[e] / (sum of counts * N).
-// Rows without an expert (ids[t, 0] < 0) get zeros.
+// Rows whose ids are all negative get zeros.
 // What the chosen experts add goes to their lanes by way of LDS, which is zero but
 // there (each lane looking through its experts for each of them was a third of the
 // arithmetic).  65573 rows of 256 in bf16, six to a row: 20 us, 3.7 TB/s, bound by
@@ -444,19 +444,21 @@ __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, cons
     float w[kKept], g[kKept];
     float z[kPer], dz[kPer], top;
     load_logits<kBf16, kLanes, kPer, kVec>(p.logits, from, p.experts, l, z);
-    const bool wanted = ids[from * p.topk] >= 0;
-    if (grad_weights) {
+    uint32_t some = 0;
 #pragma unroll
-      for (uint32_t i = 0; i < kKept; ++i) {
-        const uint32_t j = l + kLanes * i;
-        id[i] = -1, w[i] = 0.f, g[i] = 0.f;
-        if (j < p.topk) {
-          id[i] = ids[from * p.topk + j];
+    for (uint32_t i = 0; i < kKept; ++i) {
+      const uint32_t j = l + kLanes * i;
+      id[i] = -1, w[i] = 0.f, g[i] = 0.f;
+      if (j < p.topk) {
+        id[i] = ids[from * p.topk + j];
+        if (grad_weights) {
           w[i] = weights[from * p.topk + j];
           g[i] = grad_weights[from * p.topk + j];
         }
       }
+      some |= (uint32_t)(id[i] >= 0);
     }
+    const bool wanted = row_max<kLanes>(some) != 0;  // whichever of its pairs stands
     const float each = 1.f / row_softmax<kLanes, kPer>(z, top);
     float dot = 0.f;
 #pragma unroll
