@@ -1505,6 +1505,8 @@ class _Step:
             if param == torch.bfloat16:
                 raise ValueError("copies are for fp32 parameters")
             self.put(copies, 6, "copies", _BF16_ONLY)
+        else:  # an earlier step may have had some
+            self.words[6::_TENSOR_WORDS] = array("q", bytes(8 * self.count))
         if grad_scale is not None:
             _fit(grad_scale, "grad_scale", params[0], _F32, 1)
         if self.mx8 and seed is None:
