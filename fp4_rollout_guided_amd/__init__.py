@@ -1482,6 +1482,7 @@ class _Step:
         self.words = array("q", bytes(8 * _TENSOR_WORDS * self.count))
         _tensor_lists.check(params, -1, "params", _F32_OR_BF16, self.device, self.numels, None, 0, 0)
         self.words[7::_TENSOR_WORDS] = self.numels
+        self.blocks = None
 
     def put(self, ts, column, name, dtypes, part=-1, numels=None):
         return _tensor_lists.check(ts, part, name, dtypes, self.device, self.numels if numels is None else numels,
@@ -1493,10 +1494,11 @@ class _Step:
             self.put(avgs, 2, "exp_avgs", _F32)
             self.put(sqs, 3, "exp_avg_sqs", _F32)
             return
-        blocks = array("q", [(n + 31) // 32 for n in self.numels])
+        if self.blocks is None:
+            self.blocks = array("q", [(n + 31) // 32 for n in self.numels])
         for ts, name, column in ((avgs, "exp_avgs", 2), (sqs, "exp_avg_sqs", 3)):
             self.put(ts, column, name + " codes", _U8, 1)
-            self.put(ts, column + 2, name + " scales", _U8, 0, blocks)
+            self.put(ts, column + 2, name + " scales", _U8, 0, self.blocks)
 
     def run(self, params, grads, copies, step, lr, betas, eps, weight_decay, grad_scale, seed):
         param = self.put(params, 0, "params", _F32_OR_BF16)
@@ -1573,7 +1575,6 @@ class AdamW:
                     torch.zeros(n, dtype=torch.uint8, device=p.device))
 
         self._avgs, self._sqs = [zeros(p) for p in self.params], [zeros(p) for p in self.params]
-        self._words.put_states(self._avgs, self._sqs)
 
     def step(self, grads=None, grad_scale=None):
         """One step with these gradients, or the parameters' own .grad."""
@@ -1584,6 +1585,7 @@ class AdamW:
                 raise ValueError("a parameter has no gradient")
         t = self.steps + 1
         seed = None if self.seed is None else (self.seed + t) % (1 << 64)
+        self._words.put_states(self._avgs, self._sqs)  # where they lie now: their storage is the user's to move
         self._words.run(params, _list(grads), self.copies, t, self.lr, self.betas, self.eps, self.weight_decay,
                         grad_scale, seed)
         self.steps = t

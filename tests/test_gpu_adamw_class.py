@@ -29,3 +29,34 @@ def test_copies_given_up(device):
     opt.copies = copies
     opt.step(grads)
     assert all(torch.equal(c, p.to(torch.bfloat16)) for c, p in zip(copies, params))
+
+
+@pytest.mark.parametrize("states", ["fp32", "mx8"])
+def test_states_that_moved(device, states):
+    """A step works on the states where they lie now, not where they lay when they were made."""
+    import fp4_rollout_guided_amd as tr
+    _say("case moved states", states)
+    make = lambda: [torch.nn.Parameter(torch.linspace(-1, 1, n, device=device)) for n in (70, 4100)]  # noqa: E731
+    grads = [torch.randn(n, device=device) for n in (70, 4100)]
+    a, b = make(), make()
+    one, two = (tr.AdamW(p, lr=0.1, states=states, seed=3) for p in (a, b))
+    one.step(grads), two.step(grads)
+    flat = lambda o: [t for k in ("exp_avgs", "exp_avg_sqs") for s in o.state_dict()[k]  # noqa: E731
+                      for t in (s if isinstance(s, tuple) else (s,))]
+    former = [t.data for t in flat(two)]
+    held = [t.clone() for t in former]
+    for t in flat(two):
+        t.data = t.data.clone()
+    one.step(grads), two.step(grads)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert all(torch.equal(x, y) for x, y in zip(flat(one), flat(two)))
+    assert all(torch.equal(x, y) for x, y in zip(former, held))
+    for t in flat(two):
+        t.data = t.data.cpu()
+    with pytest.raises(ValueError):
+        two.step(grads)
+    assert two.steps == 2
+    for t in flat(two):
+        t.data = t.data.to(device)
+    one.step(grads), two.step(grads)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
