@@ -1482,13 +1482,14 @@ class _Step:
         self.words = array("q", bytes(8 * _TENSOR_WORDS * self.count))
         _tensor_lists.check(params, -1, "params", _F32_OR_BF16, self.device, self.numels, None, 0, 0)
         self.words[7::_TENSOR_WORDS] = self.numels
-        self.blocks = None
+        self.blocks, self.copied = None, False
 
     def put(self, ts, column, name, dtypes, part=-1, numels=None):
         return _tensor_lists.check(ts, part, name, dtypes, self.device, self.numels if numels is None else numels,
                                    self.words, _TENSOR_WORDS, column)
 
     def put_states(self, avgs, sqs):
+        self.states = avgs, sqs
         self.mx8 = len(avgs) > 0 and isinstance(avgs[0], (tuple, list))
         if not self.mx8:
             self.put(avgs, 2, "exp_avgs", _F32)
@@ -1507,8 +1508,9 @@ class _Step:
             if param == torch.bfloat16:
                 raise ValueError("copies are for fp32 parameters")
             self.put(copies, 6, "copies", _BF16_ONLY)
-        else:  # an earlier step may have had some
+        elif self.copied:  # the addresses of an earlier step's
             self.words[6::_TENSOR_WORDS] = array("q", bytes(8 * self.count))
+        self.copied = copies is not None
         if grad_scale is not None:
             _fit(grad_scale, "grad_scale", params[0], _F32, 1)
         if self.mx8 and seed is None:
@@ -1519,7 +1521,8 @@ class _Step:
                                 grad == torch.bfloat16, self.mx8, seed is not None)
         _launch("trace_adamw_step", params[0], self.words.buffer_info()[0], self.count, ctypes.addressof(options),
                 _addr(grad_scale))
-        _tensor_lists.changed(params)
+        for written in (params, copies or (), *self.states):
+            _tensor_lists.changed(written)
 
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,

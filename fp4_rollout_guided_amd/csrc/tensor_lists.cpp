@@ -108,7 +108,14 @@ PyObject* check(PyObject*, PyObject* args) {
   END_HANDLE_TH_ERRORS
 }
 
-// changed(tensors): autograd is told that they have been written to.
+void count_write(PyObject* item) {
+  if (!THPVariable_Check(item)) return;
+  const at::Tensor& t = THPVariable_Unpack(item);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// changed(tensors): autograd is told that they, or the tensors of tuples among them,
+// have been written to.
 PyObject* changed(PyObject*, PyObject* list) {
   HANDLE_TH_ERRORS
   if (!PyList_Check(list) && !PyTuple_Check(list)) {
@@ -117,9 +124,11 @@ PyObject* changed(PyObject*, PyObject* list) {
   }
   for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(list); ++i) {
     PyObject* item = PySequence_Fast_GET_ITEM(list, i);
-    if (!THPVariable_Check(item)) continue;
-    const at::Tensor& t = THPVariable_Unpack(item);
-    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    if (PyTuple_Check(item)) {
+      for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(item); ++k) count_write(PyTuple_GET_ITEM(item, k));
+    } else {
+      count_write(item);
+    }
   }
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
@@ -196,7 +205,7 @@ PyObject* fits(PyObject*, PyObject* const* args, Py_ssize_t count) {
 }
 
 PyMethodDef methods[] = {{"check", check, METH_VARARGS, "Checks a list of tensors and writes its addresses down."},
-                         {"changed", changed, METH_O, "Counts a write to each of the tensors."},
+                         {"changed", changed, METH_O, "Counts a write to each of the tensors, also those in tuples."},
                          {"empties", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empties)), METH_FASTCALL,
                           "Several empty tensors."},
                          {"fits", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fits)), METH_FASTCALL,

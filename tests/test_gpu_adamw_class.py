@@ -60,3 +60,24 @@ def test_states_that_moved(device, states):
         t.data = t.data.to(device)
     one.step(grads), two.step(grads)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("states", ["fp32", "mx8"])
+def test_backward_sees_all_that_the_step_writes(device, states):
+    """A graph that saved a copy refuses its backward pass; states count their writes as well."""
+    import fp4_rollout_guided_amd as tr
+    _say("case versions of copies", states)
+    w = torch.randn(64, 64, device=device)
+    c = w.to(torch.bfloat16)
+    if states == "fp32":
+        m, v = torch.zeros_like(w), torch.zeros_like(w)
+        written = [m, v]
+    else:
+        m, v = ((torch.zeros(128, dtype=torch.uint8, device=device), torch.zeros(4096, dtype=torch.uint8, device=device)) for _ in range(2))
+        written = [*m, *v]
+    y = (torch.randn(64, 64, device=device).to(torch.bfloat16).requires_grad_(True) @ c).sum()
+    before = [t._version for t in written]
+    tr.adamw_step([w], [torch.ones_like(w)], [m], [v], 1, 1e-3, copies=[c], seed=1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    assert all(t._version > b for t, b in zip(written, before))
