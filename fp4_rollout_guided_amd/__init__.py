@@ -1554,12 +1554,14 @@ class AdamW:
     MXFP8 records (states="mx8").  The random bits of step t are those of seed
     + t; seed None: fp32 states, bf16 parameters rounded to nearest.  lr, betas,
     eps and weight_decay are plain attributes, read at each step.  copies: as for
-    ``adamw_step``."""
+    ``adamw_step``; a forward pass through them leaves the gradients with them,
+    and the step takes a copy's .grad where its parameter has none."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, states="fp32", copies=None,
                  seed=None):
         self.params = list(params)
-        self.lr, self.betas, self.eps, self.weight_decay, self.copies = lr, betas, eps, weight_decay, copies
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.copies = None if copies is None else list(copies)
         self.steps, self.seed = 0, seed
         if states not in ("fp32", "mx8"):
             raise ValueError(f'states must be "fp32" or "mx8", got {states!r}')
@@ -1580,10 +1582,13 @@ class AdamW:
         self._avgs, self._sqs = [zeros(p) for p in self.params], [zeros(p) for p in self.params]
 
     def step(self, grads=None, grad_scale=None):
-        """One step with these gradients, or the parameters' own .grad."""
+        """One step with these gradients, or the .grad of each parameter or else of
+        its copy."""
         params = self.params
         if grads is None:
             grads = [p.grad for p in params]
+            if self.copies is not None:
+                grads = [c.grad if g is None else g for g, c in zip(grads, self.copies)]
             if any(g is None for g in grads):
                 raise ValueError("a parameter has no gradient")
         t = self.steps + 1
@@ -1594,7 +1599,7 @@ class AdamW:
         self.steps = t
 
     def zero_grad(self):
-        for p in self.params:
+        for p in (*self.params, *(self.copies or ())):
             p.grad = None
 
     def state_dict(self):

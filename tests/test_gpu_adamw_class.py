@@ -81,3 +81,34 @@ def test_backward_sees_all_that_the_step_writes(device, states):
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
     assert all(t._version > b for t, b in zip(written, before))
+
+
+def test_gradients_of_copies(device):
+    """The forward's weights are the copies: their gradients are the step's, and zero_grad clears them."""
+    import fp4_rollout_guided_amd as tr
+    _say("case gradients of copies")
+    masters = [torch.nn.Parameter(torch.randn(s, device=device)) for s in ((48, 32), (48,))]
+    other = [p.detach().clone() for p in masters]
+    copies = [p.detach().to(torch.bfloat16).requires_grad_(True) for p in masters]
+    opt = tr.AdamW(masters, lr=0.1, copies=(c for c in copies))
+    m, v = ([torch.zeros_like(p) for p in other] for _ in range(2))
+    x = torch.randn(7, 32, device=device).to(torch.bfloat16)
+    for t in (1, 2):
+        opt.zero_grad()
+        assert all(c.grad is None for c in copies)
+        (x @ copies[0].t() + copies[1]).float().square().sum().backward()
+        grads = [c.grad.clone() for c in copies]
+        opt.step()
+        tr.adamw_step(other, grads, m, v, t, 0.1)
+        assert all(torch.equal(a, b) for a, b in zip(masters, other))
+        assert all(torch.equal(c, p.to(torch.bfloat16)) for c, p in zip(copies, other))
+    # a parameter's own gradient comes first
+    for p in masters:
+        p.grad = torch.ones_like(p)
+    opt.step()
+    tr.adamw_step(other, [torch.ones_like(p) for p in other], m, v, 3, 0.1)
+    assert all(torch.equal(a, b) for a, b in zip(masters, other))
+    opt.zero_grad()
+    assert all(t.grad is None for t in (*masters, *copies))
+    with pytest.raises(ValueError):
+        opt.step()
