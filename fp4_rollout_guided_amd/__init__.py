@@ -1607,14 +1607,20 @@ class AdamW:
         return {"steps": self.steps, "seed": self.seed, "exp_avgs": list(self._avgs), "exp_avg_sqs": list(self._sqs)}
 
     def load_state_dict(self, state):
-        """Copies states of the same kind and sizes into these."""
-        avgs, sqs = state["exp_avgs"], state["exp_avg_sqs"]
-        theirs = _Step(self.params)
-        theirs.put_states(avgs, sqs)  # the checks
-        if theirs.mx8 != self._mx8:
-            raise TypeError("the states are of the other kind")
-        for mine, theirs in ((self._avgs, avgs), (self._sqs, sqs)):
-            for to, of in zip(mine, theirs):
+        """Copies states of the same kind and sizes, on any device, into these."""
+        pairs = []
+        for name, mine in (("exp_avgs", self._avgs), ("exp_avg_sqs", self._sqs)):
+            if len(state[name]) != len(mine):
+                raise ValueError(f"{name} must be one for each parameter")
+            for i, (to, of) in enumerate(zip(mine, state[name])):
+                if isinstance(of, (tuple, list)) != self._mx8 or (self._mx8 and len(of) != 2):
+                    raise TypeError("the states are of the other kind")
                 for a, b in zip(to, of) if self._mx8 else ((to, of),):
-                    a.copy_(b.view(a.shape))
+                    if not isinstance(b, torch.Tensor) or b.dtype != a.dtype:
+                        raise TypeError(f"{name}[{i}] must be of {a.dtype}")
+                    if b.numel() != a.numel():
+                        raise ValueError(f"{name}[{i}] must hold {a.numel()} elements, got {b.numel()}")
+                    pairs.append((a, b))
+        for a, b in pairs:  # nothing is changed before all are known to fit
+            a.copy_(b.reshape(a.shape))
         self.steps, self.seed = state["steps"], state["seed"]

@@ -1,4 +1,6 @@
 """AdamW's class: copies of the weights, their gradients, states that move, and checkpoints."""
+import copy
+import io
 import sys
 
 import pytest
@@ -112,3 +114,39 @@ def test_gradients_of_copies(device):
     assert all(t.grad is None for t in (*masters, *copies))
     with pytest.raises(ValueError):
         opt.step()
+
+
+@pytest.mark.parametrize("states", ["fp32", "mx8"])
+def test_checkpoint_on_the_host(device, states):
+    """States saved, read back to the host, and loaded."""
+    import fp4_rollout_guided_amd as tr
+    _say("case checkpoint", states)
+    make = lambda: [torch.nn.Parameter(torch.linspace(-1, 1, n, device=device).view(-1, 10)) for n in (70, 4100)]  # noqa: E731
+    a, b = make(), make()
+    grads = [torch.randn_like(p) for p in a]
+    one, two = tr.AdamW(a, lr=0.1, states=states, seed=3), tr.AdamW(b, lr=0.1, states=states, seed=8)
+    one.step(grads)
+    file = io.BytesIO()
+    torch.save(one.state_dict(), file)
+    file.seek(0)
+    saved = torch.load(file, map_location="cpu", weights_only=True)
+    for p, q in zip(b, a):
+        p.data.copy_(q.data)
+    lists = copy.deepcopy(saved)
+    if states == "mx8":  # as other containers give them back
+        lists["exp_avgs"] = [list(s) for s in lists["exp_avgs"]]
+    for state in (saved, lists):
+        two.load_state_dict(state)
+        assert two.steps == 1 and two.seed == 3
+        for x, y in zip(one.state_dict()["exp_avgs"] + one.state_dict()["exp_avg_sqs"],
+                        two.state_dict()["exp_avgs"] + two.state_dict()["exp_avg_sqs"]):
+            for s, t in zip(x, y) if states == "mx8" else ((x, y),):
+                assert t.is_cuda and torch.equal(s, t)
+    one.step(grads), two.step(grads)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    short = dict(saved, exp_avgs=saved["exp_avgs"][:1])
+    with pytest.raises((TypeError, ValueError)):
+        two.load_state_dict(short)
+    with pytest.raises((TypeError, ValueError)):
+        two.load_state_dict(dict(saved, exp_avg_sqs=saved["exp_avg_sqs"][::-1]))
+    assert two.steps == 2
