@@ -71,7 +71,11 @@ LISTS_LIB = os.path.join(PKG, "_tensor_lists.so")
 
 
 def _lists_command(out):
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """None without torch: only the binding needs the module, and torch itself."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     include, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
             "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
@@ -99,10 +103,14 @@ def _c_smoke_command(out):
 
 def build(verbose: bool = False) -> str:
     """Compile every source into fp4_rollout_guided_amd/libtrace.so (and the
-    small-grid test build beside it), always rebuilding, and return the
-    library's path."""
-    jobs = [(LIB, _command(LIB + ".tmp")), (SMALLGRID_LIB, _command(SMALLGRID_LIB + ".tmp", SMALLGRID_DEFINES)),
-            (LISTS_LIB, _lists_command(LISTS_LIB + ".tmp"))]
+    small-grid test build and the binding's module beside it), always
+    rebuilding, and return the library's path."""
+    jobs = [(LIB, _command(LIB + ".tmp")), (SMALLGRID_LIB, _command(SMALLGRID_LIB + ".tmp", SMALLGRID_DEFINES))]
+    lists = _lists_command(LISTS_LIB + ".tmp")
+    if lists is not None:
+        jobs.append((LISTS_LIB, lists))
+    else:
+        sys.stderr.write(f"torch is not installed: {os.path.basename(LISTS_LIB)} is not built\n")
     if os.path.exists(CEILING_SRC):
         os.makedirs(os.path.dirname(CEILING_BIN), exist_ok=True)
         jobs.append((CEILING_BIN, [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17",

@@ -1,0 +1,43 @@
+"""The build where torch is not installed, on the CPU: the C library needs none of it."""
+import importlib.util
+import os
+import sys
+
+import pytest
+
+from tests.conftest import ROOT
+
+
+def _script():
+    """The build script by path, as a module of its own."""
+    spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(ROOT, "fp4_rollout_guided_amd", "build.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("torch_there", [True, False])
+def test_build_without_torch(monkeypatch, tmp_path, torch_there):
+    build = _script()
+    started, put = [], []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+        def __init__(self, cmd, **_):
+            started.append(cmd)
+
+        def communicate(self):
+            return "", ""
+    monkeypatch.setattr(build.subprocess, "Popen", Done)
+    monkeypatch.setattr(build.subprocess, "run", Done)
+    monkeypatch.setattr(build.os, "replace", lambda a, b: put.append(b))
+    monkeypatch.setattr(build, "CEILING_BIN", str(tmp_path / "ceiling" / "bin"))
+    if not torch_there:
+        monkeypatch.setitem(sys.modules, "torch", None)
+        find = importlib.util.find_spec
+        monkeypatch.setattr(build.importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
+    assert build.build() == build.LIB
+    assert build.LIB in put and build.SMALLGRID_LIB in put
+    assert (build.LISTS_LIB in put) == torch_there
+    assert any("tensor_lists.cpp" in str(c) for c in started) == torch_there
