@@ -194,7 +194,16 @@ lib = load_library(LIB_PATH)
 try:
     from . import _tensor_lists
 except ImportError as e:
-    raise ImportError(f"{e}: build it with `python fp4_rollout_guided_amd/build.py`") from None
+    class _Missing:
+        """In the module's place: everything that does not use it is there all the same."""
+
+        def __init__(self, why):
+            self._why = why
+
+        def __getattr__(self, name):
+            raise ImportError(f"{self._why}: build it with `python fp4_rollout_guided_amd/build.py`")
+
+    _tensor_lists = _Missing(str(e))
 
 
 def abi_version() -> int:

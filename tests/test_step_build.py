@@ -1,6 +1,8 @@
-"""The build where torch is not installed, on the CPU: the C library needs none of it."""
+"""What the build and the import need, on the CPU: the C library does without torch, and the binding's older parts
+without the module that checks lists of tensors."""
 import importlib.util
 import os
+import subprocess
 import sys
 
 import pytest
@@ -41,3 +43,18 @@ def test_build_without_torch(monkeypatch, tmp_path, torch_there):
     assert build.LIB in put and build.SMALLGRID_LIB in put
     assert (build.LISTS_LIB in put) == torch_there
     assert any("tensor_lists.cpp" in str(c) for c in started) == torch_there
+
+
+def test_binding_without_its_list_module():
+    """What does not use the module (built for another torch, say) is there without it; what does says what is missing."""
+    code = ("import sys; sys.modules['fp4_rollout_guided_amd._tensor_lists'] = None\n"
+            "import torch, fp4_rollout_guided_amd as tr\n"
+            "assert tr.abi_version() > 0 and tr.step_revision() > 0\n"
+            "t = torch.zeros(4)\n"
+            "try:\n"
+            "    tr._outs(t, 16, None, (None, 'out', (4,), torch.float32))\n"
+            "except ImportError as e:\n"
+            "    assert 'build.py' in str(e)\n"
+            "    print('refused')\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    assert out.returncode == 0 and out.stdout.strip().endswith("refused"), out.stdout
