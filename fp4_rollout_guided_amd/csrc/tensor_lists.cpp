@@ -11,7 +11,15 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <utility>
+
 namespace {
+
+// The interpreter's lock is let go for this object's life.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // A buffer of 64-bit words, released at the end of its scope.
 struct Words {
@@ -163,9 +171,14 @@ PyObject* empties(PyObject*, PyObject* const* args, Py_ssize_t count) {
       return nullptr;
     }
     PyObject* made = nullptr;
+    const at::ScalarType type = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
     try {
-      made = THPVariable_Wrap(
-          at::empty(at::IntArrayRef(dims, (size_t)rank), like.dtype(reinterpret_cast<THPDtype*>(dtype)->scalar_type)));
+      at::Tensor t;
+      {
+        Unlocked unlocked;  // an allocation may take long
+        t = at::empty(at::IntArrayRef(dims, (size_t)rank), like.dtype(type));
+      }
+      made = THPVariable_Wrap(std::move(t));
     } catch (...) {
       Py_DECREF(out);
       throw;
