@@ -856,6 +856,7 @@ bool small_tiles(uint64_t n, uint64_t m) {
 
 // Few tokens are not listed: every one is computed, in its own place.
 constexpr uint64_t kFew = 64;
+constexpr uint32_t kJoinEach = 16;  // listed tokens to a workgroup where their tiles are joined
 constexpr uint32_t kFewGroups = 1024;  // workgroups for them, of 64 rows of w at least
 
 // Sums that the forward leaves for each token.
@@ -939,7 +940,8 @@ uint64_t cross_entropy_bwd_workspace_bytes(uint64_t tokens, uint32_t vocab, uint
 
 hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* lse, hipStream_t stream) {
   const ForwardSpace s(p.tokens, p.vocab, p.k);
-  if (tiles_in(p.tokens, p.vocab, 256) > kMostTiles) return hipErrorInvalidConfiguration;
+  if (tiles_in(p.tokens, p.vocab, 256) > kMostTiles || (p.tokens > kFew && p.tokens / kJoinEach >= kMostTiles))
+    return hipErrorInvalidConfiguration;
   char* const at = static_cast<char*>(p.workspace);
   const bool listed = p.tokens > kFew;
   LogitsArgs a{};
@@ -985,7 +987,7 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& p, float* loss, float* l
                        (const TopSum*)a.part, s.pitch, (uint32_t)s.tiles, (const float*)a.hit, loss, lse);
   };
   if (listed)  // neighbouring tokens' parts lie together
-    join(16u, cross_entropy_join_kernel<16>);
+    join(kJoinEach, cross_entropy_join_kernel<kJoinEach>);
   else
     join(1u, cross_entropy_join_kernel<1>);
   return hipGetLastError();
