@@ -537,6 +537,8 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
       __builtin_amdgcn_sched_barrier(0);  // a block's values at a time: all of them would not fit the registers
       const int32_t target = about.target - (int32_t)(v0 + wi);
       const bool hits = __ballot(target >= 0 && target < 16 * T::kI) != 0;
+      // rows past the last token are zero whatever w holds: grad_w's products take them in
+      const uint32_t there = about.target < 0 ? 0u : ~0u;
 #pragma unroll
       for (int q = 0; q < T::kI / 2; ++q) {
         uint32_t u[4];
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(256, kPerCu) void cross_entropy_logits_kernel(Logit
             if (hits && target == (int32_t)row) v -= 1.f;
             d[o] = ends && v0 + wi + row >= v_end ? 0.f : v * about.over;
           }
-          u[e / 2] = two_bf16(d[0], d[1]);
+          u[e / 2] = two_bf16(d[0], d[1]) & there;
         }
         block.put(16 * (j & 1) + r, 4 * q + g, make_uint4(u[0], u[1], u[2], u[3]));
       }

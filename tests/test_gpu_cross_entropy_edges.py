@@ -40,3 +40,35 @@ def test_confident_tokens_lose_nothing(device, tokens, vocab, scale):
     each = torch.expm1(2 * size * ((k + 3) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -21)
     near = want * each + (100 + vocab / 64) * 2.0 ** -24 + want * 2.0 ** -22
     assert ((loss.double() - want).abs() <= near)[largest].all()
+
+
+@pytest.mark.parametrize("tokens", [256, 300, 1100])
+def test_vocabulary_rows_of_minus_infinity(device, tokens):
+    """An entry whose logit is -infinity for every token has no probability: the loss and the other rows' gradients are
+    those without it, and its own row's gradient is zero, however the rows fill their tiles."""
+    import fp4_rollout_guided_amd as tr
+    _say("case rows of -infinity", tokens)
+    g = torch.Generator(device=device)
+    g.manual_seed(tokens)
+    vocab, k = 700, 96
+    x = torch.randn(tokens, k, generator=g, device=device).to(torch.bfloat16)
+    x[:, 0] = 1.0
+    w = (torch.randn(vocab, k, generator=g, device=device) / k ** 0.5).to(torch.bfloat16)
+    targets = torch.randint(5, vocab - 5, (tokens,), generator=g, device=device)
+    targets = torch.where(targets == 300, 301, targets)
+    grad = torch.randn(tokens, generator=g, device=device)
+    gone = [3, 300, vocab - 1]
+    w[gone, 0] = -float("inf")
+    loss, lse = tr.linear_cross_entropy(x, w, targets)
+    without = w.clone()
+    without[gone] = 0
+    keep = torch.ones(vocab, dtype=torch.bool, device=device)
+    keep[gone] = False
+    place = torch.cumsum(keep, 0) - 1
+    want, want_lse, has = U.loss(x, w[keep], place[targets])
+    tol = U.loss_tolerance(x, w[keep], has, 1.0, want_lse)
+    assert ((lse.double() - want_lse).abs() <= tol).all() and ((loss.double() - want).abs() <= 2 * tol).all()
+    _, gw = tr.linear_cross_entropy_bwd(grad, x, w, targets, lse, want_x=False)
+    _, ww, _, sw = U.loss_gradients(grad, x, w[keep], place[targets])
+    assert not gw[gone].any()
+    U.gradients_close(gw[keep], ww, sw, tokens + 8, x, w[keep], 1.0, ("minus infinity", "grad_w"))
