@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import step_util as U
+from tests.test_gpu_cross_entropy import check, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,21 @@ def test_vocabulary_rows_of_minus_infinity(device, tokens):
     _, ww, _, sw = U.loss_gradients(grad, x, w[keep], place[targets])
     assert not gw[gone].any()
     U.gradients_close(gw[keep], ww, sw, tokens + 8, x, w[keep], 1.0, ("minus infinity", "grad_w"))
+
+
+# the products in tiles of 256 (grad_w of the last case in those of 128), over more stages than the ring holds: k past whole
+# tiles and with a last half stage, grad_x in parts, a last slice shorter than the others, ignored tokens
+@pytest.mark.parametrize("tokens,vocab,k,ignored", [(4000, 20000, 2080, 0.3), (4096, 33000, 2048, 0.0), (33000, 16600, 1056, 0.2)])
+def test_tiles_of_the_largest_calls(device, tokens, vocab, k, ignored):
+    import fp4_rollout_guided_amd as tr
+    _say("case largest tiles", tokens, vocab, k)
+    check(tr, *inputs(tokens, vocab, k, device, ignored=ignored), 0.8, (tokens, vocab, k))
+
+
+# few tokens whose rows are multiples of 4 KiB: each workgroup begins at a place of its own in k, several tiles to a share
+@pytest.mark.parametrize("tokens,vocab,k", [(1, 65536 + 333, 2048), (33, 131072 + 77, 2048), (64, 100003, 4096), (16, 140000, 4096),
+                                            (32, 70000, 6144), (5, 300, 2048), (64, 17, 2048)])
+def test_few_tokens_of_long_rows(device, tokens, vocab, k):
+    import fp4_rollout_guided_amd as tr
+    _say("case few tokens, long rows", tokens, vocab, k)
+    check(tr, *inputs(tokens, vocab, k, device, ignored=0.2 if tokens > 1 else 0.0), 1.1, (tokens, vocab, k))
