@@ -34,6 +34,7 @@ namespace trace_dev {
 
 using trace_host::AdamwScalars;
 using trace_host::AdamwTensor;
+using trace_host::mix_bits;
 
 constexpr uint32_t kAdamThreads = 256;
 constexpr uint32_t kAdamChunk = 4096;
@@ -63,17 +64,6 @@ static_assert(sizeof(AdamwBatch<true>) + sizeof(AdamwScalars) + 16 <= 4096, "ker
 static_assert(sizeof(AdamwBatch<false>) + sizeof(AdamwScalars) + 16 <= 4096, "kernel arguments");
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// A 32-bit integer to another one, each bit of which depends on all of its
-// bits: shifts and products with odd numbers, the fractions of the square roots
-// of two and three.
-__host__ __device__ inline uint32_t mix_bits(uint32_t h) {
-  h ^= h >> 16;
-  h *= 0x6a09e667u;
-  h ^= h >> 15;
-  h *= 0xbb67ae85u;
-  return h ^ (h >> 16);
-}
 
 // kPer consecutive elements of a tensor in fp32 or bf16, raw, at element i of
 // `from`; kWhole: all of them exist, otherwise the first `left` do.

@@ -93,14 +93,6 @@ trace_status route_bwd(const float* grad_weights, const float* grad_balance, con
 
 constexpr int32_t kMaxTensors = 1 << 20;
 
-uint32_t mix_bits(uint32_t h) {  // the kernel's
-  h ^= h >> 16;
-  h *= 0x6a09e667u;
-  h ^= h >> 15;
-  h *= 0xbb67ae85u;
-  return h ^ (h >> 16);
-}
-
 struct Span {
   uintptr_t lo, hi;
   bool written;
@@ -189,7 +181,7 @@ trace_status adamw(const trace_adamw_tensor* tensors, int32_t count, const trace
   s.decay = (float)(1 - o->lr * o->weight_decay);
   s.rate = (float)(o->lr / rest1);
   s.root = (float)(1 / sqrt(rest2));
-  s.key = mix_bits(mix_bits((uint32_t)o->seed) + (uint32_t)(o->seed >> 32));
+  s.key = trace_host::mix_bits(trace_host::mix_bits((uint32_t)o->seed) + (uint32_t)(o->seed >> 32));
   const trace_host::AdamwTypes types{o->param_bf16 != 0, o->grad_bf16 != 0, mx8, o->randomly != 0};
   static_assert(sizeof(trace_host::AdamwTensor) == sizeof(trace_adamw_tensor), "the same layout");
   return launch_status(trace_host::launch_adamw(reinterpret_cast<const trace_host::AdamwTensor*>(tensors),

@@ -44,6 +44,17 @@ hipError_t launch_route_bwd(const RouteArgs& p, const float* grad_weights, const
                             hipStream_t stream);
 
 // The optimiser step.
+
+// A 32-bit integer to another one, each bit of which depends on all of its
+// bits: shifts and products with odd numbers, the fractions of the square roots
+// of two and three.  The seed's on the host, each element's place on the GPU.
+__host__ __device__ inline uint32_t mix_bits(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x6a09e667u;
+  h ^= h >> 15;
+  h *= 0xbb67ae85u;
+  return h ^ (h >> 16);
+}
 struct AdamwTensor {
   void* param;
   const void* grad;
