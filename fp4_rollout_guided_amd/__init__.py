@@ -1541,7 +1541,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     params: all fp32 or all bf16; grads: likewise, independently.  exp_avgs,
     exp_avg_sqs: fp32 tensors, or MXFP8 records (scales u8[ceil(n/32)], codes
     u8[n]) of the first moment and of the second one's square root, zeros to
-    begin with.  step: 1 for the first.  grad_scale: fp32[1] on the device, a
+    begin with (the root keeps its mean; its square settles some 5% above that
+    of fp32 states with beta2 = 0.999).  step: 1 for the first.  grad_scale: fp32[1] on the device, a
     factor of every gradient (clipping, unscaling).  copies: bf16 tensors that
     fp32 parameters are rounded into (the forward's weights).  seed: random
     roundings of the records and of bf16 parameters, which keep their means;

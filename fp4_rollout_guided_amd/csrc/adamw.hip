@@ -13,13 +13,17 @@
 // by 0.05% a step at most downwards, and codes lie 6 to 12% apart.  They are
 // rounded to either neighbour with the probability that keeps the mean, by random
 // bits from the caller's seed and the element's place.  Parameters in bf16
-// are rounded likewise where a seed is given, or to nearest.
+// are rounded likewise where a seed is given, or to nearest.  It is the root whose mean is
+// kept: v, its square, gains the roundings' variance on every step, and under steady
+// gradients settles 5% above their mean square with b2 = 0.999, 4% with 0.99, 2.6% with 0.95
+// (8192 elements simulated), which makes steps 1 to 2.5% shorter.
 //
 // Bound by memory: each element's bytes once in, once out, 16 bytes per lane of
 // an fp32 tensor.  A workgroup owns 4096 consecutive elements of one tensor and
 // loads all of them before the first arithmetic.  94 million elements with fp32 states
 // and bf16 gradients and copies: 0.45 ms, 5.8 TB/s.  With 8-bit states and bf16 parameters the
-// arithmetic counts (two records, random bits, exact root and quotient): 0.24 ms, 4.0 TB/s.
+// arithmetic counts (two records, random bits, exact root and quotient): 0.23 to 0.26 ms between
+// cards, 4.2 to 3.7 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -248,7 +248,7 @@ __device__ __forceinline__ uint32_t rank_key(float z, uint32_t e) {
 }
 
 // Bound by the arithmetic of the rounds: 16384 rows of 128 in fp32, eight to a row, 9.5
-// us (a copy of them takes 2), and the totals 5; 65573 rows of 256 in bf16, six to a row, 36 us
+// us (a copy of them takes 2), and the totals 5; 65573 rows of 256 in bf16, six to a row, 32 us
 // together.  24 rows of 128: 6.6 us, the latencies of one workgroup.
 template <bool kBf16, int kLanes, int kPer, int kVec>
 __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p, const uint8_t* __restrict__ valid,
@@ -393,8 +393,8 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs p
 // Rows whose ids are all negative get zeros.
 // What the chosen experts add goes to their lanes by way of LDS, which is zero but
 // there (each lane looking through its experts for each of them was a third of the
-// arithmetic).  65573 rows of 256 in bf16, six to a row: 20 us, 3.7 TB/s, bound by
-// arithmetic; 16384 rows of 128 in fp32: 6.7 us.
+// arithmetic).  65573 rows of 256 in bf16, six to a row: 17 us, 4.2 TB/s, bound by
+// arithmetic; 16384 rows of 128 in fp32: 6.6 us.
 template <bool kBf16, int kLanes, int kPer, int kVec>
 __global__ __launch_bounds__(256) void expert_route_bwd_kernel(RouteArgs p, const float* __restrict__ grad_weights,
                                                                const float* __restrict__ grad_balance,

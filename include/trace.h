@@ -837,7 +837,8 @@ TRACE_API trace_status trace_expert_route_bwd_f32(const float* grad_weights, con
  *   copy   : bf16[n], param rounded to nearest (fp32 params), or NULL.
  * 8-bit states, and bf16 params with `randomly` not 0, are rounded to one of
  * their two neighbours at random, so that the mean is kept, by bits of `seed`
- * and the element's place in the list; other roundings are to nearest.
+ * and the element's place in the list; other roundings are to nearest.  The mean
+ * is sqrt(v)'s: v itself settles some 5% above that of fp32 states (beta2 = 0.999).
  * The tensors are the same in type.  Data 16-byte aligned (codes 8-byte,
  * scale bytes any).  No element may belong to two tensors. */
 typedef struct trace_adamw_tensor {
