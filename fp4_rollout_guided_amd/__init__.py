@@ -63,6 +63,7 @@ and ``GuidedFakeQuant``, ``MxMatmul``, ``ExpertDispatch``, ``ExpertCombine``,
 autograd functions; ``AdamW`` keeps the optimiser's states.
 """
 import ctypes
+import importlib
 import math
 import os
 from array import array
@@ -192,7 +193,7 @@ def load_library(path):
 
 lib = load_library(LIB_PATH)
 try:
-    from . import _tensor_lists
+    _tensor_lists = importlib.import_module(__name__ + "._tensor_lists")
 except ImportError as e:
     class _Missing:
         """In the module's place: everything that does not use it is there all the same."""

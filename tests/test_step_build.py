@@ -58,3 +58,14 @@ def test_binding_without_its_list_module():
             "    print('refused')\n")
     out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     assert out.returncode == 0 and out.stdout.strip().endswith("refused"), out.stdout
+
+
+def test_list_module_built_after_the_first_import():
+    """Loaded again, the binding finds the module that was missing before."""
+    code = ("import importlib, sys; name = 'fp4_rollout_guided_amd._tensor_lists'; sys.modules[name] = None\n"
+            "import fp4_rollout_guided_amd as tr\n"
+            "del sys.modules[name]\n"
+            "importlib.reload(tr)\n"
+            "assert tr._tensor_lists.changed([]) is None\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    assert out.returncode == 0, out.stdout
